@@ -291,6 +291,109 @@ int a4w4_gemm_noalloc(const void* A_bf16, int M, int K, const void* Wq, const vo
                       void* C_bf16, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Paged key/value cache in MXFP4, and attention over it (no counterpart on the
+ * source pages: the attention side of a decoder whose GEMMs are the ones above,
+ * with the same E2M1 / E8M0 rule).
+ *
+ * Cache layout.  Pages of page_size tokens (16, 32, 64 or 128), each page_size /
+ * 16 chunks of 16 tokens per key/value head.  Chunk c (of page_size / 16) of
+ * head h of page p starts at byte ((p * Hkv + h) * (page_size / 16) + c) * 17 * D
+ * and holds, for tokens r = 0..15 of the chunk (D = 64 or 128, J = D / 32):
+ *   key codes     8*D bytes   the byte of dimensions n, n+1 (n even) of token r
+ *                             at r*(D/2) + (t*J + j)*4 + b, with j = n / 32,
+ *                             t = n % 32 / 8, b = n % 8 / 2
+ *   key scales    D/2 bytes   E8M0 of 32-block j of token r at r*J + j
+ *   value codes   8*D bytes   the byte of dimensions n, n+1 of token r at
+ *                             (r/8)*4*D + (g*4 + r%8/2)*(D/8) + (r%2)*(D/16) + i,
+ *                             with i = n / 16, g = n % 16 / 2
+ *   value scales  D/2 bytes   as the key scales
+ * (code of dimension n in the low nibble).  A thread of the attention kernels
+ * finds the codes of its tensor-core fragments in one run of bytes: keys in
+ * blocks of 8 dimensions, values in pairs of tokens.  Slot s is token
+ * s % page_size of page s / page_size. */
+size_t a4w4_kv_cache_bytes(int num_pages, int page_size, int Hkv, int D);
+
+/* Block tables, slot map and positions of one serving step, from the requests'
+ * lengths, on the device.
+ *   past_lens [B]  tokens that each request already has in the cache
+ *   new_lens [B]   tokens it appends in this step (0: none); negative: the
+ *                  request is finished and gives its pages back
+ *   block_table [B, max_pages]  in/out: entry j of row b is the page of request
+ *                  b's tokens j*page_size ..; entries of new pages are written
+ *   free_ring [ring_size], ring_state [2] = {head, count}: the free pages, oldest
+ *                  first, at free_ring[(head + i) % ring_size], i < count
+ * Requests are served in order: a request needs ceil((past + new) / page_size) -
+ * ceil(past / page_size) pages, taken from the head of the ring.  The first one
+ * whose pages (or whose tokens, of max_tokens) do not suffice, and every later
+ * one, appends nothing in this step; a request whose past + new exceeds
+ * max_pages * page_size appends nothing and holds nobody up.  Pages of finished
+ * requests go to the ring's end in request order (ring_size >= all pages) and
+ * are taken from the next step on.
+ *   ring_state_out [2]  the new {head, count}  (not ring_state itself)
+ *   kv_lens [B]         tokens after this step (0 for a finished request; not
+ *                       past_lens itself)
+ *   cu_new [B + 1]      prefix sums of the tokens appended per request
+ *   slot_map [max_tokens], positions [max_tokens]  slot and position of each
+ *                       appended token, requests in order; -1 and 0 beyond
+ *                       cu_new[B]
+ *   refused [1]         requests with new_lens > 0 that append nothing
+ * All arrays int32 on the device.  1 <= B <= 4096, page_size 16, 32, 64 or 128,
+ * max_pages, ring_size >= 1, max_tokens >= 0, max_pages * page_size < 2^31.  A
+ * call that is repeated on its own outputs (same past_lens, new_lens and
+ * ring_state) gives the same ones.  Precondition: 0 <= past_lens, table entries
+ * of held pages and ring entries are page numbers below 2^31 / page_size. */
+int a4w4_kv_plan(const int32_t* past_lens, const int32_t* new_lens, int B, int page_size, int32_t* block_table,
+                 int max_pages, int32_t* free_ring, int ring_size, const int32_t* ring_state,
+                 int32_t* ring_state_out, int32_t* kv_lens, int32_t* cu_new, int32_t* slot_map,
+                 int32_t* positions, int max_tokens, int32_t* refused, void* stream);
+
+/* Quantises T new tokens' keys and values (BF16; the quantisation rule above)
+ * into the cache.  Token t's Hkv x D keys start at element t * k_stride of
+ * k_bf16 and are contiguous; values likewise (so both may be slices of one fused
+ * projection); 16-byte aligned, strides multiples of 8 and at least Hkv * D when
+ * T > 1.  A token whose slot is outside [0, num_pages * page_size) is skipped;
+ * two tokens with one slot leave either one's bytes.  T >= 0,
+ * num_pages * page_size < 2^31. */
+int a4w4_kv_append(const void* k_bf16, long long k_stride, const void* v_bf16, long long v_stride,
+                   const int32_t* slot_map, int T, int Hkv, int D, void* cache, int num_pages, int page_size,
+                   void* stream);
+
+/* The BF16 values (exact) of the cache rows at T slots: k_out, v_out [T, Hkv, D],
+ * zeros where the slot is outside [0, num_pages * page_size).  For handing a
+ * prefix to other code and for looking at what is cached. */
+int a4w4_kv_read(const void* cache, int num_pages, int page_size, const int32_t* slot_map, int T, int Hkv, int D,
+                 void* k_out_bf16, void* v_out_bf16, void* stream);
+
+/* Causal attention of the newest tokens of B requests over their cached keys and
+ * values (the new tokens' own included: append first).
+ *   q_bf16     row t (a new token) holds Hq x D at element t * q_stride
+ *              (16-byte aligned, stride a multiple of 8, >= Hq * D)
+ *   cu_q [B+1] rows of request b are cu_q[b] .. cu_q[b+1] - 1; at most max_q each
+ *              and total_q in all (rows beyond are not computed)
+ *   kv_lens [B], block_table [B, max_pages]  as a4w4_kv_plan writes them
+ * Query i of the n rows of request b sees the keys at positions 0 .. kv_lens[b] -
+ * n + i; query head h reads key/value head h / (Hq / Hkv).
+ *   out_bf16 [total_q, Hq, D] = softmax(sm_scale q k^T) v
+ *   lse [total_q, Hq] float, or NULL: log sum exp of the scaled scores
+ * A row that sees no key (empty request, more queries than keys) gives zeros and
+ * lse = -infinity.  Keys and values enter as the values they stand for; sums,
+ * softmax statistics and the output accumulator are fp32.  The reduction order
+ * depends on the lengths alone: results are bitwise deterministic.
+ * Hq % Hkv == 0, D 64 or 128, sm_scale finite and > 0, B >= 1, total_q >= 0, max_q >= 1,
+ * max_pages >= 1, max_pages * page_size < 2^31, num_pages * page_size < 2^31.
+ * Lengths are clamped to the table's width and page numbers to [0, num_pages):
+ * nothing outside the cache is read.  Workspace: a4w4_kv_attention_workspace_bytes
+ * bytes, 16-byte aligned, zeroed once with a4w4_workspace_init (it begins with
+ * ticket counters that each call leaves at zero; zero it again after
+ * A4W4_ERR_TIMEOUT); calls of any sizes may share one workspace one after
+ * another. */
+size_t a4w4_kv_attention_workspace_bytes(int B, int max_q, int Hq, int Hkv, int D);
+int a4w4_kv_attention(const void* q_bf16, long long q_stride, const int32_t* cu_q, int B, int total_q, int max_q,
+                      const int32_t* kv_lens, const int32_t* block_table, int max_pages, const void* cache,
+                      int num_pages, int page_size, int Hq, int Hkv, int D, float sm_scale, void* out_bf16,
+                      float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Synchronises `stream`, then returns and clears the device status word:
  * A4W4_OK, A4W4_ERR_TIMEOUT, or A4W4_ERR_LAUNCH if the stream reported an error. */
 int a4w4_get_device_status(void* stream);

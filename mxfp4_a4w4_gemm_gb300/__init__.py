@@ -27,6 +27,12 @@ from ._native import (  # noqa: F401
     a4w4_gemm_noalloc,
     a4w4_gemm_workspace_bytes,
     a4w4_get_device_status,
+    a4w4_kv_append,
+    a4w4_kv_attention,
+    a4w4_kv_attention_workspace_bytes,
+    a4w4_kv_cache_bytes,
+    a4w4_kv_plan,
+    a4w4_kv_read,
     a4w4_moe_gemm1,
     a4w4_moe_gemm1_ex,
     a4w4_moe_gemm1_workspace_bytes,

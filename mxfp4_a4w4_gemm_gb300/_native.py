@@ -15,6 +15,7 @@ LIB_PATH = os.path.join(PKG, "_lib", "liba4w4.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "a4w4.h")
 
 _c_int, _c_size, _vp, _i32p = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p
+_c_ll = ctypes.c_longlong
 
 # name -> (restype, argtypes), in the order of include/a4w4.h
 SIGNATURES = {
@@ -48,6 +49,14 @@ SIGNATURES = {
     "a4w4_moe_gemm2": (_c_int, [_vp, _vp, _c_int, _c_int, _i32p, _i32p, _i32p, _c_int, _vp, _vp, _vp, _c_int,
                                 _c_int, _vp, _vp, _c_size, _vp]),
     "a4w4_gemm_noalloc": (_c_int, [_vp, _c_int, _c_int, _vp, _vp, _c_int, _vp, _vp]),
+    "a4w4_kv_cache_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int]),
+    "a4w4_kv_plan": (_c_int, [_i32p, _i32p, _c_int, _c_int, _i32p, _c_int, _i32p, _c_int, _i32p, _i32p, _i32p, _i32p,
+                              _i32p, _i32p, _c_int, _i32p, _vp]),
+    "a4w4_kv_append": (_c_int, [_vp, _c_ll, _vp, _c_ll, _i32p, _c_int, _c_int, _c_int, _vp, _c_int, _c_int, _vp]),
+    "a4w4_kv_read": (_c_int, [_vp, _c_int, _c_int, _i32p, _c_int, _c_int, _c_int, _vp, _vp, _vp]),
+    "a4w4_kv_attention_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_int]),
+    "a4w4_kv_attention": (_c_int, [_vp, _c_ll, _i32p, _c_int, _c_int, _c_int, _i32p, _i32p, _c_int, _vp, _c_int,
+                                   _c_int, _c_int, _c_int, _c_int, ctypes.c_float, _vp, _vp, _vp, _c_size, _vp]),
     "a4w4_get_device_status": (_c_int, [_vp]),
     "a4w4_strerror": (ctypes.c_char_p, [_c_int]),
     "a4w4_set_wait_limit_ns": (None, [ctypes.c_ulonglong]),
@@ -101,6 +110,15 @@ def _ptr(x):
             raise ValueError("tensor arguments must be contiguous")
         return x.data_ptr()
     raise TypeError(f"expected a tensor, an int pointer or None, got {type(x)}")
+
+
+def _rows_ptr(x, stride):
+    """Rows of [heads, D] values, `stride` elements apart: only the rows themselves must be contiguous."""
+    if hasattr(x, "data_ptr"):
+        if x.dim() != 3 or (x.numel() > 0 and not x[0].is_contiguous()) or (x.size(0) > 1 and x.stride(0) != stride):
+            raise ValueError("rows must be a [T, heads, D] tensor with contiguous [heads, D] and the given row stride")
+        return x.data_ptr()
+    return _ptr(x)
 
 
 def _stream(s):
@@ -253,6 +271,43 @@ def a4w4_gemm_noalloc(A, M, K, Wq, Ws, N, C, stream=None):
     be serialised."""
     _check("a4w4_gemm_noalloc", lib().a4w4_gemm_noalloc(_ptr(A), M, K, _ptr(Wq), _ptr(Ws), N, _ptr(C),
                                                          _stream(stream)))
+
+
+def a4w4_kv_cache_bytes(num_pages, page_size, Hkv, D):
+    return lib().a4w4_kv_cache_bytes(num_pages, page_size, Hkv, D)
+
+
+def a4w4_kv_plan(past_lens, new_lens, B, page_size, block_table, max_pages, free_ring, ring_size, ring_state,
+                 ring_state_out, kv_lens, cu_new, slot_map, positions, max_tokens, refused, stream=None):
+    _check("a4w4_kv_plan", lib().a4w4_kv_plan(_ptr(past_lens), _ptr(new_lens), B, page_size, _ptr(block_table),
+                                              max_pages, _ptr(free_ring), ring_size, _ptr(ring_state),
+                                              _ptr(ring_state_out), _ptr(kv_lens), _ptr(cu_new), _ptr(slot_map),
+                                              _ptr(positions), max_tokens, _ptr(refused), _stream(stream)))
+
+
+def a4w4_kv_append(k, k_stride, v, v_stride, slot_map, T, Hkv, D, cache, num_pages, page_size, stream=None):
+    """Rows of k and v may be slices of one fused projection: [T, Hkv, D] views with a row stride (in elements)."""
+    _check("a4w4_kv_append", lib().a4w4_kv_append(_rows_ptr(k, k_stride), k_stride, _rows_ptr(v, v_stride), v_stride,
+                                                  _ptr(slot_map), T, Hkv, D, _ptr(cache), num_pages, page_size,
+                                                  _stream(stream)))
+
+
+def a4w4_kv_read(cache, num_pages, page_size, slot_map, T, Hkv, D, k_out, v_out, stream=None):
+    _check("a4w4_kv_read", lib().a4w4_kv_read(_ptr(cache), num_pages, page_size, _ptr(slot_map), T, Hkv, D,
+                                              _ptr(k_out), _ptr(v_out), _stream(stream)))
+
+
+def a4w4_kv_attention_workspace_bytes(B, max_q, Hq, Hkv, D):
+    return lib().a4w4_kv_attention_workspace_bytes(B, max_q, Hq, Hkv, D)
+
+
+def a4w4_kv_attention(q, q_stride, cu_q, B, total_q, max_q, kv_lens, block_table, max_pages, cache, num_pages,
+                      page_size, Hq, Hkv, D, sm_scale, out, lse=None, ws=None, ws_bytes=0, stream=None):
+    """q: a [total_q, Hq, D] view with a row stride (in elements), e.g. a slice of a fused projection."""
+    _check("a4w4_kv_attention",
+           lib().a4w4_kv_attention(_rows_ptr(q, q_stride), q_stride, _ptr(cu_q), B, total_q, max_q, _ptr(kv_lens),
+                                   _ptr(block_table), max_pages, _ptr(cache), num_pages, page_size, Hq, Hkv, D,
+                                   sm_scale, _ptr(out), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream)))
 
 
 def a4w4_get_device_status(stream=None):

@@ -1,6 +1,7 @@
 // api.cu -- the extern "C" boundary of liba4w4.so (declared in include/a4w4.h):
 // argument validation, device checks, launch, and the device status word.
 #include <atomic>
+#include <cfloat>
 #include <cstdint>
 #include <cstdio>
 
@@ -65,6 +66,19 @@ int sizing_sms() {
 }
 
 bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The key/value cache's shape: slots are 32-bit.
+bool page_size_ok(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128; }
+bool kv_shape_ok(int num_pages, int page_size, int Hkv, int D) {
+  return page_size_ok(page_size) && Hkv > 0 && Hkv <= 65535 && (D == 64 || D == 128) &&
+         static_cast<long long>(num_pages) * page_size <= INT32_MAX;
+}
+// Rows of H x D BF16 values `stride` elements apart, read 16 bytes at a time.
+bool row_stride_ok(long long stride, int rows, int H, int D) {
+  return stride % 8 == 0 && (rows <= 1 || stride >= static_cast<long long>(H) * D);
+}
 
 cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
@@ -335,6 +349,92 @@ int a4w4_moe_gemm2(const void* A_q, const void* A_s, int T, int I, const int32_t
                                                    topk, topk_weights, W2q, W2s, E, D, partial, st, wait, status, sms);
   if (rc != 0) return rc == -1 ? A4W4_ERR_ARG : rc;
   return a4w4::launch_moe_sum(partial, T, topk, D, Y_bf16, st, sms);
+}
+
+// ---------------------------------------------------------------------------
+// Paged MXFP4 key/value cache and attention
+
+size_t a4w4_kv_cache_bytes(int num_pages, int page_size, int Hkv, int D) {
+  if (num_pages <= 0 || !kv_shape_ok(num_pages, page_size, Hkv, D)) return 0;
+  return static_cast<size_t>(num_pages) * Hkv * (page_size / 16) * 17 * D;
+}
+
+int a4w4_kv_plan(const int32_t* past_lens, const int32_t* new_lens, int B, int page_size, int32_t* block_table,
+                 int max_pages, int32_t* free_ring, int ring_size, const int32_t* ring_state,
+                 int32_t* ring_state_out, int32_t* kv_lens, int32_t* cu_new, int32_t* slot_map,
+                 int32_t* positions, int max_tokens, int32_t* refused, void* stream) {
+  if (B <= 0 || B > 4096 || !page_size_ok(page_size) || max_pages <= 0 || ring_size <= 0 || max_tokens < 0)
+    return A4W4_ERR_ARG;
+  if (static_cast<long long>(max_pages) * page_size > INT32_MAX) return A4W4_ERR_ARG;
+  if (!aligned4(past_lens) || !aligned4(new_lens) || !aligned4(block_table) || !aligned4(free_ring) ||
+      !aligned4(ring_state) || !aligned4(ring_state_out) || !aligned4(kv_lens) || !aligned4(cu_new) ||
+      !aligned4(refused) || (max_tokens > 0 && (!aligned4(slot_map) || !aligned4(positions))))
+    return A4W4_ERR_ARG;
+  if (ring_state == ring_state_out || past_lens == kv_lens || new_lens == kv_lens) return A4W4_ERR_ARG;
+  const int sms = current_device_sms();
+  if (sms < 0) return sms;
+  return a4w4::launch_kv_plan(past_lens, new_lens, B, page_size, block_table, max_pages, free_ring, ring_size,
+                              ring_state, ring_state_out, kv_lens, cu_new, slot_map, positions, max_tokens, refused,
+                              as_stream(stream), sms);
+}
+
+int a4w4_kv_append(const void* k_bf16, long long k_stride, const void* v_bf16, long long v_stride,
+                   const int32_t* slot_map, int T, int Hkv, int D, void* cache, int num_pages, int page_size,
+                   void* stream) {
+  if (T < 0 || num_pages <= 0 || !kv_shape_ok(num_pages, page_size, Hkv, D)) return A4W4_ERR_ARG;
+  if (!row_stride_ok(k_stride, T, Hkv, D) || !row_stride_ok(v_stride, T, Hkv, D)) return A4W4_ERR_ARG;
+  if (!aligned16(cache)) return A4W4_ERR_ARG;
+  if (T > 0 && (!aligned16(k_bf16) || !aligned16(v_bf16) || !aligned4(slot_map))) return A4W4_ERR_ARG;
+  const int sms = current_device_sms();
+  if (sms < 0) return sms;
+  if (T == 0) return A4W4_OK;
+  return a4w4::launch_kv_append(k_bf16, k_stride, v_bf16, v_stride, slot_map, T, Hkv, D, cache, num_pages, page_size,
+                                as_stream(stream), sms);
+}
+
+int a4w4_kv_read(const void* cache, int num_pages, int page_size, const int32_t* slot_map, int T, int Hkv, int D,
+                 void* k_out_bf16, void* v_out_bf16, void* stream) {
+  if (T < 0 || num_pages <= 0 || !kv_shape_ok(num_pages, page_size, Hkv, D) || !aligned16(cache)) return A4W4_ERR_ARG;
+  if (T > 0 && (!aligned16(k_out_bf16) || !aligned16(v_out_bf16) || !aligned4(slot_map))) return A4W4_ERR_ARG;
+  const int sms = current_device_sms();
+  if (sms < 0) return sms;
+  if (T == 0) return A4W4_OK;
+  return a4w4::launch_kv_read(cache, num_pages, page_size, slot_map, T, Hkv, D, k_out_bf16, v_out_bf16,
+                              as_stream(stream), sms);
+}
+
+size_t a4w4_kv_attention_workspace_bytes(int B, int max_q, int Hq, int Hkv, int D) {
+  if (B <= 0 || max_q <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
+  return a4w4::kv_attention_ws_bytes(B, max_q, Hq, Hkv, D, sizing_sms());
+}
+
+int a4w4_kv_attention(const void* q_bf16, long long q_stride, const int32_t* cu_q, int B, int total_q, int max_q,
+                      const int32_t* kv_lens, const int32_t* block_table, int max_pages, const void* cache,
+                      int num_pages, int page_size, int Hq, int Hkv, int D, float sm_scale, void* out_bf16,
+                      float* lse, void* ws, size_t ws_bytes, void* stream) {
+  if (B <= 0 || total_q < 0 || max_q <= 0 || max_pages <= 0 || num_pages <= 0 ||
+      !kv_shape_ok(num_pages, page_size, Hkv, D) || Hq <= 0 || Hq % Hkv != 0)
+    return A4W4_ERR_ARG;
+  if (static_cast<long long>(max_pages) * page_size > INT32_MAX || !row_stride_ok(q_stride, total_q, Hq, D))
+    return A4W4_ERR_ARG;
+  // grid and tile counts are 32-bit
+  if (static_cast<long long>(B) * max_q > INT32_MAX / Hq) return A4W4_ERR_ARG;
+  if (!(sm_scale > 0.f) || !(sm_scale <= FLT_MAX)) return A4W4_ERR_ARG;
+  if (!aligned16(cache) || !aligned4(cu_q) || !aligned4(kv_lens) || !aligned4(block_table)) return A4W4_ERR_ARG;
+  if (total_q > 0 && (!aligned16(q_bf16) || !aligned16(out_bf16))) return A4W4_ERR_ARG;
+  if (lse != nullptr && !aligned4(lse)) return A4W4_ERR_ARG;
+  const size_t need = a4w4_kv_attention_workspace_bytes(B, max_q, Hq, Hkv, D);
+  if (need > 0 && (ws_bytes < need || !aligned16(ws))) return A4W4_ERR_WORKSPACE;
+  const int sms = current_device_sms();
+  if (sms < 0) return sms;
+  unsigned int* status = status_ptr();
+  if (status == nullptr) return A4W4_ERR_LAUNCH;
+  if (total_q == 0) return A4W4_OK;
+  const a4w4::KvAttentionArgs p{static_cast<const uint16_t*>(q_bf16), q_stride, cu_q, kv_lens, block_table,
+                                static_cast<const uint8_t*>(cache), static_cast<uint16_t*>(out_bf16), lse, ws, B,
+                                total_q, max_q, max_pages, num_pages, page_size, Hq, Hkv, sm_scale,
+                                g_wait_ns.load(std::memory_order_relaxed), status};
+  return a4w4::launch_kv_attention(p, D, as_stream(stream), sms);
 }
 
 // ---------------------------------------------------------------------------

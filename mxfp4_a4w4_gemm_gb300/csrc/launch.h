@@ -133,4 +133,32 @@ int launch_moe_sort_aux(const int32_t* ids, int T, int topk, int E, int bm, int3
                         void* ws, cudaStream_t st, int sms, unsigned long long wait_ns, unsigned int* status);
 size_t moe_sort_aux_ws_bytes(int T, int topk, int E, int sms);
 
+// Paged MXFP4 key/value cache (kv.cu) and attention over it (kv_attention.cu).
+int launch_kv_plan(const int32_t* past_lens, const int32_t* new_lens, int B, int page_size, int32_t* block_table,
+                   int max_pages, int32_t* free_ring, int ring_size, const int32_t* ring_state,
+                   int32_t* ring_state_out, int32_t* kv_lens, int32_t* cu_new, int32_t* slot_map, int32_t* positions,
+                   int max_tokens, int32_t* refused, cudaStream_t st, int sms);
+int launch_kv_append(const void* k, long long k_stride, const void* v, long long v_stride, const int32_t* slot_map,
+                     int T, int Hkv, int D, void* cache, int num_pages, int page_size, cudaStream_t st, int sms);
+int launch_kv_read(const void* cache, int num_pages, int page_size, const int32_t* slot_map, int T, int Hkv, int D,
+                   void* k, void* v, cudaStream_t st, int sms);
+
+struct KvAttentionArgs {
+  const uint16_t* q;            // row t, head h at q + t * q_stride + h * D
+  long long q_stride;
+  const int32_t* cu_q;          // [B + 1]
+  const int32_t* kv_lens;       // [B]
+  const int32_t* block_table;   // [B, max_pages]
+  const uint8_t* cache;
+  uint16_t* out;                // [total_q, Hq, D]
+  float* lse;                   // [total_q, Hq] or nullptr
+  void* ws;
+  int B, total_q, max_q, max_pages, num_pages, page_size, Hq, Hkv;
+  float sm_scale;
+  unsigned long long wait_ns;
+  unsigned int* status;
+};
+size_t kv_attention_ws_bytes(int B, int max_q, int Hq, int Hkv, int D, int sms);
+int launch_kv_attention(const KvAttentionArgs& p, int D, cudaStream_t st, int sms);
+
 }  // namespace a4w4

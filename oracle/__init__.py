@@ -33,9 +33,10 @@ Modules:
   gemm   -- the dense A4W4 GEMM (exact products, fp64 sums, BF16 output)
   moe    -- routed-row sort, the grouped GEMM1 + SwiGLU (or SiLU) + MXFP4
             requant, and GEMM2 (down projection, top-k weighted sum)
+  kv     -- the paged key/value cache: step plan, cache bytes, attention
 
 Parity status of every function is pinned by ``tests/test_oracle_*.py``
 (-m "not gpu"); none is "parity unpinned".
 """
 
-from . import mxfp4, gemm, moe  # noqa: F401
+from . import mxfp4, gemm, moe, kv  # noqa: F401
