@@ -405,7 +405,7 @@ int a4w4_kv_read(const void* cache, int num_pages, int page_size, const int32_t*
 
 size_t a4w4_kv_attention_workspace_bytes(int B, int max_q, int Hq, int Hkv, int D) {
   if (B <= 0 || max_q <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
-  return a4w4::kv_attention_ws_bytes(B, max_q, Hq, Hkv, D, sizing_sms());
+  return a4w4::kv_attention_ws_bytes(max_q, Hq / Hkv, D, sizing_sms());
 }
 
 int a4w4_kv_attention(const void* q_bf16, long long q_stride, const int32_t* cu_q, int B, int total_q, int max_q,
@@ -417,8 +417,10 @@ int a4w4_kv_attention(const void* q_bf16, long long q_stride, const int32_t* cu_
     return A4W4_ERR_ARG;
   if (static_cast<long long>(max_pages) * page_size > INT32_MAX || !row_stride_ok(q_stride, total_q, Hq, D))
     return A4W4_ERR_ARG;
-  // grid and tile counts are 32-bit
+  // the kernels count rows and steps of 32 keys in 32 bits
   if (static_cast<long long>(B) * max_q > INT32_MAX / Hq) return A4W4_ERR_ARG;
+  if (static_cast<long long>(B) * Hkv > INT32_MAX / ((static_cast<long long>(max_pages) * page_size + 31) / 32))
+    return A4W4_ERR_ARG;
   if (!(sm_scale > 0.f) || !(sm_scale <= FLT_MAX)) return A4W4_ERR_ARG;
   if (!aligned16(cache) || !aligned4(cu_q) || !aligned4(kv_lens) || !aligned4(block_table)) return A4W4_ERR_ARG;
   if (total_q > 0 && (!aligned16(q_bf16) || !aligned16(out_bf16))) return A4W4_ERR_ARG;
@@ -433,6 +435,7 @@ int a4w4_kv_attention(const void* q_bf16, long long q_stride, const int32_t* cu_
   const a4w4::KvAttentionArgs p{static_cast<const uint16_t*>(q_bf16), q_stride, cu_q, kv_lens, block_table,
                                 static_cast<const uint8_t*>(cache), static_cast<uint16_t*>(out_bf16), lse, ws, B,
                                 total_q, max_q, max_pages, num_pages, page_size, Hq, Hkv, sm_scale,
+                                65536u / (Hq / Hkv) + (65536u % (Hq / Hkv) != 0 ? 1u : 0u),
                                 g_wait_ns.load(std::memory_order_relaxed), status};
   return a4w4::launch_kv_attention(p, D, as_stream(stream), sms);
 }

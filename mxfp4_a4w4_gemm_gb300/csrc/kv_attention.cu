@@ -2,6 +2,7 @@
 // cache (include/a4w4.h).
 #include "device.cuh"
 #include "kv.cuh"
+#include "kv_walk.cuh"
 #include "launch.h"
 
 #include <cmath>
@@ -29,12 +30,10 @@ __global__ void __launch_bounds__(128) kv_attention_rows_kernel(const KvAttentio
   griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, b = blockIdx.z, hq = blockIdx.y, i = blockIdx.x;
-  const int r0 = p.cu_q[b], n = min(p.cu_q[b + 1] - r0, p.max_q);
-  const long long row = static_cast<long long>(r0) + i;
-  if (i >= n || row < 0 || row >= p.total_q) return;
-  const int cap = p.max_pages * p.page_size;
-  const int len = max(0, min(p.kv_lens[b], cap));
-  const int seen = max(0, len - n + i + 1);
+  const KvRequest rq = kv_request(p, b);
+  if (i >= rq.rows) return;
+  const long long row = static_cast<long long>(rq.row0) + i;
+  const int seen = max(0, rq.len - rq.all + i + 1);
   const int h = hq / (p.Hq / p.Hkv);
   for (int d = tid; d < D; d += 128)
     s_q[d] = __uint_as_float(static_cast<uint32_t>(p.q[row * p.q_stride + hq * D + d]) << 16) * p.sm_scale;
@@ -91,10 +90,12 @@ __global__ void __launch_bounds__(128) kv_attention_rows_kernel(const KvAttentio
 
 }  // namespace
 
-// The ticket counters of units split over CTAs come first.
-size_t kv_attention_ws_bytes(int, int, int, int, int, int) { return 16384; }
+size_t kv_attention_ws_bytes(int max_q, int group, int D, int sms) {
+  return kv_decode_ws_bytes(max_q <= 16 / group ? max_q * group : 16, D, sms);
+}
 
 int launch_kv_attention(const KvAttentionArgs& p, int D, cudaStream_t st, int sms) {
+  if (p.max_q <= 16 / (p.Hq / p.Hkv)) return launch_kv_decode(p, D, st, sms);
   const dim3 grid(p.max_q, p.Hq, p.B);
   if (D == 64) kv_attention_rows_kernel<64><<<grid, 128, 0, st>>>(p);
   else kv_attention_rows_kernel<128><<<grid, 128, 0, st>>>(p);

@@ -1,0 +1,119 @@
+// kv_walk.cuh -- how the attention kernels share out ragged work.
+//
+// A unit is what one softmax runs over for one block of query rows: request b,
+// key/value head h (and block of rows).  Its keys are cut into steps; the steps
+// of all units, in order, form one line, which is cut into equal runs, one per
+// worker: every worker gets the same work to within one step whatever the
+// lengths are, and units that are cut are joined afterwards.  The cut depends on
+// the lengths alone.
+#pragma once
+
+#include <cstdint>
+
+#include "device.cuh"
+#include "launch.h"
+
+namespace a4w4 {
+
+// The first kTickets 32-bit words of the workspace count the CTAs that have
+// stored their part of a cut unit (indexed by the unit's first CTA, of which a
+// cut unit is the last one); the last to arrive joins the parts and puts the
+// counter back to zero.
+constexpr int kTickets = 4096;
+
+// Lengths of request b as the kernels use them: clamped, so that nothing in the
+// arrays can lead outside the buffers.
+struct KvRequest {
+  int row0, rows;   // new tokens: first row, and rows to compute
+  int all;          // new tokens as cu_q has them: row i sees the keys below len - all + i + 1
+  int len;          // keys
+};
+__device__ __forceinline__ KvRequest kv_request(const KvAttentionArgs& p, int b) {
+  KvRequest r;
+  const int c0 = __ldg(p.cu_q + b), c1 = __ldg(p.cu_q + b + 1);
+  const int cap = p.max_pages * p.page_size;
+  r.row0 = c0;
+  r.all = c0 < 0 ? 0 : max(0, c1 - c0);
+  r.rows = min(r.all, max(0, min(p.total_q - c0, p.max_q)));
+  r.len = max(0, min(__ldg(p.kv_lens + b), cap));
+  return r;
+}
+
+// Entry i of request b's row of the block table.
+__device__ __forceinline__ int kv_page(const KvAttentionArgs& p, int b, int i) {
+  const int id = __ldg(p.block_table + static_cast<long long>(b) * p.max_pages + i);
+  return min(max(id, 0), p.num_pages - 1);
+}
+
+// The line's cut: the first `more` workers take each + 1 steps, the others `each`.
+struct KvShare {
+  uint32_t total;           // steps of the line
+  uint32_t workers;
+  uint32_t each, more;
+  __device__ __forceinline__ uint32_t first(uint32_t v) const { return v * each + min(v, more); }
+  // the worker that holds step f
+  __device__ __forceinline__ uint32_t holder(uint32_t f) const {
+    const uint32_t wide = more * (each + 1);
+    return f < wide ? f / (each + 1) : more + (f - wide) / each;
+  }
+};
+
+// Where a worker's run starts: request b, `rest` steps after its first.
+struct KvStart {
+  uint32_t b, rest;
+};
+
+// Block-wide: cuts the line (`steps(b)` steps for the units of request b; fewer
+// than 2^31 in all) for at most gridDim.x * PER workers of at least `least`
+// steps; warp w < PER learns the start of worker blockIdx.x * PER + w, if there
+// is one.  Every thread calls it; scratch: THREADS + 32 words of shared memory.
+// Returns false if the CTA has nothing to do.
+template <int THREADS, int PER, typename Steps>
+__device__ __forceinline__ bool kv_locate(int B, Steps steps, uint32_t least, uint32_t* scratch, KvShare& share,
+                                          KvStart& start) {
+  constexpr int W = THREADS / 32;
+  static_assert(W <= 32 && PER <= W, "a search per warp");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (B + THREADS - 1) / THREADS;             // requests per thread
+  const int b0 = tid * per, b1 = min(B, b0 + per);
+  uint32_t sum = 0;
+  for (int b = b0; b < b1; ++b) sum += steps(b);
+  uint32_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  scratch[tid] = inc;                                       // within the warp
+  __syncthreads();
+  uint32_t wsum = lane < W ? scratch[lane * 32 + 31] : 0u;  // the warps' sums, scanned by every warp
+#pragma unroll
+  for (int o = 1; o < W; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, wsum, o);
+    if (lane >= o) wsum += u;
+  }
+  share.total = __shfl_sync(0xFFFFFFFFu, wsum, W - 1);
+  share.workers = min(static_cast<uint32_t>(gridDim.x) * PER, (share.total + least - 1) / least);
+  const uint32_t v0 = blockIdx.x * PER;
+  if (v0 >= share.workers) return false;
+  share.each = share.total / share.workers;
+  share.more = share.total - share.each * share.workers;
+  if (warp >= PER || v0 + warp >= share.workers) return true;
+  const uint32_t f = share.first(v0 + warp);
+  // the warp's run of requests, then the thread's, that holds step f
+  const int wi = __popc(__ballot_sync(0xFFFFFFFFu, lane < W && wsum <= f));
+  const uint32_t wlo = __shfl_sync(0xFFFFFFFFu, wsum, wi > 0 ? wi - 1 : 0);
+  const uint32_t ti = scratch[wi * 32 + lane];
+  uint32_t lo = wi > 0 ? wlo : 0u;
+  const int li = __popc(__ballot_sync(0xFFFFFFFFu, lo + ti <= f));
+  const uint32_t tlo = __shfl_sync(0xFFFFFFFFu, ti, li > 0 ? li - 1 : 0);
+  lo += li > 0 ? tlo : 0u;
+  int b = (wi * 32 + li) * per;
+  if (per > 1) {
+    for (uint32_t n = steps(b); f >= lo + n; n = steps(++b)) lo += n;
+  }
+  start = KvStart{static_cast<uint32_t>(b), f - lo};
+  return true;
+}
+
+}  // namespace a4w4

@@ -50,10 +50,11 @@ int ensure_func_attrs(std::atomic<unsigned long long>& done, SetFn set) {
 // griddepcontrol.wait, so they may start while the previous grid finishes).
 // Returns 0 or -4.
 template <typename... Params, typename... Args>
-int launch_pdl(void (*kern)(Params...), int grid, int block, cudaStream_t st, Args... args) {
+int launch_pdl_smem(void (*kern)(Params...), int grid, int block, size_t smem, cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(block, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -62,6 +63,11 @@ int launch_pdl(void (*kern)(Params...), int grid, int block, cudaStream_t st, Ar
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return -4;
   return cudaGetLastError() == cudaSuccess ? 0 : -4;
+}
+
+template <typename... Params, typename... Args>
+int launch_pdl(void (*kern)(Params...), int grid, int block, cudaStream_t st, Args... args) {
+  return launch_pdl_smem(kern, grid, block, 0, st, args...);
 }
 
 // Shared by the C ABI entry points (defined in api.cu): SM count of the
@@ -155,10 +161,18 @@ struct KvAttentionArgs {
   void* ws;
   int B, total_q, max_q, max_pages, num_pages, page_size, Hq, Hkv;
   float sm_scale;
+  unsigned int group_recip;     // ceil(65536 / G), G = Hq / Hkv
   unsigned long long wait_ns;
   unsigned int* status;
+#ifdef __CUDACC__
+  // new token of row r of a key/value head's rows (r < 256, G <= 256: exact)
+  __device__ __forceinline__ int row_of(int r) const { return static_cast<int>(r * group_recip >> 16); }
+#endif
 };
-size_t kv_attention_ws_bytes(int B, int max_q, int Hq, int Hkv, int D, int sms);
+size_t kv_attention_ws_bytes(int max_q, int group, int D, int sms);
 int launch_kv_attention(const KvAttentionArgs& p, int D, cudaStream_t st, int sms);
+// At most 16 query rows (max_q * Hq / Hkv) per key/value head (kv_decode.cu).
+size_t kv_decode_ws_bytes(int rows, int D, int sms);
+int launch_kv_decode(const KvAttentionArgs& p, int D, cudaStream_t st, int sms);
 
 }  // namespace a4w4
