@@ -379,8 +379,10 @@ int a4w4_kv_read(const void* cache, int num_pages, int page_size, const int32_t*
  * lse = -infinity.  Keys and values enter as the values they stand for; sums,
  * softmax statistics and the output accumulator are fp32.  The reduction order
  * depends on the lengths alone: results are bitwise deterministic.
- * Hq % Hkv == 0, D 64 or 128, sm_scale finite and > 0, B >= 1, total_q >= 0, max_q >= 1,
- * max_pages >= 1, max_pages * page_size < 2^31, num_pages * page_size < 2^31.
+ * Hq % Hkv == 0, Hq / Hkv <= 256, D 64 or 128, sm_scale finite and > 0, B >= 1, total_q >= 0,
+ * max_q >= 1, max_pages >= 1, max_pages * page_size < 2^31 - 255, num_pages * page_size < 2^31, and
+ * the steps of all rows together (32 keys for each key/value head up to 16 rows of it,
+ * else 128 keys for each 256 rows) at most 2^31 - 1.
  * Lengths are clamped to the table's width and page numbers to [0, num_pages):
  * nothing outside the cache is read.  Workspace: a4w4_kv_attention_workspace_bytes
  * bytes, 16-byte aligned, zeroed once with a4w4_workspace_init (it begins with

@@ -413,9 +413,9 @@ int a4w4_kv_attention(const void* q_bf16, long long q_stride, const int32_t* cu_
                       int num_pages, int page_size, int Hq, int Hkv, int D, float sm_scale, void* out_bf16,
                       float* lse, void* ws, size_t ws_bytes, void* stream) {
   if (B <= 0 || total_q < 0 || max_q <= 0 || max_pages <= 0 || num_pages <= 0 ||
-      !kv_shape_ok(num_pages, page_size, Hkv, D) || Hq <= 0 || Hq % Hkv != 0)
+      !kv_shape_ok(num_pages, page_size, Hkv, D) || Hq <= 0 || Hq % Hkv != 0 || Hq / Hkv > 256)
     return A4W4_ERR_ARG;
-  if (static_cast<long long>(max_pages) * page_size > INT32_MAX || !row_stride_ok(q_stride, total_q, Hq, D))
+  if (static_cast<long long>(max_pages) * page_size > INT32_MAX - 255 || !row_stride_ok(q_stride, total_q, Hq, D))
     return A4W4_ERR_ARG;
   // the kernels count rows and steps of 32 keys in 32 bits
   if (static_cast<long long>(B) * max_q > INT32_MAX / Hq) return A4W4_ERR_ARG;

@@ -1,0 +1,722 @@
+// kv_prefill.cu -- attention over the paged MXFP4 cache for many query rows per
+// key/value head (prompt chunks, longer drafts, large groups): tcgen05.
+//
+// Rows are packed: the G query heads of a key/value head times the new tokens
+// are the rows of one matrix, so keys are decoded once for all of them.  A unit
+// is 256 such rows (two tiles of 128) against the keys that the last of them
+// sees, a step is 128 keys.  Per step and tile
+//   S = Q K^T   [128 x 128], BF16 operands in shared memory, fp32 in TMEM
+//   P = 2^(S f - m), BF16, written over S in TMEM
+//   O += P V    [128 x D], A = P from TMEM, B = V as it lies (tokens x D)
+// The two tiles take turns: while one's scores go through the softmax the other's
+// products run.  Codes become BF16 exactly (E2M1 magnitude bits placed in a BF16
+// read as the value times 2^-126; one or two exact multiplies by powers of two
+// apply the E8M0 scale), so the only roundings are P's to BF16 and the fp32 sums.
+// The running maximum follows with slack: O is rescaled only when a row's maximum
+// has grown by more than 2^8, P staying below 2^8 meanwhile.
+//
+//   warps 0-3, 4-7   softmax of tile 0, 1 (a thread per row): stage Q, scores ->
+//                    probabilities, output
+//   warps 8-15       decoders: codes -> BF16 key and value tiles, two slots each
+//   warp 16          TMEM owner and MMA issuer
+//   warp 17          copies of the cache chunks, two slots
+#include "kv_walk.cuh"
+#include "kv.cuh"
+
+#include <atomic>
+#include <cmath>
+
+namespace a4w4 {
+
+namespace {
+
+constexpr int kKeys = 128;                    // keys of a step
+constexpr int kRows = 256;                    // rows of a unit
+constexpr int kLeastSteps = 4;                // steps of a worker, at least
+constexpr int kMaxCtas = 512;
+constexpr float kNoMax = -3.0e38f;            // running maximum before the first key
+
+template <int D>
+struct PreCfg {
+  using Ch = KvChunk<D>;
+  static constexpr int DEC_WARPS = 8;
+  static constexpr int THREADS = 32 * (8 + DEC_WARPS + 2);
+  static constexpr int ATOM = 128 * 128;                         // 128 rows x 64 BF16, 128-byte swizzle
+  static constexpr int ATOMS = D / 64;
+  static constexpr int TILE = ATOMS * ATOM;                      // 128 rows x D
+  static constexpr int RAW = 8 * Ch::kBytes;                     // a step's chunks
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + 2 * TILE;
+  static constexpr int OFF_V = OFF_K + 2 * TILE;
+  static constexpr int OFF_RAW = OFF_V + 2 * TILE;
+  static constexpr int OFF_BAR = OFF_RAW + 2 * RAW;
+  // raw full, empty x 2; K full, empty x 2; V full, empty x 2; Q full, S full, P full, O full per tile; drain
+  static constexpr int NBAR = 12 + 8 + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM = OFF_MISC + 40;
+  static constexpr int SCOL = 0, OCOL = 256;                     // TMEM columns: S of the tiles, then O
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int PART = kRows * (D + 2);                   // floats of a stored part: O, then m and l
+  static_assert(SMEM <= 232448 && OFF_RAW % 16 == 0 && OFF_BAR % 8 == 0, "shared memory");
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+         "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+// Shared-memory descriptor of a B operand stored K x N with N contiguous
+// (MN-major, 128-byte swizzle): blocks of 64 N elements `lead` bytes apart,
+// groups of 8 K rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lead) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(lead >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+constexpr uint32_t kIdescBMajorN = 1u << 16;   // instruction descriptor: B is MN-major
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// BF16x2 words of a code's value times 2^-126 -> times 2^(e - 127): one multiply by 2^(e - 1) while that is a BF16,
+// else two.  e0 scales the low halves, e1 the high ones.
+__device__ __forceinline__ uint4 scale_words(uint4 o, uint32_t e0, uint32_t e1) {
+  uint32_t f = (e0 + 126u) << 7 | (e1 + 126u) << 23;
+  if (max(e0, e1) > 128u) {
+    constexpr uint32_t kUp = 0x7E807E80u;       // 2^126
+    o.x = mul_bf16x2(o.x, kUp); o.y = mul_bf16x2(o.y, kUp); o.z = mul_bf16x2(o.z, kUp); o.w = mul_bf16x2(o.w, kUp);
+    f = max(e0 << 7, 0x40u) | max(e1 << 7, 0x40u) << 16;        // 2^(e - 127)
+  }
+  o.x = mul_bf16x2(o.x, f); o.y = mul_bf16x2(o.y, f); o.z = mul_bf16x2(o.z, f); o.w = mul_bf16x2(o.w, f);
+  return o;
+}
+// Eight E2M1 codes (nibble k of w) with scales e0 (codes 0..3) and e1 (codes 4..7) -> BF16x2 words of elements
+// (k, k + 4), k = 0..3: magnitude bits to 6..8 of a BF16, sign to 15, read as the value times 2^-126.
+__device__ __forceinline__ uint4 e2m1x8_scaled(uint32_t w, uint32_t e0, uint32_t e1) {
+  constexpr uint32_t kMag = 0x01C001C0u, kSign = 0x80008000u;
+  uint4 o;
+  o.x = ((w << 6) & kMag) | ((w << 12) & kSign);
+  o.y = ((w << 2) & kMag) | ((w << 8) & kSign);
+  o.z = ((w >> 2) & kMag) | ((w << 4) & kSign);
+  o.w = ((w >> 6) & kMag) | (w & kSign);
+  return scale_words(o, e0, e1);
+}
+
+// sum over k = 0 .. n - 1 of floor((a k + b) / m); n, a, b >= 0, m > 0
+__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long s = 0;
+  while (n > 0) {
+    s += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const long long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const long long x = m;
+    m = a;
+    a = x;
+  }
+  return s;
+}
+
+// A request's units: blocks of `tq` new tokens (all their group's rows), each
+// with the keys that its last token sees.
+struct Blocks {
+  int len, all, rows, row0, tq, n;             // n: blocks
+  __device__ __forceinline__ Blocks() {}
+  __device__ __forceinline__ Blocks(const KvAttentionArgs& p, int b, int tq_) {
+    const KvRequest r = kv_request(p, b);
+    len = r.len; all = r.all; rows = r.rows; row0 = r.row0;
+    tq = tq_;
+    n = (rows + tq - 1) / tq;
+  }
+  __device__ __forceinline__ int steps(int k) const {
+    const int seen = len - all + min((k + 1) * tq, rows);
+    return max(1, (seen + kKeys - 1) / kKeys);
+  }
+  // steps of blocks 0 .. k - 1, k < n
+  __device__ __forceinline__ uint32_t before(int k) const {
+    const int base = len - all;
+    // the first blocks may see nothing: one empty step each
+    const int none = base < 0 ? min(k, -base / tq) : 0;
+    return static_cast<uint32_t>(none + floor_sum(k - none, kKeys, tq, static_cast<long long>(base) + (none + 1ll) * tq + kKeys - 1));
+  }
+  __device__ __forceinline__ uint32_t total() const { return n > 0 ? before(n - 1) + steps(n - 1) : 0u; }
+};
+
+// A walk along the CTA's run: one piece (a run of one unit's steps) at a time.
+struct PreWalk {
+  Blocks q;
+  int b, h, k, t, n, left;                     // request, head, block, first step of the piece, steps of the unit
+  __device__ __forceinline__ int steps() const { return min(left, n - t); }
+  __device__ __forceinline__ void next(const KvAttentionArgs& p) {
+    left -= steps();
+    t = 0;
+    if (left <= 0) return;
+    if (++k == q.n) {
+      k = 0;
+      if (++h == p.Hkv) {
+        h = 0;
+        do { ++b; q = Blocks(p, b, q.tq); } while (q.n == 0);
+      }
+    }
+    n = q.steps(k);
+  }
+  // rows of the unit
+  __device__ __forceinline__ int rows(int G) const { return min(q.tq, q.rows - k * q.tq) * G; }
+};
+
+template <int D>
+__global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(const KvAttentionArgs p) {
+  using Cf = PreCfg<D>;
+  using Ch = KvChunk<D>;
+  constexpr int J = Ch::J;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t bar0 = base + Cf::OFF_BAR;
+  auto raw_full = [&](int s) { return bar0 + 8u * s; };
+  auto raw_empty = [&](int s) { return bar0 + 8u * (2 + s); };
+  auto k_full = [&](int s) { return bar0 + 8u * (4 + s); };
+  auto k_empty = [&](int s) { return bar0 + 8u * (6 + s); };
+  auto v_full = [&](int s) { return bar0 + 8u * (8 + s); };
+  auto v_empty = [&](int s) { return bar0 + 8u * (10 + s); };
+  auto q_full = [&](int w) { return bar0 + 8u * (12 + w); };
+  auto s_full = [&](int w) { return bar0 + 8u * (14 + w); };
+  auto p_full = [&](int w) { return bar0 + 8u * (16 + w); };
+  auto o_full = [&](int w) { return bar0 + 8u * (18 + w); };
+  const uint32_t drain = bar0 + 8u * 20;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cf::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cf::OFF_MISC + 8);
+  volatile int* never = abort_flag + 1;
+  volatile int* last_flag = abort_flag + 2;
+  int* start_at = reinterpret_cast<int*>(smem + Cf::OFF_MISC + 24);     // request, head, block, step
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(raw_full(s), 1);
+      mbar_init(raw_empty(s), Cf::DEC_WARPS);
+      mbar_init(k_full(s), Cf::DEC_WARPS);
+      mbar_init(k_empty(s), 1);
+      mbar_init(v_full(s), Cf::DEC_WARPS);
+      mbar_init(v_empty(s), 1);
+      mbar_init(q_full(s), 4);
+      mbar_init(s_full(s), 1);
+      mbar_init(p_full(s), 4);
+      mbar_init(o_full(s), 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *never = 0;
+    fence_barrier_init();
+    if ((base & 1023u) != 0) {                 // the swizzled tiles need it
+      *abort_flag = 1;
+      atomicOr(p.status, kStatusTimeout);
+    }
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const int G = p.Hq / p.Hkv, tq = kRows / G;
+  KvShare share;
+  KvStart start;
+  auto steps_of = [&](int b) -> uint32_t { return Blocks(p, b, tq).total() * p.Hkv; };
+  if (!kv_locate<Cf::THREADS, 1>(p.B, steps_of, kLeastSteps, reinterpret_cast<uint32_t*>(smem + Cf::OFF_Q), share, start))
+    return;
+  const uint32_t cta = blockIdx.x;
+  if (warp == 0) {
+    const Blocks q(p, start.b, tq);
+    const uint32_t per = q.total();
+    const int h = start.rest / per;
+    const uint32_t rest = start.rest - h * per;
+    // the block that holds step `rest`: 32 candidates at a time
+    int lo = 0, hi = q.n;                      // before(lo) <= rest, and before(hi) > rest or hi == n
+    while (hi - lo > 1) {
+      const int stride = (hi - lo + 31) / 32;
+      const int c = lo + stride * lane;
+      const uint32_t in = __ballot_sync(0xFFFFFFFFu, c < hi && q.before(min(c, q.n - 1)) <= rest);
+      const int top = 31 - __clz(in);          // lane 0 is always in
+      lo += stride * top;
+      hi = min(hi, lo + stride);
+    }
+    if (lane == 0) {
+      start_at[0] = h;
+      start_at[1] = lo;
+      start_at[2] = rest - q.before(lo);
+      start_at[3] = start.b;
+    }
+  }
+  if (warp == 16) {
+    tmem_alloc(smem_u32(tmem_slot), Cf::TMEM_COLS);
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  PreWalk w;
+  w.b = start_at[3];
+  w.q = Blocks(p, w.b, tq);
+  w.h = start_at[0];
+  w.k = start_at[1];
+  w.t = start_at[2];
+  w.n = w.q.steps(w.k);
+  w.left = share.first(cta + 1) - share.first(cta);
+  const unsigned long long drain_ns = p.wait_ns > 100000000ull ? p.wait_ns : 100000000ull;
+  auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, p.wait_ns, p.status); };
+
+  if (warp < 8) {
+    // ---------------- softmax ----------------
+    const int tile = warp >> 2, quad = warp & 3, r = tile * 128 + quad * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t s_col = tmem + lane_base + Cf::SCOL + tile * 128, o_col = tmem + lane_base + Cf::OCOL + tile * D;
+    const float f = fmaxf(p.sm_scale * 1.4426950408889634f, 1e-44f);
+    float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + kTickets * 4);
+    uint32_t s_phase = 0, o_phase = 0;
+    bool ok = true;                            // a warp that gave up goes on through the joins, for their barriers
+    for (; w.left > 0; w.next(p)) {
+      const int R = w.rows(G);
+      const bool active = tile * 128 < R;
+      const int first_tok = w.k * tq, qi = p.row_of(r), hq = w.h * G + r - qi * G;
+      const long long row = static_cast<long long>(w.q.row0) + first_tok + qi;
+      float m = kNoMax, off = 3.0e38f, l = 0.f;
+      if (active && ok) {
+        // ---- Q tile: 16-byte pieces, dimensions of a piece in the order (0,4,1,5,2,6,3,7) as the keys' ----
+        for (int it = tid & 127; it < 128 * (D / 8); it += 128) {
+          const int rr = it / (D / 8), c = it % (D / 8), rt = tile * 128 + rr;
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (rt < R) {
+            const int qj = p.row_of(rt);
+            v = ld_global_nc_v4(p.q + (static_cast<long long>(w.q.row0) + first_tok + qj) * p.q_stride +
+                                (w.h * G + rt - qj * G) * D + c * 8);
+          }
+          *reinterpret_cast<uint4*>(smem + Cf::OFF_Q + tile * Cf::TILE + (c >> 3) * Cf::ATOM + rr * 128 +
+                                    (((c & 7) ^ (rr & 7)) << 4)) =
+              make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                         __byte_perm(v.y, v.w, 0x7632));
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();                     // the last unit's O has been read
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full(tile));
+        const int seen = r < R ? w.q.len - w.q.all + first_tok + qi + 1 : 0;
+        const int n = w.steps();
+        for (int i = 0; i < n; ++i) {
+          ok = __all_sync(0xFFFFFFFFu, wait(s_full(tile), s_phase));
+          if (!ok) break;
+          s_phase ^= 1;
+          tc_fence_after();
+          const int k0 = (w.t + i) * kKeys;
+          const bool edge = __any_sync(0xFFFFFFFFu, k0 + kKeys > seen);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[32];
+            tmem_ld32(s_col + 32 * c, x);
+            if (edge) {
+#pragma unroll
+              for (int u = 0; u < 32; ++u)
+                if (k0 + 32 * c + u < seen) mx = fmaxf(mx, __uint_as_float(x[u]));
+            } else {
+#pragma unroll
+              for (int u = 0; u < 32; ++u) mx = fmaxf(mx, __uint_as_float(x[u]));
+            }
+          }
+          // the maximum follows once it is 2^8 ahead
+          const bool grow = m == kNoMax ? mx > m : (mx - m) * f > 8.f;
+          float a = 1.f;
+          if (grow) {
+            a = ex2((m - mx) * f);
+            m = mx;
+            off = fminf(-m * f, 3.0e38f);
+            l *= a;
+          }
+          if (i > 0 && __any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t x[32];
+              tmem_ld32(o_col + 32 * c, x);
+#pragma unroll
+              for (int u = 0; u < 32; ++u) x[u] = __float_as_uint(__uint_as_float(x[u]) * a);
+              tmem_st16(o_col + 32 * c, x);
+              tmem_st16(o_col + 32 * c + 16, x + 16);
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[32], y[16];
+            tmem_ld32(s_col + 32 * c, x);
+            float e[32];
+#pragma unroll
+            for (int u = 0; u < 32; ++u) {
+              e[u] = ex2(fmaf(__uint_as_float(x[u]), f, off));
+              if (edge && k0 + 32 * c + u >= seen) e[u] = 0.f;
+            }
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int u = 0; u < 32; u += 2) {
+              s0 += e[u];
+              s1 += e[u + 1];
+              y[u / 2] = pack_bf16(e[u], e[u + 1]);
+            }
+            l += s0 + s1;
+            tmem_st16(s_col + 16 * c, y);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(tile));
+        }
+        if (ok) {
+          ok = __all_sync(0xFFFFFFFFu, wait(o_full(tile), o_phase));
+          o_phase ^= 1;
+          tc_fence_after();
+        }
+      }
+      // ---- the unit's output, or the part of it ----
+      const bool whole = w.t == 0 && w.steps() == w.n;
+      const uint32_t u0 = share.first(cta + 1) - w.left - w.t;    // the unit's first step on the line
+      float* mine = parts + static_cast<size_t>(2 * cta + (share.first(cta) < u0 ? 1 : 0)) * Cf::PART;
+      if (active) {
+        const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+#pragma unroll
+        for (int a = 0; a < D / 64; ++a) {
+          // column g * 8 + e of block a is dimension 64 a + 2 g + {0, 32, 1, 33, 16, 48, 17, 49}[e]
+          uint32_t x[64];
+          tmem_ld32(o_col + 64 * a, x);
+          tmem_ld32(o_col + 64 * a + 32, x + 32);
+          if (r < R) {
+            auto at = [&](int n) {
+              return __uint_as_float(x[n % 16 / 2 * 8 + (n / 16 == 0 ? 0 : n / 16 == 2 ? 1 : n / 16 == 1 ? 4 : 5) + 2 * (n % 2)]);
+            };
+            if (whole) {
+              uint16_t* dst = p.out + (row * p.Hq + hq) * D + 64 * a;
+#pragma unroll
+              for (int n = 0; n < 64; n += 8)
+                *reinterpret_cast<uint4*>(dst + n) =
+                    make_uint4(pack_bf16(at(n) * inv, at(n + 1) * inv), pack_bf16(at(n + 2) * inv, at(n + 3) * inv),
+                               pack_bf16(at(n + 4) * inv, at(n + 5) * inv), pack_bf16(at(n + 6) * inv, at(n + 7) * inv));
+            } else {
+              float* dst = mine + r * D + 64 * a;
+#pragma unroll
+              for (int n = 0; n < 64; n += 4)
+                *reinterpret_cast<float4*>(dst + n) = make_float4(at(n), at(n + 1), at(n + 2), at(n + 3));
+            }
+          }
+        }
+        if (r < R) {
+          const float mm = fmaxf(m * f, kNoMax);
+          if (!whole) *reinterpret_cast<float2*>(mine + kRows * D + 2 * r) = make_float2(mm, l);
+          else if (p.lse != nullptr) p.lse[row * p.Hq + hq] = l == 0.f ? -INFINITY : fmaf(mm, 0.6931471805599453f, logf(l));
+        }
+      }
+      if (!whole) {
+        // ---- the last part to arrive joins a cut unit (softmax warps only) ----
+        const int c0 = share.holder(u0), np = share.holder(u0 + w.n - 1) - c0 + 1;
+        __threadfence();
+        named_bar_sync(1, 256);
+        int* ticket = static_cast<int*>(p.ws) + c0;
+        if (tid == 0) *last_flag = atomicAdd(ticket, 1) == np - 1;
+        named_bar_sync(1, 256);
+        if (*last_flag) {
+          __threadfence();
+          const size_t head = share.first(c0) < u0 ? Cf::PART : 0;
+          auto part = [&](int k) { return parts + static_cast<size_t>(2 * (c0 + k)) * Cf::PART + (k == 0 ? head : 0); };
+          for (int rr = warp; rr < R; rr += 8) {
+            float mm = kNoMax;
+            for (int k = lane; k < np; k += 32) mm = fmaxf(mm, __ldcg(part(k) + kRows * D + 2 * rr));
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, s));
+            float ll = 0.f, y[D / 32];
+#pragma unroll
+            for (int u = 0; u < D / 32; ++u) y[u] = 0.f;
+            for (int k = 0; k < np; k += 32) {
+              const float2 q = k + lane < np ? __ldcg(reinterpret_cast<const float2*>(part(k + lane) + kRows * D + 2 * rr))
+                                             : make_float2(kNoMax, 0.f);
+              const float a = ex2(q.x - mm);
+              ll = fmaf(q.y, a, ll);
+              const int m32 = min(32, np - k);
+#pragma unroll 4
+              for (int j = 0; j < m32; ++j) {
+                const float aj = __shfl_sync(0xFFFFFFFFu, a, j);
+                const float2* src = reinterpret_cast<const float2*>(part(k + j) + rr * D + lane * (D / 32));
+#pragma unroll
+                for (int u = 0; u < D / 32; u += 2) {
+                  const float2 v = __ldcg(src + u / 2);
+                  y[u] = fmaf(v.x, aj, y[u]);
+                  y[u + 1] = fmaf(v.y, aj, y[u + 1]);
+                }
+              }
+            }
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) ll += __shfl_xor_sync(0xFFFFFFFFu, ll, s);
+            const int qj = p.row_of(rr), hj = w.h * G + rr - qj * G;
+            const long long rj = static_cast<long long>(w.q.row0) + first_tok + qj;
+            const float inv = ll == 0.f ? 0.f : 1.f / ll;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (rj * p.Hq + hj) * D + lane * (D / 32));
+#pragma unroll
+            for (int u = 0; u < D / 32; u += 2) dst[u / 2] = pack_bf16(y[u] * inv, y[u + 1] * inv);
+            if (lane == 0 && p.lse != nullptr)
+              p.lse[rj * p.Hq + hj] = ll == 0.f ? -INFINITY : fmaf(mm, 0.6931471805599453f, logf(ll));
+          }
+          if (tid == 0) *ticket = 0;
+        }
+        named_bar_sync(1, 256);                // the flag is free again
+      }
+    }
+  } else if (warp < 16) {
+    // ---------------- decoders ----------------
+    const int dw = warp - 8;                   // chunk of the step
+    uint32_t it = 0;                           // steps so far
+    bool ok = true;
+    for (; w.left > 0 && ok; w.next(p)) {
+      const int n = w.steps();
+      for (int i = 0; i < n; ++i, ++it) {
+        const int s = it & 1;
+        const uint32_t ph = it >> 1 & 1;
+        if (!(ok = __all_sync(0xFFFFFFFFu, wait(raw_full(s), ph)))) break;
+        if (!(ok = __all_sync(0xFFFFFFFFu, wait(k_empty(s), ph ^ 1)))) break;
+        const uint8_t* ch = smem + Cf::OFF_RAW + s * Cf::RAW + dw * Ch::kBytes;
+        // keys: lane = piece t of tokens r, r + 8; a quarter of the warp holds rows x and x + 4, which the swizzle
+        // spreads over all banks
+        {
+          uint8_t* kt = smem + Cf::OFF_K + s * Cf::TILE;
+          const int t = lane & 3, r8 = (lane >> 2 & 1) * 4 + (lane >> 3);
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const int r = r8 + 8 * hh, row = dw * 16 + r;
+            uint32_t wd[J], sc;
+            if constexpr (J == 4) {
+              const uint4 v = *reinterpret_cast<const uint4*>(ch + Ch::key_word(r, 0, t));
+              wd[0] = v.x; wd[1] = v.y; wd[2] = v.z; wd[3] = v.w;
+              sc = *reinterpret_cast<const uint32_t*>(ch + Ch::kKeyScales + r * J);
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(ch + Ch::key_word(r, 0, t));
+              wd[0] = v.x; wd[1] = v.y;
+              sc = *reinterpret_cast<const uint16_t*>(ch + Ch::kKeyScales + r * J);
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+              *reinterpret_cast<uint4*>(kt + (j >> 1) * Cf::ATOM + row * 128 + ((((j & 1) * 4 + t) ^ (row & 7)) << 4)) =
+                  e2m1x8_scaled(wd[j], sc >> (8 * j) & 0xFFu, sc >> (8 * j) & 0xFFu);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_full(s));
+        if (!(ok = __all_sync(0xFFFFFFFFu, wait(v_empty(s), ph ^ 1)))) break;
+        // values: lane 4 g + t = 16-byte piece g of tokens 2t, 2t + 1 of each half; tokens beyond the length are zero
+        {
+          uint8_t* vt = smem + Cf::OFF_V + s * Cf::TILE;
+          const int g = lane >> 2, t = lane & 3;
+          const int tok0 = (w.t + i) * kKeys + dw * 16;
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            uint32_t run[2][J / 2];
+            if constexpr (J == 4) {
+              const uint4 v = *reinterpret_cast<const uint4*>(ch + Ch::kValues + hh * 4 * D + lane * 16);
+              run[0][0] = v.x; run[0][1] = v.y; run[1][0] = v.z; run[1][1] = v.w;
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(ch + Ch::kValues + hh * 4 * D + lane * 8);
+              run[0][0] = v.x; run[1][0] = v.y;
+            }
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              const int r = hh * 8 + 2 * t + o, row = dw * 16 + r;
+              const bool live = tok0 + r < w.q.len;
+#pragma unroll
+              for (int q4 = 0; q4 < J / 2; ++q4) {
+                // word q4: bytes of row tiles 4 q4 ..+3: 32-blocks 2 q4 (bytes 0, 1) and 2 q4 + 1 (bytes 2, 3)
+                const uint32_t sc = *reinterpret_cast<const uint16_t*>(ch + Ch::kValueScales + r * J + 2 * q4);
+                const uint32_t wv = live ? run[o][q4] : 0u;
+                const uint32_t sv = live ? sc : 0u;
+                *reinterpret_cast<uint4*>(vt + q4 * Cf::ATOM + row * 128 + ((g ^ (row & 7)) << 4)) =
+                    e2m1x8_scaled(wv, sv & 0xFFu, sv >> 8);
+              }
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(v_full(s));
+          mbar_arrive(raw_empty(s));
+        }
+      }
+    }
+  } else if (warp == 16) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      const uint32_t id_s = idesc_bf16(kKeys), id_o = idesc_bf16(D) | kIdescBMajorN;
+      const uint64_t qd = sdesc_sw128(base + Cf::OFF_Q), kd = sdesc_sw128(base + Cf::OFF_K);
+      const uint64_t vd = sdesc_mn_sw128(base + Cf::OFF_V, Cf::ATOM);
+      uint32_t it = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+      bool ok = true;
+      auto scores = [&](int tile, int s) {
+#pragma unroll
+        for (int a = 0; a < Cf::ATOMS; ++a)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ss(tmem + Cf::SCOL + tile * 128, qd + ((tile * Cf::TILE + a * Cf::ATOM) >> 4) + 2 * kk,
+                   kd + ((s * Cf::TILE + a * Cf::ATOM) >> 4) + 2 * kk, id_s, (a | kk) ? 1u : 0u);
+        mma_commit(s_full(tile));
+      };
+      auto outputs = [&](int tile, int s, bool first) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(tmem + Cf::OCOL + tile * D, tmem + Cf::SCOL + tile * 128 + 8 * kk,
+                 vd + ((s * Cf::TILE + kk * 2048) >> 4), id_o, (first && kk == 0) ? 0u : 1u);
+      };
+      for (; w.left > 0 && ok; w.next(p)) {
+        const int n = w.steps(), tiles = w.rows(G) > 128 ? 2 : 1;
+        for (int i = 0; i <= n && ok; ++i) {
+          // products of step i - 1 and scores of step i, tile after tile
+          const int s = it & 1, sp = (it - 1) & 1;
+          const uint32_t ph = it >> 1 & 1, php = (it - 1) >> 1 & 1;
+          for (int tile = 0; tile < tiles; ++tile) {
+            if (i > 0) {
+              if (!(ok = wait(p_full(tile), p_phase[tile]))) break;
+              p_phase[tile] ^= 1;
+              if (tile == 0 && !(ok = wait(v_full(sp), php))) break;
+              tc_fence_after();
+              outputs(tile, sp, i == 1);
+              if (i == n) mma_commit(o_full(tile));
+              if (tile == tiles - 1) mma_commit(v_empty(sp));
+            }
+            if (i < n) {
+              if (i == 0) {
+                if (!(ok = wait(q_full(tile), q_phase[tile]))) break;
+                q_phase[tile] ^= 1;
+              }
+              if (tile == 0 && !(ok = wait(k_full(s), ph))) break;
+              tc_fence_after();
+              scores(tile, s);
+              if (tile == tiles - 1) mma_commit(k_empty(s));
+            }
+          }
+          if (i < n) ++it;
+        }
+      }
+      // TMEM is not released while products may still run, whoever gave up
+      mma_commit(drain);
+      mbar_wait(drain, 0, never, drain_ns, p.status);
+    }
+  } else {
+    // ---------------- copies ----------------
+    const int lg = 31 - __clz(p.page_size), chunks = p.page_size >> 4;
+    const int run = min(chunks, 8);                       // chunks of a copy
+    const uint64_t pol = policy_evict_last();             // other units read the same pages
+    uint32_t it = 0;
+    for (; w.left > 0; w.next(p)) {
+      const int n = w.steps();
+      bool ok = true;
+      for (int i = 0; i < n; ++i, ++it) {
+        const int s = it & 1;
+        const int tok0 = (w.t + i) * kKeys;
+        const int live = min(8, max(0, (w.q.len - tok0 + 15) >> 4));      // chunks that hold tokens
+        const int c = lane * run;
+        const int mine = c < live ? min(run, live - c) : 0;
+        const int page = mine > 0 ? kv_page(p, w.b, (tok0 + c * 16) >> lg) : 0;
+        ok = wait(raw_empty(s), (it >> 1 & 1) ^ 1);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(raw_full(s), live * Ch::kBytes);
+        __syncwarp();
+        if (mine > 0)
+          bulk_g2s(base + Cf::OFF_RAW + s * Cf::RAW + c * Ch::kBytes,
+                   p.cache + kv_chunk_offset<D>(page, w.h, ((tok0 >> 4) + c) & (chunks - 1), p.Hkv, chunks),
+                   mine * Ch::kBytes, raw_full(s), pol);
+      }
+      if (!ok) break;
+    }
+    // every copy issued lands before the CTA's shared memory is released
+    if (lane == 0)
+      for (uint32_t j = it > 2 ? it - 2 : 0; j < it; ++j) mbar_wait(raw_full(j & 1), j >> 1 & 1, never, drain_ns, p.status);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 16) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, Cf::TMEM_COLS);
+  }
+}
+
+}  // namespace
+
+size_t kv_prefill_ws_bytes(int D, int sms) {
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  return kTickets * 4 + 2ull * ctas * kRows * (D + 2) * 4;
+}
+
+namespace {
+
+template <int D>
+int launch_one(const KvAttentionArgs& p, int grid, cudaStream_t st) {
+  using Cf = PreCfg<D>;
+  static std::atomic<unsigned long long> attr_done{0};
+  const int rc = ensure_func_attrs(attr_done, [] {
+    return cudaFuncSetAttribute(a4w4_kv_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM) ==
+           cudaSuccess;
+  });
+  if (rc != 0) return rc;
+  return launch_pdl_smem(a4w4_kv_prefill_kernel<D>, grid, Cf::THREADS, Cf::SMEM, st, p);
+}
+
+}  // namespace
+
+int launch_kv_prefill(const KvAttentionArgs& p, int D, cudaStream_t st, int sms) {
+  // steps are counted in 32 bits
+  const int G = p.Hq / p.Hkv, tq = kRows / G;
+  const double most = static_cast<double>(p.B) * p.Hkv * ((p.max_q + tq - 1) / tq) *
+                      ((static_cast<double>(p.max_pages) * p.page_size + kKeys - 1) / kKeys + 1);
+  if (most > 2147483647.0) return -1;
+  const int grid = sms < kMaxCtas ? sms : kMaxCtas;
+  return D == 64 ? launch_one<64>(p, grid, st) : launch_one<128>(p, grid, st);
+}
+
+}  // namespace a4w4

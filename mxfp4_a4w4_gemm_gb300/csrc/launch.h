@@ -174,5 +174,8 @@ int launch_kv_attention(const KvAttentionArgs& p, int D, cudaStream_t st, int sm
 // At most 16 query rows (max_q * Hq / Hkv) per key/value head (kv_decode.cu).
 size_t kv_decode_ws_bytes(int rows, int D, int sms);
 int launch_kv_decode(const KvAttentionArgs& p, int D, cudaStream_t st, int sms);
+// Any number of rows, Hq / Hkv <= 256 (kv_prefill.cu).  -1: more work than it counts.
+size_t kv_prefill_ws_bytes(int D, int sms);
+int launch_kv_prefill(const KvAttentionArgs& p, int D, cudaStream_t st, int sms);
 
 }  // namespace a4w4
