@@ -40,7 +40,10 @@ template <int D>
 struct PreCfg {
   using Ch = KvChunk<D>;
   static constexpr int DEC_WARPS = 8;
-  static constexpr int THREADS = 32 * (8 + DEC_WARPS + 2);
+  static constexpr int THREADS = 32 * (8 + DEC_WARPS + 4);         // five warpgroups, the last one half used
+  // registers a thread, by warpgroup: softmax, decoders, the rest; together what the CTA was launched with
+  static constexpr int REGS = 96, REGS_SOFTMAX = 160, REGS_DECODE = 56, REGS_REST = 48;
+  static_assert(256 * REGS_SOFTMAX + 256 * REGS_DECODE + 128 * REGS_REST <= THREADS * REGS, "register split");
   static constexpr int ATOM = 128 * 128;                         // 128 rows x 64 BF16, 128-byte swizzle
   static constexpr int ATOMS = D / 64;
   static constexpr int TILE = ATOMS * ATOM;                      // 128 rows x D
@@ -60,6 +63,7 @@ struct PreCfg {
   static_assert(SMEM <= 232448 && OFF_RAW % 16 == 0 && OFF_BAR % 8 == 0, "shared memory");
 };
 
+// 32 columns of this warp's lanes; the values may be used after tmem_wait_ld() on them.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -70,7 +74,47 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+// Orders the uses of r[0..15] after the wait.
+__device__ __forceinline__ void tmem_landed16(uint32_t* r) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; i += 16) tmem_landed16(r + i);
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// Two fp32 operations at a time.
+__device__ __forceinline__ uint64_t pair_f32(uint32_t lo, uint32_t hi) {
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
@@ -79,6 +123,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
       :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -311,6 +360,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
 
   if (warp < 8) {
     // ---------------- softmax ----------------
+    regs_up<Cf::REGS_SOFTMAX>();
     const int tile = warp >> 2, quad = warp & 3, r = tile * 128 + quad * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t s_col = tmem + lane_base + Cf::SCOL + tile * 128, o_col = tmem + lane_base + Cf::OCOL + tile * D;
@@ -352,20 +402,25 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
           tc_fence_after();
           const int k0 = (w.t + i) * kKeys;
           const bool edge = __any_sync(0xFFFFFFFFu, k0 + kKeys > seen);
-          float mx = -INFINITY;
+          uint32_t x[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, x + 32 * c);
+          tmem_wait_ld<128>(x);
+          if (edge) {
+            const int k1 = seen - k0;                             // columns that the row sees
+#pragma unroll
+            for (int u = 0; u < 128; ++u)
+              if (u >= k1) x[u] = 0xFF800000u;                    // -infinity
+          }
+          float top[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            uint32_t x[32];
-            tmem_ld32(s_col + 32 * c, x);
-            if (edge) {
+            top[c] = __uint_as_float(x[c]);
 #pragma unroll
-              for (int u = 0; u < 32; ++u)
-                if (k0 + 32 * c + u < seen) mx = fmaxf(mx, __uint_as_float(x[u]));
-            } else {
-#pragma unroll
-              for (int u = 0; u < 32; ++u) mx = fmaxf(mx, __uint_as_float(x[u]));
-            }
+            for (int u = c + 4; u < 128; u += 8)
+              top[c] = fmaxf(top[c], u + 4 < 128 ? fmaxf(__uint_as_float(x[u]), __uint_as_float(x[u + 4])) : __uint_as_float(x[u]));
           }
+          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
           // the maximum follows once it is 2^8 ahead
           const bool grow = m == kNoMax ? mx > m : (mx - m) * f > 8.f;
           float a = 1.f;
@@ -376,36 +431,35 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
             l *= a;
           }
           if (i > 0 && __any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t y[16];
+              tmem_ld16(o_col + 16 * c, y);
+              tmem_wait_ld<16>(y);
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t x[32];
-              tmem_ld32(o_col + 32 * c, x);
-#pragma unroll
-              for (int u = 0; u < 32; ++u) x[u] = __float_as_uint(__uint_as_float(x[u]) * a);
-              tmem_st16(o_col + 32 * c, x);
-              tmem_st16(o_col + 32 * c + 16, x + 16);
+              for (int u = 0; u < 16; ++u) y[u] = __float_as_uint(__uint_as_float(y[u]) * a);
+              tmem_st16(o_col + 16 * c, y);
             }
           }
+          const uint64_t f2 = pair_f32(__float_as_uint(f), __float_as_uint(f));
+          const uint64_t off2 = pair_f32(__float_as_uint(off), __float_as_uint(off));
+          uint64_t sum0 = 0, sum1 = 0;                            // two pairs of partial sums
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t x[32], y[16];
-            tmem_ld32(s_col + 32 * c, x);
-            float e[32];
+          for (int c = 0; c < 8; ++c) {
+            uint32_t y[8];
 #pragma unroll
-            for (int u = 0; u < 32; ++u) {
-              e[u] = ex2(fmaf(__uint_as_float(x[u]), f, off));
-              if (edge && k0 + 32 * c + u >= seen) e[u] = 0.f;
+            for (int u = 0; u < 8; ++u) {
+              const uint64_t z = fma_f32x2(pair_f32(x[16 * c + 2 * u], x[16 * c + 2 * u + 1]), f2, off2);
+              const float e0 = ex2(__uint_as_float(static_cast<uint32_t>(z)));
+              const float e1 = ex2(__uint_as_float(static_cast<uint32_t>(z >> 32)));
+              const uint64_t e = pair_f32(__float_as_uint(e0), __float_as_uint(e1));
+              if (u & 1) sum1 = add_f32x2(sum1, e); else sum0 = add_f32x2(sum0, e);
+              y[u] = pack_bf16(e0, e1);
             }
-            float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-            for (int u = 0; u < 32; u += 2) {
-              s0 += e[u];
-              s1 += e[u + 1];
-              y[u / 2] = pack_bf16(e[u], e[u + 1]);
-            }
-            l += s0 + s1;
-            tmem_st16(s_col + 16 * c, y);
+            tmem_st8(s_col + 8 * c, y);
           }
+          sum0 = add_f32x2(sum0, sum1);
+          l += __uint_as_float(static_cast<uint32_t>(sum0)) + __uint_as_float(static_cast<uint32_t>(sum0 >> 32));
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -429,6 +483,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
           uint32_t x[64];
           tmem_ld32(o_col + 64 * a, x);
           tmem_ld32(o_col + 64 * a + 32, x + 32);
+          tmem_wait_ld<64>(x);
           if (r < R) {
             auto at = [&](int n) {
               return __uint_as_float(x[n % 16 / 2 * 8 + (n / 16 == 0 ? 0 : n / 16 == 2 ? 1 : n / 16 == 1 ? 4 : 5) + 2 * (n % 2)]);
@@ -510,6 +565,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
     }
   } else if (warp < 16) {
     // ---------------- decoders ----------------
+    regs_down<Cf::REGS_DECODE>();
     const int dw = warp - 8;                   // chunk of the step
     uint32_t it = 0;                           // steps so far
     bool ok = true;
@@ -588,7 +644,9 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
         }
       }
     }
-  } else if (warp == 16) {
+  } else {
+   regs_down<Cf::REGS_REST>();
+   if (warp == 16) {
     // ---------------- MMA issuer ----------------
     if (lane == 0) {
       const uint32_t id_s = idesc_bf16(kKeys), id_o = idesc_bf16(D) | kIdescBMajorN;
@@ -645,7 +703,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
       mma_commit(drain);
       mbar_wait(drain, 0, never, drain_ns, p.status);
     }
-  } else {
+   } else if (warp == 17) {
     // ---------------- copies ----------------
     const int lg = 31 - __clz(p.page_size), chunks = p.page_size >> 4;
     const int run = min(chunks, 8);                       // chunks of a copy
@@ -676,6 +734,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
     // every copy issued lands before the CTA's shared memory is released
     if (lane == 0)
       for (uint32_t j = it > 2 ? it - 2 : 0; j < it; ++j) mbar_wait(raw_full(j & 1), j >> 1 & 1, never, drain_ns, p.status);
+   }
   }
   tc_fence_before();
   __syncthreads();
