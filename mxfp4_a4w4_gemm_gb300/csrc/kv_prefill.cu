@@ -131,17 +131,27 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// D (TMEM) (+)= A B, descriptors as their two words.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}"
+      :: "r"(d), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate) : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}"
+      :: "r"(d), "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
 }
 // Shared-memory descriptor of a B operand stored K x N with N contiguous
 // (MN-major, 128-byte swizzle): blocks of 64 N elements `lead` bytes apart,
@@ -521,42 +531,50 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
           __threadfence();
           const size_t head = share.first(c0) < u0 ? Cf::PART : 0;
           auto part = [&](int k) { return parts + static_cast<size_t>(2 * (c0 + k)) * Cf::PART + (k == 0 ? head : 0); };
-          for (int rr = warp; rr < R; rr += 8) {
-            float mm = kNoMax;
-            for (int k = lane; k < np; k += 32) mm = fmaxf(mm, __ldcg(part(k) + kRows * D + 2 * rr));
+          // a thread per row: maximum and sum over the parts; then all threads over the rows' pieces of 16 bytes,
+          // four at a time.  The rows' figures go where Q was: its products are done.
+          float2* rows = reinterpret_cast<float2*>(smem + Cf::OFF_Q);
+          if (tid < R) {
+            float mm = kNoMax, ll = 0.f;
+            for (int k = 0; k < np; ++k) mm = fmaxf(mm, __ldcg(part(k) + kRows * D + 2 * tid));
+            for (int k = 0; k < np; ++k) {
+              const float2 q = __ldcg(reinterpret_cast<const float2*>(part(k) + kRows * D + 2 * tid));
+              ll = fmaf(q.y, ex2(q.x - mm), ll);
+            }
+            rows[tid] = make_float2(mm, ll == 0.f ? 0.f : 1.f / ll);
+            if (p.lse != nullptr) p.lse[row * p.Hq + hq] = ll == 0.f ? -INFINITY : fmaf(mm, 0.6931471805599453f, logf(ll));
+          }
+          named_bar_sync(1, 256);
+          constexpr int Q4 = D / 4;                                        // 16-byte pieces of a row
+          for (int it0 = tid; it0 < R * Q4; it0 += 4 * 256) {
+            float4 y[4];
+            float2 st[4];
 #pragma unroll
-            for (int s = 16; s > 0; s >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, s));
-            float ll = 0.f, y[D / 32];
+            for (int u = 0; u < 4; ++u) {
+              y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+              st[u] = rows[min((it0 + u * 256) / Q4, R - 1)];
+            }
+            for (int k = 0; k < np; ++k) {
+              const float* src = part(k);
 #pragma unroll
-            for (int u = 0; u < D / 32; ++u) y[u] = 0.f;
-            for (int k = 0; k < np; k += 32) {
-              const float2 q = k + lane < np ? __ldcg(reinterpret_cast<const float2*>(part(k + lane) + kRows * D + 2 * rr))
-                                             : make_float2(kNoMax, 0.f);
-              const float a = ex2(q.x - mm);
-              ll = fmaf(q.y, a, ll);
-              const int m32 = min(32, np - k);
-#pragma unroll 4
-              for (int j = 0; j < m32; ++j) {
-                const float aj = __shfl_sync(0xFFFFFFFFu, a, j);
-                const float2* src = reinterpret_cast<const float2*>(part(k + j) + rr * D + lane * (D / 32));
-#pragma unroll
-                for (int u = 0; u < D / 32; u += 2) {
-                  const float2 v = __ldcg(src + u / 2);
-                  y[u] = fmaf(v.x, aj, y[u]);
-                  y[u + 1] = fmaf(v.y, aj, y[u + 1]);
-                }
+              for (int u = 0; u < 4; ++u) {
+                const int it = min(it0 + u * 256, R * Q4 - 1);
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(src) + it);
+                const float a = ex2(__ldcg(src + kRows * D + 2 * (it / Q4)) - st[u].x) * st[u].y;
+                y[u].x = fmaf(v.x, a, y[u].x); y[u].y = fmaf(v.y, a, y[u].y);
+                y[u].z = fmaf(v.z, a, y[u].z); y[u].w = fmaf(v.w, a, y[u].w);
               }
             }
 #pragma unroll
-            for (int s = 16; s > 0; s >>= 1) ll += __shfl_xor_sync(0xFFFFFFFFu, ll, s);
-            const int qj = p.row_of(rr), hj = w.h * G + rr - qj * G;
-            const long long rj = static_cast<long long>(w.q.row0) + first_tok + qj;
-            const float inv = ll == 0.f ? 0.f : 1.f / ll;
-            uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (rj * p.Hq + hj) * D + lane * (D / 32));
-#pragma unroll
-            for (int u = 0; u < D / 32; u += 2) dst[u / 2] = pack_bf16(y[u] * inv, y[u + 1] * inv);
-            if (lane == 0 && p.lse != nullptr)
-              p.lse[rj * p.Hq + hj] = ll == 0.f ? -INFINITY : fmaf(mm, 0.6931471805599453f, logf(ll));
+            for (int u = 0; u < 4; ++u) {
+              const int it = it0 + u * 256;
+              if (it < R * Q4) {
+                const int rj = it / Q4, qj = p.row_of(rj), hj = w.h * G + rj - qj * G;
+                const long long gr = static_cast<long long>(w.q.row0) + first_tok + qj;
+                *reinterpret_cast<uint2*>(p.out + (gr * p.Hq + hj) * D + it % Q4 * 4) =
+                    make_uint2(pack_bf16(y[u].x, y[u].y), pack_bf16(y[u].z, y[u].w));
+              }
+            }
           }
           if (tid == 0) *ticket = 0;
         }
@@ -647,62 +665,79 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
   } else {
    regs_down<Cf::REGS_REST>();
    if (warp == 16) {
-    // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      const uint32_t id_s = idesc_bf16(kKeys), id_o = idesc_bf16(D) | kIdescBMajorN;
-      const uint64_t qd = sdesc_sw128(base + Cf::OFF_Q), kd = sdesc_sw128(base + Cf::OFF_K);
-      const uint64_t vd = sdesc_mn_sw128(base + Cf::OFF_V, Cf::ATOM);
-      uint32_t it = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-      bool ok = true;
-      auto scores = [&](int tile, int s) {
+    // ---------------- MMA issuer: the whole warp walks, so that addresses stay in uniform registers ----------------
+    const uint32_t id_s = idesc_bf16(kKeys), id_o = idesc_bf16(D) | kIdescBMajorN;
+    const uint64_t qd = sdesc_sw128(base + Cf::OFF_Q), kd = sdesc_sw128(base + Cf::OFF_K);
+    const uint64_t vd = sdesc_mn_sw128(base + Cf::OFF_V, Cf::ATOM);
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    uint32_t it = 0, q_phase = 0, p_phase = 0;                   // a phase bit per tile
+    bool ok = true;
+    auto sure = [&](uint32_t bar, uint32_t parity) {
+      ok = __all_sync(0xFFFFFFFFu, wait(bar, parity));
+      return ok;
+    };
+    auto scores = [&](int tile, int s) {
+      const uint32_t q_lo = static_cast<uint32_t>(qd) + tile * (Cf::TILE >> 4), q_hi = static_cast<uint32_t>(qd >> 32);
+      const uint32_t k_lo = static_cast<uint32_t>(kd) + s * (Cf::TILE >> 4), k_hi = static_cast<uint32_t>(kd >> 32);
+      const uint32_t d = tm + Cf::SCOL + tile * 128;
+      if (elect_one()) {
 #pragma unroll
         for (int a = 0; a < Cf::ATOMS; ++a)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ss(tmem + Cf::SCOL + tile * 128, qd + ((tile * Cf::TILE + a * Cf::ATOM) >> 4) + 2 * kk,
-                   kd + ((s * Cf::TILE + a * Cf::ATOM) >> 4) + 2 * kk, id_s, (a | kk) ? 1u : 0u);
+            mma_ss(d, q_lo + (a * Cf::ATOM >> 4) + 2 * kk, q_hi, k_lo + (a * Cf::ATOM >> 4) + 2 * kk, k_hi, id_s,
+                   (a | kk) ? 1u : 0u);
         mma_commit(s_full(tile));
-      };
-      auto outputs = [&](int tile, int s, bool first) {
+      }
+      __syncwarp();
+    };
+    auto outputs = [&](int tile, int s, bool first, bool last_step, bool last_tile) {
+      const uint32_t v_lo = static_cast<uint32_t>(vd) + s * (Cf::TILE >> 4), v_hi = static_cast<uint32_t>(vd >> 32);
+      const uint32_t d = tm + Cf::OCOL + tile * D, a = tm + Cf::SCOL + tile * 128;
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tmem + Cf::OCOL + tile * D, tmem + Cf::SCOL + tile * 128 + 8 * kk,
-                 vd + ((s * Cf::TILE + kk * 2048) >> 4), id_o, (first && kk == 0) ? 0u : 1u);
-      };
-      for (; w.left > 0 && ok; w.next(p)) {
-        const int n = w.steps(), tiles = w.rows(G) > 128 ? 2 : 1;
-        for (int i = 0; i <= n && ok; ++i) {
-          // products of step i - 1 and scores of step i, tile after tile
-          const int s = it & 1, sp = (it - 1) & 1;
-          const uint32_t ph = it >> 1 & 1, php = (it - 1) >> 1 & 1;
-          for (int tile = 0; tile < tiles; ++tile) {
-            if (i > 0) {
-              if (!(ok = wait(p_full(tile), p_phase[tile]))) break;
-              p_phase[tile] ^= 1;
-              if (tile == 0 && !(ok = wait(v_full(sp), php))) break;
-              tc_fence_after();
-              outputs(tile, sp, i == 1);
-              if (i == n) mma_commit(o_full(tile));
-              if (tile == tiles - 1) mma_commit(v_empty(sp));
+          mma_ts(d, a + 8 * kk, v_lo + (kk * 2048 >> 4), v_hi, id_o, kk == 0 && first ? 0u : 1u);
+        if (last_step) mma_commit(o_full(tile));
+        if (last_tile) mma_commit(v_empty(s));
+      }
+      __syncwarp();
+    };
+    for (; w.left > 0 && ok; w.next(p)) {
+      const int n = w.steps(), tiles = w.rows(G) > 128 ? 2 : 1;
+      for (int i = 0; i <= n && ok; ++i) {
+        // products of step i - 1 and scores of step i, tile after tile
+        const int s = it & 1, sp = (it - 1) & 1;
+        const uint32_t ph = it >> 1 & 1, php = (it - 1) >> 1 & 1;
+        for (int tile = 0; tile < tiles; ++tile) {
+          if (i > 0) {
+            if (!sure(p_full(tile), p_phase >> tile & 1)) break;
+            p_phase ^= 1u << tile;
+            if (tile == 0 && !sure(v_full(sp), php)) break;
+            tc_fence_after();
+            outputs(tile, sp, i == 1, i == n, tile == tiles - 1);
+          }
+          if (i < n) {
+            if (i == 0) {
+              if (!sure(q_full(tile), q_phase >> tile & 1)) break;
+              q_phase ^= 1u << tile;
             }
-            if (i < n) {
-              if (i == 0) {
-                if (!(ok = wait(q_full(tile), q_phase[tile]))) break;
-                q_phase[tile] ^= 1;
-              }
-              if (tile == 0 && !(ok = wait(k_full(s), ph))) break;
-              tc_fence_after();
-              scores(tile, s);
-              if (tile == tiles - 1) mma_commit(k_empty(s));
+            if (tile == 0 && !sure(k_full(s), ph)) break;
+            tc_fence_after();
+            scores(tile, s);
+            if (tile == tiles - 1) {
+              if (elect_one()) mma_commit(k_empty(s));
+              __syncwarp();
             }
           }
-          if (i < n) ++it;
         }
+        if (i < n) ++it;
       }
-      // TMEM is not released while products may still run, whoever gave up
-      mma_commit(drain);
-      mbar_wait(drain, 0, never, drain_ns, p.status);
     }
+    // TMEM is not released while products may still run, whoever gave up
+    if (elect_one()) mma_commit(drain);
+    __syncwarp();
+    mbar_wait(drain, 0, never, drain_ns, p.status);
    } else if (warp == 17) {
     // ---------------- copies ----------------
     const int lg = 31 - __clz(p.page_size), chunks = p.page_size >> 4;
