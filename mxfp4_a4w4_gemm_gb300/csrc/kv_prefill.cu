@@ -5,13 +5,20 @@
 // are the rows of one matrix, so keys are decoded once for all of them.  A unit
 // is 256 such rows (two tiles of 128) against the keys that the last of them
 // sees, a step is 128 keys.  Per step and tile
-//   S = Q K^T   [128 x 128], BF16 operands in shared memory, fp32 in TMEM
+//   S = Q K^T   [128 x 128], FP16 operands in shared memory, fp32 in TMEM
 //   P = 2^(S f - m), BF16, written over S in TMEM
-//   O += P V    [128 x D], A = P from TMEM, B = V as it lies (tokens x D)
+//   O += P V    [128 x D], BF16, A = P from TMEM, B = V as it lies (tokens x D)
 // The two tiles take turns: while one's scores go through the softmax the other's
-// products run.  Codes become BF16 exactly (E2M1 magnitude bits placed in a BF16
-// read as the value times 2^-126; one or two exact multiplies by powers of two
-// apply the E8M0 scale), so the only roundings are P's to BF16 and the fp32 sums.
+// products run.  Beside the products and the softmax the decoding counts (a third
+// of the instructions), hence two forms:
+// * Keys become FP16 by the hardware's conversion, times 2^(e - ref + 13) with ref
+//   the largest scale of the step: exact for scales down to 2^-36 of it.  Queries
+//   become FP16 times a power of two per row (largest element at 2^14).  Both
+//   powers go back in the factor f of the row and step.
+// * Values become BF16, since P wants its exponents: E2M1 magnitude bits placed in
+//   a BF16 read as the value times 2^-126, and one or two exact multiplies by
+//   powers of two apply the scale.
+// So the only roundings are P's to BF16 and the fp32 sums.
 // The running maximum follows with slack: O is rescaled only when a row's maximum
 // has grown by more than 2^8, P staying below 2^8 meanwhile.
 //
@@ -32,7 +39,7 @@ namespace {
 
 constexpr int kKeys = 128;                    // keys of a step
 constexpr int kRows = 256;                    // rows of a unit
-constexpr int kLeastSteps = 4;                // steps of a worker, at least
+constexpr int kLeastSteps = 2;                // steps of a worker, at least
 constexpr int kMaxCtas = 512;
 constexpr float kNoMax = -3.0e38f;            // running maximum before the first key
 
@@ -56,7 +63,7 @@ struct PreCfg {
   // raw full, empty x 2; K full, empty x 2; V full, empty x 2; Q full, S full, P full, O full per tile; drain
   static constexpr int NBAR = 12 + 8 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int SMEM = OFF_MISC + 40;
+  static constexpr int SMEM = OFF_MISC + 56;
   static constexpr int SCOL = 0, OCOL = 256;                     // TMEM columns: S of the tiles, then O
   static constexpr int TMEM_COLS = 512;
   static constexpr int PART = kRows * (D + 2);                   // floats of a stored part: O, then m and l
@@ -165,6 +172,8 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lead
   d |= static_cast<uint64_t>(2) << 61;
   return d;
 }
+// FP16 A and B, both K-major (idesc_bf16's with the formats 0).
+__device__ __forceinline__ uint32_t idesc_f16(uint32_t n) { return idesc_bf16(n) & ~(1u << 7 | 1u << 10); }
 constexpr uint32_t kIdescBMajorN = 1u << 16;   // instruction descriptor: B is MN-major
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -182,29 +191,38 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// BF16x2 words of a code's value times 2^-126 -> times 2^(e - 127): one multiply by 2^(e - 1) while that is a BF16,
-// else two.  e0 scales the low halves, e1 the high ones.
-__device__ __forceinline__ uint4 scale_words(uint4 o, uint32_t e0, uint32_t e1) {
-  uint32_t f = (e0 + 126u) << 7 | (e1 + 126u) << 23;
-  if (max(e0, e1) > 128u) {
-    constexpr uint32_t kUp = 0x7E807E80u;       // 2^126
-    o.x = mul_bf16x2(o.x, kUp); o.y = mul_bf16x2(o.y, kUp); o.z = mul_bf16x2(o.z, kUp); o.w = mul_bf16x2(o.w, kUp);
-    f = max(e0 << 7, 0x40u) | max(e1 << 7, 0x40u) << 16;        // 2^(e - 127)
-  }
-  o.x = mul_bf16x2(o.x, f); o.y = mul_bf16x2(o.y, f); o.z = mul_bf16x2(o.z, f); o.w = mul_bf16x2(o.w, f);
-  return o;
+// Eight E2M1 codes as FP16x2 words, in order.
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t* o) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]) : "r"(w));
 }
-// Eight E2M1 codes (nibble k of w) with scales e0 (codes 0..3) and e1 (codes 4..7) -> BF16x2 words of elements
-// (k, k + 4), k = 0..3: magnitude bits to 6..8 of a BF16, sign to 15, read as the value times 2^-126.
-__device__ __forceinline__ uint4 e2m1x8_scaled(uint32_t w, uint32_t e0, uint32_t e1) {
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// Eight E2M1 codes (nibble k of w) -> BF16x2 words of elements (k, k + 4), k = 0..3, times 2^-126: magnitude bits
+// to 6..8 of a BF16, sign to 15.
+__device__ __forceinline__ uint4 e2m1x8_to_bf16x2(uint32_t w) {
   constexpr uint32_t kMag = 0x01C001C0u, kSign = 0x80008000u;
-  uint4 o;
-  o.x = ((w << 6) & kMag) | ((w << 12) & kSign);
-  o.y = ((w << 2) & kMag) | ((w << 8) & kSign);
-  o.z = ((w >> 2) & kMag) | ((w << 4) & kSign);
-  o.w = ((w >> 6) & kMag) | (w & kSign);
-  return scale_words(o, e0, e1);
+  return make_uint4(((w << 6) & kMag) | ((w << 12) & kSign), ((w << 2) & kMag) | ((w << 8) & kSign),
+                    ((w >> 2) & kMag) | ((w << 4) & kSign), ((w >> 6) & kMag) | (w & kSign));
 }
+__device__ __forceinline__ uint4 mul_bf16x8(uint4 o, uint32_t f) {
+  return make_uint4(mul_bf16x2(o.x, f), mul_bf16x2(o.y, f), mul_bf16x2(o.z, f), mul_bf16x2(o.w, f));
+}
+// 2^k as a float, k in [-126, 127]
+__device__ __forceinline__ float pow2i(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
 
 // sum over k = 0 .. n - 1 of floor((a k + b) / m); n, a, b >= 0, m > 0
 __device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
@@ -295,7 +313,9 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cf::OFF_MISC + 8);
   volatile int* never = abort_flag + 1;
   volatile int* last_flag = abort_flag + 2;
-  int* start_at = reinterpret_cast<int*>(smem + Cf::OFF_MISC + 24);     // request, head, block, step
+  int* start_at = reinterpret_cast<int*>(smem + Cf::OFF_MISC + 24);     // head, block, step, request
+  // largest key scale of a step; a slot is used again four steps later, when its readers are past the step after
+  int* key_ref = reinterpret_cast<int*>(smem + Cf::OFF_MISC + 40);
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(raw_full(s), 1);
@@ -374,7 +394,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
     const int tile = warp >> 2, quad = warp & 3, r = tile * 128 + quad * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t s_col = tmem + lane_base + Cf::SCOL + tile * 128, o_col = tmem + lane_base + Cf::OCOL + tile * D;
-    const float f = fmaxf(p.sm_scale * 1.4426950408889634f, 1e-44f);
+    uint32_t it = 0;                           // steps so far
     float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + kTickets * 4);
     uint32_t s_phase = 0, o_phase = 0;
     bool ok = true;                            // a warp that gave up goes on through the joins, for their barriers
@@ -383,21 +403,37 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
       const bool active = tile * 128 < R;
       const int first_tok = w.k * tq, qi = p.row_of(r), hq = w.h * G + r - qi * G;
       const long long row = static_cast<long long>(w.q.row0) + first_tok + qi;
-      float m = kNoMax, off = 3.0e38f, l = 0.f;
+      float m = kNoMax, off = 3.0e38f, l = 0.f;   // running maximum in log2 units, -m, sum
+      int q_pow = 0;                             // the row's power of two
       if (active && ok) {
-        // ---- Q tile: 16-byte pieces, dimensions of a piece in the order (0,4,1,5,2,6,3,7) as the keys' ----
-        for (int it = tid & 127; it < 128 * (D / 8); it += 128) {
-          const int rr = it / (D / 8), c = it % (D / 8), rt = tile * 128 + rr;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (rt < R) {
-            const int qj = p.row_of(rt);
-            v = ld_global_nc_v4(p.q + (static_cast<long long>(w.q.row0) + first_tok + qj) * p.q_stride +
-                                (w.h * G + rt - qj * G) * D + c * 8);
+        // ---- the warp's 32 rows of the Q tile: C lanes to a row, 32 / C rows at a time ----
+        constexpr int C = D / 8, AT = 32 / C, BATCH = 8;
+        const int c = lane % C;
+#pragma unroll 1
+        for (int j0 = 0; j0 < 32 / AT; j0 += BATCH) {
+          uint4 v[BATCH];
+#pragma unroll
+          for (int j = 0; j < BATCH; ++j) {
+            const int rt = tile * 128 + quad * 32 + (j0 + j) * AT + lane / C, qj = p.row_of(rt);
+            v[j] = rt < R ? ld_global_nc_v4(p.q + (static_cast<long long>(w.q.row0) + first_tok + qj) * p.q_stride +
+                                            (w.h * G + rt - qj * G) * D + c * 8)
+                          : make_uint4(0u, 0u, 0u, 0u);
           }
-          *reinterpret_cast<uint4*>(smem + Cf::OFF_Q + tile * Cf::TILE + (c >> 3) * Cf::ATOM + rr * 128 +
-                                    (((c & 7) ^ (rr & 7)) << 4)) =
-              make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                         __byte_perm(v.y, v.w, 0x7632));
+#pragma unroll
+          for (int j = 0; j < BATCH; ++j) {
+            uint32_t top = max_abs_bf16x2(max_abs_bf16x2(v[j].x, v[j].y), max_abs_bf16x2(v[j].z, v[j].w)) & 0x7FFF7FFFu;
+            uint32_t e = max(top & 0xFFFFu, top >> 16) >> 7;
+#pragma unroll
+            for (int s = C / 2; s > 0; s >>= 1) e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, s));
+            const int k = min(141 - static_cast<int>(e), 127);
+            const float fk = pow2i(k);
+            auto two = [&](uint32_t b) { return pack_f16(__uint_as_float(b << 16) * fk, __uint_as_float(b & 0xFFFF0000u) * fk); };
+            const int rr = quad * 32 + (j0 + j) * AT + lane / C;
+            *reinterpret_cast<uint4*>(smem + Cf::OFF_Q + tile * Cf::TILE + (c >> 3) * Cf::ATOM + rr * 128 +
+                                      (((c & 7) ^ (rr & 7)) << 4)) = make_uint4(two(v[j].x), two(v[j].y), two(v[j].z), two(v[j].w));
+            const int mine = __shfl_sync(0xFFFFFFFFu, k, (lane % AT) * C);
+            if (lane / AT == j0 + j) q_pow = mine;               // this thread's own row
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before();                     // the last unit's O has been read
@@ -411,6 +447,9 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
           s_phase ^= 1;
           tc_fence_after();
           const int k0 = (w.t + i) * kKeys;
+          // score -> log2 units; positive, so that a masked score stays -infinity
+          const int ref = *reinterpret_cast<volatile int*>(key_ref + ((it + i) & 3));
+          const float f = fmaxf(p.sm_scale * 1.4426950408889634f * pow2i(max(-126, min(127, ref - 140 - q_pow))), 1e-44f);
           const bool edge = __any_sync(0xFFFFFFFFu, k0 + kKeys > seen);
           uint32_t x[128];
 #pragma unroll
@@ -430,14 +469,14 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
             for (int u = c + 4; u < 128; u += 8)
               top[c] = fmaxf(top[c], u + 4 < 128 ? fmaxf(__uint_as_float(x[u]), __uint_as_float(x[u + 4])) : __uint_as_float(x[u]));
           }
-          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f;
           // the maximum follows once it is 2^8 ahead
-          const bool grow = m == kNoMax ? mx > m : (mx - m) * f > 8.f;
+          const bool grow = m == kNoMax ? mx > m : mx - m > 8.f;
           float a = 1.f;
           if (grow) {
-            a = ex2((m - mx) * f);
+            a = ex2(m - mx);
             m = mx;
-            off = fminf(-m * f, 3.0e38f);
+            off = -m;
             l *= a;
           }
           if (i > 0 && __any_sync(0xFFFFFFFFu, grow)) {
@@ -481,6 +520,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
           tc_fence_after();
         }
       }
+      it += w.steps();
       // ---- the unit's output, or the part of it ----
       const bool whole = w.t == 0 && w.steps() == w.n;
       const uint32_t u0 = share.first(cta + 1) - w.left - w.t;    // the unit's first step on the line
@@ -514,7 +554,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
           }
         }
         if (r < R) {
-          const float mm = fmaxf(m * f, kNoMax);
+          const float mm = fmaxf(m, kNoMax);
           if (!whole) *reinterpret_cast<float2*>(mine + kRows * D + 2 * r) = make_float2(mm, l);
           else if (p.lse != nullptr) p.lse[row * p.Hq + hq] = l == 0.f ? -INFINITY : fmaf(mm, 0.6931471805599453f, logf(l));
         }
@@ -594,7 +634,24 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
         const uint32_t ph = it >> 1 & 1;
         if (!(ok = __all_sync(0xFFFFFFFFu, wait(raw_full(s), ph)))) break;
         if (!(ok = __all_sync(0xFFFFFFFFu, wait(k_empty(s), ph ^ 1)))) break;
-        const uint8_t* ch = smem + Cf::OFF_RAW + s * Cf::RAW + dw * Ch::kBytes;
+        const uint8_t* raw = smem + Cf::OFF_RAW + s * Cf::RAW;
+        const uint8_t* ch = raw + dw * Ch::kBytes;
+        const int tok0 = (w.t + i) * kKeys;
+        // the step's largest key scale: 4 bytes a time, lanes over the 8 chunks
+        uint32_t top = 0;
+#pragma unroll
+        for (int u = 0; u < J; ++u) {
+          const int word = u * 32 + lane, r16 = word / (4 * J), at = word % (4 * J) * 4;      // chunk, byte of its scales
+          const uint32_t x = *reinterpret_cast<const uint32_t*>(raw + r16 * Ch::kBytes + Ch::kKeyScales + at);
+          const int tok = tok0 + r16 * 16 + at / J;
+#pragma unroll
+          for (int bb = 0; bb < 4; ++bb) {
+            const uint32_t e = x >> (8 * bb) & 0xFFu;
+            if (tok + bb / J < w.q.len) top = max(top, e);
+          }
+        }
+        const int ref = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, top));
+        if (dw == 0 && lane == 0) *reinterpret_cast<volatile int*>(key_ref + (it & 3)) = ref;
         // keys: lane = piece t of tokens r, r + 8; a quarter of the warp holds rows x and x + 4, which the swizzle
         // spreads over all banks
         {
@@ -614,9 +671,16 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
               sc = *reinterpret_cast<const uint16_t*>(ch + Ch::kKeyScales + r * J);
             }
 #pragma unroll
-            for (int j = 0; j < J; ++j)
+            for (int j = 0; j < J; ++j) {
+              // 2^(e - ref + 13), in FP16 down to 2^-24 (cells beyond the length: anything)
+              const int k = static_cast<int>(sc >> (8 * j) & 0xFFu) - ref + 140;
+              const float fk = __uint_as_float(static_cast<uint32_t>(max(k, 0)) << 23);
+              const uint32_t f2 = pack_f16(fk, fk);
+              uint32_t x[4];
+              e2m1x8_to_f16x2(wd[j], x);
               *reinterpret_cast<uint4*>(kt + (j >> 1) * Cf::ATOM + row * 128 + ((((j & 1) * 4 + t) ^ (row & 7)) << 4)) =
-                  e2m1x8_scaled(wd[j], sc >> (8 * j) & 0xFFu, sc >> (8 * j) & 0xFFu);
+                  make_uint4(mul_f16x2(x[0], f2), mul_f16x2(x[1], f2), mul_f16x2(x[2], f2), mul_f16x2(x[3], f2));
+            }
           }
         }
         fence_proxy_async_smem();
@@ -627,7 +691,6 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
         {
           uint8_t* vt = smem + Cf::OFF_V + s * Cf::TILE;
           const int g = lane >> 2, t = lane & 3;
-          const int tok0 = (w.t + i) * kKeys + dw * 16;
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
             uint32_t run[2][J / 2];
@@ -641,15 +704,30 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
 #pragma unroll
             for (int o = 0; o < 2; ++o) {
               const int r = hh * 8 + 2 * t + o, row = dw * 16 + r;
-              const bool live = tok0 + r < w.q.len;
+              uint32_t sc;
+              if constexpr (J == 4) sc = *reinterpret_cast<const uint32_t*>(ch + Ch::kValueScales + r * J);
+              else sc = *reinterpret_cast<const uint16_t*>(ch + Ch::kValueScales + r * J);
+              if (tok0 + dw * 16 + r >= w.q.len) {
+                sc = 0u;
+#pragma unroll
+                for (int q4 = 0; q4 < J / 2; ++q4) run[o][q4] = 0u;
+              }
+              uint4 y[J / 2];
+#pragma unroll
+              for (int q4 = 0; q4 < J / 2; ++q4) y[q4] = e2m1x8_to_bf16x2(run[o][q4]);
+              // word q4: bytes of row tiles 4 q4 ..+3: 32-blocks 2 q4 (low halves) and 2 q4 + 1 (high halves), so the
+              // factor's halves are the two blocks' 2^(e - 1); for e > 127 2^126 first, then 2^(e - 127)
+              uint32_t plus = 0x3F003F00u;
+              if ((sc & 0x80808080u) != 0u) {
+#pragma unroll
+                for (int q4 = 0; q4 < J / 2; ++q4) y[q4] = mul_bf16x8(y[q4], 0x7E807E80u);
+                plus = 0u;
+              }
 #pragma unroll
               for (int q4 = 0; q4 < J / 2; ++q4) {
-                // word q4: bytes of row tiles 4 q4 ..+3: 32-blocks 2 q4 (bytes 0, 1) and 2 q4 + 1 (bytes 2, 3)
-                const uint32_t sc = *reinterpret_cast<const uint16_t*>(ch + Ch::kValueScales + r * J + 2 * q4);
-                const uint32_t wv = live ? run[o][q4] : 0u;
-                const uint32_t sv = live ? sc : 0u;
-                *reinterpret_cast<uint4*>(vt + q4 * Cf::ATOM + row * 128 + ((g ^ (row & 7)) << 4)) =
-                    e2m1x8_scaled(wv, sv & 0xFFu, sv >> 8);
+                uint32_t f2 = __byte_perm(sc, 0u, q4 ? 0x4342 : 0x4140) * 128u + plus;
+                if (plus == 0u) f2 = max(f2 & 0xFFFFu, 0x40u) | max(f2 >> 16, 0x40u) << 16;    // 2^-127 for e = 0
+                *reinterpret_cast<uint4*>(vt + q4 * Cf::ATOM + row * 128 + ((g ^ (row & 7)) << 4)) = mul_bf16x8(y[q4], f2);
               }
             }
           }
@@ -666,7 +744,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
    regs_down<Cf::REGS_REST>();
    if (warp == 16) {
     // ---------------- MMA issuer: the whole warp walks, so that addresses stay in uniform registers ----------------
-    const uint32_t id_s = idesc_bf16(kKeys), id_o = idesc_bf16(D) | kIdescBMajorN;
+    const uint32_t id_s = idesc_f16(kKeys), id_o = idesc_bf16(D) | kIdescBMajorN;
     const uint64_t qd = sdesc_sw128(base + Cf::OFF_Q), kd = sdesc_sw128(base + Cf::OFF_K);
     const uint64_t vd = sdesc_mn_sw128(base + Cf::OFF_V, Cf::ATOM);
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
