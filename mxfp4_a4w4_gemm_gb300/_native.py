@@ -101,9 +101,7 @@ def lib():
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
     if hasattr(x, "data_ptr"):
         if not x.is_contiguous():
@@ -115,16 +113,30 @@ def _ptr(x):
 def _rows_ptr(x, stride):
     """Rows of [heads, D] values, `stride` elements apart: only the rows themselves must be contiguous."""
     if hasattr(x, "data_ptr"):
-        if x.dim() != 3 or (x.numel() > 0 and not x[0].is_contiguous()) or (x.size(0) > 1 and x.stride(0) != stride):
+        if x.dim() != 3 or x.numel() == 0:
+            ok = x.numel() == 0
+        else:
+            (T, H, D), (st, sh, sd) = x.shape, x.stride()
+            ok = (D == 1 or sd == 1) and (H == 1 or sh == D) and (T == 1 or st == stride)
+        if not ok:
             raise ValueError("rows must be a [T, heads, D] tensor with contiguous [heads, D] and the given row stride")
         return x.data_ptr()
     return _ptr(x)
 
 
+_current_stream = None
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _current_stream
+        if _current_stream is None:
+            import torch
+            torch.cuda.init()
+            # the handle itself, without a Stream object around it
+            raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            _current_stream = lambda: raw(device())  # noqa: E731
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -389,7 +389,7 @@ int a4w4_kv_append(const void* k_bf16, long long k_stride, const void* v_bf16, l
   if (sms < 0) return sms;
   if (T == 0) return A4W4_OK;
   return a4w4::launch_kv_append(k_bf16, k_stride, v_bf16, v_stride, slot_map, T, Hkv, D, cache, num_pages, page_size,
-                                as_stream(stream), sms);
+                                as_stream(stream));
 }
 
 int a4w4_kv_read(const void* cache, int num_pages, int page_size, const int32_t* slot_map, int T, int Hkv, int D,
@@ -400,7 +400,7 @@ int a4w4_kv_read(const void* cache, int num_pages, int page_size, const int32_t*
   if (sms < 0) return sms;
   if (T == 0) return A4W4_OK;
   return a4w4::launch_kv_read(cache, num_pages, page_size, slot_map, T, Hkv, D, k_out_bf16, v_out_bf16,
-                              as_stream(stream), sms);
+                              as_stream(stream));
 }
 
 size_t a4w4_kv_attention_workspace_bytes(int B, int max_q, int Hq, int Hkv, int D) {

@@ -148,93 +148,120 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs p)
   }
 }
 
-// One thread per 32-block of one token and head.
+// Thread -> (token, head, 32-block) of the append and read kernels: a warp takes
+// one head of 32 / J consecutive tokens.  New tokens mostly follow one another
+// in a page, so that the warp's pieces of a chunk lie side by side (32 / J tokens
+// x 2 J bytes of every value run) while each token's BF16 row is still touched in
+// runs of 64 J bytes.
+template <int D>
+struct RowItem {
+  static constexpr int J = D / 32, TOK = 32 / J;
+  int t, h, j;
+  __device__ __forceinline__ RowItem(int Hkv) {
+    const int lane = threadIdx.x & 31;
+    const long long wid = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    const int group = static_cast<int>(wid / Hkv);
+    h = static_cast<int>(wid - static_cast<long long>(group) * Hkv);
+    j = lane % J;
+    t = group * TOK + lane / J;
+  }
+};
+
+// Quantises one 32-block of a token's keys and the same one of its values: 128
+// bytes read, 34 written.  HBM-bound.
 template <int D>
 __global__ void __launch_bounds__(256) kv_append_kernel(const uint16_t* __restrict__ k, long long k_stride,
                                                         const uint16_t* __restrict__ v, long long v_stride,
                                                         const int32_t* __restrict__ slot_map, int T, int Hkv,
-                                                        uint8_t* __restrict__ cache, int slots, int page_size) {
+                                                        uint8_t* __restrict__ cache, int slots, int page_lg) {
   using Ch = KvChunk<D>;
   griddep_wait();
   griddep_launch_dependents();
-  const int blocks = Hkv * Ch::J;                     // per token, for keys and again for values
-  const long long total = 2ll * T * blocks;
-  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += stride) {
-    const long long row = i / blocks;
-    const int hj = static_cast<int>(i - row * blocks), h = hj / Ch::J, j = hj % Ch::J;
-    const bool is_v = row >= T;
-    const long long t = is_v ? row - T : row;
-    const int slot = slot_map[t];
-    if (static_cast<unsigned>(slot) >= static_cast<unsigned>(slots)) continue;
-    const uint16_t* src = (is_v ? v + t * v_stride : k + t * k_stride) + hj * 32;
-    uint32_t w[16], c[4];
+  const RowItem<D> it(Hkv);
+  if (it.t >= T) return;
+  const int slot = slot_map[it.t];
+  if (static_cast<unsigned>(slot) >= static_cast<unsigned>(slots)) return;
+  const int j = it.j, at = it.h * D + 32 * j;
+  uint32_t wk[16], wv[16], c[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint4 x = ld_global_nc_v4(src + 8 * u);
-      w[4 * u] = x.x; w[4 * u + 1] = x.y; w[4 * u + 2] = x.z; w[4 * u + 3] = x.w;
-    }
-    const uint32_t e = quant32_bf16(w, c);
-    const int page = slot / page_size, r = slot % 16, ch = slot % page_size / 16;
-    uint8_t* chunk = cache + kv_chunk_offset<D>(page, h, ch, Hkv, page_size / 16);
-    if (!is_v) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) *reinterpret_cast<uint32_t*>(chunk + Ch::key_word(r, j, u)) = c[u];
-      chunk[Ch::kKeyScales + r * Ch::J + j] = static_cast<uint8_t>(e);
-    } else {
-      // byte g of each half block 16 i belongs to run g, at i
-#pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        const uint32_t lo = c[g / 4] >> (8 * (g % 4)) & 0xFFu, hi = c[2 + g / 4] >> (8 * (g % 4)) & 0xFFu;
-        *reinterpret_cast<uint16_t*>(chunk + Ch::value_run(r, g) + 2 * j) = static_cast<uint16_t>(lo | hi << 8);
-      }
-      chunk[Ch::kValueScales + r * Ch::J + j] = static_cast<uint8_t>(e);
-    }
+  for (int u = 0; u < 4; ++u) {
+    const uint4 x = ld_global_nc_v4(k + it.t * k_stride + at + 8 * u), y = ld_global_nc_v4(v + it.t * v_stride + at + 8 * u);
+    wk[4 * u] = x.x; wk[4 * u + 1] = x.y; wk[4 * u + 2] = x.z; wk[4 * u + 3] = x.w;
+    wv[4 * u] = y.x; wv[4 * u + 1] = y.y; wv[4 * u + 2] = y.z; wv[4 * u + 3] = y.w;
   }
+  const int r = slot & 15, chunks = 1 << (page_lg - 4);
+  uint8_t* chunk = cache + kv_chunk_offset<D>(slot >> page_lg, it.h, (slot >> 4) & (chunks - 1), Hkv, chunks);
+  const uint32_t ek = quant32_bf16(wk, c);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) *reinterpret_cast<uint32_t*>(chunk + Ch::key_word(r, j, u)) = c[u];
+  chunk[Ch::kKeyScales + r * Ch::J + j] = static_cast<uint8_t>(ek);
+  const uint32_t ev = quant32_bf16(wv, c);
+  // byte g of each half block 16 i belongs to run g, at i = 2 j, 2 j + 1
+#pragma unroll
+  for (int g = 0; g < 8; ++g)
+    *reinterpret_cast<uint16_t*>(chunk + Ch::value_run(r, g) + 2 * j) =
+        static_cast<uint16_t>(__byte_perm(c[g / 4], c[2 + g / 4], (g % 4) | (4 + g % 4) << 4));
+  chunk[Ch::kValueScales + r * Ch::J + j] = static_cast<uint8_t>(ev);
 }
 
-// Two E2M1 codes of a byte times 2^(e - 127), as BF16x2 (exact).
-__device__ __forceinline__ uint32_t e2m1x2_to_bf16x2(uint32_t byte, uint32_t e) {
-  constexpr float kMag[8] = {0.f, 0.5f, 1.f, 1.5f, 2.f, 3.f, 4.f, 6.f};
-  const float s = e == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(e << 23);
-  const float a = kMag[byte & 7u] * s, b = kMag[byte >> 4 & 7u] * s;
-  const uint32_t ua = __float_as_uint(a) | (byte & 8u) << 28, ub = __float_as_uint(b) | (byte & 0x80u) << 24;
-  return ua >> 16 | (ub & 0xFFFF0000u);
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
-// One thread per 32-block of one token and head.
+// Eight E2M1 codes (nibble n of w) times 2^(e - 127) -> eight BF16, exact:
+// magnitude bits placed at 6..8 of a BF16 and the sign at 15 read as the value
+// times 2^-126; the scale follows in two multiplies by powers of two.
+__device__ __forceinline__ uint4 e2m1x8_to_bf16x8(uint32_t w, uint32_t e) {
+  constexpr uint32_t kMag = 0x01C001C0u, kSign = 0x80008000u;
+  const uint32_t f = max(e << 7, 0x40u) * 0x00010001u;                // 2^(e - 127)
+  uint32_t o[4];                                                       // elements (n, n + 4)
+  o[0] = ((w << 6) & kMag) | ((w << 12) & kSign);
+  o[1] = ((w << 2) & kMag) | ((w << 8) & kSign);
+  o[2] = ((w >> 2) & kMag) | ((w << 4) & kSign);
+  o[3] = ((w >> 6) & kMag) | (w & kSign);
+#pragma unroll
+  for (int n = 0; n < 4; ++n) o[n] = mul_bf16x2(mul_bf16x2(o[n], 0x7E807E80u), f);
+  return make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410), __byte_perm(o[0], o[1], 0x7632),
+                    __byte_perm(o[2], o[3], 0x7632));
+}
+
+// The inverse: 34 bytes read, 128 written.  HBM-bound.
 template <int D>
-__global__ void __launch_bounds__(256) kv_read_kernel(const uint8_t* __restrict__ cache, int slots, int page_size,
+__global__ void __launch_bounds__(256) kv_read_kernel(const uint8_t* __restrict__ cache, int slots, int page_lg,
                                                       const int32_t* __restrict__ slot_map, int T, int Hkv,
                                                       uint16_t* __restrict__ k, uint16_t* __restrict__ v) {
   using Ch = KvChunk<D>;
   griddep_wait();
   griddep_launch_dependents();
-  const int blocks = Hkv * Ch::J;
-  const long long total = 2ll * T * blocks;
-  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += stride) {
-    const long long row = i / blocks;
-    const int hj = static_cast<int>(i - row * blocks), h = hj / Ch::J, j = hj % Ch::J;
-    const bool is_v = row >= T;
-    const long long t = is_v ? row - T : row;
-    const int slot = slot_map[t];
-    uint32_t o[16];
+  const RowItem<D> it(Hkv);
+  if (it.t >= T) return;
+  const int slot = slot_map[it.t], j = it.j;
+  uint32_t wk[4] = {0u, 0u, 0u, 0u}, wv[4] = {0u, 0u, 0u, 0u}, ek = 0u, ev = 0u;
+  if (static_cast<unsigned>(slot) < static_cast<unsigned>(slots)) {
+    const int r = slot & 15, chunks = 1 << (page_lg - 4);
+    const uint8_t* chunk = cache + kv_chunk_offset<D>(slot >> page_lg, it.h, (slot >> 4) & (chunks - 1), Hkv, chunks);
+    uint32_t b[8];
 #pragma unroll
-    for (int u = 0; u < 16; ++u) o[u] = 0u;
-    if (static_cast<unsigned>(slot) < static_cast<unsigned>(slots)) {
-      const int page = slot / page_size, r = slot % 16, ch = slot % page_size / 16;
-      const uint8_t* chunk = cache + kv_chunk_offset<D>(page, h, ch, Hkv, page_size / 16);
-      const uint32_t e = chunk[(is_v ? Ch::kValueScales : Ch::kKeyScales) + r * Ch::J + j];
+    for (int u = 0; u < 4; ++u) wk[u] = *reinterpret_cast<const uint32_t*>(chunk + Ch::key_word(r, j, u));
 #pragma unroll
-      for (int u = 0; u < 16; ++u) {
-        const uint32_t byte = is_v ? chunk[Ch::value_run(r, u % 8) + 2 * j + u / 8] : chunk[Ch::key_word(r, j, u / 4) + u % 4];
-        o[u] = e2m1x2_to_bf16x2(byte, e);
-      }
+    for (int g = 0; g < 8; ++g) b[g] = *reinterpret_cast<const uint16_t*>(chunk + Ch::value_run(r, g) + 2 * j);
+    ek = chunk[Ch::kKeyScales + r * Ch::J + j];
+    ev = chunk[Ch::kValueScales + r * Ch::J + j];
+    // low bytes: dimensions 0..15 of the block, high bytes: 16..31
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t p01 = __byte_perm(b[4 * q], b[4 * q + 1], 0x5140), p23 = __byte_perm(b[4 * q + 2], b[4 * q + 3], 0x5140);
+      wv[q] = __byte_perm(p01, p23, 0x5410);
+      wv[2 + q] = __byte_perm(p01, p23, 0x7632);
     }
-    uint4* dst = reinterpret_cast<uint4*>((is_v ? v : k) + t * blocks * 32 + hj * 32);
+  }
+  const long long at = (static_cast<long long>(it.t) * Hkv + it.h) * D + 32 * j;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) dst[u] = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+  for (int u = 0; u < 4; ++u) {
+    *reinterpret_cast<uint4*>(k + at + 8 * u) = e2m1x8_to_bf16x8(wk[u], ek);
+    *reinterpret_cast<uint4*>(v + at + 8 * u) = e2m1x8_to_bf16x8(wv[u], ev);
   }
 }
 
@@ -255,19 +282,35 @@ int launch_kv_plan(const int32_t* past_lens, const int32_t* new_lens, int B, int
   return launch_pdl(kv_plan_kernel, grid, kPlanThreads, st, p);
 }
 
+namespace {
+
+// CTAs of 256 threads for T tokens, Hkv heads, J blocks (RowItem); -1: too many.
+int row_grid(int T, int Hkv, int D) {
+  const int tok = 32 / (D / 32);
+  const long long warps = (static_cast<long long>(T) + tok - 1) / tok * Hkv;
+  const long long g = (warps + 7) / 8;
+  return g > INT32_MAX ? -1 : static_cast<int>(g);
+}
+
+int log2_of(int page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7; }
+
+}  // namespace
+
 int launch_kv_append(const void* k, long long k_stride, const void* v, long long v_stride, const int32_t* slot_map,
-                     int T, int Hkv, int D, void* cache, int num_pages, int page_size, cudaStream_t st, int sms) {
-  const int grid = grid_for(2ll * T * Hkv * (D / 32), 256, sms * 8);
+                     int T, int Hkv, int D, void* cache, int num_pages, int page_size, cudaStream_t st) {
+  const int grid = row_grid(T, Hkv, D);
+  if (grid < 0) return -1;
   return launch_pdl(D == 64 ? kv_append_kernel<64> : kv_append_kernel<128>, grid, 256, st,
                     static_cast<const uint16_t*>(k), k_stride, static_cast<const uint16_t*>(v), v_stride, slot_map, T,
-                    Hkv, static_cast<uint8_t*>(cache), num_pages * page_size, page_size);
+                    Hkv, static_cast<uint8_t*>(cache), num_pages * page_size, log2_of(page_size));
 }
 
 int launch_kv_read(const void* cache, int num_pages, int page_size, const int32_t* slot_map, int T, int Hkv, int D,
-                   void* k, void* v, cudaStream_t st, int sms) {
-  const int grid = grid_for(2ll * T * Hkv * (D / 32), 256, sms * 8);
+                   void* k, void* v, cudaStream_t st) {
+  const int grid = row_grid(T, Hkv, D);
+  if (grid < 0) return -1;
   return launch_pdl(D == 64 ? kv_read_kernel<64> : kv_read_kernel<128>, grid, 256, st,
-                    static_cast<const uint8_t*>(cache), num_pages * page_size, page_size, slot_map, T, Hkv,
+                    static_cast<const uint8_t*>(cache), num_pages * page_size, log2_of(page_size), slot_map, T, Hkv,
                     static_cast<uint16_t*>(k), static_cast<uint16_t*>(v));
 }
 

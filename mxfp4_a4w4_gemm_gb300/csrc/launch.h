@@ -145,9 +145,9 @@ int launch_kv_plan(const int32_t* past_lens, const int32_t* new_lens, int B, int
                    int32_t* ring_state_out, int32_t* kv_lens, int32_t* cu_new, int32_t* slot_map, int32_t* positions,
                    int max_tokens, int32_t* refused, cudaStream_t st, int sms);
 int launch_kv_append(const void* k, long long k_stride, const void* v, long long v_stride, const int32_t* slot_map,
-                     int T, int Hkv, int D, void* cache, int num_pages, int page_size, cudaStream_t st, int sms);
+                     int T, int Hkv, int D, void* cache, int num_pages, int page_size, cudaStream_t st);
 int launch_kv_read(const void* cache, int num_pages, int page_size, const int32_t* slot_map, int T, int Hkv, int D,
-                   void* k, void* v, cudaStream_t st, int sms);
+                   void* k, void* v, cudaStream_t st);
 
 struct KvAttentionArgs {
   const uint16_t* q;            // row t, head h at q + t * q_stride + h * D
