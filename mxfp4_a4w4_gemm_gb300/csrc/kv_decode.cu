@@ -50,7 +50,7 @@ namespace {
 
 constexpr int kStep = 32;                     // tokens of a step
 constexpr int kLeast = 2;                     // steps of a worker, at least
-constexpr int kMaxParts = 512;                // CTAs of a launch, and so parts of a cut unit
+constexpr int kMaxParts = 256;                // CTAs of a launch, and so parts of a cut unit
 constexpr float kNoMax = -3.0e38f;            // running maximum before the first key
 
 template <int D, int NT>
@@ -70,14 +70,14 @@ struct DecCfg {
   static constexpr int OFF_ML = OFF_O + WARPS * ROWS * PITCH * 4;   // maxima and sums: [tail or head][warp][row]
   static constexpr int OFF_BAR = OFF_ML + 2 * WARPS * ROWS * 8;
   static constexpr int OFF_OPEN = OFF_BAR + WARPS * STAGES * 8;
-  static constexpr int OFF_MISC = OFF_OPEN + (WARPS + 1) * 16;
+  static constexpr int OFF_MISC = OFF_OPEN + (WARPS + 1) * 20;
   static constexpr int SMEM = OFF_MISC + 16;
   static constexpr int OFF_SCAN = OFF_O;                         // the cut's scratch, before there are parts
   static constexpr int PART = ROWS * (D + 2);                    // floats of a stored part: O, then m and l
   static_assert(STAGE % 16 == 0 && OFF_KS % 16 == 0 && OFF_VS % 16 == 0 && OFF_O % 16 == 0, "alignment");
-  static_assert(kMaxParts <= WARPS * PITCH && kMaxParts <= kTickets && PART % 4 == 0, "join");
+  static_assert(2 * kMaxParts <= WARPS * PITCH && kMaxParts <= kTickets && PART % 4 == 0, "join");
   static_assert(ROWS * PITCH * 4 <= STAGES * STAGE, "a part fits in the warp's drained ring");
-  static_assert(OFF_OPEN % 16 == 0 && (THREADS + 32) * 4 <= WARPS * ROWS * PITCH * 4, "scratch");
+  static_assert(OFF_OPEN % 4 == 0 && (THREADS + 32) * 4 <= WARPS * ROWS * PITCH * 4, "scratch");
   static_assert(OFF_BAR % 8 == 0 && SMEM <= 232448, "shared memory");
 };
 
@@ -170,8 +170,8 @@ __device__ __forceinline__ void load_runs(const uint8_t* codes, int lane, uint32
 
 // A unit of which a part waits in this CTA's shared memory.
 struct Open {
-  int b, h;
-  uint32_t u0, n;             // its place on the line; n == 0: none
+  int row0, h, rows;          // first row of the request, head, rows to join; rows == 0: none
+  uint32_t v0, v1;            // the workers that hold its first and its last step
 };
 
 // A walk along the worker's run: one piece (a run of one unit's steps) at a time.
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
   const uint32_t sbase = smem_u32(smem);
   auto full = [&](int s) { return sbase + Cf::OFF_BAR + 8u * (warp * S + s); };
   if (tid == 0) { *abort_flag = 0; *never = 0; }
-  if (tid <= W) open[tid].n = 0;
+  if (tid <= W) open[tid].rows = 0;
   if (lane == 0)
     for (int s = 0; s < S; ++s) mbar_init(full(s), 1);
   fence_barrier_init();
@@ -266,7 +266,8 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
       page0 = tok < pw.len ? kv_page(p, pw.b, tok >> lg) : 0;
       if (lg == 4) page1 = tok + 16 < pw.len ? kv_page(p, pw.b, (tok + 16) >> 4) : 0;
     }
-    const int id0 = __shfl_sync(0xFFFFFFFFu, page0, pi & 31), id1 = __shfl_sync(0xFFFFFFFFu, page1, pi & 31);
+    const int id0 = __shfl_sync(0xFFFFFFFFu, page0, pi & 31);
+    const int id1 = lg == 4 ? __shfl_sync(0xFFFFFFFFu, page1, pi & 31) : 0;
     if (lane == 0) {
       const int slot = issued % S;
       const bool two = pw.len - ptok > 16;
@@ -311,7 +312,6 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
     if (!first_piece) load_queries();
     first_piece = false;
     float fcol[NT][2];                         // raw score -> log2 units, per column
-    int lim[NT][2];                            // keys seen by the column's row
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       uint32_t top = 0;
@@ -335,7 +335,6 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         fcol[nt][u] = __shfl_sync(0xFFFFFFFFu, back, (2 * t + u) * 4);
-        lim[nt][u] = len - cw.all + p.row_of(nt * 8 + 2 * t + u) + 1;
       }
     }
     const int all_seen = len - cw.all + 1;                     // keys that every row sees
@@ -367,7 +366,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
 
       // ---- scale factors, lane = token; the value factor of a cell beyond the length is finite ----
       uint32_t vw;
-      bool vlow = false;                                       // a value factor that FP16 does not hold
+      bool vlow;                                               // a value factor that FP16 does not hold
       int nref;
       {
         const uint8_t* c = st + (lane >> 4) * Ch::kBytes + (lane & 15) * J;
@@ -380,21 +379,29 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
           vw = *reinterpret_cast<const uint16_t*>(c + Ch::kValueScales);
         }
         if (tok0 + lane >= len) vw = 0u;                       // such a cell holds anything
-        uint32_t kf[J], vmax = 0;
+        uint32_t kf[J];                                        // 2^(e - 127)
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-          kf[j] = max((kw >> (8 * j) & 0xFFu) << 23, 0x00400000u);       // 2^(e - 127)
-          vmax = max(vmax, vw >> (8 * j) & 0xFFu);
-        }
+        for (int j = 0; j < J; ++j)
+          kf[j] = max((j < 3 ? kw << (23 - 8 * j) : kw >> 1) & 0x7F800000u, 0x00400000u);
         if constexpr (J == 4) *reinterpret_cast<uint4*>(ks + lane * 4) = make_uint4(kf[0], kf[1], kf[2], kf[3]);
         else *reinterpret_cast<uint2*>(ks + lane * 2) = make_uint2(kf[0], kf[1]);
-        nref = max(ref, static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, vmax)));
-        uint8_t* dst = vs + (lane >> 1 & 3) * 16 + (lane >> 4) * 8 + (lane >> 3 & 1) * 4 + (lane & 1) * 2;
+        // value scales, two blocks to a word
+        uint32_t e2[J / 2], top = 0u, least = 0xFFFFFFFFu;     // least: smallest e - 1, zero blocks left out
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const int e = static_cast<int>(vw >> (8 * j) & 0xFFu), k = e - nref + 9;
-          vlow |= k < 0 && e > 0;
-          *reinterpret_cast<uint16_t*>(dst + j * 64) = static_cast<uint16_t>(max(k + 15, 0) << 10);
+        for (int q = 0; q < J / 2; ++q) {
+          e2[q] = __byte_perm(vw, 0u, q ? 0x4342 : 0x4140);
+          top = __vmaxu2(top, e2[q]);
+          least = __viaddmin_u16x2(e2[q], 0xFFFFFFFFu, least);
+        }
+        nref = max(ref, static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16))));
+        vlow = static_cast<int>(min(least & 0xFFFFu, least >> 16)) < nref - 10;
+        uint8_t* dst = vs + (lane >> 1 & 3) * 16 + (lane >> 4) * 8 + (lane >> 3 & 1) * 4 + (lane & 1) * 2;
+        const uint32_t up = (24u - static_cast<uint32_t>(nref) & 0xFFFFu) * 0x00010001u;
+#pragma unroll
+        for (int q = 0; q < J / 2; ++q) {
+          const uint32_t f2 = __viaddmax_s16x2_relu(e2[q], up, 0u) << 10;      // 2^(e - nref + 9), exponent field >= 0
+          *reinterpret_cast<uint16_t*>(dst + q * 128) = static_cast<uint16_t>(f2);
+          *reinterpret_cast<uint16_t*>(dst + q * 128 + 64) = static_cast<uint16_t>(f2 >> 16);
         }
       }
       __syncwarp();
@@ -445,12 +452,14 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
       if (tok0 + kStep > all_seen) {
         asm volatile("" ::: "memory");                         // a branch, not selects in every step
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              if (tok0 + c * 16 + g + (u >> 1) * 8 >= lim[nt][u & 1]) x[c][nt][u] = -INFINITY;
+          for (int u = 0; u < 4; ++u) {
+            // keys that the column's row sees, from the step's first on
+            const int lim = all_seen + p.row_of(nt * 8 + 2 * t + (u & 1)) - tok0 - g - (u >> 1) * 8;
+            if (0 >= lim) x[0][nt][u] = -INFINITY;
+            if (16 >= lim) x[1][nt][u] = -INFINITY;
+          }
       }
 
       // ---- running maximum and value reference ----
@@ -636,8 +645,10 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
       }
     // the CTA's list of cut units: by the warp that holds their beginning, or by
     // the first warp if that lies in an earlier CTA
-    if (lane == 0 && ((back && !front) || (front && warp == 0)))
-      open[front ? 0 : warp + 1] = Open{cw.b, h, share.first(me + 1) - cw.left - cw.t, static_cast<uint32_t>(cw.n)};
+    if (lane == 0 && ((back && !front) || (front && warp == 0))) {
+      const uint32_t u0 = share.first(me + 1) - cw.left - cw.t;   // the unit's first step on the line
+      open[front ? 0 : warp + 1] = Open{cw.row0, h, R, share.holder(u0), share.holder(u0 + cw.n - 1)};
+    }
     cw.next(p);
   }
   __syncthreads();
@@ -646,17 +657,16 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
   const uint32_t cta = blockIdx.x;
   const float2* mls = reinterpret_cast<const float2*>(smem + Cf::OFF_ML);
   float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + kTickets * 4);
-  const uint32_t opened = __ballot_sync(0xFFFFFFFFu, lane <= W && open[min(lane, W)].n != 0);
-  bool outside = false;
+  const uint32_t opened = __ballot_sync(0xFFFFFFFFu, lane <= W && open[min(lane, W)].rows != 0);
+  uint32_t outside = 0;                                          // the units that reach into other CTAs: two at most
   int turn = 0;                                                  // rows are dealt to the warps in turn
   for (uint32_t left = opened; left != 0; left &= left - 1) {
     const Open un = open[__ffs(left) - 1];
-    const KvRequest rq = kv_request(p, un.b);
-    const int R = min(rq.rows * G, Cf::ROWS);
-    const uint32_t v0 = share.holder(un.u0), v1 = share.holder(un.u0 + un.n - 1);
+    const int R = un.rows;
+    const uint32_t v0 = un.v0, v1 = un.v1;
     const int w0 = v0 < cta * W ? 0 : v0 - cta * W, w1 = v1 >= cta * W + W ? W - 1 : v1 - cta * W;
     const bool whole = v0 >= cta * W && v1 < cta * W + W;
-    outside |= !whole;
+    if (!whole) outside |= left & -left;
     // all parts are tails but the one with the unit's end
     const int head = v1 < cta * W + W ? w1 : W;
     // two places per CTA outside: for a unit that began before it, and for one that goes on after it
@@ -692,7 +702,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
       }
       if (whole) {
         const int qi = p.row_of(r), hq = un.h * G + r - qi * G;
-        const long long row = static_cast<long long>(rq.row0) + qi;
+        const long long row = static_cast<long long>(un.row0) + qi;
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
         uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (row * p.Hq + hq) * D + lane * (D / 32));
 #pragma unroll
@@ -713,58 +723,76 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
   // ---- units that reach into other CTAs: the last to arrive joins ----
   __threadfence();
   __syncthreads();
-  for (uint32_t left = opened; left != 0; left &= left - 1) {
+  if (warp == 0) {                                               // a lane per unit draws its ticket
+    const bool mine = (outside >> lane & 1u) != 0;
+    bool last = false;
+    if (mine) {
+      const int c0 = open[lane].v0 / W, np = open[lane].v1 / W - c0 + 1;
+      last = atomicAdd(static_cast<int*>(p.ws) + c0, 1) == np - 1;
+    }
+    const uint32_t lasts = __ballot_sync(0xFFFFFFFFu, last);
+    if (lane == 0) *last_flag = static_cast<int>(lasts);
+  }
+  __syncthreads();
+  for (uint32_t left = static_cast<uint32_t>(*last_flag); left != 0; left &= left - 1) {
     const Open un = open[__ffs(left) - 1];
-    const int c0 = share.holder(un.u0) / W, np = share.holder(un.u0 + un.n - 1) / W - c0 + 1;
-    if (np == 1) continue;
-    int* ticket = static_cast<int*>(p.ws) + c0;
-    if (tid == 0) *last_flag = atomicAdd(ticket, 1) == np - 1;
-    __syncthreads();
-    if (*last_flag) {
+    const int c0 = un.v0 / W, np = un.v1 / W - c0 + 1, R = un.rows;
+    {
       __threadfence();
-      const KvRequest rq = kv_request(p, un.b);
-      const int R = min(rq.rows * G, Cf::ROWS);
       auto part = [&](int k) { return parts + (2 * (c0 + k) + (k == 0 ? 1 : 0)) * Cf::PART; };
-      float* wts = reinterpret_cast<float*>(smem + Cf::OFF_O);          // [row][part], the parts here are spent
-      float* sums = reinterpret_cast<float*>(smem + Cf::OFF_ML);        // [row]: m, l
-      // a warp per row: maximum, weights and sum of the parts
+      // maxima and sums of the parts, all on their way at once; then a warp per row turns them into weights
+      float2* stats = reinterpret_cast<float2*>(smem + Cf::OFF_O);       // [row][part], the parts here are spent
+      for (int i = tid; i < R * np; i += Cf::THREADS) {
+        const int r = i / np, k = i - r * np;
+        stats[r * kMaxParts + k] = __ldcg(reinterpret_cast<const float2*>(part(k) + Cf::ROWS * D + 2 * r));
+      }
+      __syncthreads();
       for (int r = warp; r < R; r += W) {
         float mm = kNoMax;
-        for (int k = lane; k < np; k += 32) mm = fmaxf(mm, __ldcg(part(k) + Cf::ROWS * D + 2 * r));
+        for (int k = lane; k < np; k += 32) mm = fmaxf(mm, stats[r * kMaxParts + k].x);
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, s));
         float ll = 0.f;
         for (int k = lane; k < np; k += 32) {
-          const float2 q = __ldcg(reinterpret_cast<const float2*>(part(k) + Cf::ROWS * D + 2 * r));
+          const float2 q = stats[r * kMaxParts + k];
           const float a = ex2(q.x - mm);
-          wts[r * kMaxParts + k] = a;
           ll = fmaf(q.y, a, ll);
+          stats[r * kMaxParts + k].x = a;
         }
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) ll += __shfl_xor_sync(0xFFFFFFFFu, ll, s);
-        if (lane == 0) { sums[2 * r] = mm; sums[2 * r + 1] = ll; }
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        __syncwarp();
+        for (int k = lane; k < np; k += 32) stats[r * kMaxParts + k].x *= inv;
+        if (lane == 0 && p.lse != nullptr) {
+          const int qi = p.row_of(r);
+          p.lse[(static_cast<long long>(un.row0) + qi) * p.Hq + un.h * G + r - qi * G] =
+              ll == 0.f ? -INFINITY : fmaf(mm, 0.6931471805599453f, logf(ll));
+        }
       }
       __syncthreads();
-      for (int it = tid; it < R * (D / 2); it += Cf::THREADS) {
-        const int r = it / (D / 2), d = it % (D / 2) * 2;
-        float y0 = 0.f, y1 = 0.f;
-#pragma unroll 8
-        for (int k = 0; k < np; ++k) {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(part(k) + r * D + d));
-          const float a = wts[r * kMaxParts + k];
-          y0 = fmaf(v.x, a, y0);
-          y1 = fmaf(v.y, a, y1);
+      // 16 bytes of a row per thread, 16 parts at a time
+      for (int it = tid; it < R * (D / 4); it += Cf::THREADS) {
+        const int r = it / (D / 4), d = it % (D / 4) * 4;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 < np; k0 += 16) {
+          float4 v[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            v[k] = __ldcg(reinterpret_cast<const float4*>(part(min(k0 + k, np - 1)) + r * D + d));
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float a = k0 + k < np ? stats[r * kMaxParts + k0 + k].x : 0.f;
+            y.x = fmaf(v[k].x, a, y.x); y.y = fmaf(v[k].y, a, y.y); y.z = fmaf(v[k].z, a, y.z); y.w = fmaf(v[k].w, a, y.w);
+          }
         }
-        const float ll = sums[2 * r + 1], inv = ll == 0.f ? 0.f : 1.f / ll;
         const int qi = p.row_of(r), hq = un.h * G + r - qi * G;
-        const long long row = static_cast<long long>(rq.row0) + qi;
-        *reinterpret_cast<uint32_t*>(p.out + (row * p.Hq + hq) * D + d) = pack_bf16(y0 * inv, y1 * inv);
-        if (d == 0 && p.lse != nullptr)
-          p.lse[row * p.Hq + hq] = ll == 0.f ? -INFINITY : fmaf(sums[2 * r], 0.6931471805599453f, logf(ll));
+        const long long row = static_cast<long long>(un.row0) + qi;
+        *reinterpret_cast<uint2*>(p.out + (row * p.Hq + hq) * D + d) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
       }
-      if (tid == 0) *ticket = 0;
+      if (tid == 0) static_cast<int*>(p.ws)[c0] = 0;
     }
-    __syncthreads();                                             // the weights and the flag are free again
+    __syncthreads();                                             // the weights are free again
   }
 }
 

@@ -594,6 +594,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
               y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
               st[u] = rows[min((it0 + u * 256) / Q4, R - 1)];
             }
+#pragma unroll 4
             for (int k = 0; k < np; ++k) {
               const float* src = part(k);
 #pragma unroll
