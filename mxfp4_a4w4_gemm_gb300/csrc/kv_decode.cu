@@ -49,7 +49,8 @@ namespace a4w4 {
 namespace {
 
 constexpr int kStep = 32;                     // tokens of a step
-constexpr int kLeast = 2;                     // steps of a worker, at least
+constexpr int kLeast = 1;                     // steps of a worker, at least
+constexpr int kFew = 4;                       // workers of a CTA, at least
 constexpr int kMaxParts = 256;                // CTAs of a launch, and so parts of a cut unit
 constexpr float kNoMax = -3.0e38f;            // running maximum before the first key
 
@@ -224,13 +225,14 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
     const KvRequest r = kv_request(p, b);
     return r.rows > 0 ? max(1, (r.len + kStep - 1) / kStep) * p.Hkv : 0;
   };
-  if (!kv_locate<Cf::THREADS, W>(p.B, steps_of, kLeast, reinterpret_cast<uint32_t*>(smem + Cf::OFF_SCAN), share, start))
+  if (!kv_locate<Cf::THREADS, W>(p.B, steps_of, kLeast, kFew, reinterpret_cast<uint32_t*>(smem + Cf::OFF_SCAN), share,
+                                 start))
     return;
-  const uint32_t me = blockIdx.x * W + warp;
+  const uint32_t per = share.per, me = blockIdx.x * per + warp;
 
   Walk cw;
   cw.left = 0;
-  if (me < share.workers) {
+  if (warp < per && me < share.workers) {
     cw.b = start.b;
     cw.load(p);
     cw.h = start.rest / cw.n;
@@ -664,13 +666,14 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
     const Open un = open[__ffs(left) - 1];
     const int R = un.rows;
     const uint32_t v0 = un.v0, v1 = un.v1;
-    const int w0 = v0 < cta * W ? 0 : v0 - cta * W, w1 = v1 >= cta * W + W ? W - 1 : v1 - cta * W;
-    const bool whole = v0 >= cta * W && v1 < cta * W + W;
+    const uint32_t mine0 = cta * per, mine1 = mine0 + per;         // this CTA's workers
+    const int w0 = v0 < mine0 ? 0 : v0 - mine0, w1 = v1 >= mine1 ? per - 1 : v1 - mine0;
+    const bool whole = v0 >= mine0 && v1 < mine1;
     if (!whole) outside |= left & -left;
     // all parts are tails but the one with the unit's end
-    const int head = v1 < cta * W + W ? w1 : W;
+    const int head = v1 < mine1 ? w1 : W;
     // two places per CTA outside: for a unit that began before it, and for one that goes on after it
-    float* mine = parts + (2 * cta + (v0 < cta * W ? 0 : 1)) * Cf::PART;
+    float* mine = parts + (2 * cta + (v0 < mine0 ? 0 : 1)) * Cf::PART;
     const int np = w1 - w0 + 1;
     for (int r = (warp - turn % W + W) % W; r < R; r += W) {
       const int w = w0 + lane;                                   // lane: a part
@@ -727,7 +730,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
     const bool mine = (outside >> lane & 1u) != 0;
     bool last = false;
     if (mine) {
-      const int c0 = open[lane].v0 / W, np = open[lane].v1 / W - c0 + 1;
+      const int c0 = open[lane].v0 / per, np = open[lane].v1 / per - c0 + 1;
       last = atomicAdd(static_cast<int*>(p.ws) + c0, 1) == np - 1;
     }
     const uint32_t lasts = __ballot_sync(0xFFFFFFFFu, last);
@@ -736,7 +739,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
   __syncthreads();
   for (uint32_t left = static_cast<uint32_t>(*last_flag); left != 0; left &= left - 1) {
     const Open un = open[__ffs(left) - 1];
-    const int c0 = un.v0 / W, np = un.v1 / W - c0 + 1, R = un.rows;
+    const int c0 = un.v0 / per, np = un.v1 / per - c0 + 1, R = un.rows;
     {
       __threadfence();
       auto part = [&](int k) { return parts + (2 * (c0 + k) + (k == 0 ? 1 : 0)) * Cf::PART; };
@@ -823,7 +826,7 @@ int launch_kv_decode(const KvAttentionArgs& p, int D, cudaStream_t st, int sms) 
   // as many CTAs as there can be work for, one per SM at most
   const long long per = (static_cast<long long>(p.max_pages) * p.page_size + kStep - 1) / kStep;
   const int most = sms < kMaxParts ? sms : kMaxParts;
-  const long long ctas = (per * p.B * p.Hkv + kLeast * 10 - 1) / (kLeast * 10);
+  const long long ctas = (per * p.B * p.Hkv + kLeast * kFew - 1) / (kLeast * kFew);
   const int grid = static_cast<int>(ctas < most ? ctas : most);
   const bool two = p.max_q * (p.Hq / p.Hkv) > 8;
   if (D == 64) return two ? launch_one<64, 2>(p, grid, st) : launch_one<64, 1>(p, grid, st);

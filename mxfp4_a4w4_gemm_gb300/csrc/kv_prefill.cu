@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
   KvShare share;
   KvStart start;
   auto steps_of = [&](int b) -> uint32_t { return Blocks(p, b, tq).total() * p.Hkv; };
-  if (!kv_locate<Cf::THREADS, 1>(p.B, steps_of, kLeastSteps, reinterpret_cast<uint32_t*>(smem + Cf::OFF_Q), share, start))
+  if (!kv_locate<Cf::THREADS, 1>(p.B, steps_of, kLeastSteps, 1, reinterpret_cast<uint32_t*>(smem + Cf::OFF_Q), share, start))
     return;
   const uint32_t cta = blockIdx.x;
   if (warp == 0) {

@@ -50,6 +50,7 @@ struct KvShare {
   uint32_t total;           // steps of the line
   uint32_t workers;
   uint32_t each, more;
+  uint32_t per;             // workers of a CTA
   __device__ __forceinline__ uint32_t first(uint32_t v) const { return v * each + min(v, more); }
   // the worker that holds step f
   __device__ __forceinline__ uint32_t holder(uint32_t f) const {
@@ -65,12 +66,12 @@ struct KvStart {
 
 // Block-wide: cuts the line (`steps(b)` steps for the units of request b; fewer
 // than 2^31 in all) for at most gridDim.x * PER workers of at least `least`
-// steps; warp w < PER learns the start of worker blockIdx.x * PER + w, if there
-// is one.  Every thread calls it; scratch: THREADS + 32 words of shared memory.
+// steps, at least `few` of them to a CTA; warp w learns the start of worker
+// blockIdx.x * per + w, if there is one.  Every thread calls it; scratch: THREADS + 32 words of shared memory.
 // Returns false if the CTA has nothing to do.
 template <int THREADS, int PER, typename Steps>
-__device__ __forceinline__ bool kv_locate(int B, Steps steps, uint32_t least, uint32_t* scratch, KvShare& share,
-                                          KvStart& start) {
+__device__ __forceinline__ bool kv_locate(int B, Steps steps, uint32_t least, uint32_t few, uint32_t* scratch,
+                                          KvShare& share, KvStart& start) {
   constexpr int W = THREADS / 32;
   static_assert(W <= 32 && PER <= W, "a search per warp");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -94,11 +95,12 @@ __device__ __forceinline__ bool kv_locate(int B, Steps steps, uint32_t least, ui
   }
   share.total = __shfl_sync(0xFFFFFFFFu, wsum, W - 1);
   share.workers = min(static_cast<uint32_t>(gridDim.x) * PER, (share.total + least - 1) / least);
-  const uint32_t v0 = blockIdx.x * PER;
+  share.per = max(few, (share.workers + gridDim.x - 1) / gridDim.x);
+  const uint32_t v0 = blockIdx.x * share.per;
   if (v0 >= share.workers) return false;
   share.each = share.total / share.workers;
   share.more = share.total - share.each * share.workers;
-  if (warp >= PER || v0 + warp >= share.workers) return true;
+  if (warp >= share.per || v0 + warp >= share.workers) return true;
   const uint32_t f = share.first(v0 + warp);
   // the warp's run of requests, then the thread's, that holds step f
   const int wi = __popc(__ballot_sync(0xFFFFFFFFu, lane < W && wsum <= f));
