@@ -8,7 +8,8 @@ namespace {
 // The decode kernel holds up to 16 query rows per key/value head; from there on
 // the tcgen05 kernel, whose 256-row units decode a key once for all their rows,
 // takes over.
-bool few_rows(int max_q, int group) { return max_q <= 16 / group; }
+constexpr int kFewRows = 48;
+bool few_rows(int max_q, int group) { return max_q <= kFewRows / group; }
 
 }  // namespace
 

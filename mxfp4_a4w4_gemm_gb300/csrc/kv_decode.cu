@@ -1,6 +1,6 @@
 // kv_decode.cu -- attention over the paged MXFP4 cache for few query rows per
-// key/value head (single tokens, short drafts): R = new tokens x (Hq / Hkv)
-// <= 16 rows.
+// key/value head (single tokens, short drafts): R = new tokens x (Hq / Hkv) rows,
+// 8 or 16 at a time.
 //
 //   O[r, :] = sum_k 2^(x_rk - m_r) v_k / sum_k 2^(x_rk - m_r),
 //   x_rk = log2(e) sm_scale q_r . k_k
@@ -57,7 +57,7 @@ constexpr float kNoMax = -3.0e38f;            // running maximum before the firs
 template <int D, int NT>
 struct DecCfg {
   using Ch = KvChunk<D>;
-  static constexpr int WARPS = NT == 1 ? 16 : 8;
+  static constexpr int WARPS = NT == 1 ? 16 : NT == 2 && D == 64 ? 12 : 8;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int ROWS = 8 * NT;
   static constexpr int J = D / 32, I = D / 16;
@@ -71,7 +71,7 @@ struct DecCfg {
   static constexpr int OFF_ML = OFF_O + WARPS * ROWS * PITCH * 4;   // maxima and sums: [tail or head][warp][row]
   static constexpr int OFF_BAR = OFF_ML + 2 * WARPS * ROWS * 8;
   static constexpr int OFF_OPEN = OFF_BAR + WARPS * STAGES * 8;
-  static constexpr int OFF_MISC = OFF_OPEN + (WARPS + 1) * 20;
+  static constexpr int OFF_MISC = OFF_OPEN + (WARPS + 1) * 24;
   static constexpr int SMEM = OFF_MISC + 16;
   static constexpr int OFF_SCAN = OFF_O;                         // the cut's scratch, before there are parts
   static constexpr int PART = ROWS * (D + 2);                    // floats of a stored part: O, then m and l
@@ -171,30 +171,32 @@ __device__ __forceinline__ void load_runs(const uint8_t* codes, int lane, uint32
 
 // A unit of which a part waits in this CTA's shared memory.
 struct Open {
-  int row0, h, rows;          // first row of the request, head, rows to join; rows == 0: none
+  int row0, h, r0, rows;      // first row of the request, head, first row of the block, rows to join; rows == 0: none
   uint32_t v0, v1;            // the workers that hold its first and its last step
 };
 
 // A walk along the worker's run: one piece (a run of one unit's steps) at a time.
 struct Walk {
-  int b, h, t, n;             // request, head, first step of the piece, steps of the unit
-  int len, rows, all, row0;
+  int b, h, k, t, n;          // request, head, block of rows, first step of the piece, steps of the unit
+  int len, rows, all, row0;   // rows: the request's, all its heads'
   int left;                   // steps of the run from this piece on
-  __device__ __forceinline__ void load(const KvAttentionArgs& p) {
+  __device__ __forceinline__ void load(const KvAttentionArgs& p, int G) {
     const KvRequest r = kv_request(p, b);
-    len = r.len; rows = r.rows; all = r.all; row0 = r.row0;
+    len = r.len; rows = r.rows * G; all = r.all; row0 = r.row0;
     n = rows > 0 ? max(1, (len + kStep - 1) / kStep) : 0;
   }
   __device__ __forceinline__ int steps() const { return min(left, n - t); }
   // the token where the piece ends
   __device__ __forceinline__ int end() const { return min(len, (t + steps()) * kStep); }
-  __device__ __forceinline__ void next(const KvAttentionArgs& p) {
+  template <int ROWS>
+  __device__ __forceinline__ void next(const KvAttentionArgs& p, int G) {
     left -= steps();
     t = 0;
-    if (left > 0 && ++h == p.Hkv) {
-      h = 0;
-      do { ++b; load(p); } while (n == 0);     // a run ends in a request that has steps
-    }
+    if (left <= 0 || ++k * ROWS < rows) return;
+    k = 0;
+    if (++h < p.Hkv) return;
+    h = 0;
+    do { ++b; load(p, G); } while (n == 0);    // a run ends in a request that has steps
   }
 };
 
@@ -219,11 +221,12 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
   griddep_wait();
   griddep_launch_dependents();
 
+  const int G = p.Hq / p.Hkv;
   KvShare share;
   KvStart start;
   auto steps_of = [&](int b) -> uint32_t {
     const KvRequest r = kv_request(p, b);
-    return r.rows > 0 ? max(1, (r.len + kStep - 1) / kStep) * p.Hkv : 0;
+    return r.rows > 0 ? max(1, (r.len + kStep - 1) / kStep) * p.Hkv * ((r.rows * G + Cf::ROWS - 1) / Cf::ROWS) : 0;
   };
   if (!kv_locate<Cf::THREADS, W>(p.B, steps_of, kLeast, kFew, reinterpret_cast<uint32_t*>(smem + Cf::OFF_SCAN), share,
                                  start))
@@ -234,15 +237,16 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
   cw.left = 0;
   if (warp < per && me < share.workers) {
     cw.b = start.b;
-    cw.load(p);
-    cw.h = start.rest / cw.n;
-    cw.t = start.rest - cw.h * cw.n;
+    cw.load(p, G);
+    const int blocks = (cw.rows + Cf::ROWS - 1) / Cf::ROWS, unit = start.rest / cw.n;
+    cw.h = unit / blocks;
+    cw.k = unit - cw.h * blocks;
+    cw.t = start.rest - unit * cw.n;
     cw.left = share.first(me + 1) - share.first(me);
   }
 
   const int lg = 31 - __clz(p.page_size), chunks = p.page_size >> 4;     // page_size is a power of two
   const long long page_bytes = static_cast<long long>(p.Hkv) * chunks * Ch::kBytes;
-  const int G = p.Hq / p.Hkv;
   uint8_t* ring = smem + warp * S * Cf::STAGE;
   float* ks = reinterpret_cast<float*>(smem + Cf::OFF_KS + warp * Cf::KS);
   uint8_t* vs = smem + Cf::OFF_VS + warp * Cf::VS;
@@ -258,7 +262,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
   auto issue = [&]() {
     while (ptok >= pend) {
       if (pw.left <= 0) return;
-      pw.next(p);
+      pw.template next<Cf::ROWS>(p, G);
       ptok = 0;
       pend = pw.left > 0 ? pw.end() : 0;
       pi = 0;
@@ -291,14 +295,13 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
   // ---- queries: the lane's words of row nt * 8 + g, 8 dimensions per 32-block ----
   uint32_t qf[NT][J][4];
   auto load_queries = [&]() {
-    const int R = min(cw.rows * G, Cf::ROWS);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = nt * 8 + g, qi = p.row_of(r);
+      const int r = cw.k * Cf::ROWS + nt * 8 + g, qi = p.row_of(r);
       const uint16_t* src = p.q + (static_cast<long long>(cw.row0) + qi) * p.q_stride + (cw.h * G + r - qi * G) * D + 8 * t;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const uint4 x = r < R ? ld_global_nc_v4(src + 32 * j) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 x = r < cw.rows ? ld_global_nc_v4(src + 32 * j) : make_uint4(0u, 0u, 0u, 0u);
         qf[nt][j][0] = x.x; qf[nt][j][1] = x.y; qf[nt][j][2] = x.z; qf[nt][j][3] = x.w;
       }
     }
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
   bool ok = true, first_piece = true;
   while (cw.left > 0) {
     const int h = cw.h, len = cw.len;
-    const int R = min(cw.rows * G, Cf::ROWS);
+    const int r0 = cw.k * Cf::ROWS, R = min(cw.rows - r0, Cf::ROWS);
     if (!first_piece) load_queries();
     first_piece = false;
     float fcol[NT][2];                         // raw score -> log2 units, per column
@@ -458,7 +461,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             // keys that the column's row sees, from the step's first on
-            const int lim = all_seen + p.row_of(nt * 8 + 2 * t + (u & 1)) - tok0 - g - (u >> 1) * 8;
+            const int lim = all_seen + p.row_of(r0 + nt * 8 + 2 * t + (u & 1)) - tok0 - g - (u >> 1) * 8;
             if (0 >= lim) x[0][nt][u] = -INFINITY;
             if (16 >= lim) x[1][nt][u] = -INFINITY;
           }
@@ -634,7 +637,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
             *reinterpret_cast<float2*>(po + col * Cf::PITCH + 16 * i + 2 * g) =
                 make_float2(o[i][nt][u] * fa * fb, o[i][nt][u + 2] * fa * fb);
         } else if (col < R) {
-          const int qi = p.row_of(col), hq = h * G + col - qi * G;
+          const int qi = p.row_of(r0 + col), hq = h * G + r0 + col - qi * G;
           const long long row = static_cast<long long>(cw.row0) + qi;
           const float inv = s == 0.f ? 0.f : 1.f / s;
 #pragma unroll
@@ -649,9 +652,9 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
     // the first warp if that lies in an earlier CTA
     if (lane == 0 && ((back && !front) || (front && warp == 0))) {
       const uint32_t u0 = share.first(me + 1) - cw.left - cw.t;   // the unit's first step on the line
-      open[front ? 0 : warp + 1] = Open{cw.row0, h, R, share.holder(u0), share.holder(u0 + cw.n - 1)};
+      open[front ? 0 : warp + 1] = Open{cw.row0, h, r0, R, share.holder(u0), share.holder(u0 + cw.n - 1)};
     }
-    cw.next(p);
+    cw.template next<Cf::ROWS>(p, G);
   }
   __syncthreads();
 
@@ -704,7 +707,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
         }
       }
       if (whole) {
-        const int qi = p.row_of(r), hq = un.h * G + r - qi * G;
+        const int qi = p.row_of(un.r0 + r), hq = un.h * G + un.r0 + r - qi * G;
         const long long row = static_cast<long long>(un.row0) + qi;
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
         uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (row * p.Hq + hq) * D + lane * (D / 32));
@@ -768,8 +771,8 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
         __syncwarp();
         for (int k = lane; k < np; k += 32) stats[r * kMaxParts + k].x *= inv;
         if (lane == 0 && p.lse != nullptr) {
-          const int qi = p.row_of(r);
-          p.lse[(static_cast<long long>(un.row0) + qi) * p.Hq + un.h * G + r - qi * G] =
+          const int qi = p.row_of(un.r0 + r);
+          p.lse[(static_cast<long long>(un.row0) + qi) * p.Hq + un.h * G + un.r0 + r - qi * G] =
               ll == 0.f ? -INFINITY : fmaf(mm, 0.6931471805599453f, logf(ll));
         }
       }
@@ -789,7 +792,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
             y.x = fmaf(v[k].x, a, y.x); y.y = fmaf(v[k].y, a, y.y); y.z = fmaf(v[k].z, a, y.z); y.w = fmaf(v[k].w, a, y.w);
           }
         }
-        const int qi = p.row_of(r), hq = un.h * G + r - qi * G;
+        const int qi = p.row_of(un.r0 + r), hq = un.h * G + un.r0 + r - qi * G;
         const long long row = static_cast<long long>(un.row0) + qi;
         *reinterpret_cast<uint2*>(p.out + (row * p.Hq + hq) * D + d) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
       }
@@ -823,12 +826,13 @@ int launch_one(const KvAttentionArgs& p, int grid, cudaStream_t st) {
 }  // namespace
 
 int launch_kv_decode(const KvAttentionArgs& p, int D, cudaStream_t st, int sms) {
+  const int rows = p.max_q * (p.Hq / p.Hkv);
   // as many CTAs as there can be work for, one per SM at most
   const long long per = (static_cast<long long>(p.max_pages) * p.page_size + kStep - 1) / kStep;
   const int most = sms < kMaxParts ? sms : kMaxParts;
-  const long long ctas = (per * p.B * p.Hkv + kLeast * kFew - 1) / (kLeast * kFew);
+  const long long ctas = (per * p.B * p.Hkv * ((rows + 15) / 16) + kLeast * kFew - 1) / (kLeast * kFew);
   const int grid = static_cast<int>(ctas < most ? ctas : most);
-  const bool two = p.max_q * (p.Hq / p.Hkv) > 8;
+  const bool two = rows > 8;
   if (D == 64) return two ? launch_one<64, 2>(p, grid, st) : launch_one<64, 1>(p, grid, st);
   return two ? launch_one<128, 2>(p, grid, st) : launch_one<128, 1>(p, grid, st);
 }

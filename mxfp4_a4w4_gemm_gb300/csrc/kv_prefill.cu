@@ -224,18 +224,19 @@ __device__ __forceinline__ uint4 mul_bf16x8(uint4 o, uint32_t f) {
 // 2^k as a float, k in [-126, 127]
 __device__ __forceinline__ float pow2i(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
 
-// sum over k = 0 .. n - 1 of floor((a k + b) / m); n, a, b >= 0, m > 0
-__device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
-  long long s = 0;
+// sum over k = 0 .. n - 1 of floor((a k + b) / m) modulo 2^32; a n + b < 2^32, m > 0
+__device__ __forceinline__ uint32_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+  uint32_t s = 0;
   while (n > 0) {
-    s += n * (n - 1) / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const long long y = a * n + b;
+    const uint32_t qa = a / m, qb = b / m;
+    s += (n & 1 ? (n - 1) / 2 * n : n / 2 * (n - 1)) * qa + n * qb;
+    a -= qa * m;
+    b -= qb * m;
+    const uint32_t y = a * n + b;
     if (y < m) break;
     n = y / m;
-    b = y % m;
-    const long long x = m;
+    b = y - n * m;
+    const uint32_t x = m;
     m = a;
     a = x;
   }
@@ -262,7 +263,7 @@ struct Blocks {
     const int base = len - all;
     // the first blocks may see nothing: one empty step each
     const int none = base < 0 ? min(k, -base / tq) : 0;
-    return static_cast<uint32_t>(none + floor_sum(k - none, kKeys, tq, static_cast<long long>(base) + (none + 1ll) * tq + kKeys - 1));
+    return none + floor_sum(k - none, kKeys, tq, static_cast<uint32_t>(base + (none + 1) * tq + kKeys - 1));
   }
   __device__ __forceinline__ uint32_t total() const { return n > 0 ? before(n - 1) + steps(n - 1) : 0u; }
 };
