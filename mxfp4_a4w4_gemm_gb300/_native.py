@@ -101,27 +101,30 @@ def lib():
 
 
 def _ptr(x):
-    if x is None or isinstance(x, int):
-        return x
-    if hasattr(x, "data_ptr"):
-        if not x.is_contiguous():
-            raise ValueError("tensor arguments must be contiguous")
-        return x.data_ptr()
-    raise TypeError(f"expected a tensor, an int pointer or None, got {type(x)}")
+    try:                                     # a tensor; the usual case comes first, these calls are short
+        if x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        if x is None or isinstance(x, int):
+            return x
+        raise TypeError(f"expected a tensor, an int pointer or None, got {type(x)}") from None
+    raise ValueError("tensor arguments must be contiguous")
 
 
 def _rows_ptr(x, stride):
     """Rows of [heads, D] values, `stride` elements apart: only the rows themselves must be contiguous."""
-    if hasattr(x, "data_ptr"):
-        if x.dim() != 3 or x.numel() == 0:
-            ok = x.numel() == 0
-        else:
-            (T, H, D), (st, sh, sd) = x.shape, x.stride()
-            ok = (D == 1 or sd == 1) and (H == 1 or sh == D) and (T == 1 or st == stride)
-        if not ok:
-            raise ValueError("rows must be a [T, heads, D] tensor with contiguous [heads, D] and the given row stride")
+    try:
+        if x.is_contiguous() and (x.numel() == 0 or x.size(0) == 1 or x.stride(0) == stride):
+            return x.data_ptr()
+        T, H, D = x.shape
+        st, sh, sd = x.stride()
+    except AttributeError:
+        return _ptr(x)
+    except ValueError:
+        raise ValueError("rows must be a [T, heads, D] tensor") from None
+    if (D == 1 or sd == 1) and (H == 1 or sh == D) and (T == 1 or st == stride):
         return x.data_ptr()
-    return _ptr(x)
+    raise ValueError("rows must be a [T, heads, D] tensor with contiguous [heads, D] and the given row stride")
 
 
 _current_stream = None
