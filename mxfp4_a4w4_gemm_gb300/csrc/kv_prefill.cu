@@ -60,8 +60,8 @@ struct PreCfg {
   static constexpr int OFF_V = OFF_K + 2 * TILE;
   static constexpr int OFF_RAW = OFF_V + 2 * TILE;
   static constexpr int OFF_BAR = OFF_RAW + 2 * RAW;
-  // raw full, empty x 2; K full, empty x 2; V full, empty x 2; Q full, S full, P full, O full per tile; drain
-  static constexpr int NBAR = 12 + 8 + 1;
+  // raw full, empty x 2; K full, empty x 2; V full, empty x 2; Q full, S full, P half, P full, O full per tile; drain
+  static constexpr int NBAR = 12 + 10 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 56;
   static constexpr int SCOL = 0, OCOL = 256;                     // TMEM columns: S of the tiles, then O
@@ -184,6 +184,11 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -309,7 +314,8 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
   auto s_full = [&](int w) { return bar0 + 8u * (14 + w); };
   auto p_full = [&](int w) { return bar0 + 8u * (16 + w); };
   auto o_full = [&](int w) { return bar0 + 8u * (18 + w); };
-  const uint32_t drain = bar0 + 8u * 20;
+  auto p_half = [&](int w) { return bar0 + 8u * (20 + w); };
+  const uint32_t drain = bar0 + 8u * 22;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cf::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cf::OFF_MISC + 8);
   volatile int* never = abort_flag + 1;
@@ -327,6 +333,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
       mbar_init(v_empty(s), 1);
       mbar_init(q_full(s), 4);
       mbar_init(s_full(s), 1);
+      mbar_init(p_half(s), 4);
       mbar_init(p_full(s), 4);
       mbar_init(o_full(s), 1);
     }
@@ -465,10 +472,10 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
           float top[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            top[c] = __uint_as_float(x[c]);
+            top[c] = max3(__uint_as_float(x[c]), __uint_as_float(x[c + 4]), __uint_as_float(x[c + 8]));
 #pragma unroll
-            for (int u = c + 4; u < 128; u += 8)
-              top[c] = fmaxf(top[c], u + 4 < 128 ? fmaxf(__uint_as_float(x[u]), __uint_as_float(x[u + 4])) : __uint_as_float(x[u]));
+            for (int u = c + 12; u < 124; u += 8) top[c] = max3(top[c], __uint_as_float(x[u]), __uint_as_float(x[u + 4]));
+            top[c] = fmaxf(top[c], __uint_as_float(x[c + 124]));
           }
           const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f;
           // the maximum follows once it is 2^8 ahead
@@ -507,6 +514,12 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
               y[u] = pack_bf16(e0, e1);
             }
             tmem_st8(s_col + 8 * c, y);
+            if (c == 3) {                                         // the products of the first 64 keys may start
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(p_half(tile));
+            }
           }
           sum0 = add_f32x2(sum0, sum1);
           l += __uint_as_float(static_cast<uint32_t>(sum0)) + __uint_as_float(static_cast<uint32_t>(sum0 >> 32));
@@ -771,13 +784,14 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
       }
       __syncwarp();
     };
-    auto outputs = [&](int tile, int s, bool first, bool last_step, bool last_tile) {
+    // the products with keys 64 part .. + 63 of the step
+    auto outputs = [&](int tile, int s, int part, bool first, bool last_step, bool last_tile) {
       const uint32_t v_lo = static_cast<uint32_t>(vd) + s * (Cf::TILE >> 4), v_hi = static_cast<uint32_t>(vd >> 32);
       const uint32_t d = tm + Cf::OCOL + tile * D, a = tm + Cf::SCOL + tile * 128;
       if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(d, a + 8 * kk, v_lo + (kk * 2048 >> 4), v_hi, id_o, kk == 0 && first ? 0u : 1u);
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ts(d, a + 32 * part + 8 * kk, v_lo + ((4 * part + kk) * 2048 >> 4), v_hi, id_o, kk == 0 && first ? 0u : 1u);
         if (last_step) mma_commit(o_full(tile));
         if (last_tile) mma_commit(v_empty(s));
       }
@@ -791,11 +805,14 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
         const uint32_t ph = it >> 1 & 1, php = (it - 1) >> 1 & 1;
         for (int tile = 0; tile < tiles; ++tile) {
           if (i > 0) {
+            if (tile == 0 && !sure(v_full(sp), php)) break;
+            if (!sure(p_half(tile), p_phase >> tile & 1)) break;
+            tc_fence_after();
+            outputs(tile, sp, 0, i == 1, false, false);
             if (!sure(p_full(tile), p_phase >> tile & 1)) break;
             p_phase ^= 1u << tile;
-            if (tile == 0 && !sure(v_full(sp), php)) break;
             tc_fence_after();
-            outputs(tile, sp, i == 1, i == n, tile == tiles - 1);
+            outputs(tile, sp, 1, false, i == n, tile == tiles - 1);
           }
           if (i < n) {
             if (i == 0) {
