@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
     for (int tok0 = cw.t * kStep; tok0 < end; tok0 += kStep) {
       const int slot = waited % S;
       if (ok) {
-        ok = mbar_wait(full(slot), (waited / S) & 1u, abort_flag, p.wait_ns, p.status);
+        ok = kv_wait(full(slot), (waited / S) & 1u, abort_flag, p.wait_ns, p.status);
         ok = __all_sync(0xFFFFFFFFu, ok);
       }
       if (!ok) continue;
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
     float2* ml = reinterpret_cast<float2*>(smem + Cf::OFF_ML) + ((back ? 0 : W) + warp) * Cf::ROWS;
     if (!ok) {                                                   // copies may still arrive in the ring
       const unsigned long long drain_ns = p.wait_ns > 100000000ull ? p.wait_ns : 100000000ull;
-      for (; waited < issued; ++waited) mbar_wait(full(waited % S), (waited / S) & 1u, never, drain_ns, p.status);
+      for (; waited < issued; ++waited) kv_wait(full(waited % S), (waited / S) & 1u, never, drain_ns, p.status);
       __syncwarp();
     }
 #pragma unroll

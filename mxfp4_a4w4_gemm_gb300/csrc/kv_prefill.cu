@@ -18,7 +18,10 @@
 // * Values become BF16, since P wants its exponents: E2M1 magnitude bits placed in
 //   a BF16 read as the value times 2^-126, and one or two exact multiplies by
 //   powers of two apply the scale.
-// So the only roundings are P's to BF16 and the fp32 sums.
+// So the only roundings are P's to BF16 and the fp32 sums.  Where the block table
+// holds few keys (kRestKeys), some of them may carry a row and their roundings do
+// not average out, and products do not make the time: there (REST) P has a second
+// BF16 term, what the rounding left, and its products are added.
 // The running maximum follows with slack: O is rescaled only when a row's maximum
 // has grown by more than 2^8, P staying below 2^8 meanwhile.
 //
@@ -41,6 +44,7 @@ constexpr int kKeys = 128;                    // keys of a step
 constexpr int kRows = 256;                    // rows of a unit
 constexpr int kLeastSteps = 2;                // steps of a worker, at least
 constexpr int kMaxCtas = 512;
+constexpr int kRestKeys = 512;                // keys of a table up to which P has two terms
 constexpr float kNoMax = -3.0e38f;            // running maximum before the first key
 
 template <int D>
@@ -295,7 +299,7 @@ struct PreWalk {
   __device__ __forceinline__ int rows(int G) const { return min(q.tq, q.rows - k * q.tq) * G; }
 };
 
-template <int D>
+template <int D, bool REST>
 __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(const KvAttentionArgs p) {
   using Cf = PreCfg<D>;
   using Ch = KvChunk<D>;
@@ -503,7 +507,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
           uint64_t sum0 = 0, sum1 = 0;                            // two pairs of partial sums
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            uint32_t y[8];
+            uint32_t y[8], rest[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
               const uint64_t z = fma_f32x2(pair_f32(x[16 * c + 2 * u], x[16 * c + 2 * u + 1]), f2, off2);
@@ -512,8 +516,10 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
               const uint64_t e = pair_f32(__float_as_uint(e0), __float_as_uint(e1));
               if (u & 1) sum1 = add_f32x2(sum1, e); else sum0 = add_f32x2(sum0, e);
               y[u] = pack_bf16(e0, e1);
+              if constexpr (REST) rest[u] = pack_bf16(e0 - __uint_as_float(y[u] << 16), e1 - __uint_as_float(y[u] & 0xFFFF0000u));
             }
             tmem_st8(s_col + 8 * c, y);
+            if constexpr (REST) tmem_st8(s_col + 64 + 8 * c, rest);
             if (c == 3) {                                         // the products of the first 64 keys may start
               tmem_wait_st();
               tc_fence_before();
@@ -792,6 +798,11 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           mma_ts(d, a + 32 * part + 8 * kk, v_lo + ((4 * part + kk) * 2048 >> 4), v_hi, id_o, kk == 0 && first ? 0u : 1u);
+        if constexpr (REST) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ts(d, a + 64 + 32 * part + 8 * kk, v_lo + ((4 * part + kk) * 2048 >> 4), v_hi, id_o, 1u);
+        }
         if (last_step) mma_commit(o_full(tile));
         if (last_tile) mma_commit(v_empty(s));
       }
@@ -886,16 +897,16 @@ size_t kv_prefill_ws_bytes(int D, int sms) {
 
 namespace {
 
-template <int D>
+template <int D, bool REST>
 int launch_one(const KvAttentionArgs& p, int grid, cudaStream_t st) {
   using Cf = PreCfg<D>;
   static std::atomic<unsigned long long> attr_done{0};
   const int rc = ensure_func_attrs(attr_done, [] {
-    return cudaFuncSetAttribute(a4w4_kv_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM) ==
+    return cudaFuncSetAttribute(a4w4_kv_prefill_kernel<D, REST>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM) ==
            cudaSuccess;
   });
   if (rc != 0) return rc;
-  return launch_pdl_smem(a4w4_kv_prefill_kernel<D>, grid, Cf::THREADS, Cf::SMEM, st, p);
+  return launch_pdl_smem(a4w4_kv_prefill_kernel<D, REST>, grid, Cf::THREADS, Cf::SMEM, st, p);
 }
 
 }  // namespace
@@ -907,7 +918,9 @@ int launch_kv_prefill(const KvAttentionArgs& p, int D, cudaStream_t st, int sms)
                       ((static_cast<double>(p.max_pages) * p.page_size + kKeys - 1) / kKeys + 1);
   if (most > 2147483647.0) return -1;
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-  return D == 64 ? launch_one<64>(p, grid, st) : launch_one<128>(p, grid, st);
+  const bool rest = p.max_pages <= kRestKeys / p.page_size;
+  if (D == 64) return rest ? launch_one<64, true>(p, grid, st) : launch_one<64, false>(p, grid, st);
+  return rest ? launch_one<128, true>(p, grid, st) : launch_one<128, false>(p, grid, st);
 }
 
 }  // namespace a4w4

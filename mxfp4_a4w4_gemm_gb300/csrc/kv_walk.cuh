@@ -21,6 +21,32 @@ namespace a4w4 {
 // counter back to zero.
 constexpr int kTickets = 4096;
 
+// mbar_wait for limits of any size: try_wait may suspend the thread for longer than
+// these kernels' waits take, so below 100 us the barrier is only tested.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool kv_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns,
+                                        unsigned int* status) {
+  if (mbar_test(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+    if (limit_ns >= 100000ull ? mbar_try_wait(bar, parity) : mbar_test(bar, parity)) return true;
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > limit_ns) {
+      *abort = 1;
+      atomicOr(status, kStatusTimeout);
+      return false;
+    }
+  }
+}
+
 // Lengths of request b as the kernels use them: clamped, so that nothing in the
 // arrays can lead outside the buffers.
 struct KvRequest {

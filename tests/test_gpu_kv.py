@@ -312,6 +312,32 @@ def test_prompt_chunks(q_lens, kv_lens, Hq, Hkv, D, page):
     check_attention(*problem(q_lens, kv_lens, Hq, Hkv, D, page, 15))
 
 
+@pytest.mark.parametrize("q_len,Hq,Hkv,D", [(1, 48, 1, 128), (6, 8, 1, 64), (7, 7, 1, 128), (1, 49, 1, 64), (2, 64, 2, 128), (1, 100, 1, 128),
+                                            (3, 100, 1, 64), (1, 256, 1, 64), (2, 255, 1, 128), (17, 3, 1, 128), (16, 3, 1, 64)])
+def test_row_counts_around_the_kernels_limits(q_len, Hq, Hkv, D):
+    check_attention(*problem([q_len, q_len], [333, q_len - 1], Hq, Hkv, D, 32, 24))
+
+
+def test_many_short_requests():
+    # more requests than a CTA has threads: several to a thread, in both kernels
+    rng = np.random.default_rng(25)
+    kv_lens = rng.integers(0, 40, 1500).tolist()
+    check_attention(*problem([int(n > 0 or b % 3) for b, n in enumerate(kv_lens)], kv_lens, 2, 1, 64, 16, 26))
+    kv_lens = rng.integers(0, 20, 700).tolist()
+    check_attention(*problem(rng.integers(0, 4, 700).tolist(), kv_lens, 30, 1, 64, 16, 27))
+
+
+def test_cut_units_of_long_chunks():
+    check_attention(*problem([300], [5000], 4, 2, 128, 64, 28))
+    check_attention(*problem([64, 1, 20], [3000, 4000, 30], 16, 2, 64, 16, 29))
+
+
+def test_a_larger_bound_on_new_tokens_changes_the_kernel_only():
+    prob = problem([1, 2, 0, 1], [500, 40, 9, 1200], 8, 2, 128, 32, 30)
+    for max_q in (2, 12, 13, 300):
+        check_attention(*prob, max_q=max_q)
+
+
 def spread_gain(lo, hi):
     return lambda rng, shape: 2.0 ** rng.uniform(lo, hi, shape[:2] + (1,))
 
