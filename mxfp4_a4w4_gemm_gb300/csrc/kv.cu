@@ -227,17 +227,20 @@ __device__ __forceinline__ uint4 e2m1x8_to_bf16x8(uint32_t w, uint32_t e) {
                     __byte_perm(o[2], o[3], 0x7632));
 }
 
-// The inverse: 34 bytes read, 128 written.  HBM-bound.
+// The inverse: 34 bytes read, 128 written.  HBM-bound.  A thread's 64 bytes of a row
+// go out by way of shared memory, so that a warp's stores write whole rows (16-byte
+// stores 64 bytes apart touch every 32-byte sector twice).
 template <int D>
 __global__ void __launch_bounds__(256) kv_read_kernel(const uint8_t* __restrict__ cache, int slots, int page_lg,
                                                       const int32_t* __restrict__ slot_map, int T, int Hkv,
                                                       uint16_t* __restrict__ k, uint16_t* __restrict__ v) {
   using Ch = KvChunk<D>;
+  __shared__ uint4 s_row[8][2][128];
   griddep_wait();
   griddep_launch_dependents();
   const RowItem<D> it(Hkv);
-  if (it.t >= T) return;
-  const int slot = slot_map[it.t], j = it.j;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = it.j;
+  const int slot = it.t < T ? slot_map[it.t] : -1;
   uint32_t wk[4] = {0u, 0u, 0u, 0u}, wv[4] = {0u, 0u, 0u, 0u}, ek = 0u, ev = 0u;
   if (static_cast<unsigned>(slot) < static_cast<unsigned>(slots)) {
     const int r = slot & 15, chunks = 1 << (page_lg - 4);
@@ -257,11 +260,23 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const uint8_t* __restrict_
       wv[2 + q] = __byte_perm(p01, p23, 0x7632);
     }
   }
-  const long long at = (static_cast<long long>(it.t) * Hkv + it.h) * D + 32 * j;
+  // piece u of lane l at 4 l + (u ^ l / 2 % 4): both ways without bank conflicts
+  const int turn = lane >> 1 & 3;
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    *reinterpret_cast<uint4*>(k + at + 8 * u) = e2m1x8_to_bf16x8(wk[u], ek);
-    *reinterpret_cast<uint4*>(v + at + 8 * u) = e2m1x8_to_bf16x8(wv[u], ev);
+    s_row[warp][0][4 * lane + (u ^ turn)] = e2m1x8_to_bf16x8(wk[u], ek);
+    s_row[warp][1][4 * lane + (u ^ turn)] = e2m1x8_to_bf16x8(wv[u], ev);
+  }
+  __syncwarp();
+  const int t0 = it.t - lane / RowItem<D>::J;                 // the warp's first token
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int o = s * 32 + lane, l = o >> 2, t = t0 + l / RowItem<D>::J;
+    if (t >= T) break;
+    const long long at = (static_cast<long long>(t) * Hkv + it.h) * D + 32 * (l % RowItem<D>::J) + 8 * (o & 3);
+    const int from = 4 * l + ((o & 3) ^ (l >> 1 & 3));
+    *reinterpret_cast<uint4*>(k + at) = s_row[warp][0][from];
+    *reinterpret_cast<uint4*>(v + at) = s_row[warp][1][from];
   }
 }
 
