@@ -167,6 +167,11 @@ struct RowItem {
   }
 };
 
+// A warp's rows as 128 pieces of 16 bytes: piece o belongs to lane o / 4's
+// 32-block and lies at 4 l + (o ^ l / 2) % 4, without bank conflicts whether lanes
+// take pieces in order (whole rows, as global memory wants them) or four of their own.
+__device__ __forceinline__ int row_piece(int l, int u) { return 4 * l + (u ^ (l >> 1 & 3)); }
+
 // Quantises one 32-block of a token's keys and the same one of its values: 128
 // bytes read, 34 written.  HBM-bound.
 template <int D>
@@ -175,27 +180,41 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const uint16_t* __restri
                                                         const int32_t* __restrict__ slot_map, int T, int Hkv,
                                                         uint8_t* __restrict__ cache, int slots, int page_lg) {
   using Ch = KvChunk<D>;
+  __shared__ uint4 s_row[8][2][128];
   griddep_wait();
   griddep_launch_dependents();
   const RowItem<D> it(Hkv);
-  if (it.t >= T) return;
-  const int slot = slot_map[it.t];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = it.j;
+  const int slot = it.t < T ? slot_map[it.t] : -1;
+  const int t0 = it.t - lane / RowItem<D>::J;                 // the warp's first token
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int o = s * 32 + lane, l = o >> 2, t = t0 + l / RowItem<D>::J;
+    if (t >= T) break;
+    const int at = it.h * D + 32 * (l % RowItem<D>::J) + 8 * (o & 3);
+    s_row[warp][0][row_piece(l, o & 3)] = ld_global_nc_v4(k + t * k_stride + at);
+    s_row[warp][1][row_piece(l, o & 3)] = ld_global_nc_v4(v + t * v_stride + at);
+  }
+  __syncwarp();
   if (static_cast<unsigned>(slot) >= static_cast<unsigned>(slots)) return;
-  const int j = it.j, at = it.h * D + 32 * j;
-  uint32_t wk[16], wv[16], c[4];
+  uint32_t w[16], c[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const uint4 x = ld_global_nc_v4(k + it.t * k_stride + at + 8 * u), y = ld_global_nc_v4(v + it.t * v_stride + at + 8 * u);
-    wk[4 * u] = x.x; wk[4 * u + 1] = x.y; wk[4 * u + 2] = x.z; wk[4 * u + 3] = x.w;
-    wv[4 * u] = y.x; wv[4 * u + 1] = y.y; wv[4 * u + 2] = y.z; wv[4 * u + 3] = y.w;
+    const uint4 x = s_row[warp][0][row_piece(lane, u)];
+    w[4 * u] = x.x; w[4 * u + 1] = x.y; w[4 * u + 2] = x.z; w[4 * u + 3] = x.w;
   }
   const int r = slot & 15, chunks = 1 << (page_lg - 4);
   uint8_t* chunk = cache + kv_chunk_offset<D>(slot >> page_lg, it.h, (slot >> 4) & (chunks - 1), Hkv, chunks);
-  const uint32_t ek = quant32_bf16(wk, c);
+  const uint32_t ek = quant32_bf16(w, c);
 #pragma unroll
   for (int u = 0; u < 4; ++u) *reinterpret_cast<uint32_t*>(chunk + Ch::key_word(r, j, u)) = c[u];
   chunk[Ch::kKeyScales + r * Ch::J + j] = static_cast<uint8_t>(ek);
-  const uint32_t ev = quant32_bf16(wv, c);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const uint4 x = s_row[warp][1][row_piece(lane, u)];
+    w[4 * u] = x.x; w[4 * u + 1] = x.y; w[4 * u + 2] = x.z; w[4 * u + 3] = x.w;
+  }
+  const uint32_t ev = quant32_bf16(w, c);
   // byte g of each half block 16 i belongs to run g, at i = 2 j, 2 j + 1
 #pragma unroll
   for (int g = 0; g < 8; ++g)
@@ -260,12 +279,10 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const uint8_t* __restrict_
       wv[2 + q] = __byte_perm(p01, p23, 0x7632);
     }
   }
-  // piece u of lane l at 4 l + (u ^ l / 2 % 4): both ways without bank conflicts
-  const int turn = lane >> 1 & 3;
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    s_row[warp][0][4 * lane + (u ^ turn)] = e2m1x8_to_bf16x8(wk[u], ek);
-    s_row[warp][1][4 * lane + (u ^ turn)] = e2m1x8_to_bf16x8(wv[u], ev);
+    s_row[warp][0][row_piece(lane, u)] = e2m1x8_to_bf16x8(wk[u], ek);
+    s_row[warp][1][row_piece(lane, u)] = e2m1x8_to_bf16x8(wv[u], ev);
   }
   __syncwarp();
   const int t0 = it.t - lane / RowItem<D>::J;                 // the warp's first token
@@ -274,9 +291,8 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const uint8_t* __restrict_
     const int o = s * 32 + lane, l = o >> 2, t = t0 + l / RowItem<D>::J;
     if (t >= T) break;
     const long long at = (static_cast<long long>(t) * Hkv + it.h) * D + 32 * (l % RowItem<D>::J) + 8 * (o & 3);
-    const int from = 4 * l + ((o & 3) ^ (l >> 1 & 3));
-    *reinterpret_cast<uint4*>(k + at) = s_row[warp][0][from];
-    *reinterpret_cast<uint4*>(v + at) = s_row[warp][1][from];
+    *reinterpret_cast<uint4*>(k + at) = s_row[warp][0][row_piece(l, o & 3)];
+    *reinterpret_cast<uint4*>(v + at) = s_row[warp][1][row_piece(l, o & 3)];
   }
 }
 
