@@ -727,15 +727,16 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
   if (!outside) return;
 
   // ---- units that reach into other CTAs: the last to arrive joins ----
-  __threadfence();
-  __syncthreads();
+  __syncthreads();                                               // gathers the stores behind the fence below
   if (warp == 0) {                                               // a lane per unit draws its ticket
     const bool mine = (outside >> lane & 1u) != 0;
     bool last = false;
     if (mine) {
+      __threadfence();
       const int c0 = open[lane].v0 / per, np = open[lane].v1 / per - c0 + 1;
       last = atomicAdd(static_cast<int*>(p.ws) + c0, 1) == np - 1;
     }
+    if (mine) __threadfence();
     const uint32_t lasts = __ballot_sync(0xFFFFFFFFu, last);
     if (lane == 0) *last_flag = static_cast<int>(lasts);
   }
@@ -744,7 +745,6 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
     const Open un = open[__ffs(left) - 1];
     const int c0 = un.v0 / per, np = un.v1 / per - c0 + 1, R = un.rows;
     {
-      __threadfence();
       auto part = [&](int k) { return parts + (2 * (c0 + k) + (k == 0 ? 1 : 0)) * Cf::PART; };
       // maxima and sums of the parts, all on their way at once; then a warp per row turns them into weights
       float2* stats = reinterpret_cast<float2*>(smem + Cf::OFF_O);       // [row][part], the parts here are spent

@@ -409,6 +409,45 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
     uint32_t it = 0;                           // steps so far
     float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + kTickets * 4);
     uint32_t s_phase = 0, o_phase = 0;
+    int q_pow = 0;                             // the power of two of this thread's row of Q
+    // ---- the warp's 32 rows of a unit's Q tile: C lanes to a row, 32 / C rows at a time; a piece ahead of the rest,
+    // while the last products run ----
+    auto stage_queries = [&](const PreWalk& u) {
+      const int R = u.rows(G), first_tok = u.k * tq;
+      if (tile * 128 >= R) return;
+      constexpr int C = D / 8, AT = 32 / C, BATCH = 8;
+      const int c = lane % C;
+#pragma unroll 1
+      for (int j0 = 0; j0 < 32 / AT; j0 += BATCH) {
+        uint4 v[BATCH];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+          const int rt = tile * 128 + quad * 32 + (j0 + j) * AT + lane / C, qj = p.row_of(rt);
+          v[j] = rt < R ? ld_global_nc_v4(p.q + (static_cast<long long>(u.q.row0) + first_tok + qj) * p.q_stride +
+                                          (u.h * G + rt - qj * G) * D + c * 8)
+                        : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+          uint32_t top = max_abs_bf16x2(max_abs_bf16x2(v[j].x, v[j].y), max_abs_bf16x2(v[j].z, v[j].w)) & 0x7FFF7FFFu;
+          uint32_t e = max(top & 0xFFFFu, top >> 16) >> 7;
+#pragma unroll
+          for (int s = C / 2; s > 0; s >>= 1) e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, s));
+          const int k = min(141 - static_cast<int>(e), 127);
+          const float fk = pow2i(k);
+          auto two = [&](uint32_t b) { return pack_f16(__uint_as_float(b << 16) * fk, __uint_as_float(b & 0xFFFF0000u) * fk); };
+          const int rr = quad * 32 + (j0 + j) * AT + lane / C;
+          *reinterpret_cast<uint4*>(smem + Cf::OFF_Q + tile * Cf::TILE + (c >> 3) * Cf::ATOM + rr * 128 +
+                                    (((c & 7) ^ (rr & 7)) << 4)) = make_uint4(two(v[j].x), two(v[j].y), two(v[j].z), two(v[j].w));
+          const int mine = __shfl_sync(0xFFFFFFFFu, k, (lane % AT) * C);
+          if (lane / AT == j0 + j) q_pow = mine;               // this thread's own row
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full(tile));
+    };
+    if (w.left > 0) stage_queries(w);
     bool ok = true;                            // a warp that gave up goes on through the joins, for their barriers
     for (; w.left > 0; w.next(p)) {
       const int R = w.rows(G);
@@ -416,41 +455,8 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
       const int first_tok = w.k * tq, qi = p.row_of(r), hq = w.h * G + r - qi * G;
       const long long row = static_cast<long long>(w.q.row0) + first_tok + qi;
       float m = kNoMax, off = 3.0e38f, l = 0.f;   // running maximum in log2 units, -m, sum
-      int q_pow = 0;                             // the row's power of two
+      const int row_pow = q_pow;
       if (active && ok) {
-        // ---- the warp's 32 rows of the Q tile: C lanes to a row, 32 / C rows at a time ----
-        constexpr int C = D / 8, AT = 32 / C, BATCH = 8;
-        const int c = lane % C;
-#pragma unroll 1
-        for (int j0 = 0; j0 < 32 / AT; j0 += BATCH) {
-          uint4 v[BATCH];
-#pragma unroll
-          for (int j = 0; j < BATCH; ++j) {
-            const int rt = tile * 128 + quad * 32 + (j0 + j) * AT + lane / C, qj = p.row_of(rt);
-            v[j] = rt < R ? ld_global_nc_v4(p.q + (static_cast<long long>(w.q.row0) + first_tok + qj) * p.q_stride +
-                                            (w.h * G + rt - qj * G) * D + c * 8)
-                          : make_uint4(0u, 0u, 0u, 0u);
-          }
-#pragma unroll
-          for (int j = 0; j < BATCH; ++j) {
-            uint32_t top = max_abs_bf16x2(max_abs_bf16x2(v[j].x, v[j].y), max_abs_bf16x2(v[j].z, v[j].w)) & 0x7FFF7FFFu;
-            uint32_t e = max(top & 0xFFFFu, top >> 16) >> 7;
-#pragma unroll
-            for (int s = C / 2; s > 0; s >>= 1) e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, s));
-            const int k = min(141 - static_cast<int>(e), 127);
-            const float fk = pow2i(k);
-            auto two = [&](uint32_t b) { return pack_f16(__uint_as_float(b << 16) * fk, __uint_as_float(b & 0xFFFF0000u) * fk); };
-            const int rr = quad * 32 + (j0 + j) * AT + lane / C;
-            *reinterpret_cast<uint4*>(smem + Cf::OFF_Q + tile * Cf::TILE + (c >> 3) * Cf::ATOM + rr * 128 +
-                                      (((c & 7) ^ (rr & 7)) << 4)) = make_uint4(two(v[j].x), two(v[j].y), two(v[j].z), two(v[j].w));
-            const int mine = __shfl_sync(0xFFFFFFFFu, k, (lane % AT) * C);
-            if (lane / AT == j0 + j) q_pow = mine;               // this thread's own row
-          }
-        }
-        fence_proxy_async_smem();
-        tc_fence_before();                     // the last unit's O has been read
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full(tile));
         const int seen = r < R ? w.q.len - w.q.all + first_tok + qi + 1 : 0;
         const int n = w.steps();
         for (int i = 0; i < n; ++i) {
@@ -461,7 +467,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
           const int k0 = (w.t + i) * kKeys;
           // score -> log2 units; positive, so that a masked score stays -infinity
           const int ref = *reinterpret_cast<volatile int*>(key_ref + ((it + i) & 3));
-          const float f = fmaxf(p.sm_scale * 1.4426950408889634f * pow2i(max(-126, min(127, ref - 140 - q_pow))), 1e-44f);
+          const float f = fmaxf(p.sm_scale * 1.4426950408889634f * pow2i(max(-126, min(127, ref - 140 - row_pow))), 1e-44f);
           const bool edge = __any_sync(0xFFFFFFFFu, k0 + kKeys > seen);
           uint32_t x[128];
 #pragma unroll
@@ -534,11 +540,17 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
           __syncwarp();
           if (lane == 0) mbar_arrive(p_full(tile));
         }
-        if (ok) {
-          ok = __all_sync(0xFFFFFFFFu, wait(o_full(tile), o_phase));
-          o_phase ^= 1;
-          tc_fence_after();
-        }
+      }
+      // the unit's scores are done, so Q's place is free for the next one's
+      {
+        PreWalk ahead = w;
+        ahead.next(p);
+        if (ok && ahead.left > 0) stage_queries(ahead);
+      }
+      if (active && ok) {
+        ok = __all_sync(0xFFFFFFFFu, wait(o_full(tile), o_phase));
+        o_phase ^= 1;
+        tc_fence_after();
       }
       it += w.steps();
       // ---- the unit's output, or the part of it ----
@@ -582,52 +594,56 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
       if (!whole) {
         // ---- the last part to arrive joins a cut unit (softmax warps only) ----
         const int c0 = share.holder(u0), np = share.holder(u0 + w.n - 1) - c0 + 1;
-        __threadfence();
         named_bar_sync(1, 256);
         int* ticket = static_cast<int*>(p.ws) + c0;
-        if (tid == 0) *last_flag = atomicAdd(ticket, 1) == np - 1;
+        if (tid == 0) {                        // the barrier has gathered the threads' stores behind this fence
+          __threadfence();
+          *last_flag = atomicAdd(ticket, 1) == np - 1;
+          __threadfence();
+        }
         named_bar_sync(1, 256);
         if (*last_flag) {
-          __threadfence();
           const size_t head = share.first(c0) < u0 ? Cf::PART : 0;
           auto part = [&](int k) { return parts + static_cast<size_t>(2 * (c0 + k)) * Cf::PART + (k == 0 ? head : 0); };
-          // a thread per row: maximum and sum over the parts; then all threads over the rows' pieces of 16 bytes,
-          // four at a time.  The rows' figures go where Q was: its products are done.
-          float2* rows = reinterpret_cast<float2*>(smem + Cf::OFF_Q);
+          // a thread per row turns the parts' maxima into weights, where they lie
           if (tid < R) {
             float mm = kNoMax, ll = 0.f;
+#pragma unroll 4
             for (int k = 0; k < np; ++k) mm = fmaxf(mm, __ldcg(part(k) + kRows * D + 2 * tid));
+#pragma unroll 4
             for (int k = 0; k < np; ++k) {
               const float2 q = __ldcg(reinterpret_cast<const float2*>(part(k) + kRows * D + 2 * tid));
               ll = fmaf(q.y, ex2(q.x - mm), ll);
             }
-            rows[tid] = make_float2(mm, ll == 0.f ? 0.f : 1.f / ll);
+            const float inv = ll == 0.f ? 0.f : 1.f / ll;
+#pragma unroll 4
+            for (int k = 0; k < np; ++k) {
+              float* at = part(k) + kRows * D + 2 * tid;
+              __stcg(at, ex2(__ldcg(at) - mm) * inv);
+            }
             if (p.lse != nullptr) p.lse[row * p.Hq + hq] = ll == 0.f ? -INFINITY : fmaf(mm, 0.6931471805599453f, logf(ll));
           }
           named_bar_sync(1, 256);
-          constexpr int Q4 = D / 4;                                        // 16-byte pieces of a row
-          for (int it0 = tid; it0 < R * Q4; it0 += 4 * 256) {
-            float4 y[4];
-            float2 st[4];
+          // then all threads over the rows' pieces of 16 bytes, eight at a time
+          constexpr int Q4 = D / 4, AT = 8;
+          for (int it0 = tid; it0 < R * Q4; it0 += AT * 256) {
+            float4 y[AT];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-              st[u] = rows[min((it0 + u * 256) / Q4, R - 1)];
-            }
-#pragma unroll 4
+            for (int u = 0; u < AT; ++u) y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
             for (int k = 0; k < np; ++k) {
               const float* src = part(k);
 #pragma unroll
-              for (int u = 0; u < 4; ++u) {
+              for (int u = 0; u < AT; ++u) {
                 const int it = min(it0 + u * 256, R * Q4 - 1);
                 const float4 v = __ldcg(reinterpret_cast<const float4*>(src) + it);
-                const float a = ex2(__ldcg(src + kRows * D + 2 * (it / Q4)) - st[u].x) * st[u].y;
+                const float a = __ldcg(src + kRows * D + 2 * (it / Q4));
                 y[u].x = fmaf(v.x, a, y[u].x); y[u].y = fmaf(v.y, a, y[u].y);
                 y[u].z = fmaf(v.z, a, y[u].z); y[u].w = fmaf(v.w, a, y[u].w);
               }
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < AT; ++u) {
               const int it = it0 + u * 256;
               if (it < R * Q4) {
                 const int rj = it / Q4, qj = p.row_of(rj), hj = w.h * G + rj - qj * G;
