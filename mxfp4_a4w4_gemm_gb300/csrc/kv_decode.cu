@@ -51,6 +51,7 @@ namespace {
 constexpr int kStep = 32;                     // tokens of a step
 constexpr int kLeast = 1;                     // steps of a worker, at least
 constexpr int kFew = 4;                       // workers of a CTA, at least
+constexpr int kUnitCost = 2;                  // what a unit costs beside its steps, in steps (places of the line)
 constexpr int kMaxParts = 256;                // CTAs of a launch, and so parts of a cut unit
 constexpr float kNoMax = -3.0e38f;            // running maximum before the first key
 
@@ -179,7 +180,7 @@ struct Open {
 struct Walk {
   int b, h, k, t, n;          // request, head, block of rows, first step of the piece, steps of the unit
   int len, rows, all, row0;   // rows: the request's, all its heads'
-  int left;                   // steps of the run from this piece on
+  int left;                   // places of the run from the piece's first step on
   __device__ __forceinline__ void load(const KvAttentionArgs& p, int G) {
     const KvRequest r = kv_request(p, b);
     len = r.len; rows = r.rows * G; all = r.all; row0 = r.row0;
@@ -192,7 +193,9 @@ struct Walk {
   __device__ __forceinline__ void next(const KvAttentionArgs& p, int G) {
     left -= steps();
     t = 0;
-    if (left <= 0 || ++k * ROWS < rows) return;
+    if (left <= 0) return;
+    left -= kUnitCost;
+    if (++k * ROWS < rows) return;
     k = 0;
     if (++h < p.Hkv) return;
     h = 0;
@@ -226,7 +229,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
   KvStart start;
   auto steps_of = [&](int b) -> uint32_t {
     const KvRequest r = kv_request(p, b);
-    return r.rows > 0 ? max(1, (r.len + kStep - 1) / kStep) * p.Hkv * ((r.rows * G + Cf::ROWS - 1) / Cf::ROWS) : 0;
+    return r.rows > 0 ? (max(1, (r.len + kStep - 1) / kStep) + kUnitCost) * p.Hkv * ((r.rows * G + Cf::ROWS - 1) / Cf::ROWS) : 0;
   };
   if (!kv_locate<Cf::THREADS, W>(p.B, steps_of, kLeast, kFew, reinterpret_cast<uint32_t*>(smem + Cf::OFF_SCAN), share,
                                  start))
@@ -238,11 +241,12 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
   if (warp < per && me < share.workers) {
     cw.b = start.b;
     cw.load(p, G);
-    const int blocks = (cw.rows + Cf::ROWS - 1) / Cf::ROWS, unit = start.rest / cw.n;
+    const int blocks = (cw.rows + Cf::ROWS - 1) / Cf::ROWS, unit = start.rest / (cw.n + kUnitCost);
+    const int at = start.rest - unit * (cw.n + kUnitCost);
     cw.h = unit / blocks;
     cw.k = unit - cw.h * blocks;
-    cw.t = start.rest - unit * cw.n;
-    cw.left = share.first(me + 1) - share.first(me);
+    cw.t = max(0, at - kUnitCost);
+    cw.left = static_cast<int>(share.first(me + 1) - share.first(me)) - max(0, kUnitCost - at);
   }
 
   const int lg = 31 - __clz(p.page_size), chunks = p.page_size >> 4;     // page_size is a power of two
@@ -827,14 +831,16 @@ int launch_one(const KvAttentionArgs& p, int grid, cudaStream_t st) {
 
 int launch_kv_decode(const KvAttentionArgs& p, int D, cudaStream_t st, int sms) {
   const int rows = p.max_q * (p.Hq / p.Hkv);
-  // as many CTAs as there can be work for, one per SM at most
-  const long long per = (static_cast<long long>(p.max_pages) * p.page_size + kStep - 1) / kStep;
-  const int most = sms < kMaxParts ? sms : kMaxParts;
-  const long long ctas = (per * p.B * p.Hkv * ((rows + 15) / 16) + kLeast * kFew - 1) / (kLeast * kFew);
-  const int grid = static_cast<int>(ctas < most ? ctas : most);
   // 16 rows at a time, but an odd number of 8-row blocks would waste half of one (a step costs 1.9 times as much:
   // 24 requests x 20 rows 28 us in blocks of 8, 33 us in blocks of 16; 2 x 131000 keys x 16 rows 63 and 61 us)
   const bool two = (rows + 7) / 8 % 2 == 0;
+  // as many CTAs as there can be work for, one per SM at most; places of the line are counted in 32 bits
+  const double places = (static_cast<double>(p.max_pages) * p.page_size / kStep + 1 + kUnitCost) * p.B * p.Hkv *
+                        ((rows + (two ? 15 : 7)) / (two ? 16 : 8));
+  if (places > 2147483647.0) return -1;
+  const int most = sms < kMaxParts ? sms : kMaxParts;
+  const double ctas = places / (kLeast * kFew) + 1;
+  const int grid = ctas < most ? static_cast<int>(ctas) : most;
   if (D == 64) return two ? launch_one<64, 2>(p, grid, st) : launch_one<64, 1>(p, grid, st);
   return two ? launch_one<128, 2>(p, grid, st) : launch_one<128, 1>(p, grid, st);
 }

@@ -43,6 +43,9 @@ namespace {
 constexpr int kKeys = 128;                    // keys of a step
 constexpr int kRows = 256;                    // rows of a unit
 constexpr int kLeastSteps = 2;                // steps of a worker, at least
+// What a unit costs beside its steps (queries, output), in steps: so many places of
+// the line before its first step hold no work.
+constexpr int kUnitCost = 2;
 constexpr int kMaxCtas = 512;
 constexpr int kRestKeys = 512;                // keys of a table up to which P has two terms
 constexpr float kNoMax = -3.0e38f;            // running maximum before the first key
@@ -267,20 +270,21 @@ struct Blocks {
     const int seen = len - all + min((k + 1) * tq, rows);
     return max(1, (seen + kKeys - 1) / kKeys);
   }
-  // steps of blocks 0 .. k - 1, k < n
+  // places of blocks 0 .. k - 1 on the line, k < n
   __device__ __forceinline__ uint32_t before(int k) const {
     const int base = len - all;
     // the first blocks may see nothing: one empty step each
     const int none = base < 0 ? min(k, -base / tq) : 0;
-    return none + floor_sum(k - none, kKeys, tq, static_cast<uint32_t>(base + (none + 1) * tq + kKeys - 1));
+    return k * kUnitCost + none + floor_sum(k - none, kKeys, tq, static_cast<uint32_t>(base + (none + 1) * tq + kKeys - 1));
   }
-  __device__ __forceinline__ uint32_t total() const { return n > 0 ? before(n - 1) + steps(n - 1) : 0u; }
+  __device__ __forceinline__ uint32_t total() const { return n > 0 ? before(n - 1) + kUnitCost + steps(n - 1) : 0u; }
 };
 
 // A walk along the CTA's run: one piece (a run of one unit's steps) at a time.
 struct PreWalk {
   Blocks q;
-  int b, h, k, t, n, left;                     // request, head, block, first step of the piece, steps of the unit
+  int b, h, k, t, n;                           // request, head, block, first step of the piece, steps of the unit
+  int left;                                    // places of the run from the piece's first step on
   __device__ __forceinline__ int steps() const { return min(left, n - t); }
   __device__ __forceinline__ void next(const KvAttentionArgs& p) {
     left -= steps();
@@ -294,6 +298,7 @@ struct PreWalk {
       }
     }
     n = q.steps(k);
+    left -= kUnitCost;
   }
   // rows of the unit
   __device__ __forceinline__ int rows(int G) const { return min(q.tq, q.rows - k * q.tq) * G; }
@@ -324,7 +329,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cf::OFF_MISC + 8);
   volatile int* never = abort_flag + 1;
   volatile int* last_flag = abort_flag + 2;
-  int* start_at = reinterpret_cast<int*>(smem + Cf::OFF_MISC + 24);     // head, block, step, request
+  int* start_at = reinterpret_cast<int*>(smem + Cf::OFF_MISC + 24);     // head, block, place, request
   // largest key scale of a step; a slot is used again four steps later, when its readers are past the step after
   int* key_ref = reinterpret_cast<int*>(smem + Cf::OFF_MISC + 40);
   if (tid == 0) {
@@ -394,9 +399,9 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
   w.q = Blocks(p, w.b, tq);
   w.h = start_at[0];
   w.k = start_at[1];
-  w.t = start_at[2];
   w.n = w.q.steps(w.k);
-  w.left = share.first(cta + 1) - share.first(cta);
+  w.t = max(0, start_at[2] - kUnitCost);
+  w.left = static_cast<int>(share.first(cta + 1) - share.first(cta)) - max(0, kUnitCost - start_at[2]);
   const unsigned long long drain_ns = p.wait_ns > 100000000ull ? p.wait_ns : 100000000ull;
   auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, p.wait_ns, p.status); };
 
@@ -931,7 +936,7 @@ int launch_kv_prefill(const KvAttentionArgs& p, int D, cudaStream_t st, int sms)
   // steps are counted in 32 bits
   const int G = p.Hq / p.Hkv, tq = kRows / G;
   const double most = static_cast<double>(p.B) * p.Hkv * ((p.max_q + tq - 1) / tq) *
-                      ((static_cast<double>(p.max_pages) * p.page_size + kKeys - 1) / kKeys + 1);
+                      ((static_cast<double>(p.max_pages) * p.page_size + kKeys - 1) / kKeys + 1 + kUnitCost);
   if (most > 2147483647.0) return -1;
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
   const bool rest = p.max_pages <= kRestKeys / p.page_size;

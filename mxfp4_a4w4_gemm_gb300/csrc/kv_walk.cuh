@@ -4,7 +4,8 @@
 // key/value head h (and block of rows).  Its keys are cut into steps; the steps
 // of all units, in order, form one line, which is cut into equal runs, one per
 // worker: every worker gets the same work to within one step whatever the
-// lengths are, and units that are cut are joined afterwards.  The cut depends on
+// lengths are, and units that are cut are joined afterwards.  What a unit costs
+// beside its steps counts as places without work before them.  The cut depends on
 // the lengths alone.
 #pragma once
 

@@ -171,7 +171,7 @@ struct KvAttentionArgs {
 };
 size_t kv_attention_ws_bytes(int max_q, int group, int D, int sms);
 int launch_kv_attention(const KvAttentionArgs& p, int D, cudaStream_t st, int sms);
-// At most 16 query rows (max_q * Hq / Hkv) per key/value head (kv_decode.cu).
+// Few query rows (max_q * Hq / Hkv) per key/value head (kv_decode.cu).  -1: more work than it counts.
 size_t kv_decode_ws_bytes(int rows, int D, int sms);
 int launch_kv_decode(const KvAttentionArgs& p, int D, cudaStream_t st, int sms);
 // Any number of rows, Hq / Hkv <= 256 (kv_prefill.cu).  -1: more work than it counts.
