@@ -73,13 +73,13 @@ struct DecCfg {
   static constexpr int OFF_BAR = OFF_ML + 2 * WARPS * ROWS * 8;
   static constexpr int OFF_OPEN = OFF_BAR + WARPS * STAGES * 8;
   static constexpr int OFF_MISC = OFF_OPEN + (WARPS + 1) * 24;
-  static constexpr int SMEM = OFF_MISC + 16;
-  static constexpr int OFF_SCAN = OFF_O;                         // the cut's scratch, before there are parts
+  static constexpr int OFF_SCAN = OFF_MISC + 16;                 // the cut's scratch: slow warps read it while fast ones work
+  static constexpr int SMEM = OFF_SCAN + THREADS * 4;
   static constexpr int PART = ROWS * (D + 2);                    // floats of a stored part: O, then m and l
   static_assert(STAGE % 16 == 0 && OFF_KS % 16 == 0 && OFF_VS % 16 == 0 && OFF_O % 16 == 0, "alignment");
   static_assert(2 * kMaxParts <= WARPS * PITCH && kMaxParts <= kTickets && PART % 4 == 0, "join");
   static_assert(ROWS * PITCH * 4 <= STAGES * STAGE, "a part fits in the warp's drained ring");
-  static_assert(OFF_OPEN % 4 == 0 && (THREADS + 32) * 4 <= WARPS * ROWS * PITCH * 4, "scratch");
+  static_assert(OFF_OPEN % 4 == 0 && OFF_SCAN % 4 == 0, "alignment");
   static_assert(OFF_BAR % 8 == 0 && SMEM <= 232448, "shared memory");
 };
 
@@ -181,8 +181,7 @@ struct Walk {
   int b, h, k, t, n;          // request, head, block of rows, first step of the piece, steps of the unit
   int len, rows, all, row0;   // rows: the request's, all its heads'
   int left;                   // places of the run from the piece's first step on
-  __device__ __forceinline__ void load(const KvAttentionArgs& p, int G) {
-    const KvRequest r = kv_request(p, b);
+  __device__ __forceinline__ void load(const KvRequest& r, int G) {
     len = r.len; rows = r.rows * G; all = r.all; row0 = r.row0;
     n = rows > 0 ? max(1, (len + kStep - 1) / kStep) : 0;
   }
@@ -199,7 +198,7 @@ struct Walk {
     k = 0;
     if (++h < p.Hkv) return;
     h = 0;
-    do { ++b; load(p, G); } while (n == 0);    // a run ends in a request that has steps
+    do { load(kv_request(p, ++b), G); } while (n == 0);    // a run ends in a request that has steps
   }
 };
 
@@ -221,18 +220,17 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
   if (lane == 0)
     for (int s = 0; s < S; ++s) mbar_init(full(s), 1);
   fence_barrier_init();
+  __syncthreads();                               // flags and list are set before anything is put in them
   griddep_wait();
   griddep_launch_dependents();
 
   const int G = p.Hq / p.Hkv;
   KvShare share;
   KvStart start;
-  auto steps_of = [&](int b) -> uint32_t {
-    const KvRequest r = kv_request(p, b);
+  auto places = [&](const KvRequest& r) -> uint32_t {
     return r.rows > 0 ? (max(1, (r.len + kStep - 1) / kStep) + kUnitCost) * p.Hkv * ((r.rows * G + Cf::ROWS - 1) / Cf::ROWS) : 0;
   };
-  if (!kv_locate<Cf::THREADS, W>(p.B, steps_of, kLeast, kFew, reinterpret_cast<uint32_t*>(smem + Cf::OFF_SCAN), share,
-                                 start))
+  if (!kv_locate<Cf::THREADS, W>(p, places, kLeast, kFew, reinterpret_cast<uint32_t*>(smem + Cf::OFF_SCAN), share, start))
     return;
   const uint32_t per = share.per, me = blockIdx.x * per + warp;
 
@@ -240,7 +238,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
   cw.left = 0;
   if (warp < per && me < share.workers) {
     cw.b = start.b;
-    cw.load(p, G);
+    cw.load(start.req, G);
     const int blocks = (cw.rows + Cf::ROWS - 1) / Cf::ROWS, unit = start.rest / (cw.n + kUnitCost);
     const int at = start.rest - unit * (cw.n + kUnitCost);
     cw.h = unit / blocks;

@@ -260,8 +260,7 @@ __device__ __forceinline__ uint32_t floor_sum(uint32_t n, uint32_t m, uint32_t a
 struct Blocks {
   int len, all, rows, row0, tq, n;             // n: blocks
   __device__ __forceinline__ Blocks() {}
-  __device__ __forceinline__ Blocks(const KvAttentionArgs& p, int b, int tq_) {
-    const KvRequest r = kv_request(p, b);
+  __device__ __forceinline__ Blocks(const KvRequest& r, int tq_) {
     len = r.len; all = r.all; rows = r.rows; row0 = r.row0;
     tq = tq_;
     n = (rows + tq - 1) / tq;
@@ -294,7 +293,7 @@ struct PreWalk {
       k = 0;
       if (++h == p.Hkv) {
         h = 0;
-        do { ++b; q = Blocks(p, b, q.tq); } while (q.n == 0);
+        do { q = Blocks(kv_request(p, ++b), q.tq); } while (q.n == 0);
       }
     }
     n = q.steps(k);
@@ -361,12 +360,12 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
   const int G = p.Hq / p.Hkv, tq = kRows / G;
   KvShare share;
   KvStart start;
-  auto steps_of = [&](int b) -> uint32_t { return Blocks(p, b, tq).total() * p.Hkv; };
-  if (!kv_locate<Cf::THREADS, 1>(p.B, steps_of, kLeastSteps, 1, reinterpret_cast<uint32_t*>(smem + Cf::OFF_Q), share, start))
+  auto places = [&](const KvRequest& r) -> uint32_t { return Blocks(r, tq).total() * p.Hkv; };
+  if (!kv_locate<Cf::THREADS, 1>(p, places, kLeastSteps, 1, reinterpret_cast<uint32_t*>(smem + Cf::OFF_Q), share, start))
     return;
   const uint32_t cta = blockIdx.x;
   if (warp == 0) {
-    const Blocks q(p, start.b, tq);
+    const Blocks q(start.req, tq);
     const uint32_t per = q.total();
     const int h = start.rest / per;
     const uint32_t rest = start.rest - h * per;
@@ -396,7 +395,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
   const uint32_t tmem = *tmem_slot;
   PreWalk w;
   w.b = start_at[3];
-  w.q = Blocks(p, w.b, tq);
+  w.q = Blocks(kv_request(p, w.b), tq);
   w.h = start_at[0];
   w.k = start_at[1];
   w.n = w.q.steps(w.k);
