@@ -561,42 +561,48 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
       const bool whole = w.t == 0 && w.steps() == w.n;
       const uint32_t u0 = share.first(cta + 1) - w.left - w.t;    // the unit's first step on the line
       float* mine = parts + static_cast<size_t>(2 * cta + (share.first(cta) < u0 ? 1 : 0)) * Cf::PART;
+      // dimensions 64 a .. + 63 of the thread's row, times `by`; column g * 8 + e of the block (x) is dimension
+      // 64 a + 2 g + {0, 32, 1, 33, 16, 48, 17, 49}[e]
+      auto write_out = [&](int a, const uint32_t* x, float by) {
+        auto at = [&](int n) {
+          return by * __uint_as_float(x[n % 16 / 2 * 8 + (n / 16 == 0 ? 0 : n / 16 == 2 ? 1 : n / 16 == 1 ? 4 : 5) + 2 * (n % 2)]);
+        };
+        uint16_t* dst = p.out + (row * p.Hq + hq) * D + 64 * a;
+#pragma unroll
+        for (int n = 0; n < 64; n += 8)
+          *reinterpret_cast<uint4*>(dst + n) = make_uint4(pack_bf16(at(n), at(n + 1)), pack_bf16(at(n + 2), at(n + 3)),
+                                                          pack_bf16(at(n + 4), at(n + 5)), pack_bf16(at(n + 6), at(n + 7)));
+      };
+      auto write_lse = [&](float mm, float ll) {
+        if (p.lse != nullptr) p.lse[row * p.Hq + hq] = ll == 0.f ? -INFINITY : fmaf(mm, 0.6931471805599453f, logf(ll));
+      };
       if (active) {
-        const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
         for (int a = 0; a < D / 64; ++a) {
-          // column g * 8 + e of block a is dimension 64 a + 2 g + {0, 32, 1, 33, 16, 48, 17, 49}[e]
           uint32_t x[64];
           tmem_ld32(o_col + 64 * a, x);
           tmem_ld32(o_col + 64 * a + 32, x + 32);
           tmem_wait_ld<64>(x);
           if (r < R) {
-            auto at = [&](int n) {
-              return __uint_as_float(x[n % 16 / 2 * 8 + (n / 16 == 0 ? 0 : n / 16 == 2 ? 1 : n / 16 == 1 ? 4 : 5) + 2 * (n % 2)]);
-            };
             if (whole) {
-              uint16_t* dst = p.out + (row * p.Hq + hq) * D + 64 * a;
-#pragma unroll
-              for (int n = 0; n < 64; n += 8)
-                *reinterpret_cast<uint4*>(dst + n) =
-                    make_uint4(pack_bf16(at(n) * inv, at(n + 1) * inv), pack_bf16(at(n + 2) * inv, at(n + 3) * inv),
-                               pack_bf16(at(n + 4) * inv, at(n + 5) * inv), pack_bf16(at(n + 6) * inv, at(n + 7) * inv));
+              write_out(a, x, inv);
             } else {
-              float* dst = mine + r * D + 64 * a;
+              // a part: pieces of 4 columns, the rows' side by side, so that a warp writes 512 bytes in a run
+              uint4* dst = reinterpret_cast<uint4*>(mine) + a * 16 * kRows + r;
 #pragma unroll
-              for (int n = 0; n < 64; n += 4)
-                *reinterpret_cast<float4*>(dst + n) = make_float4(at(n), at(n + 1), at(n + 2), at(n + 3));
+              for (int u = 0; u < 16; ++u) dst[u * kRows] = make_uint4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
             }
           }
         }
         if (r < R) {
           const float mm = fmaxf(m, kNoMax);
-          if (!whole) *reinterpret_cast<float2*>(mine + kRows * D + 2 * r) = make_float2(mm, l);
-          else if (p.lse != nullptr) p.lse[row * p.Hq + hq] = l == 0.f ? -INFINITY : fmaf(mm, 0.6931471805599453f, logf(l));
+          if (whole) write_lse(mm, l);
+          else *reinterpret_cast<float2*>(mine + kRows * D + 2 * r) = make_float2(mm, l);
         }
       }
       if (!whole) {
-        // ---- the last part to arrive joins a cut unit (softmax warps only) ----
+        // ---- the last part to arrive joins a cut unit (softmax warps only), a thread per row ----
         const int c0 = share.holder(u0), np = share.holder(u0 + w.n - 1) - c0 + 1;
         named_bar_sync(1, 256);
         int* ticket = static_cast<int*>(p.ws) + c0;
@@ -609,53 +615,39 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
         if (*last_flag) {
           const size_t head = share.first(c0) < u0 ? Cf::PART : 0;
           auto part = [&](int k) { return parts + static_cast<size_t>(2 * (c0 + k)) * Cf::PART + (k == 0 ? head : 0); };
-          // a thread per row turns the parts' maxima into weights, where they lie
-          if (tid < R) {
+          auto stat = [&](int k) { return __ldcg(reinterpret_cast<const float2*>(part(k) + kRows * D) + r); };
+          if (r < R) {
             float mm = kNoMax, ll = 0.f;
 #pragma unroll 4
-            for (int k = 0; k < np; ++k) mm = fmaxf(mm, __ldcg(part(k) + kRows * D + 2 * tid));
+            for (int k = 0; k < np; ++k) mm = fmaxf(mm, stat(k).x);
 #pragma unroll 4
             for (int k = 0; k < np; ++k) {
-              const float2 q = __ldcg(reinterpret_cast<const float2*>(part(k) + kRows * D + 2 * tid));
+              const float2 q = stat(k);
               ll = fmaf(q.y, ex2(q.x - mm), ll);
             }
             const float inv = ll == 0.f ? 0.f : 1.f / ll;
-#pragma unroll 4
-            for (int k = 0; k < np; ++k) {
-              float* at = part(k) + kRows * D + 2 * tid;
-              __stcg(at, ex2(__ldcg(at) - mm) * inv);
-            }
-            if (p.lse != nullptr) p.lse[row * p.Hq + hq] = ll == 0.f ? -INFINITY : fmaf(mm, 0.6931471805599453f, logf(ll));
-          }
-          named_bar_sync(1, 256);
-          // then all threads over the rows' pieces of 16 bytes, eight at a time
-          constexpr int Q4 = D / 4, AT = 8;
-          for (int it0 = tid; it0 < R * Q4; it0 += AT * 256) {
-            float4 y[AT];
+#pragma unroll 1
+            for (int a = 0; a < D / 64; ++a) {
+              uint32_t y[64];
 #pragma unroll
-            for (int u = 0; u < AT; ++u) y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-            for (int k = 0; k < np; ++k) {
-              const float* src = part(k);
+              for (int u = 0; u < 64; ++u) y[u] = 0u;
+#pragma unroll 1
+              for (int k = 0; k < np; ++k) {
+                const float4* src = reinterpret_cast<const float4*>(part(k)) + a * 16 * kRows + r;
+                float4 v[16];
 #pragma unroll
-              for (int u = 0; u < AT; ++u) {
-                const int it = min(it0 + u * 256, R * Q4 - 1);
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(src) + it);
-                const float a = __ldcg(src + kRows * D + 2 * (it / Q4));
-                y[u].x = fmaf(v.x, a, y[u].x); y[u].y = fmaf(v.y, a, y[u].y);
-                y[u].z = fmaf(v.z, a, y[u].z); y[u].w = fmaf(v.w, a, y[u].w);
+                for (int u = 0; u < 16; ++u) v[u] = __ldcg(src + u * kRows);
+                const float f = ex2(stat(k).x - mm);
+                auto add = [&](uint32_t& to, float x) { to = __float_as_uint(fmaf(x, f, __uint_as_float(to))); };
+#pragma unroll
+                for (int u = 0; u < 16; ++u) {
+                  add(y[4 * u], v[u].x); add(y[4 * u + 1], v[u].y);
+                  add(y[4 * u + 2], v[u].z); add(y[4 * u + 3], v[u].w);
+                }
               }
+              write_out(a, y, inv);
             }
-#pragma unroll
-            for (int u = 0; u < AT; ++u) {
-              const int it = it0 + u * 256;
-              if (it < R * Q4) {
-                const int rj = it / Q4, qj = p.row_of(rj), hj = w.h * G + rj - qj * G;
-                const long long gr = static_cast<long long>(w.q.row0) + first_tok + qj;
-                *reinterpret_cast<uint2*>(p.out + (gr * p.Hq + hj) * D + it % Q4 * 4) =
-                    make_uint2(pack_bf16(y[u].x, y[u].y), pack_bf16(y[u].z, y[u].w));
-              }
-            }
+            write_lse(mm, ll);
           }
           if (tid == 0) *ticket = 0;
         }
