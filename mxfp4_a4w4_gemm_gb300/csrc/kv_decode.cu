@@ -52,6 +52,7 @@ constexpr int kStep = 32;                     // tokens of a step
 constexpr int kLeast = 1;                     // steps of a worker, at least
 constexpr int kFew = 4;                       // workers of a CTA, at least
 constexpr int kUnitCost = 2;                  // what a unit costs beside its steps, in steps (places of the line)
+constexpr int kWhole = 64;                    // places of the longest unit that a CTA may take whole
 constexpr int kMaxParts = 256;                // CTAs of a launch, and so parts of a cut unit
 constexpr float kNoMax = -3.0e38f;            // running maximum before the first key
 
@@ -74,7 +75,8 @@ struct DecCfg {
   static constexpr int OFF_OPEN = OFF_BAR + WARPS * STAGES * 8;
   static constexpr int OFF_MISC = OFF_OPEN + (WARPS + 1) * 24;
   static constexpr int OFF_SCAN = OFF_MISC + 16;                 // the cut's scratch: slow warps read it while fast ones work
-  static constexpr int SMEM = OFF_SCAN + THREADS * 4;
+  static constexpr int OFF_SHARE = OFF_SCAN + (THREADS + 32) * 4;       // each warp's copy of the cut: registers are short
+  static constexpr int SMEM = OFF_SHARE + WARPS * static_cast<int>(sizeof(KvShare));
   static constexpr int PART = ROWS * (D + 2);                    // floats of a stored part: O, then m and l
   static_assert(STAGE % 16 == 0 && OFF_KS % 16 == 0 && OFF_VS % 16 == 0 && OFF_O % 16 == 0, "alignment");
   static_assert(2 * kMaxParts <= WARPS * PITCH && kMaxParts <= kTickets && PART % 4 == 0, "join");
@@ -227,12 +229,16 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
   const int G = p.Hq / p.Hkv;
   KvShare share;
   KvStart start;
+  auto unit = [&](const KvRequest& r) -> uint32_t { return max(1, (r.len + kStep - 1) / kStep) + kUnitCost; };
   auto places = [&](const KvRequest& r) -> uint32_t {
-    return r.rows > 0 ? (max(1, (r.len + kStep - 1) / kStep) + kUnitCost) * p.Hkv * ((r.rows * G + Cf::ROWS - 1) / Cf::ROWS) : 0;
+    return r.rows > 0 ? unit(r) * p.Hkv * ((r.rows * G + Cf::ROWS - 1) / Cf::ROWS) : 0;
   };
-  if (!kv_locate<Cf::THREADS, W>(p, places, kLeast, kFew, reinterpret_cast<uint32_t*>(smem + Cf::OFF_SCAN), share, start))
+  if (!kv_locate<Cf::THREADS, W, kWhole>(p, places, unit, kUnitCost, kLeast, kFew,
+                                         reinterpret_cast<uint32_t*>(smem + Cf::OFF_SCAN), share, start))
     return;
   const uint32_t per = share.per, me = blockIdx.x * per + warp;
+  KvShare* cut = reinterpret_cast<KvShare*>(smem + Cf::OFF_SHARE) + warp;
+  if (lane == 0) *cut = share;
 
   Walk cw;
   cw.left = 0;
@@ -653,8 +659,8 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
     // the CTA's list of cut units: by the warp that holds their beginning, or by
     // the first warp if that lies in an earlier CTA
     if (lane == 0 && ((back && !front) || (front && warp == 0))) {
-      const uint32_t u0 = share.first(me + 1) - cw.left - cw.t;   // the unit's first step on the line
-      open[front ? 0 : warp + 1] = Open{cw.row0, h, r0, R, share.holder(u0), share.holder(u0 + cw.n - 1)};
+      const uint32_t u0 = cut->first(me + 1) - cw.left - cw.t;   // the unit's first step on the line
+      open[front ? 0 : warp + 1] = Open{cw.row0, h, r0, R, cut->holder(u0), cut->holder(u0 + cw.n - 1)};
     }
     cw.template next<Cf::ROWS>(p, G);
   }
@@ -833,11 +839,11 @@ int launch_kv_decode(const KvAttentionArgs& p, int D, cudaStream_t st, int sms) 
   // 24 requests x 20 rows 28 us in blocks of 8, 33 us in blocks of 16; 2 x 131000 keys x 16 rows 63 and 61 us)
   const bool two = (rows + 7) / 8 % 2 == 0;
   // as many CTAs as there can be work for, one per SM at most; places of the line are counted in 32 bits
-  const double places = (static_cast<double>(p.max_pages) * p.page_size / kStep + 1 + kUnitCost) * p.B * p.Hkv *
-                        ((rows + (two ? 15 : 7)) / (two ? 16 : 8));
+  const double units = static_cast<double>(p.B) * p.Hkv * ((rows + (two ? 15 : 7)) / (two ? 16 : 8));
+  const double places = (static_cast<double>(p.max_pages) * p.page_size / kStep + 1 + kUnitCost) * units;
   if (places > 2147483647.0) return -1;
   const int most = sms < kMaxParts ? sms : kMaxParts;
-  const double ctas = places / (kLeast * kFew) + 1;
+  const double ctas = fmax(units, places / (kLeast * kFew) + 1);
   const int grid = ctas < most ? static_cast<int>(ctas) : most;
   if (D == 64) return two ? launch_one<64, 2>(p, grid, st) : launch_one<64, 1>(p, grid, st);
   return two ? launch_one<128, 2>(p, grid, st) : launch_one<128, 1>(p, grid, st);

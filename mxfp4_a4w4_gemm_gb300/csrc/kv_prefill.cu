@@ -361,7 +361,8 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
   KvShare share;
   KvStart start;
   auto places = [&](const KvRequest& r) -> uint32_t { return Blocks(r, tq).total() * p.Hkv; };
-  if (!kv_locate<Cf::THREADS, 1>(p, places, kLeastSteps, 1, reinterpret_cast<uint32_t*>(smem + Cf::OFF_Q), share, start))
+  if (!kv_locate<Cf::THREADS, 1, 0>(p, places, places, 0, kLeastSteps, 1, reinterpret_cast<uint32_t*>(smem + Cf::OFF_Q),
+                                    share, start))
     return;
   const uint32_t cta = blockIdx.x;
   if (warp == 0) {

@@ -72,17 +72,22 @@ __device__ __forceinline__ int kv_page(const KvAttentionArgs& p, int b, int i) {
   return min(max(id, 0), p.num_pages - 1);
 }
 
-// The line's cut: the first `more` workers take each + 1 steps, the others `each`.
+// The cut of the line, or of this CTA's stretch of it: workers v0 .. workers - 1 share
+// the places from `base` on, the first `more` of them each + 1, the others `each`.
 struct KvShare {
-  uint32_t total;           // steps of the line
-  uint32_t workers;
+  uint32_t base, v0, workers;
   uint32_t each, more;
   uint32_t per;             // workers of a CTA
-  __device__ __forceinline__ uint32_t first(uint32_t v) const { return v * each + min(v, more); }
-  // the worker that holds step f
+  __device__ __forceinline__ void cut(uint32_t from, uint32_t total, uint32_t first_worker, uint32_t n) {
+    base = from; v0 = first_worker; workers = first_worker + n;
+    each = total / n;
+    more = total - each * n;
+  }
+  __device__ __forceinline__ uint32_t first(uint32_t v) const { return base + (v - v0) * each + min(v - v0, more); }
+  // the worker that holds place f
   __device__ __forceinline__ uint32_t holder(uint32_t f) const {
-    const uint32_t wide = more * (each + 1);
-    return f < wide ? f / (each + 1) : more + (f - wide) / each;
+    const uint32_t wide = more * (each + 1), at = f - base;
+    return v0 + (at < wide ? at / (each + 1) : more + (at - wide) / each);
   }
 };
 
@@ -106,13 +111,21 @@ __device__ __forceinline__ KvRequest shfl_request(const KvRequest& r, int lane) 
 // places, at least `few` of them to a CTA; warp w learns the start of worker
 // blockIdx.x * per + w, if there is one.  Every thread of the CTA calls it; with
 // up to 32 requests each warp finds out for itself, with more they sum together
-// (scratch: THREADS words of shared memory, in use until every warp has returned).
-// Returns false if the CTA has nothing to do.  Without a barrier for few requests
-// one token's attention over 1000 keys takes 9.4 us, with the sums of all warps
-// 10.0; 24 requests x 5 tokens 22.0 and 23.2.
-template <int THREADS, int PER, typename Places>
-__device__ __forceinline__ bool kv_locate(const KvAttentionArgs& p, Places places, uint32_t least, uint32_t few,
-                                          uint32_t* scratch, KvShare& share, KvStart& start) {
+// (scratch: THREADS + 32 words of shared memory, in use until every warp has
+// returned).  Returns false if the CTA has nothing to do.  Without a barrier for few
+// requests one token's attention over 1000 keys took 9.4 us, with the sums of all
+// warps 10.0; 24 requests x 5 tokens 22.0 and 23.2.
+//
+// Short units (unit(r) places each, `cost` of them without work; WHOLE at most) go to
+// CTAs whole, those that begin in its equal stretch of the line, which its own warps
+// then cut: a join between CTAs takes 3 to 4 us, about as long as a CTA takes for 24
+// places more than the others.  Whole and cut, one token, 8 heads of 128: 1 request
+// x 100 keys 6.6 and 9.1 us, 8 x 1000 10.1 and 12.9, 64 x 300 12.7 and 15.7, 256
+// ragged x 600 29.1 and 33.3; 64 x 2000 38.3 and 38.1; over the limits 1 x 1000 10.2
+// and 9.6, 1 x 2000 13.6 and 11.4.
+template <int THREADS, int PER, int WHOLE, typename Places, typename Unit>
+__device__ __forceinline__ bool kv_locate(const KvAttentionArgs& p, Places places, Unit unit, uint32_t cost, uint32_t least,
+                                          uint32_t few, uint32_t* scratch, KvShare& share, KvStart& start) {
   constexpr int W = THREADS / 32;
   static_assert(W <= 32 && PER <= W, "a search per warp");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -121,9 +134,12 @@ __device__ __forceinline__ bool kv_locate(const KvAttentionArgs& p, Places place
   const int b0 = (small ? lane : tid) * per, b1 = min(p.B, b0 + per);
   KvRequest mine = {0, 0, 0, 0};
   uint32_t sum = 0;
+  uint32_t longest = 0;                                          // places of the longest unit
   for (int b = b0; b < b1; ++b) {
     mine = kv_request(p, b);
-    sum += places(mine);
+    const uint32_t n = places(mine);
+    sum += n;
+    if (WHOLE > 0 && n > 0) longest = max(longest, unit(mine));
   }
   uint32_t inc = sum;                                            // inclusive, within the warp
 #pragma unroll
@@ -131,53 +147,75 @@ __device__ __forceinline__ bool kv_locate(const KvAttentionArgs& p, Places place
     const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
     if (lane >= o) inc += u;
   }
-  uint32_t wsum = 0;
+  uint32_t wsum = 0, total;
   if (small) {
-    share.total = __shfl_sync(0xFFFFFFFFu, inc, 31);
+    if (WHOLE > 0) longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+    total = __shfl_sync(0xFFFFFFFFu, inc, 31);
   } else {
+    if (WHOLE > 0) longest = __reduce_max_sync(0xFFFFFFFFu, longest);
     scratch[tid] = inc;
+    if (lane == 0) scratch[THREADS + warp] = longest;
     __syncthreads();
+    if (WHOLE > 0) longest = __reduce_max_sync(0xFFFFFFFFu, lane < W ? scratch[THREADS + lane] : 0u);
     wsum = lane < W ? scratch[lane * 32 + 31] : 0u;              // the warps' sums, scanned by every warp
 #pragma unroll
     for (int o = 1; o < W; o <<= 1) {
       const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, wsum, o);
       if (lane >= o) wsum += u;
     }
-    share.total = __shfl_sync(0xFFFFFFFFu, wsum, W - 1);
+    total = __shfl_sync(0xFFFFFFFFu, wsum, W - 1);
   }
-  share.workers = min(static_cast<uint32_t>(gridDim.x) * PER, (share.total + least - 1) / least);
-  share.per = max(few, (share.workers + gridDim.x - 1) / gridDim.x);
-  const uint32_t v0 = blockIdx.x * share.per;
-  if (v0 >= share.workers) return false;
-  share.each = share.total / share.workers;
-  share.more = share.total - share.each * share.workers;
-  if (warp >= share.per || v0 + warp >= share.workers) return true;
-  const uint32_t f = share.first(v0 + warp);
-  // the warp's run of requests, then the thread's, that holds place f
-  uint32_t lo = 0, ti = inc;
-  int base = 0;
-  if (!small) {
-    const int wi = __popc(__ballot_sync(0xFFFFFFFFu, lane < W && wsum <= f));
-    const uint32_t wlo = __shfl_sync(0xFFFFFFFFu, wsum, wi > 0 ? wi - 1 : 0);
-    lo = wi > 0 ? wlo : 0u;
-    ti = scratch[wi * 32 + lane];
-    base = wi * 32;
-  }
-  const int li = __popc(__ballot_sync(0xFFFFFFFFu, lo + ti <= f));
-  const uint32_t tlo = __shfl_sync(0xFFFFFFFFu, ti, li > 0 ? li - 1 : 0);
-  lo += li > 0 ? tlo : 0u;
-  int b = (base + li) * per;
-  if (small) {
-    start.req = shfl_request(mine, li);
-  } else {
-    start.req = kv_request(p, b);
-    for (uint32_t n = places(start.req); f >= lo + n; n = places(start.req)) {
-      lo += n;
-      start.req = kv_request(p, ++b);
+  // the request that holds place f < total: the warp's run of requests, then the thread's, then one by one
+  auto find = [&](uint32_t f) {
+    uint32_t lo = 0, ti = inc;
+    int base = 0;
+    if (!small) {
+      const int wi = __popc(__ballot_sync(0xFFFFFFFFu, lane < W && wsum <= f));
+      const uint32_t wlo = __shfl_sync(0xFFFFFFFFu, wsum, wi > 0 ? wi - 1 : 0);
+      lo = wi > 0 ? wlo : 0u;
+      ti = scratch[wi * 32 + lane];
+      base = wi * 32;
     }
+    const int li = __popc(__ballot_sync(0xFFFFFFFFu, lo + ti <= f));
+    const uint32_t tlo = __shfl_sync(0xFFFFFFFFu, ti, li > 0 ? li - 1 : 0);
+    lo += li > 0 ? tlo : 0u;
+    int b = (base + li) * per;
+    if (small) {
+      start.req = shfl_request(mine, li);
+    } else {
+      start.req = kv_request(p, b);
+      for (uint32_t n = places(start.req); f >= lo + n; n = places(start.req)) {
+        lo += n;
+        start.req = kv_request(p, ++b);
+      }
+    }
+    start.b = b;
+    start.rest = f - lo;
+  };
+  if (total == 0) return false;
+  if (WHOLE > 0 && longest <= min(static_cast<uint32_t>(WHOLE), 24u + total / gridDim.x)) {
+    KvShare even;
+    even.cut(0, total, 0, gridDim.x);
+    // the first unit that begins at place f or after it
+    auto next_unit = [&](uint32_t f) {
+      if (f >= total) return total;
+      find(f);
+      const uint32_t u = unit(start.req);
+      return f - start.rest + (start.rest + u - 1) / u * u;
+    };
+    const uint32_t from = next_unit(even.first(blockIdx.x)), to = next_unit(even.first(blockIdx.x + 1));
+    if (from == to) return false;
+    // the CTA's first places without work are left out
+    share.cut(from + cost, to - from - cost, blockIdx.x * PER, min(static_cast<uint32_t>(PER), to - from - cost));
+    share.per = PER;
+  } else {
+    const uint32_t workers = min(static_cast<uint32_t>(gridDim.x) * PER, (total + least - 1) / least);
+    share.cut(0, total, 0, workers);
+    share.per = max(few, (workers + gridDim.x - 1) / gridDim.x);
   }
-  start.b = b;
-  start.rest = f - lo;
+  const uint32_t v = blockIdx.x * share.per;
+  if (v >= share.workers) return false;
+  if (warp < share.per && v + warp < share.workers) find(share.first(v + warp));
   return true;
 }
 
