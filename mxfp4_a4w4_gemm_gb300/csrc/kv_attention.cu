@@ -5,9 +5,12 @@ namespace a4w4 {
 
 namespace {
 
-// The decode kernel holds up to 16 query rows per key/value head; from there on
-// the tcgen05 kernel, whose 256-row units decode a key once for all their rows,
-// takes over.
+// Rows per key/value head up to which the decode kernel runs.  It goes over the keys
+// once per 8 or 16 rows, the tcgen05 kernel once per 256 at the price of a whole
+// unit.  4 requests x 16384 keys x 8 heads, rows: decode and prompt kernel, D = 128:
+// 16: 36 and 69 us, 32: 56 and 69, 48: 78 and 71, 64: 100 and 71; D = 64: 32: 38 and
+// 56, 48: 51 and 56, 64: 64 and 55; 16 x 1000 keys, D = 128: 48: 34 and 35, 64: 40
+// and 36.
 constexpr int kFewRows = 48;
 bool few_rows(int max_q, int group) { return max_q <= kFewRows / group; }
 

@@ -5,14 +5,21 @@
 //   O[r, :] = sum_k 2^(x_rk - m_r) v_k / sum_k 2^(x_rk - m_r),
 //   x_rk = log2(e) sm_scale q_r . k_k
 //
-// One pass over the cache with running maximum and sum.  Bound by memory: a
-// key and a value cost 17/16 D bytes and 4 R D flops.  A warp takes 32 tokens
+// One pass over the cache with running maximum and sum: a key and a value cost
+// 17/16 D bytes and 4 R D flops, so memory is the floor.  A warp takes 32 tokens
 // at a time, streamed by bulk copies into its own ring, and keeps everything
 // else in registers; the tensor instruction is the warp-level one
 // (m16n8k16, FP16 in, fp32 sums), because its operands come straight from the
 // registers that decode the codes: a tcgen05 product would have every decoded
 // value written to shared or tensor memory first, four times the bytes that
 // the copy brought, which is more than that memory passes in the time.
+//
+// What bounds it then are the instructions that decode, some 650 a step of 32
+// tokens and 8 rows at D = 128: 64 ragged requests of up to 8192 keys 71 us (4.0
+// TB/s, with launch, cut and joins; the steps alone run at 6.3 TB/s), 2 x 131000
+// keys x 16 rows 58 us (2.5 TB/s; 16 rows cost nearly twice 8, and 255 registers
+// leave 8 warps), one request of 1000 keys 9.5 us, most of it latency: launch,
+// lengths, page numbers and cells one after the other, then the joins.
 //
 // Keys and values are the M side, query rows the N side (8 per tile), so that
 // small groups waste little:
@@ -49,9 +56,14 @@ namespace a4w4 {
 namespace {
 
 constexpr int kStep = 32;                     // tokens of a step
-constexpr int kLeast = 1;                     // steps of a worker, at least
-constexpr int kFew = 4;                       // workers of a CTA, at least
-constexpr int kUnitCost = 2;                  // what a unit costs beside its steps, in steps (places of the line)
+// Steps of a worker, at least (2: one request x 1000 keys 11.9 us instead of 9.4), and
+// workers of a CTA, at least (1: 100 keys 9.4 us instead of 8.9; alike from 1000 on).
+constexpr int kLeast = 1;
+constexpr int kFew = 4;
+// What a unit costs beside its steps, in steps: so many places of the line before its
+// first step hold no work.  0, 1, 2, 4: 64 ragged requests x 8192 keys 83, 75, 71, 72
+// us; 64 x 300 keys, cut, 1, 2, 4: 17.9, 15.7, 16.7.
+constexpr int kUnitCost = 2;
 constexpr int kWhole = 64;                    // places of the longest unit that a CTA may take whole
 constexpr int kMaxParts = 256;                // CTAs of a launch, and so parts of a cut unit
 constexpr float kNoMax = -3.0e38f;            // running maximum before the first key
@@ -59,7 +71,9 @@ constexpr float kNoMax = -3.0e38f;            // running maximum before the firs
 template <int D, int NT>
 struct DecCfg {
   using Ch = KvChunk<D>;
-  static constexpr int WARPS = NT == 1 ? 16 : NT == 2 && D == 64 ? 12 : 8;
+  // As many warps as the registers allow.  8, 12, 14, 16 warps, 64 ragged requests x 8192 keys, D = 128, 8 rows:
+  // 79.8, 74.3, 80.3, 71.1 us.  The second tile of 8 rows takes up to 255 registers at D = 128, and 12 warps spill.
+  static constexpr int WARPS = NT == 1 ? 16 : D == 64 ? 12 : 8;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int ROWS = 8 * NT;
   static constexpr int J = D / 32, I = D / 16;

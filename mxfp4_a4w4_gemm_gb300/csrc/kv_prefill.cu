@@ -25,9 +25,17 @@
 // The running maximum follows with slack: O is rescaled only when a row's maximum
 // has grown by more than 2^8, P staying below 2^8 meanwhile.
 //
+// A step does 512 R D flops for R rows and brings 136 D bytes: operations are the
+// floor.  4096 tokens x 16384 keys, 32 heads over 8 of 128: 695 us, 1384 TFLOP/s
+// (1911 measured for a plain BF16 product).  A step takes 1.84 us, of which the
+// products 57%; the rest is the chain scores -> softmax -> P of either tile, slowed by
+// the decoders, with which it shares the issue slots (64% of them taken).  Short
+// prompts pay for units beside their steps: 12 ragged requests of up to 700 tokens x
+// 1500 keys 34.6 us, 128 tokens x 128 keys 14.
+//
 //   warps 0-3, 4-7   softmax of tile 0, 1 (a thread per row): stage Q, scores ->
 //                    probabilities, output
-//   warps 8-15       decoders: codes -> BF16 key and value tiles, two slots each
+//   warps 8-15       decoders: codes -> FP16 key and BF16 value tiles, two slots each
 //   warp 16          TMEM owner and MMA issuer
 //   warp 17          copies of the cache chunks, two slots
 #include "kv_walk.cuh"
@@ -42,12 +50,18 @@ namespace {
 
 constexpr int kKeys = 128;                    // keys of a step
 constexpr int kRows = 256;                    // rows of a unit
-constexpr int kLeastSteps = 2;                // steps of a worker, at least
+// Steps of a worker, at least.  1, 2, 4: 128 tokens x 1024 keys 39.7, 32.1, 32.9 us
+// (parts were joined more slowly then), 128 x 128 keys 13.6, 13.9, 22.4, 8 ragged x 100
+// tokens x 1000 keys now 21.9 and 33.8 with 2 and 4.
+constexpr int kLeastSteps = 2;
 // What a unit costs beside its steps (queries, output), in steps: so many places of
-// the line before its first step hold no work.
+// the line before its first step hold no work.  0 and 2: 12 ragged prompts x 700
+// tokens 46.8 and 39.0 us; 2 and 3: 38.4 and 39.1, 4 x 512 x 512 51.3 and 54.6.
 constexpr int kUnitCost = 2;
 constexpr int kMaxCtas = 512;
-constexpr int kRestKeys = 512;                // keys of a table up to which P has two terms
+// Keys of a table up to which P has two terms.  With one term and with two: 128 tokens
+// x 128 keys 13.3 and 14.0 us, 4 x 512 x 512 46.8 and 51.3, 2048 x 8192 205 and 294.
+constexpr int kRestKeys = 512;
 constexpr float kNoMax = -3.0e38f;            // running maximum before the first key
 
 template <int D>
