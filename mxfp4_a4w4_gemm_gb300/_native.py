@@ -114,12 +114,18 @@ def _ptr(x):
 def _rows_ptr(x, stride):
     """Rows of [heads, D] values, `stride` elements apart: only the rows themselves must be contiguous."""
     try:
-        if x.is_contiguous() and (x.numel() == 0 or x.size(0) == 1 or x.stride(0) == stride):
-            return x.data_ptr()
-        T, H, D = x.shape
         st, sh, sd = x.stride()
+        if sd == 1 and st == stride and sh == x.size(2):
+            return x.data_ptr()
     except AttributeError:
         return _ptr(x)
+    except ValueError:                       # not three dimensions
+        pass
+    if x.is_contiguous() and (x.numel() == 0 or x.size(0) == 1 or x.stride(0) == stride):
+        return x.data_ptr()
+    try:
+        T, H, D = x.shape
+        st, sh, sd = x.stride()
     except ValueError:
         raise ValueError("rows must be a [T, heads, D] tensor") from None
     if (D == 1 or sd == 1) and (H == 1 or sh == D) and (T == 1 or st == stride):

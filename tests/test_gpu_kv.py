@@ -327,6 +327,16 @@ def test_many_short_requests():
     check_attention(*problem(rng.integers(0, 4, 700).tolist(), kv_lens, 30, 1, 64, 16, 27))
 
 
+@pytest.mark.parametrize("B,longest,q_len,Hq,Hkv,D,page", [
+    (1, 700, 1, 8, 8, 128, 64), (1, 960, 1, 8, 8, 128, 64), (7, 1030, 1, 32, 8, 64, 32), (32, 500, 1, 8, 4, 128, 16),
+    (33, 500, 1, 8, 4, 128, 16), (64, 900, 2, 16, 4, 64, 64), (100, 1990, 1, 16, 4, 64, 128), (20, 300, 5, 8, 2, 128, 16)])
+def test_short_units_among_many(B, longest, q_len, Hq, Hkv, D, page):
+    # units that are not cut, several to a thread block or one, and lengths around the limit from which they are
+    kv_lens = np.random.default_rng(32).integers(0, longest + 1, B)
+    kv_lens[-1], kv_lens[0] = longest, longest // 2 if B > 1 else longest
+    check_attention(*problem([q_len] * B, kv_lens.tolist(), Hq, Hkv, D, page, 33))
+
+
 def test_cut_units_of_long_chunks():
     check_attention(*problem([300], [5000], 4, 2, 128, 64, 28))
     check_attention(*problem([64, 1, 20], [3000, 4000, 30], 16, 2, 64, 16, 29))
