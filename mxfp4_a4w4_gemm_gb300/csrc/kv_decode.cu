@@ -15,10 +15,10 @@
 // the copy brought, which is more than that memory passes in the time.
 //
 // What bounds it then are the instructions that decode, some 650 a step of 32
-// tokens and 8 rows at D = 128: 64 ragged requests of up to 8192 keys 71 us (4.0
-// TB/s, with launch, cut and joins; the steps alone run at 6.3 TB/s), 2 x 131000
-// keys x 16 rows 58 us (2.5 TB/s; 16 rows cost nearly twice 8, and 255 registers
-// leave 8 warps), one request of 1000 keys 9.5 us, most of it latency: launch,
+// tokens and 8 rows at D = 128: 64 ragged requests of up to 8192 keys 69 us (4.1
+// TB/s), 2 x 131000 keys x 16 rows 56 us (2.5 TB/s; a step of 16 rows has a fifth
+// more instructions than one of 8, but 255 registers leave 8 warps to hide each
+// other's latencies), one request of 1000 keys 8.7 us, most of it latency: launch,
 // lengths, page numbers and cells one after the other, then the joins.
 //
 // Keys and values are the M side, query rows the N side (8 per tile), so that
@@ -56,8 +56,8 @@ namespace a4w4 {
 namespace {
 
 constexpr int kStep = 32;                     // tokens of a step
-// Steps of a worker, at least (2: one request x 1000 keys 11.9 us instead of 9.4), and
-// workers of a CTA, at least (1: 100 keys 9.4 us instead of 8.9; alike from 1000 on).
+// Steps of a worker, at least (2: one request x 1000 keys 2.5 us more), and workers of
+// a CTA, at least (1: 100 keys, cut, 0.6 us more; alike from 1000 on).
 constexpr int kLeast = 1;
 constexpr int kFew = 4;
 // What a unit costs beside its steps, in steps: so many places of the line before its
@@ -93,7 +93,7 @@ struct DecCfg {
   static constexpr int SMEM = OFF_SHARE + WARPS * static_cast<int>(sizeof(KvShare));
   static constexpr int PART = ROWS * (D + 2);                    // floats of a stored part: O, then m and l
   static_assert(STAGE % 16 == 0 && OFF_KS % 16 == 0 && OFF_VS % 16 == 0 && OFF_O % 16 == 0, "alignment");
-  static_assert(2 * kMaxParts <= WARPS * PITCH && kMaxParts <= kTickets && PART % 4 == 0, "join");
+  static_assert(kMaxParts <= kTickets && PART % 4 == 0, "join");
   static_assert(ROWS * PITCH * 4 <= STAGES * STAGE, "a part fits in the warp's drained ring");
   static_assert(OFF_OPEN % 4 == 0 && OFF_SCAN % 4 == 0, "alignment");
   static_assert(OFF_BAR % 8 == 0 && SMEM <= 232448, "shared memory");
@@ -766,61 +766,46 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
   for (uint32_t left = static_cast<uint32_t>(*last_flag); left != 0; left &= left - 1) {
     const Open un = open[__ffs(left) - 1];
     const int c0 = un.v0 / per, np = un.v1 / per - c0 + 1, R = un.rows;
-    {
-      auto part = [&](int k) { return parts + (2 * (c0 + k) + (k == 0 ? 1 : 0)) * Cf::PART; };
-      // maxima and sums of the parts, all on their way at once; then a warp per row turns them into weights
-      float2* stats = reinterpret_cast<float2*>(smem + Cf::OFF_O);       // [row][part], the parts here are spent
-      for (int i = tid; i < R * np; i += Cf::THREADS) {
-        const int r = i / np, k = i - r * np;
-        stats[r * kMaxParts + k] = __ldcg(reinterpret_cast<const float2*>(part(k) + Cf::ROWS * D + 2 * r));
-      }
-      __syncthreads();
-      for (int r = warp; r < R; r += W) {
-        float mm = kNoMax;
-        for (int k = lane; k < np; k += 32) mm = fmaxf(mm, stats[r * kMaxParts + k].x);
+    auto part = [&](int k) { return parts + (2 * (c0 + k) + (k == 0 ? 1 : 0)) * Cf::PART; };
+    // 16 bytes of a row per thread, every thread with its own copy of the row's maximum and sum: one trip to memory
+    // for 12 parts (one request x 1000 keys 8.7 us; with a trip and a barrier for the statistics first, 9.6)
+    constexpr int AT = 12;
+    for (int it = tid; it < R * (D / 4); it += Cf::THREADS) {
+      const int r = it / (D / 4), d = it % (D / 4) * 4;
+      float mm = kNoMax, ll = 0.f;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k0 = 0; k0 < np; k0 += AT) {
+        float2 q[AT];
+        float4 v[AT];
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, s));
-        float ll = 0.f;
-        for (int k = lane; k < np; k += 32) {
-          const float2 q = stats[r * kMaxParts + k];
-          const float a = ex2(q.x - mm);
-          ll = fmaf(q.y, a, ll);
-          stats[r * kMaxParts + k].x = a;
+        for (int k = 0; k < AT; ++k) {
+          const float* src = part(min(k0 + k, np - 1));
+          q[k] = __ldcg(reinterpret_cast<const float2*>(src + Cf::ROWS * D + 2 * r));
+          v[k] = __ldcg(reinterpret_cast<const float4*>(src + r * D + d));
         }
+        float top = mm;
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) ll += __shfl_xor_sync(0xFFFFFFFFu, ll, s);
-        const float inv = ll == 0.f ? 0.f : 1.f / ll;
-        __syncwarp();
-        for (int k = lane; k < np; k += 32) stats[r * kMaxParts + k].x *= inv;
-        if (lane == 0 && p.lse != nullptr) {
-          const int qi = p.row_of(un.r0 + r);
-          p.lse[(static_cast<long long>(un.row0) + qi) * p.Hq + un.h * G + un.r0 + r - qi * G] =
-              ll == 0.f ? -INFINITY : fmaf(mm, 0.6931471805599453f, logf(ll));
+        for (int k = 0; k < AT; ++k) top = fmaxf(top, q[k].x);
+        const float f = ex2(mm - top);
+        mm = top;
+        ll *= f;
+        y.x *= f; y.y *= f; y.z *= f; y.w *= f;
+#pragma unroll
+        for (int k = 0; k < AT; ++k) {
+          const float a = k0 + k < np ? ex2(q[k].x - mm) : 0.f;
+          ll = fmaf(q[k].y, a, ll);
+          y.x = fmaf(v[k].x, a, y.x); y.y = fmaf(v[k].y, a, y.y); y.z = fmaf(v[k].z, a, y.z); y.w = fmaf(v[k].w, a, y.w);
         }
       }
-      __syncthreads();
-      // 16 bytes of a row per thread, 16 parts at a time
-      for (int it = tid; it < R * (D / 4); it += Cf::THREADS) {
-        const int r = it / (D / 4), d = it % (D / 4) * 4;
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k0 = 0; k0 < np; k0 += 16) {
-          float4 v[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            v[k] = __ldcg(reinterpret_cast<const float4*>(part(min(k0 + k, np - 1)) + r * D + d));
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float a = k0 + k < np ? stats[r * kMaxParts + k0 + k].x : 0.f;
-            y.x = fmaf(v[k].x, a, y.x); y.y = fmaf(v[k].y, a, y.y); y.z = fmaf(v[k].z, a, y.z); y.w = fmaf(v[k].w, a, y.w);
-          }
-        }
-        const int qi = p.row_of(un.r0 + r), hq = un.h * G + un.r0 + r - qi * G;
-        const long long row = static_cast<long long>(un.row0) + qi;
-        *reinterpret_cast<uint2*>(p.out + (row * p.Hq + hq) * D + d) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
-      }
-      if (tid == 0) static_cast<int*>(p.ws)[c0] = 0;
+      const float inv = ll == 0.f ? 0.f : 1.f / ll;
+      const int qi = p.row_of(un.r0 + r), hq = un.h * G + un.r0 + r - qi * G;
+      const long long row = static_cast<long long>(un.row0) + qi;
+      *reinterpret_cast<uint2*>(p.out + (row * p.Hq + hq) * D + d) =
+          make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+      if (d == 0 && p.lse != nullptr)
+        p.lse[row * p.Hq + hq] = ll == 0.f ? -INFINITY : fmaf(mm, 0.6931471805599453f, logf(ll));
     }
-    __syncthreads();                                             // the weights are free again
+    if (tid == 0) static_cast<int*>(p.ws)[c0] = 0;
   }
 }
 

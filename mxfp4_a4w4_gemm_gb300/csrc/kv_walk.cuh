@@ -112,17 +112,17 @@ __device__ __forceinline__ KvRequest shfl_request(const KvRequest& r, int lane) 
 // blockIdx.x * per + w, if there is one.  Every thread of the CTA calls it; with
 // up to 32 requests each warp finds out for itself, with more they sum together
 // (scratch: THREADS + 32 words of shared memory, in use until every warp has
-// returned).  Returns false if the CTA has nothing to do.  Without a barrier for few
-// requests one token's attention over 1000 keys took 9.4 us, with the sums of all
-// warps 10.0; 24 requests x 5 tokens 22.0 and 23.2.
+// returned).  Returns false if the CTA has nothing to do.  For few requests, without
+// and with the sums of all warps (a barrier): one token over 1000 keys 9.4 and 10.0
+// us, 24 requests x 5 tokens 22.0 and 23.2 (both faster since, by their joins).
 //
 // Short units (unit(r) places each, `cost` of them without work; WHOLE at most) go to
 // CTAs whole, those that begin in its equal stretch of the line, which its own warps
-// then cut: a join between CTAs takes 3 to 4 us, about as long as a CTA takes for 24
+// then cut: a join between CTAs takes some 3 us, about as long as a CTA takes for 21
 // places more than the others.  Whole and cut, one token, 8 heads of 128: 1 request
-// x 100 keys 6.6 and 9.1 us, 8 x 1000 10.1 and 12.9, 64 x 300 12.7 and 15.7, 256
-// ragged x 600 29.1 and 33.3; 64 x 2000 38.3 and 38.1; over the limits 1 x 1000 10.2
-// and 9.6, 1 x 2000 13.6 and 11.4.
+// x 100 keys 6.6 and 8.3 us, 8 x 300 7.4 and 8.9, 8 x 1000 10.1 and 11.1, 64 x 300
+// 12.9 and 13.9, 256 ragged x 600 29.2 and 31.8; over the limits 1 x 800 9.6 and 8.6,
+// 1 x 1000 10.2 and 8.7, 1 x 2000 13.6 and 9.9.
 template <int THREADS, int PER, int WHOLE, typename Places, typename Unit>
 __device__ __forceinline__ bool kv_locate(const KvAttentionArgs& p, Places places, Unit unit, uint32_t cost, uint32_t least,
                                           uint32_t few, uint32_t* scratch, KvShare& share, KvStart& start) {
@@ -193,7 +193,7 @@ __device__ __forceinline__ bool kv_locate(const KvAttentionArgs& p, Places place
     start.rest = f - lo;
   };
   if (total == 0) return false;
-  if (WHOLE > 0 && longest <= min(static_cast<uint32_t>(WHOLE), 24u + total / gridDim.x)) {
+  if (WHOLE > 0 && longest <= min(static_cast<uint32_t>(WHOLE), 21u + total / gridDim.x)) {
     KvShare even;
     even.cut(0, total, 0, gridDim.x);
     // the first unit that begins at place f or after it
