@@ -237,10 +237,10 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
     for (int s = 0; s < S; ++s) mbar_init(full(s), 1);
   fence_barrier_init();
   __syncthreads();                               // flags and list are set before anything is put in them
+  const int G = p.Hq / p.Hkv;
   griddep_wait();
   griddep_launch_dependents();
 
-  const int G = p.Hq / p.Hkv;
   KvShare share;
   KvStart start;
   auto unit = [&](const KvRequest& r) -> uint32_t { return max(1, (r.len + kStep - 1) / kStep) + kUnitCost; };

@@ -250,9 +250,17 @@ __device__ __forceinline__ uint4 mul_bf16x8(uint4 o, uint32_t f) {
 // 2^k as a float, k in [-126, 127]
 __device__ __forceinline__ float pow2i(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
 
-// sum over k = 0 .. n - 1 of floor((a k + b) / m) modulo 2^32; a n + b < 2^32, m > 0
-__device__ __forceinline__ uint32_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
-  uint32_t s = 0;
+// sum over k = 0 .. n - 1 of floor((a k + b) / M) modulo 2^32; a n + b < 2^32
+template <uint32_t M>
+__device__ __forceinline__ uint32_t floor_sum(uint32_t n, uint32_t a, uint32_t b) {
+  if (n == 0) return 0;
+  // the first round, whose divisor is a constant, apart: the others divide slowly
+  uint32_t s = (n & 1 ? (n - 1) / 2 * n : n / 2 * (n - 1)) * (a / M) + n * (b / M), m = a % M;
+  const uint32_t y0 = m * n + b % M;
+  if (y0 < M) return s;
+  n = y0 / M;
+  b = y0 % M;
+  a = M;
   while (n > 0) {
     const uint32_t qa = a / m, qb = b / m;
     s += (n & 1 ? (n - 1) / 2 * n : n / 2 * (n - 1)) * qa + n * qb;
@@ -288,7 +296,7 @@ struct Blocks {
     const int base = len - all;
     // the first blocks may see nothing: one empty step each
     const int none = base < 0 ? min(k, -base / tq) : 0;
-    return k * kUnitCost + none + floor_sum(k - none, kKeys, tq, static_cast<uint32_t>(base + (none + 1) * tq + kKeys - 1));
+    return k * kUnitCost + none + floor_sum<kKeys>(k - none, tq, static_cast<uint32_t>(base + (none + 1) * tq + kKeys - 1));
   }
   __device__ __forceinline__ uint32_t total() const { return n > 0 ? before(n - 1) + kUnitCost + steps(n - 1) : 0u; }
 };
@@ -368,10 +376,10 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
       atomicOr(p.status, kStatusTimeout);
     }
   }
+  const int G = p.Hq / p.Hkv, tq = kRows / G;
   griddep_wait();
   griddep_launch_dependents();
 
-  const int G = p.Hq / p.Hkv, tq = kRows / G;
   KvShare share;
   KvStart start;
   auto places = [&](const KvRequest& r) -> uint32_t { return Blocks(r, tq).total() * p.Hkv; };
@@ -381,23 +389,26 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
   const uint32_t cta = blockIdx.x;
   if (warp == 0) {
     const Blocks q(start.req, tq);
-    const uint32_t per = q.total();
+    const uint32_t per = start.places / p.Hkv;                   // q.total()
     const int h = start.rest / per;
     const uint32_t rest = start.rest - h * per;
     // the block that holds step `rest`: 32 candidates at a time
     int lo = 0, hi = q.n;                      // before(lo) <= rest, and before(hi) > rest or hi == n
+    uint32_t lo_at = 0;                        // before(lo)
     while (hi - lo > 1) {
       const int stride = (hi - lo + 31) / 32;
       const int c = lo + stride * lane;
-      const uint32_t in = __ballot_sync(0xFFFFFFFFu, c < hi && q.before(min(c, q.n - 1)) <= rest);
+      const uint32_t at = q.before(min(c, q.n - 1));
+      const uint32_t in = __ballot_sync(0xFFFFFFFFu, c < hi && at <= rest);
       const int top = 31 - __clz(in);          // lane 0 is always in
       lo += stride * top;
+      lo_at = __shfl_sync(0xFFFFFFFFu, at, top);
       hi = min(hi, lo + stride);
     }
     if (lane == 0) {
       start_at[0] = h;
       start_at[1] = lo;
-      start_at[2] = rest - q.before(lo);
+      start_at[2] = rest - lo_at;
       start_at[3] = start.b;
     }
   }
@@ -627,43 +638,49 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
           __threadfence();
         }
         named_bar_sync(1, 256);
-        if (*last_flag) {
+        if (*last_flag && active) {            // whole warps, the lanes beyond the rows go along
           const size_t head = share.first(c0) < u0 ? Cf::PART : 0;
-          auto part = [&](int k) { return parts + static_cast<size_t>(2 * (c0 + k)) * Cf::PART + (k == 0 ? head : 0); };
-          auto stat = [&](int k) { return __ldcg(reinterpret_cast<const float2*>(part(k) + kRows * D) + r); };
-          if (r < R) {
+          const int own = cta - c0, rr = min(r, R - 1);
+#pragma unroll 1
+          for (int a = 0; a < D / 64; ++a) {
             float mm = kNoMax, ll = 0.f;
-#pragma unroll 4
-            for (int k = 0; k < np; ++k) mm = fmaxf(mm, stat(k).x);
-#pragma unroll 4
-            for (int k = 0; k < np; ++k) {
-              const float2 q = stat(k);
-              ll = fmaf(q.y, ex2(q.x - mm), ll);
-            }
-            const float inv = ll == 0.f ? 0.f : 1.f / ll;
-#pragma unroll 1
-            for (int a = 0; a < D / 64; ++a) {
-              uint32_t y[64];
+            float y[64];
 #pragma unroll
-              for (int u = 0; u < 64; ++u) y[u] = 0u;
+            for (int u = 0; u < 64; ++u) y[u] = 0.f;
 #pragma unroll 1
-              for (int k = 0; k < np; ++k) {
-                const float4* src = reinterpret_cast<const float4*>(part(k)) + a * 16 * kRows + r;
-                float4 v[16];
-#pragma unroll
-                for (int u = 0; u < 16; ++u) v[u] = __ldcg(src + u * kRows);
-                const float f = ex2(stat(k).x - mm);
-                auto add = [&](uint32_t& to, float x) { to = __float_as_uint(fmaf(x, f, __uint_as_float(to))); };
+            for (int k = 0; k < np; ++k) {                        // in the parts' order, whoever joins
+              uint32_t x[64];
+              float2 q;
+              if (k == own) {                                     // still in TMEM
+                tmem_ld32(o_col + 64 * a, x);
+                tmem_ld32(o_col + 64 * a + 32, x + 32);
+                tmem_wait_ld<64>(x);
+                q = make_float2(fmaxf(m, kNoMax), l);
+              } else {
+                const float* src = parts + static_cast<size_t>(2 * (c0 + k)) * Cf::PART + (k == 0 ? head : 0);
+                q = __ldcg(reinterpret_cast<const float2*>(src + kRows * D) + rr);
 #pragma unroll
                 for (int u = 0; u < 16; ++u) {
-                  add(y[4 * u], v[u].x); add(y[4 * u + 1], v[u].y);
-                  add(y[4 * u + 2], v[u].z); add(y[4 * u + 3], v[u].w);
+                  const uint4 v = __ldcg(reinterpret_cast<const uint4*>(src) + (a * 16 + u) * kRows + rr);
+                  x[4 * u] = v.x; x[4 * u + 1] = v.y; x[4 * u + 2] = v.z; x[4 * u + 3] = v.w;
                 }
               }
-              write_out(a, y, inv);
+              const float top = fmaxf(mm, q.x), f = ex2(mm - top), e = ex2(q.x - top);
+              mm = top;
+              ll = fmaf(q.y, e, ll * f);
+#pragma unroll
+              for (int u = 0; u < 64; ++u) y[u] = fmaf(__uint_as_float(x[u]), e, y[u] * f);
             }
-            write_lse(mm, ll);
+            if (r < R) {
+              uint32_t x[64];
+#pragma unroll
+              for (int u = 0; u < 64; ++u) x[u] = __float_as_uint(y[u]);
+              write_out(a, x, ll == 0.f ? 0.f : 1.f / ll);
+              if (a == 0) write_lse(mm, ll);
+            }
           }
+        }
+        if (*last_flag) {
           if (tid == 0) *ticket = 0;
         }
         named_bar_sync(1, 256);                // the flag is free again

@@ -93,7 +93,7 @@ struct KvShare {
 
 // Where a worker's run starts: request b, `rest` places after its first.
 struct KvStart {
-  uint32_t b, rest;
+  uint32_t b, rest, places; // places: all of the request's
   KvRequest req;            // request b's lengths
 };
 
@@ -182,10 +182,11 @@ __device__ __forceinline__ bool kv_locate(const KvAttentionArgs& p, Places place
     int b = (base + li) * per;
     if (small) {
       start.req = shfl_request(mine, li);
+      start.places = __shfl_sync(0xFFFFFFFFu, sum, li);
     } else {
       start.req = kv_request(p, b);
-      for (uint32_t n = places(start.req); f >= lo + n; n = places(start.req)) {
-        lo += n;
+      for (start.places = places(start.req); f >= lo + start.places; start.places = places(start.req)) {
+        lo += start.places;
         start.req = kv_request(p, ++b);
       }
     }
