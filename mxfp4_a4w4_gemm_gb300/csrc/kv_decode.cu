@@ -749,16 +749,14 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
   if (!outside) return;
 
   // ---- units that reach into other CTAs: the last to arrive joins ----
-  __syncthreads();                                               // gathers the stores behind the fence below
+  __syncthreads();
   if (warp == 0) {                                               // a lane per unit draws its ticket
     const bool mine = (outside >> lane & 1u) != 0;
     bool last = false;
     if (mine) {
-      __threadfence();
       const int c0 = open[lane].v0 / per, np = open[lane].v1 / per - c0 + 1;
-      last = atomicAdd(static_cast<int*>(p.ws) + c0, 1) == np - 1;
+      last = draw_ticket(static_cast<int*>(p.ws) + c0) == np - 1;
     }
-    if (mine) __threadfence();
     const uint32_t lasts = __ballot_sync(0xFFFFFFFFu, last);
     if (lane == 0) *last_flag = static_cast<int>(lasts);
   }

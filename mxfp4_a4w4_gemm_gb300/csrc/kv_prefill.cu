@@ -632,11 +632,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
         const int c0 = share.holder(u0), np = share.holder(u0 + w.n - 1) - c0 + 1;
         named_bar_sync(1, 256);
         int* ticket = static_cast<int*>(p.ws) + c0;
-        if (tid == 0) {                        // the barrier has gathered the threads' stores behind this fence
-          __threadfence();
-          *last_flag = atomicAdd(ticket, 1) == np - 1;
-          __threadfence();
-        }
+        if (tid == 0) *last_flag = draw_ticket(ticket) == np - 1;
         named_bar_sync(1, 256);
         if (*last_flag && active) {            // whole warps, the lanes beyond the rows go along
           const size_t head = share.first(c0) < u0 ? Cf::PART : 0;

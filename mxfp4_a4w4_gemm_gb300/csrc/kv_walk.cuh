@@ -22,6 +22,15 @@ namespace a4w4 {
 // counter back to zero.
 constexpr int kTickets = 4096;
 
+// Draws a ticket: what the CTA's threads stored before the barrier before this is
+// visible to whoever draws later, and what earlier drawers stored is to this CTA
+// after its next barrier.
+__device__ __forceinline__ int draw_ticket(int* at) {
+  int old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(at) : "memory");
+  return old;
+}
+
 // mbar_wait for limits of any size: try_wait may suspend the thread for longer than
 // these kernels' waits take, so below 100 us the barrier is only tested.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
