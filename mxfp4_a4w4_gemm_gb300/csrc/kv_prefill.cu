@@ -687,7 +687,9 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
     regs_down<Cf::REGS_DECODE>();
     const int dw = warp - 8;                   // chunk of the step
     uint32_t it = 0;                           // steps so far
-    bool ok = true;
+    // the first cells: a wait that a limit shorter than the hardware's suspension of a waiting warp ends too (in the
+    // loops this form of waiting costs 3%)
+    bool ok = w.left <= 0 || __all_sync(0xFFFFFFFFu, kv_wait(raw_full(0), 0, abort_flag, p.wait_ns, p.status));
     for (; w.left > 0 && ok; w.next(p)) {
       const int n = w.steps();
       for (int i = 0; i < n; ++i, ++it) {
