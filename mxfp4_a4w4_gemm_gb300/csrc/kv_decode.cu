@@ -58,7 +58,7 @@ namespace {
 constexpr int kStep = 32;                     // tokens of a step
 // Steps of a worker, at least (2: one request x 1000 keys 2.5 us more), and workers of
 // a CTA, at least (1: 100 keys, cut, 0.6 us more; alike from 1000 on).
-constexpr int kLeast = 1;
+constexpr uint32_t kLeast = 1;
 constexpr int kFew = 4;
 // What a unit costs beside its steps, in steps: so many places of the line before its
 // first step hold no work.  0, 1, 2, 4: 64 ragged requests x 8192 keys 83, 75, 71, 72
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
   auto places = [&](const KvRequest& r) -> uint32_t {
     return r.rows > 0 ? unit(r) * p.Hkv * ((r.rows * G + Cf::ROWS - 1) / Cf::ROWS) : 0;
   };
-  if (!kv_locate<Cf::THREADS, W, kWhole>(p, places, unit, kUnitCost, kLeast, kFew,
+  if (!kv_locate<Cf::THREADS, W, kWhole>(p, places, unit, kUnitCost, [](uint32_t) { return kLeast; }, kFew,
                                          reinterpret_cast<uint32_t*>(smem + Cf::OFF_SCAN), share, start))
     return;
   const uint32_t per = share.per, me = blockIdx.x * per + warp;

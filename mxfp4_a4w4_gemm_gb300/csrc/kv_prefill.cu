@@ -26,12 +26,12 @@
 // has grown by more than 2^8, P staying below 2^8 meanwhile.
 //
 // A step does 512 R D flops for R rows and brings 136 D bytes: operations are the
-// floor.  4096 tokens x 16384 keys, 32 heads over 8 of 128: 695 us, 1384 TFLOP/s
-// (1911 measured for a plain BF16 product).  A step takes 1.84 us, of which the
-// products 57%; the rest is the chain scores -> softmax -> P of either tile, slowed by
+// floor.  4096 tokens x 16384 keys, 32 heads over 8 of 128: 679 us, 1417 TFLOP/s
+// (1911 measured for a plain BF16 product).  A step takes 1.8 us, of which the
+// products 58%; the rest is the chain scores -> softmax -> P of either tile, slowed by
 // the decoders, with which it shares the issue slots (64% of them taken).  Short
 // prompts pay for units beside their steps: 12 ragged requests of up to 700 tokens x
-// 1500 keys 34.6 us, 128 tokens x 128 keys 14.
+// 1500 keys 32.3 us, 128 tokens x 128 keys 13.4.
 //
 //   warps 0-3, 4-7   softmax of tile 0, 1 (a thread per row): stage Q, scores ->
 //                    probabilities, output
@@ -53,7 +53,11 @@ constexpr int kRows = 256;                    // rows of a unit
 // Steps of a worker, at least.  1, 2, 4: 128 tokens x 1024 keys 39.7, 32.1, 32.9 us
 // (parts were joined more slowly then), 128 x 128 keys 13.6, 13.9, 22.4, 8 ragged x 100
 // tokens x 1000 keys now 21.9 and 33.8 with 2 and 4.
-constexpr int kLeastSteps = 2;
+constexpr uint32_t kLeastSteps = 2;
+// What a part adds to a join, in steps (128 KB through one SM).  A unit of n steps in runs of s takes s + 0.7 n / s
+// steps, so runs have sqrt(0.7 n) steps at least.  0, 0.4, 0.7, 1.2: 64 tokens x 8192 keys 49.9, 44.7, 39.6, 41.5 us;
+// where there is work for more than that (128 x 8192, 50 x 50000) it makes no difference.
+constexpr float kJoinCost = 0.7f;
 // What a unit costs beside its steps (queries, output), in steps: so many places of
 // the line before its first step hold no work.  0 and 2: 12 ragged prompts x 700
 // tokens 46.8 and 39.0 us; 2 and 3: 38.4 and 39.1, 4 x 512 x 512 51.3 and 54.6.
@@ -383,7 +387,9 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
   KvShare share;
   KvStart start;
   auto places = [&](const KvRequest& r) -> uint32_t { return Blocks(r, tq).total() * p.Hkv; };
-  if (!kv_locate<Cf::THREADS, 1, 0>(p, places, places, 0, kLeastSteps, 1, reinterpret_cast<uint32_t*>(smem + Cf::OFF_Q),
+  auto longest_unit = [&](const KvRequest& r) -> uint32_t { const Blocks q(r, tq); return q.steps(q.n - 1); };
+  auto least = [](uint32_t steps) { return max(kLeastSteps, static_cast<uint32_t>(sqrtf(kJoinCost * steps))); };
+  if (!kv_locate<Cf::THREADS, 1, 0>(p, places, longest_unit, 0, least, 1, reinterpret_cast<uint32_t*>(smem + Cf::OFF_Q),
                                     share, start))
     return;
   const uint32_t cta = blockIdx.x;

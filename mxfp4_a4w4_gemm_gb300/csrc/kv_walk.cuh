@@ -116,8 +116,8 @@ __device__ __forceinline__ KvRequest shfl_request(const KvRequest& r, int lane) 
 }
 
 // Cuts the line (places(r) places for the units of a request with lengths r;
-// fewer than 2^31 in all) for at most gridDim.x * PER workers of at least `least`
-// places, at least `few` of them to a CTA; warp w learns the start of worker
+// fewer than 2^31 in all) for at most gridDim.x * PER workers of at least
+// least(the longest unit's) places, at least `few` of them to a CTA; warp w learns the start of worker
 // blockIdx.x * per + w, if there is one.  Every thread of the CTA calls it; with
 // up to 32 requests each warp finds out for itself, with more they sum together
 // (scratch: THREADS + 32 words of shared memory, in use until every warp has
@@ -132,8 +132,8 @@ __device__ __forceinline__ KvRequest shfl_request(const KvRequest& r, int lane) 
 // x 100 keys 6.6 and 8.3 us, 8 x 300 7.4 and 8.9, 8 x 1000 10.1 and 11.1, 64 x 300
 // 12.9 and 13.9, 256 ragged x 600 29.2 and 31.8; over the limits 1 x 800 9.6 and 8.6,
 // 1 x 1000 10.2 and 8.7, 1 x 2000 13.6 and 9.9.
-template <int THREADS, int PER, int WHOLE, typename Places, typename Unit>
-__device__ __forceinline__ bool kv_locate(const KvAttentionArgs& p, Places places, Unit unit, uint32_t cost, uint32_t least,
+template <int THREADS, int PER, int WHOLE, typename Places, typename Unit, typename Least>
+__device__ __forceinline__ bool kv_locate(const KvAttentionArgs& p, Places places, Unit unit, uint32_t cost, Least least,
                                           uint32_t few, uint32_t* scratch, KvShare& share, KvStart& start) {
   constexpr int W = THREADS / 32;
   static_assert(W <= 32 && PER <= W, "a search per warp");
@@ -148,7 +148,7 @@ __device__ __forceinline__ bool kv_locate(const KvAttentionArgs& p, Places place
     mine = kv_request(p, b);
     const uint32_t n = places(mine);
     sum += n;
-    if (WHOLE > 0 && n > 0) longest = max(longest, unit(mine));
+    if (n > 0) longest = max(longest, unit(mine));
   }
   uint32_t inc = sum;                                            // inclusive, within the warp
 #pragma unroll
@@ -158,14 +158,14 @@ __device__ __forceinline__ bool kv_locate(const KvAttentionArgs& p, Places place
   }
   uint32_t wsum = 0, total;
   if (small) {
-    if (WHOLE > 0) longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+    longest = __reduce_max_sync(0xFFFFFFFFu, longest);
     total = __shfl_sync(0xFFFFFFFFu, inc, 31);
   } else {
-    if (WHOLE > 0) longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+    longest = __reduce_max_sync(0xFFFFFFFFu, longest);
     scratch[tid] = inc;
     if (lane == 0) scratch[THREADS + warp] = longest;
     __syncthreads();
-    if (WHOLE > 0) longest = __reduce_max_sync(0xFFFFFFFFu, lane < W ? scratch[THREADS + lane] : 0u);
+    longest = __reduce_max_sync(0xFFFFFFFFu, lane < W ? scratch[THREADS + lane] : 0u);
     wsum = lane < W ? scratch[lane * 32 + 31] : 0u;              // the warps' sums, scanned by every warp
 #pragma unroll
     for (int o = 1; o < W; o <<= 1) {
@@ -219,7 +219,8 @@ __device__ __forceinline__ bool kv_locate(const KvAttentionArgs& p, Places place
     share.cut(from + cost, to - from - cost, blockIdx.x * PER, min(static_cast<uint32_t>(PER), to - from - cost));
     share.per = PER;
   } else {
-    const uint32_t workers = min(static_cast<uint32_t>(gridDim.x) * PER, (total + least - 1) / least);
+    const uint32_t fewest = least(longest);
+    const uint32_t workers = min(static_cast<uint32_t>(gridDim.x) * PER, (total + fewest - 1) / fewest);
     share.cut(0, total, 0, workers);
     share.per = max(few, (workers + gridDim.x - 1) / gridDim.x);
   }
