@@ -540,6 +540,16 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
         for (int u = 1; u < 4; ++u) mn = fminf(mn, fminf(x[0][nt][u], x[1][nt][u]));
         low |= mn < -14.f;
       }
+      if (tok0 + kStep > all_seen) {                           // masked keys are none of these: their zeros are exact
+        asm volatile("" ::: "memory");
+        low = vlow;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) low |= x[c][nt][u] < -14.f && x[c][nt][u] > -INFINITY;
+      }
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll

@@ -227,8 +227,9 @@ def call_attention(q, cu, lens, table, cache, pages, page, Hq, Hkv, D, scale, ma
     return out, l
 
 
-def check_attention(q_bits, q_lens, kv_lens, Hq, Hkv, D, page, table, cache, pages, rows, scale, max_q=None):
-    """One call against the oracle; rows[b] = (keys, values) float64 [len, Hkv, D] of request b."""
+def check_attention(q_bits, q_lens, kv_lens, Hq, Hkv, D, page, table, cache, pages, rows, scale, max_q=None, p_extra=0.0):
+    """One call against the oracle; rows[b] = (keys, values) float64 [len, Hkv, D] of request b; p_extra: what a
+    probability's rounding may be off by beyond the bound's 2^-9, relatively."""
     cu = np.concatenate([[0], np.cumsum(q_lens)])
     out, lse = call_attention(dev_bits(q_bits), i32(cu), i32(kv_lens), i32(table), cache, pages, page, Hq, Hkv, D, scale,
                               max_q or max(1, max(q_lens)))
@@ -241,6 +242,7 @@ def check_attention(q_bits, q_lens, kv_lens, Hq, Hkv, D, page, table, cache, pag
         sl = slice(cu[b], cu[b + 1])
         o, l, spread, reach = kv.attention(q[sl], rows[b][0], rows[b][1], float(np.float32(scale)))
         bo, bl = kv.attention_bounds(o, l, spread, reach)
+        bo = bo + p_extra * spread
         empty = np.isneginf(l)
         assert np.array_equal(np.isneginf(gl[sl]), empty), b
         assert np.all(got[sl][empty] == 0)
@@ -316,6 +318,21 @@ def test_prompt_chunks(q_lens, kv_lens, Hq, Hkv, D, page):
                                             (3, 100, 1, 64), (1, 256, 1, 64), (2, 255, 1, 128), (17, 3, 1, 128), (16, 3, 1, 64)])
 def test_row_counts_around_the_kernels_limits(q_len, Hq, Hkv, D):
     check_attention(*problem([q_len, q_len], [333, q_len - 1], Hq, Hkv, D, 32, 24))
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,Hq,Hkv,D,page", [
+    ([128], [128], 1, 1, 128, 16), ([49], [700], 1, 1, 64, 32), ([60, 7, 0, 33], [200, 0, 90, 1100], 8, 2, 128, 64),
+    ([7, 7], [333, 6], 7, 1, 128, 32), ([1, 1], [333, 0], 100, 1, 128, 32), ([30, 17, 80], [29, 1000, 80], 12, 4, 64, 128),
+    ([240], [1025], 1, 1, 64, 64)])
+def test_little_work_on_wide_tables(q_lens, kv_lens, Hq, Hkv, D, page):
+    # the table allows for more work than there is, so the kernel for larger calls takes it; its probabilities have
+    # BF16's 8 bits there, rounded by up to 2^-8
+    prob = list(problem(q_lens, kv_lens, Hq, Hkv, D, page, 34))
+    check_attention(*prob)
+    table = np.zeros((len(q_lens), 131072 // page), np.int32)
+    table[:, :prob[7].shape[1]] = prob[7]
+    prob[7] = table
+    check_attention(*prob, p_extra=2.0 ** -9)
 
 
 def test_many_short_requests():
