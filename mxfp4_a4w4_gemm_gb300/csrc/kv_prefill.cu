@@ -88,7 +88,7 @@ struct PreCfg {
   // raw full, empty x 2; K full, empty x 2; V full, empty x 2; Q full, S full, P half, P full, O full per tile; drain
   static constexpr int NBAR = 12 + 10 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int SMEM = OFF_MISC + 56;
+  static constexpr int SMEM = OFF_MISC + 64 + 48;
   static constexpr int SCOL = 0, OCOL = 256;                     // TMEM columns: S of the tiles, then O
   static constexpr int TMEM_COLS = 512;
   static constexpr int PART = kRows * (D + 2);                   // floats of a stored part: O, then m and l
@@ -354,7 +354,8 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cf::OFF_MISC + 8);
   volatile int* never = abort_flag + 1;
   volatile int* last_flag = abort_flag + 2;
-  int* start_at = reinterpret_cast<int*>(smem + Cf::OFF_MISC + 24);     // head, block, place, request
+  PreWalk* start_at = reinterpret_cast<PreWalk*>(smem + Cf::OFF_MISC + 64);
+  static_assert(sizeof(PreWalk) == 48 && Cf::SMEM <= 232448, "shared memory");
   // largest key scale of a step; a slot is used again four steps later, when its readers are past the step after
   int* key_ref = reinterpret_cast<int*>(smem + Cf::OFF_MISC + 40);
   if (tid == 0) {
@@ -412,10 +413,16 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
       hi = min(hi, lo + stride);
     }
     if (lane == 0) {
-      start_at[0] = h;
-      start_at[1] = lo;
-      start_at[2] = rest - lo_at;
-      start_at[3] = start.b;
+      const int place = rest - lo_at;
+      PreWalk w;
+      w.b = start.b;
+      w.q = q;
+      w.h = h;
+      w.k = lo;
+      w.n = q.steps(lo);
+      w.t = max(0, place - kUnitCost);
+      w.left = static_cast<int>(share.first(cta + 1) - share.first(cta)) - max(0, kUnitCost - place);
+      *start_at = w;
     }
   }
   if (warp == 16) {
@@ -425,14 +432,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  PreWalk w;
-  w.b = start_at[3];
-  w.q = Blocks(kv_request(p, w.b), tq);
-  w.h = start_at[0];
-  w.k = start_at[1];
-  w.n = w.q.steps(w.k);
-  w.t = max(0, start_at[2] - kUnitCost);
-  w.left = static_cast<int>(share.first(cta + 1) - share.first(cta)) - max(0, kUnitCost - start_at[2]);
+  PreWalk w = *start_at;
   const unsigned long long drain_ns = p.wait_ns > 100000000ull ? p.wait_ns : 100000000ull;
   auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, p.wait_ns, p.status); };
 
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
     auto stage_queries = [&](const PreWalk& u) {
       const int R = u.rows(G), first_tok = u.k * tq;
       if (tile * 128 >= R) return;
-      constexpr int C = D / 8, AT = 32 / C, BATCH = 8;
+      constexpr int C = D / 8, AT = 32 / C, BATCH = 32 / AT;
       const int c = lane % C;
 #pragma unroll 1
       for (int j0 = 0; j0 < 32 / AT; j0 += BATCH) {
