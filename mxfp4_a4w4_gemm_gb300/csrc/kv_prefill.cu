@@ -163,6 +163,12 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ void st_global_v8(void* at, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
+                                             uint32_t g, uint32_t h) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               :: "l"(at), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h) : "memory");
+}
+
 // D (TMEM) (+)= A B, descriptors as their two words.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
                                        uint32_t idesc, uint32_t accumulate) {
@@ -445,6 +451,9 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
     uint32_t it = 0;                           // steps so far
     float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + kTickets * 4);
     uint32_t s_phase = 0, o_phase = 0;
+    // output in whole sectors, with half the stores: 128 tokens x 128 keys 12.9 -> 12.3 us, 16 x 64 x 512 37.5 -> 36.7;
+    // at D = 64 12 ragged prompts take 33.1 instead of 32.4
+    const bool wide_out = D == 128 && (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
     int q_pow = 0;                             // the power of two of this thread's row of Q
     // ---- the warp's 32 rows of a unit's Q tile: C lanes to a row, 32 / C rows at a time; a piece ahead of the rest,
     // while the last products run ----
@@ -600,10 +609,16 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
           return by * __uint_as_float(x[n % 16 / 2 * 8 + (n / 16 == 0 ? 0 : n / 16 == 2 ? 1 : n / 16 == 1 ? 4 : 5) + 2 * (n % 2)]);
         };
         uint16_t* dst = p.out + (row * p.Hq + hq) * D + 64 * a;
+        auto two = [&](int n) { return pack_bf16(at(n), at(n + 1)); };
 #pragma unroll
-        for (int n = 0; n < 64; n += 8)
-          *reinterpret_cast<uint4*>(dst + n) = make_uint4(pack_bf16(at(n), at(n + 1)), pack_bf16(at(n + 2), at(n + 3)),
-                                                          pack_bf16(at(n + 4), at(n + 5)), pack_bf16(at(n + 6), at(n + 7)));
+        for (int n = 0; n < 64; n += 16) {
+          if (wide_out) {
+            st_global_v8(dst + n, two(n), two(n + 2), two(n + 4), two(n + 6), two(n + 8), two(n + 10), two(n + 12), two(n + 14));
+          } else {
+            *reinterpret_cast<uint4*>(dst + n) = make_uint4(two(n), two(n + 2), two(n + 4), two(n + 6));
+            *reinterpret_cast<uint4*>(dst + n + 8) = make_uint4(two(n + 8), two(n + 10), two(n + 12), two(n + 14));
+          }
+        }
       };
       auto write_lse = [&](float mm, float ll) {
         if (p.lse != nullptr) p.lse[row * p.Hq + hq] = ll == 0.f ? -INFINITY : fmaf(mm, 0.6931471805599453f, logf(ll));

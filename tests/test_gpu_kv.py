@@ -401,6 +401,23 @@ def test_strided_queries_no_lse_own_stream_and_determinism():
         assert torch.equal(out.view(torch.int16), want.view(torch.int16))
 
 
+@pytest.mark.parametrize("q_lens,D", [([300, 9], 128), ([300, 9], 64), ([2, 1], 128)])
+def test_output_on_16_bytes(q_lens, D):
+    # rows that begin in the middle of a 32-byte sector
+    Hq, Hkv, page = 4, 2, 32
+    prob = problem(q_lens, [411, 200], Hq, Hkv, D, page, 35)
+    q_bits, _, kv_lens, _, _, _, _, table, cache, pages, _, scale = prob
+    want, _ = check_attention(*prob)
+    buf = torch.full((want.numel() + 16,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    out = buf[8:8 + want.numel()].view(want.shape)
+    assert out.data_ptr() % 32 == 16
+    cu = i32(np.concatenate([[0], np.cumsum(q_lens)]))
+    call_attention(dev_bits(q_bits), cu, i32(kv_lens), i32(table), cache, pages, page, Hq, Hkv, D, scale, max(q_lens), out=out)
+    ok()
+    assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+    assert torch.isnan(buf[:8]).all() and torch.isnan(buf[8 + want.numel():]).all()
+
+
 def test_one_workspace_serves_calls_of_other_sizes():
     probs = [problem([1] * 9, [2000 - 100 * b for b in range(9)], 16, 2, 128, 64, 18), problem([30], [900], 8, 1, 64, 16, 19),
              problem([1], [5000], 4, 1, 64, 16, 20)]
