@@ -31,7 +31,7 @@
 // products 58%; the rest is the chain scores -> softmax -> P of either tile, slowed by
 // the decoders, with which it shares the issue slots (64% of them taken).  Short
 // prompts pay for units beside their steps: 12 ragged requests of up to 700 tokens x
-// 1500 keys 32.3 us, 128 tokens x 128 keys 13.4.
+// 1500 keys 32.3 us, 128 tokens x 128 keys 12.4.
 //
 //   warps 0-3, 4-7   softmax of tile 0, 1 (a thread per row): stage Q, scores ->
 //                    probabilities, output
