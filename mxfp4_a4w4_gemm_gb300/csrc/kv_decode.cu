@@ -61,8 +61,8 @@ constexpr int kStep = 32;                     // tokens of a step
 constexpr uint32_t kLeast = 1;
 constexpr int kFew = 4;
 // What a unit costs beside its steps, in steps: so many places of the line before its
-// first step hold no work.  0, 1, 2, 4: 64 ragged requests x 8192 keys 83, 75, 71, 72
-// us; 64 x 300 keys, cut, 1, 2, 4: 17.9, 15.7, 16.7.
+// first step hold no work.  1, 2, 3: 64 ragged requests x 8192 keys 71.9, 69.4, 70.4
+// us (0: 12 us more), 24 ragged x 5 tokens x 3001 20.6, 20.0, 20.4.
 constexpr int kUnitCost = 2;
 constexpr int kWhole = 64;                    // places of the longest unit that a CTA may take whole
 constexpr int kMaxParts = 256;                // CTAs of a launch, and so parts of a cut unit

@@ -50,17 +50,18 @@ namespace {
 
 constexpr int kKeys = 128;                    // keys of a step
 constexpr int kRows = 256;                    // rows of a unit
-// Steps of a worker, at least.  1, 2, 4: 128 tokens x 1024 keys 39.7, 32.1, 32.9 us
-// (parts were joined more slowly then), 128 x 128 keys 13.6, 13.9, 22.4, 8 ragged x 100
-// tokens x 1000 keys now 21.9 and 33.8 with 2 and 4.
+// Steps of a worker, at least.  1, 2, 4: 128 tokens x 1024 keys 39.7, 32.1, 32.9 us,
+// 128 x 128 keys 13.6, 13.9, 22.4; 2 and 4: 8 ragged x 100 x 1000 21.9 and 33.8 (all
+// shorter by now: parts are joined faster).
 constexpr uint32_t kLeastSteps = 2;
 // What a part adds to a join, in steps (128 KB through one SM).  A unit of n steps in runs of s takes s + 0.7 n / s
 // steps, so runs have sqrt(0.7 n) steps at least.  0, 0.4, 0.7, 1.2: 64 tokens x 8192 keys 49.9, 44.7, 39.6, 41.5 us;
 // where there is work for more than that (128 x 8192, 50 x 50000) it makes no difference.
 constexpr float kJoinCost = 0.7f;
 // What a unit costs beside its steps (queries, output), in steps: so many places of
-// the line before its first step hold no work.  0 and 2: 12 ragged prompts x 700
-// tokens 46.8 and 39.0 us; 2 and 3: 38.4 and 39.1, 4 x 512 x 512 51.3 and 54.6.
+// the line before its first step hold no work.  1, 2, 3: 12 ragged prompts x 700
+// tokens 35.6, 32.3, 32.9 us, 4 x 512 x 512 42.3, 39.4, 41.7, 3 ragged x 3205 47.0,
+// 39.0, 39.7 (0, with slower joins: 12 ragged prompts 46.8 where 2 took 39.0).
 constexpr int kUnitCost = 2;
 constexpr int kMaxCtas = 512;
 // Keys of a table up to which P has two terms.  With one term and with two: 128 tokens
