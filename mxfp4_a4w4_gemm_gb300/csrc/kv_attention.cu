@@ -8,9 +8,9 @@ namespace {
 // Rows per key/value head up to which the decode kernel runs.  It goes over the keys
 // once per 8 or 16 rows, the tcgen05 kernel once per 256 at the price of a whole
 // unit.  4 requests x 16384 keys x 8 heads, rows: decode and prompt kernel, D = 128:
-// 16: 36 and 69 us, 32: 56 and 69, 48: 78 and 71, 64: 100 and 71; D = 64: 32: 38 and
-// 56, 48: 51 and 56, 64: 64 and 55; 16 x 1000 keys, D = 128: 48: 34 and 35, 64: 40
-// and 36.
+// 16: 34 and 72 us, 32: 55 and 71, 48: 76 and 72, 64: 100 and 72; D = 64: 32: 35 and
+// 54, 48: 48 and 55, 64: 61 and 53; 16 x 1000 keys, D = 128: 48: 29 and 33, 64: 36
+// and 34.
 constexpr int kFewRows = 48;
 bool few_rows(int max_q, int group) { return max_q <= kFewRows / group; }
 

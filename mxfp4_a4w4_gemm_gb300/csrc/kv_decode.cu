@@ -842,8 +842,9 @@ int launch_one(const KvAttentionArgs& p, int grid, cudaStream_t st) {
 
 int launch_kv_decode(const KvAttentionArgs& p, int D, cudaStream_t st, int sms) {
   const int rows = p.max_q * (p.Hq / p.Hkv);
-  // 16 rows at a time, but an odd number of 8-row blocks would waste half of one (a step costs 1.9 times as much:
-  // 24 requests x 20 rows 28 us in blocks of 8, 33 us in blocks of 16; 2 x 131000 keys x 16 rows 63 and 61 us)
+  // 16 rows at a time, but an odd number of 8-row blocks would waste half of one.  In blocks of 8 and of 16: 24 ragged
+  // requests x 20 rows 20.0 and 21.6 us (D = 64), 4 x 16384 keys x 24 rows 53.1 and 52.3 (D = 128), 2 x 131000 keys x
+  // 16 rows 59.2 and 55.5 (D = 128), 40.9 and 34.5 (D = 64)
   const bool two = (rows + 7) / 8 % 2 == 0;
   // as many CTAs as there can be work for, one per SM at most; places of the line are counted in 32 bits
   const double units = static_cast<double>(p.B) * p.Hkv * ((rows + (two ? 15 : 7)) / (two ? 16 : 8));
