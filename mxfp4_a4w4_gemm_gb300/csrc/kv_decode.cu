@@ -290,9 +290,9 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
       pi = 0;
     }
     if ((pi & 31) == 0) {
-      const int tok = ptok + lane * kStep;
-      page0 = tok < pw.len ? kv_page(p, pw.b, tok >> lg) : 0;
-      if (lg == 4) page1 = tok + 16 < pw.len ? kv_page(p, pw.b, (tok + 16) >> 4) : 0;
+      const int ahead = lane * kStep, rest = pw.len - ptok;    // compared like this, since ptok + ahead may pass 2^31
+      page0 = ahead < rest ? kv_page(p, pw.b, (ptok + ahead) >> lg) : 0;
+      if (lg == 4) page1 = ahead + 16 < rest ? kv_page(p, pw.b, (ptok + ahead + 16) >> 4) : 0;
     }
     const int id0 = __shfl_sync(0xFFFFFFFFu, page0, pi & 31);
     const int id1 = lg == 4 ? __shfl_sync(0xFFFFFFFFu, page1, pi & 31) : 0;

@@ -1,0 +1,42 @@
+"""The cache's calls at the largest arguments that they accept, and just beyond what they once took."""
+
+import numpy as np
+import pytest
+import torch
+
+import mxfp4_a4w4_gemm_gb300 as a4w4
+from oracle import kv
+from test_gpu_kv import call_attention, i32, ok
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from mxfp4_a4w4_gemm_gb300 import build
+    build.build()
+    a4w4.lib()
+
+
+def ones_cache(pages, page, Hkv, D):
+    """Keys of zeros and values of ones in every cell."""
+    z = np.zeros((page, Hkv, D), np.uint8)
+    e = np.full((page, Hkv, D // 32), 127, np.uint8)
+    return torch.from_numpy(kv.cache_from_rows(z, e, z + 2, e, page)).repeat(pages).cuda()
+
+
+@pytest.mark.parametrize("max_q", [1, 256])                    # the kernel for few rows, and the one for many
+@pytest.mark.parametrize("page,short", [(128, 0), (128, 700), (16, 0), (16, 345)])
+def test_contexts_that_end_just_below_2_to_31(page, short, max_q):
+    """Positions near the end of a table of 2^31 - 256 tokens (its pages repeat): lookups of whole runs of steps stay
+    in the request's row of the table."""
+    D, pages = 64, 1024
+    width = (2 ** 31 - 256) // page
+    lens = [width * page - short, 5]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    table = torch.randint(0, pages, (2, width), generator=g, device="cuda", dtype=torch.int32)
+    q = torch.randn(2, 1, D, generator=g, device="cuda").bfloat16()
+    out, lse = call_attention(q, i32([0, 1, 2]), i32(lens), table, ones_cache(pages, page, 1, D), pages, page, 1, 1, D, 0.125, max_q)
+    ok()
+    assert (out == 1).all()
+    assert np.allclose(lse.cpu().numpy()[:, 0], np.log(np.array(lens, np.float64)), rtol=2.0 ** -18, atol=0)
