@@ -135,7 +135,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs p)
     p.free_ring[(static_cast<long long>(head) + count + i) % p.ring_size] =
         p.block_table[static_cast<long long>(b) * p.max_pages + i - s_back[b]];
   }
-  for (int i = first; i < p.max_tokens; i += step) {
+  for (uint32_t u = first; u < static_cast<uint32_t>(p.max_tokens); u += step) {   // the last stride may pass 2^31
+    const int i = static_cast<int>(u);
     int slot = -1, pos = 0;
     if (i < T) {
       const int b = run_of(s_tok, B, i);

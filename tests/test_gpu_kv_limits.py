@@ -40,3 +40,21 @@ def test_contexts_that_end_just_below_2_to_31(page, short, max_q):
     ok()
     assert (out == 1).all()
     assert np.allclose(lse.cpu().numpy()[:, 0], np.log(np.array(lens, np.float64)), rtol=2.0 ** -18, atol=0)
+
+
+def test_a_plan_for_2_to_31_tokens():
+    """max_tokens at its largest: the loop over the tokens ends, and every entry beyond the tokens is padding."""
+    most, page = 2 ** 31 - 1, 16
+    past, new = [30, 0, 7], [20, 1, -1]
+    table = np.arange(12, dtype=np.int32).reshape(3, 4)
+    ring = np.arange(20, 36, dtype=np.int32)
+    want = kv.plan(past, new, page, table, ring, 3, 9, 64)
+    t, r, state = i32(table), i32(ring), i32([3, 9])
+    so, lens, cu, refused = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (2, 3, 4, 1))
+    slots, positions = (torch.full((most,), 7, dtype=torch.int32, device="cuda") for _ in range(2))
+    a4w4.a4w4_kv_plan(i32(past), i32(new), 3, page, t, 4, r, 16, state, so, lens, cu, slots, positions, most, refused)
+    ok()
+    for k, x in (("block_table", t), ("free_ring", r), ("ring_state", so), ("kv_lens", lens), ("cu_new", cu), ("refused", refused),
+                 ("slot_map", slots[:64]), ("positions", positions[:64])):
+        assert np.array_equal(x.cpu().numpy(), want[k]), k
+    assert int((slots[64:] != -1).sum()) == 0 and int((positions[64:] != 0).sum()) == 0
