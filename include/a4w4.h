@@ -340,8 +340,10 @@ size_t a4w4_kv_cache_bytes(int num_pages, int page_size, int Hkv, int D);
  * All arrays int32 on the device.  1 <= B <= 4096, page_size 16, 32, 64 or 128,
  * max_pages, ring_size >= 1, max_tokens >= 0, max_pages * page_size < 2^31.  A
  * call that is repeated on its own outputs (same past_lens, new_lens and
- * ring_state) gives the same ones.  Precondition: 0 <= past_lens, table entries
- * of held pages and ring entries are page numbers below 2^31 / page_size. */
+ * ring_state) gives the same ones.  A finished request longer than its row of the
+ * table gives back max_pages pages.  Precondition: 0 <= past_lens, 0 <= head <
+ * ring_size, 0 <= count, table entries of held pages and ring entries are page
+ * numbers below 2^31 / page_size. */
 int a4w4_kv_plan(const int32_t* past_lens, const int32_t* new_lens, int B, int page_size, int32_t* block_table,
                  int max_pages, int32_t* free_ring, int ring_size, const int32_t* ring_state,
                  int32_t* ring_state_out, int32_t* kv_lens, int32_t* cu_new, int32_t* slot_map,

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs p)
       const long long held = (past + ps - 1) / ps;
       at += want;
       ap += (past + want + ps - 1) / ps - held;
-      ab += nw < 0 ? held : 0;
+      ab += nw < 0 ? min(held, static_cast<long long>(p.max_pages)) : 0;   // a row holds no more
     }
     tok[i] = at; page[i] = ap; back[i] = ab;
   }

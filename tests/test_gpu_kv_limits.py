@@ -58,3 +58,24 @@ def test_a_plan_for_2_to_31_tokens():
                  ("slot_map", slots[:64]), ("positions", positions[:64])):
         assert np.array_equal(x.cpu().numpy(), want[k]), k
     assert int((slots[64:] != -1).sum()) == 0 and int((positions[64:] != 0).sum()) == 0
+
+
+@pytest.mark.parametrize("past", [[65, 64, 4], [1000, 3, 70], [2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1]])
+def test_a_plan_gives_back_no_more_than_a_row_of_the_table(past):
+    """Finished requests longer than their rows (4 pages of 16), and one that is refused for its length."""
+    page, new = 16, [-1, 2, -1]
+    table = np.arange(12, dtype=np.int32).reshape(3, 4)
+    ring = np.full(40, -3, np.int32)
+    ring[:5] = np.arange(20, 25)
+    want = kv.plan(past, new, page, table, ring, 0, 5, 8)
+    buf = torch.full((36,), -9, dtype=torch.int32, device="cuda")      # the table with nothing of its own around it
+    t = buf[12:24]
+    t.copy_(i32(table.reshape(-1)))
+    r, state = i32(ring), i32([0, 5])
+    so, lens, cu, refused, slots, positions = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (2, 3, 4, 1, 8, 8))
+    a4w4.a4w4_kv_plan(i32(past), i32(new), 3, page, t, 4, r, 40, state, so, lens, cu, slots, positions, 8, refused)
+    ok()
+    for k, x in (("block_table", t.view(3, 4)), ("free_ring", r), ("ring_state", so), ("kv_lens", lens), ("cu_new", cu),
+                 ("refused", refused), ("slot_map", slots), ("positions", positions)):
+        assert np.array_equal(x.cpu().numpy(), want[k]), k
+    assert (buf[:12] == -9).all() and (buf[24:] == -9).all()
