@@ -385,9 +385,12 @@ int a4w4_kv_read(const void* cache, int num_pages, int page_size, const int32_t*
  * of up to 512 keys).  The reduction order depends on the arguments and the lengths
  * alone: results are bitwise deterministic.
  * Hq % Hkv == 0, Hq / Hkv <= 256, D 64 or 128, sm_scale finite and > 0, B >= 1, total_q >= 0,
- * max_q >= 1, max_pages >= 1, max_pages * page_size < 2^31 - 255, num_pages * page_size < 2^31, and
- * the work of the largest call that the arguments allow (steps of 32 keys for each 8 rows of a
- * key/value head, or of 128 keys for each 256 rows, and up to 4 more for each) below 2^31.
+ * max_q >= 1, max_pages >= 1, max_pages * page_size < 2^31 - 255, num_pages * page_size < 2^31,
+ * total_q * Hq < 2^31, with max_q > total_q also B * max_q * Hq < 2^31, and the work of the largest
+ * call that the arguments allow (steps of 32 keys of the table's width for each 8 rows of a key/value
+ * head, or of 128 keys for each 256 rows, and up to 4 more for each; as many rows as B * max_q or as
+ * total_q and a block more for each request) below 2^31.  Row lists that overlap (cu_q not
+ * non-decreasing) stay inside the buffers too, but what is then written is not defined.
  * Lengths are clamped to the table's width and page numbers to [0, num_pages):
  * nothing outside the cache is read.  Workspace: a4w4_kv_attention_workspace_bytes
  * bytes, 16-byte aligned, zeroed once with a4w4_workspace_init (it begins with

@@ -417,8 +417,10 @@ int a4w4_kv_attention(const void* q_bf16, long long q_stride, const int32_t* cu_
     return A4W4_ERR_ARG;
   if (static_cast<long long>(max_pages) * page_size > INT32_MAX - 255 || !row_stride_ok(q_stride, total_q, Hq, D))
     return A4W4_ERR_ARG;
-  // rows are counted in 32 bits; so are the kernels' steps, which their launchers check
-  if (static_cast<long long>(B) * max_q > INT32_MAX / Hq) return A4W4_ERR_ARG;
+  // rows are counted in 32 bits; so are the kernels' steps, which their launchers check.  A max_q beyond total_q says
+  // nothing of the rows, so it is held to what any batch of B such requests may have.
+  if (total_q > INT32_MAX / Hq) return A4W4_ERR_ARG;
+  if (max_q > total_q && static_cast<long long>(B) * max_q > INT32_MAX / Hq) return A4W4_ERR_ARG;
   if (!(sm_scale > 0.f) || !(sm_scale <= FLT_MAX)) return A4W4_ERR_ARG;
   if (!aligned16(cache) || !aligned4(cu_q) || !aligned4(kv_lens) || !aligned4(block_table)) return A4W4_ERR_ARG;
   if (total_q > 0 && (!aligned16(q_bf16) || !aligned16(out_bf16))) return A4W4_ERR_ARG;

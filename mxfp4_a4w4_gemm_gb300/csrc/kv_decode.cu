@@ -846,10 +846,10 @@ int launch_kv_decode(const KvAttentionArgs& p, int D, cudaStream_t st, int sms) 
   // requests x 20 rows 20.0 and 21.6 us (D = 64), 4 x 16384 keys x 24 rows 53.1 and 52.3 (D = 128), 2 x 131000 keys x
   // 16 rows 59.2 and 55.5 (D = 128), 40.9 and 34.5 (D = 64)
   const bool two = (rows + 7) / 8 % 2 == 0;
-  // as many CTAs as there can be work for, one per SM at most; places of the line are counted in 32 bits
+  // as many CTAs as there can be work for, one per SM at most
   const double units = static_cast<double>(p.B) * p.Hkv * ((rows + (two ? 15 : 7)) / (two ? 16 : 8));
-  const double places = (static_cast<double>(p.max_pages) * p.page_size / kStep + 1 + kUnitCost) * units;
-  if (places > 2147483647.0) return -1;
+  const double unit = static_cast<double>(p.max_pages) * p.page_size / kStep + 1 + kUnitCost, places = unit * units;
+  if (unit * most_units(p, two ? 16 : 8) >= kTooMany) return -1;
   const int most = sms < kMaxParts ? sms : kMaxParts;
   const double ctas = fmax(units, places / (kLeast * kFew) + 1);
   const int grid = ctas < most ? static_cast<int>(ctas) : most;

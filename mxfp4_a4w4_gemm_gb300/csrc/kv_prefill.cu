@@ -976,11 +976,9 @@ int launch_one(const KvAttentionArgs& p, int grid, cudaStream_t st) {
 }  // namespace
 
 int launch_kv_prefill(const KvAttentionArgs& p, int D, cudaStream_t st, int sms) {
-  // steps are counted in 32 bits
-  const int G = p.Hq / p.Hkv, tq = kRows / G;
-  const double most = static_cast<double>(p.B) * p.Hkv * ((p.max_q + tq - 1) / tq) *
-                      ((static_cast<double>(p.max_pages) * p.page_size + kKeys - 1) / kKeys + 1 + kUnitCost);
-  if (most > 2147483647.0) return -1;
+  const int G = p.Hq / p.Hkv;
+  const double unit = static_cast<double>(p.max_pages) * p.page_size / kKeys + 1 + kUnitCost;
+  if (unit * most_units(p, kRows / G * G) >= kTooMany) return -1;
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
   const bool rest = p.max_pages <= kRestKeys / p.page_size;
   if (D == 64) return rest ? launch_one<64, true>(p, grid, st) : launch_one<64, false>(p, grid, st);

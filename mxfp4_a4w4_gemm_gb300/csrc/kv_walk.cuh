@@ -9,6 +9,7 @@
 // the lengths alone.
 #pragma once
 
+#include <cmath>
 #include <cstdint>
 
 #include "device.cuh"
@@ -115,8 +116,21 @@ __device__ __forceinline__ KvRequest shfl_request(const KvRequest& r, int lane) 
   return o;
 }
 
-// Cuts the line (places(r) places for the units of a request with lengths r;
-// fewer than 2^31 in all) for at most gridDim.x * PER workers of at least
+// The line's places are counted in 32 bits.  The launchers see to it that lists of rows (cu_q) that do not overlap give
+// fewer than kTooMany; sums stop there, and a line of so many is not walked.
+constexpr uint32_t kTooMany = 0x7FFFFFFFu;
+__device__ __forceinline__ uint32_t add_places(uint32_t a, uint32_t b) { return min(a + b, kTooMany); }
+
+// Units of B requests (blocks of `rows` of a head's rows), as many as there can be: every request max_q tokens, or
+// total_q tokens in all, with one block more for each request that has any.
+inline double most_units(const KvAttentionArgs& p, int rows) {
+  const int G = p.Hq / p.Hkv;
+  const double each = std::ceil(static_cast<double>(p.max_q) * G / rows) * p.B;
+  const double all = static_cast<double>(p.total_q) * G / rows + (p.B < p.total_q ? p.B : p.total_q);
+  return (each < all ? each : all) * p.Hkv;
+}
+
+// Cuts the line (places(r) places for the units of a request with lengths r) for at most gridDim.x * PER workers of at least
 // least(the longest unit's) places, at least `few` of them to a CTA; warp w learns the start of worker
 // blockIdx.x * per + w, if there is one.  Every thread of the CTA calls it; with
 // up to 32 requests each warp finds out for itself, with more they sum together
@@ -147,14 +161,14 @@ __device__ __forceinline__ bool kv_locate(const KvAttentionArgs& p, Places place
   for (int b = b0; b < b1; ++b) {
     mine = kv_request(p, b);
     const uint32_t n = places(mine);
-    sum += n;
+    sum = add_places(sum, n);
     if (n > 0) longest = max(longest, unit(mine));
   }
   uint32_t inc = sum;                                            // inclusive, within the warp
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-    if (lane >= o) inc += u;
+    if (lane >= o) inc = add_places(inc, u);
   }
   uint32_t wsum = 0, total;
   if (small) {
@@ -170,7 +184,7 @@ __device__ __forceinline__ bool kv_locate(const KvAttentionArgs& p, Places place
 #pragma unroll
     for (int o = 1; o < W; o <<= 1) {
       const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, wsum, o);
-      if (lane >= o) wsum += u;
+      if (lane >= o) wsum = add_places(wsum, u);
     }
     total = __shfl_sync(0xFFFFFFFFu, wsum, W - 1);
   }
@@ -202,7 +216,7 @@ __device__ __forceinline__ bool kv_locate(const KvAttentionArgs& p, Places place
     start.b = b;
     start.rest = f - lo;
   };
-  if (total == 0) return false;
+  if (total == 0 || total == kTooMany) return false;
   if (WHOLE > 0 && longest <= min(static_cast<uint32_t>(WHOLE), 21u + total / gridDim.x)) {
     KvShare even;
     even.cut(0, total, 0, gridDim.x);
