@@ -133,15 +133,23 @@ def attention(q, keys, values, sm_scale):
     return out, lse, spread, reach
 
 
-def attention_bounds(out, lse, spread, reach):
-    """Error bounds of a kernel that holds exact products and fp32 sums, rounds each probability to BF16 or
-    finer and the output to BF16.
+# What rounding may put a probability off by, relatively: half a unit in the last place of a type of n significant bits
+# is up to 2^-n of the value (a value just above a power of two).
+P_ONE_BF16 = 2.0 ** -8       # one BF16 term
+P_TWO_BF16 = 2.0 ** -16      # two: the second holds what the first leaves, to 2^-8 of it
+# FP16, 2^-11; its product with a value's power of two may fall to FP16's last exponent but one, where 10 bits are left
+P_FP16 = 2.0 ** -11 + 2.0 ** -10
+
+
+def attention_bounds(out, lse, spread, reach, p_round=2.0 ** -9):
+    """Error bounds of a kernel that holds exact products and fp32 sums, rounds each probability by at most p_round
+    of it (the default covers FP16 and two BF16 terms; one BF16 term takes P_ONE_BF16) and the output to BF16.
 
     A score is a sum of at most 128 exact products in fp32: its error is at most 128 * 2^-24 * reach, plus a few
     roundings of the score itself (2^-22 |x| <= 2^-22 reach).  A probability is then off by that much relatively,
-    in the numerator and in the sum (twice), and by BF16's 2^-9 and the exponential's and the sums' few 2^-22
-    (2^-18 in all).  The output's own rounding is 2^-9 of it; the sum over keys adds n * 2^-24 at most, below
-    2^-10 up to 16384 keys.  The log-sum-exp takes the score's error once."""
+    in the numerator and in the sum (twice), by p_round in the numerator, whose rounding follows the sum's, and by
+    the exponential's and the sums' few 2^-22 (2^-18 in all).  The output's own rounding is 2^-8 of it; the sum over
+    keys adds n * 2^-24 at most, 2^-10 up to 16384 keys.  The log-sum-exp takes the score's error once."""
     dx = (2.0 ** -17 + 2.0 ** -22) * reach
-    rel = 2 * np.expm1(dx) + 2.0 ** -9 + 2.0 ** -10 + 2.0 ** -18
+    rel = 2 * np.expm1(dx) + p_round + 2.0 ** -10 + 2.0 ** -18
     return 2.0 ** -8 * np.abs(out) + rel[..., None] * spread, dx + 2.0 ** -18 * (1 + np.where(np.isfinite(lse), np.abs(lse), 0))
