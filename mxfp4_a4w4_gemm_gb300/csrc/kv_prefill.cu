@@ -18,10 +18,9 @@
 // * Values become BF16, since P wants its exponents: E2M1 magnitude bits placed in
 //   a BF16 read as the value times 2^-126, and one or two exact multiplies by
 //   powers of two apply the scale.
-// So the only roundings are P's to BF16 and the fp32 sums.  Where the block table
-// holds few keys (kRestKeys), some of them may carry a row and their roundings do
-// not average out, and products do not make the time: there (REST) P has a second
-// BF16 term, what the rounding left, and its products are added.
+// So the only roundings are P's to BF16 and the fp32 sums.  A row that sees few keys
+// (kRestKeys) has no others for their roundings to average out with: in its unit
+// (REST) P has a second BF16 term, what the rounding left, and its products are added.
 // The running maximum follows with slack: O is rescaled only when a row's maximum
 // has grown by more than 2^8, P staying below 2^8 meanwhile.
 //
@@ -31,7 +30,7 @@
 // products 58%; the rest is the chain scores -> softmax -> P of either tile, slowed by
 // the decoders, with which it shares the issue slots (64% of them taken).  Short
 // prompts pay for units beside their steps: 12 ragged requests of up to 700 tokens x
-// 1500 keys 32.3 us, 128 tokens x 128 keys 12.4.
+// 1500 keys 33.8 us, 128 tokens x 128 keys 12.0.
 //
 //   warps 0-3, 4-7   softmax of tile 0, 1 (a thread per row): stage Q, scores ->
 //                    probabilities, output
@@ -43,6 +42,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 namespace a4w4 {
 
@@ -64,9 +64,12 @@ constexpr float kJoinCost = 0.7f;
 // 39.0, 39.7 (0, with slower joins: 12 ragged prompts 46.8 where 2 took 39.0).
 constexpr int kUnitCost = 2;
 constexpr int kMaxCtas = 512;
-// Keys of a table up to which P has two terms.  With one term and with two: 128 tokens
-// x 128 keys 13.3 and 14.0 us, 4 x 512 x 512 46.8 and 51.3, 2048 x 8192 205 and 294.
-constexpr int kRestKeys = 512;
+// Keys that a unit's first row sees, up to which P has two terms: a step's, so that the
+// answers hang on what a row sees and not on the table's width.  None, 128, 512: 12
+// ragged prompts 32.3, 33.8, 39.5 us, 4096 tokens x 4096 keys 162, 168, 186, 3 ragged x
+// 3205 39.0, 41.3, 45.6 (their steps take up to 1.4 times as long, which the cut does
+// not know); 4 x 512 x 512 36.9 with 128, 38.9 with 512.
+constexpr int kRestKeys = 128;
 constexpr float kNoMax = -3.0e38f;            // running maximum before the first key
 
 template <int D>
@@ -332,11 +335,13 @@ struct PreWalk {
     n = q.steps(k);
     left -= kUnitCost;
   }
+  // whether the unit's first row, and so some row, sees few keys: then P has two terms
+  __device__ __forceinline__ bool few_keys() const { return q.len - q.all + k * q.tq < kRestKeys; }
   // rows of the unit
   __device__ __forceinline__ int rows(int G) const { return min(q.tq, q.rows - k * q.tq) * G; }
 };
 
-template <int D, bool REST>
+template <int D>
 __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(const KvAttentionArgs p) {
   using Cf = PreCfg<D>;
   using Ch = KvChunk<D>;
@@ -505,87 +510,91 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
       if (active && ok) {
         const int seen = r < R ? w.q.len - w.q.all + first_tok + qi + 1 : 0;
         const int n = w.steps();
-        for (int i = 0; i < n; ++i) {
-          ok = __all_sync(0xFFFFFFFFu, wait(s_full(tile), s_phase));
-          if (!ok) break;
-          s_phase ^= 1;
-          tc_fence_after();
-          const int k0 = (w.t + i) * kKeys;
-          // score -> log2 units; positive, so that a masked score stays -infinity
-          const int ref = *reinterpret_cast<volatile int*>(key_ref + ((it + i) & 3));
-          const float f = fmaxf(p.sm_scale * 1.4426950408889634f * pow2i(max(-126, min(127, ref - 140 - row_pow))), 1e-44f);
-          const bool edge = __any_sync(0xFFFFFFFFu, k0 + kKeys > seen);
-          uint32_t x[128];
+        auto softmax = [&](auto two_terms) {
+          constexpr bool REST = decltype(two_terms)::value;
+          for (int i = 0; i < n; ++i) {
+            ok = __all_sync(0xFFFFFFFFu, wait(s_full(tile), s_phase));
+            if (!ok) break;
+            s_phase ^= 1;
+            tc_fence_after();
+            const int k0 = (w.t + i) * kKeys;
+            // score -> log2 units; positive, so that a masked score stays -infinity
+            const int ref = *reinterpret_cast<volatile int*>(key_ref + ((it + i) & 3));
+            const float f = fmaxf(p.sm_scale * 1.4426950408889634f * pow2i(max(-126, min(127, ref - 140 - row_pow))), 1e-44f);
+            const bool edge = __any_sync(0xFFFFFFFFu, k0 + kKeys > seen);
+            uint32_t x[128];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, x + 32 * c);
-          tmem_wait_ld<128>(x);
-          if (edge) {
-            const int k1 = seen - k0;                             // columns that the row sees
+            for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, x + 32 * c);
+            tmem_wait_ld<128>(x);
+            if (edge) {
+              const int k1 = seen - k0;                             // columns that the row sees
 #pragma unroll
-            for (int u = 0; u < 128; ++u)
-              if (u >= k1) x[u] = 0xFF800000u;                    // -infinity
-          }
-          float top[4];
+              for (int u = 0; u < 128; ++u)
+                if (u >= k1) x[u] = 0xFF800000u;                    // -infinity
+            }
+            float top[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            top[c] = max3(__uint_as_float(x[c]), __uint_as_float(x[c + 4]), __uint_as_float(x[c + 8]));
+            for (int c = 0; c < 4; ++c) {
+              top[c] = max3(__uint_as_float(x[c]), __uint_as_float(x[c + 4]), __uint_as_float(x[c + 8]));
 #pragma unroll
-            for (int u = c + 12; u < 124; u += 8) top[c] = max3(top[c], __uint_as_float(x[u]), __uint_as_float(x[u + 4]));
-            top[c] = fmaxf(top[c], __uint_as_float(x[c + 124]));
-          }
-          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f;
-          // the maximum follows once it is 2^8 ahead
-          const bool grow = m == kNoMax ? mx > m : mx - m > 8.f;
-          float a = 1.f;
-          if (grow) {
-            a = ex2(m - mx);
-            m = mx;
-            off = -m;
-            l *= a;
-          }
-          if (i > 0 && __any_sync(0xFFFFFFFFu, grow)) {
+              for (int u = c + 12; u < 124; u += 8) top[c] = max3(top[c], __uint_as_float(x[u]), __uint_as_float(x[u + 4]));
+              top[c] = fmaxf(top[c], __uint_as_float(x[c + 124]));
+            }
+            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * f;
+            // the maximum follows once it is 2^8 ahead
+            const bool grow = m == kNoMax ? mx > m : mx - m > 8.f;
+            float a = 1.f;
+            if (grow) {
+              a = ex2(m - mx);
+              m = mx;
+              off = -m;
+              l *= a;
+            }
+            if (i > 0 && __any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t y[16];
-              tmem_ld16(o_col + 16 * c, y);
-              tmem_wait_ld<16>(y);
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t y[16];
+                tmem_ld16(o_col + 16 * c, y);
+                tmem_wait_ld<16>(y);
 #pragma unroll
-              for (int u = 0; u < 16; ++u) y[u] = __float_as_uint(__uint_as_float(y[u]) * a);
-              tmem_st16(o_col + 16 * c, y);
+                for (int u = 0; u < 16; ++u) y[u] = __float_as_uint(__uint_as_float(y[u]) * a);
+                tmem_st16(o_col + 16 * c, y);
+              }
             }
+            const uint64_t f2 = pair_f32(__float_as_uint(f), __float_as_uint(f));
+            const uint64_t off2 = pair_f32(__float_as_uint(off), __float_as_uint(off));
+            uint64_t sum0 = 0, sum1 = 0;                            // two pairs of partial sums
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              uint32_t y[8], rest[8];
+#pragma unroll
+              for (int u = 0; u < 8; ++u) {
+                const uint64_t z = fma_f32x2(pair_f32(x[16 * c + 2 * u], x[16 * c + 2 * u + 1]), f2, off2);
+                const float e0 = ex2(__uint_as_float(static_cast<uint32_t>(z)));
+                const float e1 = ex2(__uint_as_float(static_cast<uint32_t>(z >> 32)));
+                const uint64_t e = pair_f32(__float_as_uint(e0), __float_as_uint(e1));
+                if (u & 1) sum1 = add_f32x2(sum1, e); else sum0 = add_f32x2(sum0, e);
+                y[u] = pack_bf16(e0, e1);
+                if constexpr (REST) rest[u] = pack_bf16(e0 - __uint_as_float(y[u] << 16), e1 - __uint_as_float(y[u] & 0xFFFF0000u));
+              }
+              tmem_st8(s_col + 8 * c, y);
+              if constexpr (REST) tmem_st8(s_col + 64 + 8 * c, rest);
+              if (c == 3) {                                         // the products of the first 64 keys may start
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_half(tile));
+              }
+            }
+            sum0 = add_f32x2(sum0, sum1);
+            l += __uint_as_float(static_cast<uint32_t>(sum0)) + __uint_as_float(static_cast<uint32_t>(sum0 >> 32));
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full(tile));
           }
-          const uint64_t f2 = pair_f32(__float_as_uint(f), __float_as_uint(f));
-          const uint64_t off2 = pair_f32(__float_as_uint(off), __float_as_uint(off));
-          uint64_t sum0 = 0, sum1 = 0;                            // two pairs of partial sums
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint32_t y[8], rest[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const uint64_t z = fma_f32x2(pair_f32(x[16 * c + 2 * u], x[16 * c + 2 * u + 1]), f2, off2);
-              const float e0 = ex2(__uint_as_float(static_cast<uint32_t>(z)));
-              const float e1 = ex2(__uint_as_float(static_cast<uint32_t>(z >> 32)));
-              const uint64_t e = pair_f32(__float_as_uint(e0), __float_as_uint(e1));
-              if (u & 1) sum1 = add_f32x2(sum1, e); else sum0 = add_f32x2(sum0, e);
-              y[u] = pack_bf16(e0, e1);
-              if constexpr (REST) rest[u] = pack_bf16(e0 - __uint_as_float(y[u] << 16), e1 - __uint_as_float(y[u] & 0xFFFF0000u));
-            }
-            tmem_st8(s_col + 8 * c, y);
-            if constexpr (REST) tmem_st8(s_col + 64 + 8 * c, rest);
-            if (c == 3) {                                         // the products of the first 64 keys may start
-              tmem_wait_st();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(p_half(tile));
-            }
-          }
-          sum0 = add_f32x2(sum0, sum1);
-          l += __uint_as_float(static_cast<uint32_t>(sum0)) + __uint_as_float(static_cast<uint32_t>(sum0 >> 32));
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(p_full(tile));
-        }
+        };
+        if (w.few_keys()) softmax(std::true_type{}); else softmax(std::false_type{});
       }
       // the unit's scores are done, so Q's place is free for the next one's
       {
@@ -855,14 +864,14 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
       __syncwarp();
     };
     // the products with keys 64 part .. + 63 of the step
-    auto outputs = [&](int tile, int s, int part, bool first, bool last_step, bool last_tile) {
+    auto outputs = [&](int tile, int s, int part, bool rest, bool first, bool last_step, bool last_tile) {
       const uint32_t v_lo = static_cast<uint32_t>(vd) + s * (Cf::TILE >> 4), v_hi = static_cast<uint32_t>(vd >> 32);
       const uint32_t d = tm + Cf::OCOL + tile * D, a = tm + Cf::SCOL + tile * 128;
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           mma_ts(d, a + 32 * part + 8 * kk, v_lo + ((4 * part + kk) * 2048 >> 4), v_hi, id_o, kk == 0 && first ? 0u : 1u);
-        if constexpr (REST) {
+        if (rest) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_ts(d, a + 64 + 32 * part + 8 * kk, v_lo + ((4 * part + kk) * 2048 >> 4), v_hi, id_o, 1u);
@@ -874,6 +883,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
     };
     for (; w.left > 0 && ok; w.next(p)) {
       const int n = w.steps(), tiles = w.rows(G) > 128 ? 2 : 1;
+      const bool rest = w.few_keys();
       for (int i = 0; i <= n && ok; ++i) {
         // products of step i - 1 and scores of step i, tile after tile
         const int s = it & 1, sp = (it - 1) & 1;
@@ -883,11 +893,11 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
             if (tile == 0 && !sure(v_full(sp), php)) break;
             if (!sure(p_half(tile), p_phase >> tile & 1)) break;
             tc_fence_after();
-            outputs(tile, sp, 0, i == 1, false, false);
+            outputs(tile, sp, 0, rest, i == 1, false, false);
             if (!sure(p_full(tile), p_phase >> tile & 1)) break;
             p_phase ^= 1u << tile;
             tc_fence_after();
-            outputs(tile, sp, 1, false, i == n, tile == tiles - 1);
+            outputs(tile, sp, 1, rest, false, i == n, tile == tiles - 1);
           }
           if (i < n) {
             if (i == 0) {
@@ -961,16 +971,16 @@ size_t kv_prefill_ws_bytes(int D, int sms) {
 
 namespace {
 
-template <int D, bool REST>
+template <int D>
 int launch_one(const KvAttentionArgs& p, int grid, cudaStream_t st) {
   using Cf = PreCfg<D>;
   static std::atomic<unsigned long long> attr_done{0};
   const int rc = ensure_func_attrs(attr_done, [] {
-    return cudaFuncSetAttribute(a4w4_kv_prefill_kernel<D, REST>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM) ==
+    return cudaFuncSetAttribute(a4w4_kv_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM) ==
            cudaSuccess;
   });
   if (rc != 0) return rc;
-  return launch_pdl_smem(a4w4_kv_prefill_kernel<D, REST>, grid, Cf::THREADS, Cf::SMEM, st, p);
+  return launch_pdl_smem(a4w4_kv_prefill_kernel<D>, grid, Cf::THREADS, Cf::SMEM, st, p);
 }
 
 }  // namespace
@@ -980,9 +990,7 @@ int launch_kv_prefill(const KvAttentionArgs& p, int D, cudaStream_t st, int sms)
   const double unit = static_cast<double>(p.max_pages) * p.page_size / kKeys + 1 + kUnitCost;
   if (unit * most_units(p, kRows / G * G) >= kTooMany) return -1;
   const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-  const bool rest = p.max_pages <= kRestKeys / p.page_size;
-  if (D == 64) return rest ? launch_one<64, true>(p, grid, st) : launch_one<64, false>(p, grid, st);
-  return rest ? launch_one<128, true>(p, grid, st) : launch_one<128, false>(p, grid, st);
+  return D == 64 ? launch_one<64>(p, grid, st) : launch_one<128>(p, grid, st);
 }
 
 }  // namespace a4w4
