@@ -380,9 +380,9 @@ int a4w4_kv_read(const void* cache, int num_pages, int page_size, const int32_t*
  * A row that sees no key (empty request, more queries than keys) gives zeros and
  * lse = -infinity.  Keys and values enter as the values they stand for; sums,
  * softmax statistics and the output accumulator are fp32.  Probabilities enter
- * the products in FP16 (11 bits) or, where their range asks for it and in larger
- * calls with over 48 rows of a key/value head, in BF16 (8 bits; 16 in those calls
- * for rows that see up to 128 keys).  The reduction order depends on the arguments and the lengths
+ * the products in FP16 (11 bits) or, where their range asks for it, in two BF16
+ * terms (16 bits); in larger calls with over 48 rows of a key/value head in BF16
+ * (8 bits; 16 for rows that see up to 128 keys).  The reduction order depends on the arguments and the lengths
  * alone: results are bitwise deterministic.
  * Hq % Hkv == 0, Hq / Hkv <= 256, D 64 or 128, sm_scale finite and > 0, B >= 1, total_q >= 0,
  * max_q >= 1, max_pages >= 1, max_pages * page_size < 2^31 - 255, num_pages * page_size < 2^31,

@@ -38,7 +38,10 @@
 //   exponent the warp has met, in FP16 down to 2^-24; O is rescaled when R
 //   grows, as it is when the maximum does.  P is 2^(x - m + 6): FP16 holds it
 //   to 11 bits down to 2^-20 of the row's largest, and the sum of a row's P is
-//   taken in fp32 before that rounding.
+//   taken in fp32 before that rounding.  A step with a P below that (or a value
+//   scale far below R) takes BF16 products with P in two terms, 16 bits: 64 x 4096
+//   keys with one dominant key per row 84 us, 68 without (one term, 8 bits: 78 and
+//   67; the second term as a second pass over the values: 113 and 80).
 // A warp is a worker of kv_walk.cuh: it walks its own run of 32-token steps, unit
 // after unit, and writes the units that lie in it whole.  Parts of cut units stay
 // in shared memory; when all warps are through, the CTA joins them, and units
@@ -600,7 +603,19 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
           }
         }
       } else {
-        // the same in BF16, whose exponents reach
+        // the same in BF16, whose exponents reach, P in two terms: its rounding and what that leaves
+        uint32_t pb[2][NT][2], rest[2][NT][2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const float y0 = x[c][nt][2 * u], y1 = x[c][nt][2 * u + 1];
+              const uint32_t w = pack_bf16(y0, y1);
+              pb[c][nt][u] = movmatrix_trans(w);
+              rest[c][nt][u] = movmatrix_trans(pack_bf16(y0 - __uint_as_float(w << 16), y1 - __uint_as_float(w & 0xFFFF0000u)));
+            }
         __syncwarp();
         uint8_t* dst = vs + (lane >> 1 & 3) * 16 + (lane >> 4) * 8 + (lane >> 3 & 1) * 4 + (lane & 1) * 2;
 #pragma unroll
@@ -609,13 +624,8 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
           *reinterpret_cast<uint16_t*>(dst + j * 64) = static_cast<uint16_t>(max(k + 127, 0) << 7);
         }
         __syncwarp();
-        for (int c = 0; c < 2; ++c) {
-          uint32_t pb[NT][2];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            pb[nt][0] = movmatrix_trans(c ? pack_bf16(x[1][nt][0], x[1][nt][1]) : pack_bf16(x[0][nt][0], x[0][nt][1]));
-            pb[nt][1] = movmatrix_trans(c ? pack_bf16(x[1][nt][2], x[1][nt][3]) : pack_bf16(x[0][nt][2], x[0][nt][3]));
-          }
+        for (int c = 0; c < 2; ++c) {
           uint32_t run[2][2][I / 4];
           load_runs<D>(st + c * Ch::kBytes + Ch::kValues, lane, run);
 #pragma unroll
@@ -627,11 +637,14 @@ __global__ void __launch_bounds__(DecCfg<D, NT>::THREADS, 1) a4w4_kv_decode_kern
               e2m1x4_to_bf16x2(__byte_perm(run[hh][0][j / 2], run[hh][1][j / 2], j & 1 ? 0x7632 : 0x5410), v[hh]);
             const uint32_t a0[4] = {v[0][0], v[0][1], v[1][0], v[1][1]}, a1[4] = {v[0][2], v[0][3], v[1][2], v[1][3]};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint32_t b0 = mul_bf16x2(pb[nt][0], f.x), b1 = mul_bf16x2(pb[nt][1], f.y);
-              mma_bf16(o[2 * j][nt], a0, b0, b1);
-              mma_bf16(o[2 * j + 1][nt], a1, b0, b1);
-            }
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t* q = k ? (c ? rest[1][nt] : rest[0][nt]) : c ? pb[1][nt] : pb[0][nt];
+                const uint32_t b0 = mul_bf16x2(q[0], f.x), b1 = mul_bf16x2(q[1], f.y);
+                mma_bf16(o[2 * j][nt], a0, b0, b1);
+                mma_bf16(o[2 * j + 1][nt], a1, b0, b1);
+              }
           }
         }
       }

@@ -51,7 +51,7 @@ def two_keys(B, G, D, kv_len, page, seed):
 
 @pytest.mark.parametrize("kv_len", [2, 60, 128])
 @pytest.mark.parametrize("D,G", [(64, 1), (128, 4), (64, 12), (128, 16)])
-@pytest.mark.parametrize("max_q,p_round", [(PROMPT, kv.P_TWO_BF16)])
+@pytest.mark.parametrize("max_q,p_round", [(PROMPT, kv.P_TWO_BF16), (1, kv.P_FP16)])
 def test_few_keys_carry_a_row(kv_len, D, G, max_q, p_round):
     """Up to 128 keys: the output is off by its own rounding and little more, on a table of any width."""
     B, page = 400 // G, 16
