@@ -101,11 +101,13 @@ def lib():
 
 
 def _ptr(x):
-    try:                                     # a tensor; the usual case comes first, these calls are short
+    if x is None or type(x) is int:
+        return x
+    try:                                     # a tensor
         if x.is_contiguous():
             return x.data_ptr()
     except AttributeError:
-        if x is None or isinstance(x, int):
+        if isinstance(x, int):
             return x
         raise TypeError(f"expected a tensor, an int pointer or None, got {type(x)}") from None
     raise ValueError("tensor arguments must be contiguous")
@@ -113,6 +115,8 @@ def _ptr(x):
 
 def _rows_ptr(x, stride):
     """Rows of [heads, D] values, `stride` elements apart: only the rows themselves must be contiguous."""
+    if x is None or type(x) is int:
+        return x
     try:
         st, sh, sd = x.stride()
         if sd == 1 and st == stride and sh == x.size(2):
