@@ -235,12 +235,6 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const uint16_t* __restri
   chunk[Ch::kValueScales + r * Ch::J + j] = static_cast<uint8_t>(ev);
 }
 
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
 // Eight E2M1 codes (nibble n of w) times 2^(e - 127) -> eight BF16, exact:
 // magnitude bits placed at 6..8 of a BF16 and the sign at 15 read as the value
 // times 2^-126; the scale follows in two multiplies by powers of two.

@@ -69,7 +69,6 @@ constexpr int kFew = 4;
 constexpr int kUnitCost = 2;
 constexpr int kWhole = 64;                    // places of the longest unit that a CTA may take whole
 constexpr int kMaxParts = 256;                // CTAs of a launch, and so parts of a cut unit
-constexpr float kNoMax = -3.0e38f;            // running maximum before the first key
 
 template <int D, int NT>
 struct DecCfg {
@@ -114,30 +113,10 @@ __device__ __forceinline__ void mma_f16_first(float* c, const uint32_t* a, uint3
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
-// The four bytes of w, each two E2M1 codes, as FP16x2 (low nibble in the low half).
-__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t* o) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]) : "r"(w));
-}
 __device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
 }
 // Four E2M1 codes in each half of w (nibble k of both halves to o[k]) as BF16x2: the code's magnitude bits at 6..8
 // of a BF16 read as the value times 2^-126, which one exact multiply puts right.
@@ -152,26 +131,6 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
   return d;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// 2^k as a float, k in [-149, 127] (zero below).
-__device__ __forceinline__ float pow2i(int k) {
-  return k >= -126 ? __uint_as_float(static_cast<uint32_t>(k + 127) << 23)
-                   : k >= -149 ? __uint_as_float(1u << (k + 149)) : 0.f;
 }
 
 // The bytes of a chunk's value codes that lane 4 g + t needs: tokens 2t, 2t+1 of both halves.

@@ -70,7 +70,6 @@ constexpr int kMaxCtas = 512;
 // 3205 39.0, 41.3, 45.6 (their steps take up to 1.4 times as long, which the cut does
 // not know); 4 x 512 x 512 36.9 with 128, 38.9 with 512.
 constexpr int kRestKeys = 128;
-constexpr float kNoMax = -3.0e38f;            // running maximum before the first key
 
 template <int D>
 struct PreCfg {
@@ -211,44 +210,9 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lead
 __device__ __forceinline__ uint32_t idesc_f16(uint32_t n) { return idesc_bf16(n) & ~(1u << 7 | 1u << 10); }
 constexpr uint32_t kIdescBMajorN = 1u << 16;   // instruction descriptor: B is MN-major
 
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// Eight E2M1 codes as FP16x2 words, in order.
-__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t* o) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]) : "r"(w));
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
 // Eight E2M1 codes (nibble k of w) -> BF16x2 words of elements (k, k + 4), k = 0..3, times 2^-126: magnitude bits
@@ -261,8 +225,6 @@ __device__ __forceinline__ uint4 e2m1x8_to_bf16x2(uint32_t w) {
 __device__ __forceinline__ uint4 mul_bf16x8(uint4 o, uint32_t f) {
   return make_uint4(mul_bf16x2(o.x, f), mul_bf16x2(o.y, f), mul_bf16x2(o.z, f), mul_bf16x2(o.w, f));
 }
-// 2^k as a float, k in [-126, 127]
-__device__ __forceinline__ float pow2i(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
 
 // sum over k = 0 .. n - 1 of floor((a k + b) / M) modulo 2^32; a n + b < 2^32
 template <uint32_t M>
@@ -485,7 +447,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
 #pragma unroll
           for (int s = C / 2; s > 0; s >>= 1) e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, s));
           const int k = min(141 - static_cast<int>(e), 127);
-          const float fk = pow2i(k);
+          const float fk = pow2i_normal(k);
           auto two = [&](uint32_t b) { return pack_f16(__uint_as_float(b << 16) * fk, __uint_as_float(b & 0xFFFF0000u) * fk); };
           const int rr = quad * 32 + (j0 + j) * AT + lane / C;
           *reinterpret_cast<uint4*>(smem + Cf::OFF_Q + tile * Cf::TILE + (c >> 3) * Cf::ATOM + rr * 128 +
@@ -520,7 +482,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
             const int k0 = (w.t + i) * kKeys;
             // score -> log2 units; positive, so that a masked score stays -infinity
             const int ref = *reinterpret_cast<volatile int*>(key_ref + ((it + i) & 3));
-            const float f = fmaxf(p.sm_scale * 1.4426950408889634f * pow2i(max(-126, min(127, ref - 140 - row_pow))), 1e-44f);
+            const float f = fmaxf(p.sm_scale * 1.4426950408889634f * pow2i_normal(max(-126, min(127, ref - 140 - row_pow))), 1e-44f);
             const bool edge = __any_sync(0xFFFFFFFFu, k0 + kKeys > seen);
             uint32_t x[128];
 #pragma unroll
