@@ -378,12 +378,16 @@ int a4w4_kv_read(const void* cache, int num_pages, int page_size, const int32_t*
  *   out_bf16 [total_q, Hq, D] = softmax(sm_scale q k^T) v
  *   lse [total_q, Hq] float, or NULL: log sum exp of the scaled scores
  * A row that sees no key (empty request, more queries than keys) gives zeros and
- * lse = -infinity.  Keys and values enter as the values they stand for; sums,
- * softmax statistics and the output accumulator are fp32.  Probabilities enter
- * the products in FP16 (11 bits) or, where their range asks for it, in two BF16
- * terms (16 bits); in larger calls with over 48 rows of a key/value head in BF16
- * (8 bits; 16 for rows that see up to 128 keys).  The reduction order depends on the arguments and the lengths
- * alone: results are bitwise deterministic.
+ * lse = -infinity.  Queries, keys and values enter as the values they stand for,
+ * but query elements below 2^-28 of their row's largest lose bits, and so do, in
+ * larger calls with over 48 rows of a key/value head, key blocks of a scale below
+ * 2^-36 of the largest of 128 keys; keys or values of 2^104 and more may overflow
+ * the sums.  Sums, softmax statistics and the output accumulator are fp32.
+ * Probabilities enter the products in FP16 (11 bits) or, where their range asks
+ * for it, in two BF16 terms (16 bits); in the larger calls in BF16 (8 bits; 16 for
+ * rows that see up to 128 keys).  Which calls are larger depends on the arguments,
+ * the table's width (max_pages) among them; the reduction order on the arguments
+ * and the lengths alone: results are bitwise deterministic.
  * Hq % Hkv == 0, Hq / Hkv <= 256, D 64 or 128, sm_scale finite and > 0, B >= 1, total_q >= 0,
  * max_q >= 1, max_pages >= 1, max_pages * page_size < 2^31 - 255, num_pages * page_size < 2^31,
  * total_q * Hq < 2^31, with max_q > total_q also B * max_q * Hq < 2^31, and the work of the largest

@@ -47,9 +47,11 @@ __device__ __forceinline__ long long warp_scan(long long v, int lane) {
 // less than a second launch or a grid-wide wait, and then writes its share of
 // the outputs.  No output is read: table entries of held pages and ring entries
 // of free pages are not written by this call.  Bound by latency: lengths, sums,
-// search, page number, one after the other: 8 requests 3.8 us, 2000 requests with
-// 128000 tokens 7.5 us (two tokens per thread; one per thread in twice the CTAs 9.1,
-// CTAs of 1024 threads 8.3).
+// search, page number, one after the other: 8 requests 3.9 us.  2000 requests with
+// 128000 tokens 7.9 us: to the same trips come the arithmetic of four requests and two
+// tokens a thread (64-bit sums, of which 20 bytes spill, divisions by page_size and
+// ring_size), which was not timed apart (one token per thread in twice the CTAs 9.1 where
+// two took 7.5, CTAs of 1024 threads 8.3).
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanArgs p) {
   __shared__ int s_tok[kPlanMaxB + 1], s_page[kPlanMaxB + 1], s_back[kPlanMaxB + 1];
   __shared__ long long s_warp[3][kPlanThreads / 32];
@@ -182,9 +184,13 @@ __device__ __forceinline__ void copy16(uint4* dst, const uint16_t* src) {
 }
 
 // Quantises one 32-block of a token's keys and the same one of its values: 128
-// bytes read, 34 written.  HBM-bound.  With the reader after it, 8191 tokens x 8
-// heads of 128: 12.6 us, 6.7 TB/s (15.0 us when the rows reach shared memory by way of
-// registers, 16.9 when every thread loads its own 64 bytes).
+// bytes read, 34 written.  8191 tokens x 8 heads of 128: 8.4 us alone, with buffers
+// beyond L2 in turn (5.1 TB/s, 75% of the copy rate), 33.3 for 40000 tokens (6.2 TB/s,
+// 92%): 32 KB of shared memory let six CTAs on an SM, so that the 1024 CTAs of 8191
+// tokens are a wave and an eighth.  With the reader after it 16.3 us; over the same
+// buffers again and again, whose cells the reader then finds in L2, 12.0 (there 15.0 when
+// the rows reach shared memory by way of registers, 16.9 when every thread loads its own
+// 64 bytes).
 template <int D>
 __global__ void __launch_bounds__(256) kv_append_kernel(const uint16_t* __restrict__ k, long long k_stride,
                                                         const uint16_t* __restrict__ v, long long v_stride,
@@ -252,7 +258,7 @@ __device__ __forceinline__ uint4 e2m1x8_to_bf16x8(uint32_t w, uint32_t e) {
                     __byte_perm(o[2], o[3], 0x7632));
 }
 
-// The inverse: 34 bytes read, 128 written.  HBM-bound.  A thread's 64 bytes of a row
+// The inverse: 34 bytes read, 128 written.  Bound by HBM in long runs.  A thread's 64 bytes of a row
 // go out by way of shared memory, so that a warp's stores write whole rows (16-byte
 // stores 64 bytes apart touch every 32-byte sector twice): 40000 tokens x 8 heads of
 // 128 36.6 us, 5.7 TB/s; stored directly 55.5.

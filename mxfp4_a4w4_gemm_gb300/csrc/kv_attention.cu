@@ -8,8 +8,8 @@ namespace {
 // Rows per key/value head up to which the decode kernel runs.  It goes over the keys
 // once per 8 or 16 rows, the tcgen05 kernel once per 256 at the price of a whole
 // unit.  4 requests x 16384 keys x 8 heads, rows: decode and prompt kernel, D = 128:
-// 16: 34 and 72 us, 32: 55 and 71, 48: 76 and 72, 64: 100 and 72; D = 64: 32: 35 and
-// 54, 48: 48 and 55, 64: 61 and 53; 16 x 1000 keys, D = 128: 48: 29 and 33, 64: 36
+// 16: 34 and 75 us, 32: 57 and 73, 48: 80 and 74, 64: 106 and 73; D = 64: 32: 37 and
+// 56, 48: 52 and 56, 64: 68 and 55; 16 x 1000 keys, D = 128: 48: 29 and 35, 64: 37
 // and 34.
 constexpr int kFewRows = 48;
 bool few_rows(int max_q, int group) { return max_q <= kFewRows / group; }
@@ -17,11 +17,11 @@ bool few_rows(int max_q, int group) { return max_q <= kFewRows / group; }
 // More rows than that, but so little work (as the table and max_q bound it) that time
 // goes into starting and joining, where the decode kernel is faster: steps of 16 rows
 // x 32 keys for each of 8 warps per SM.  Steps: decode and prompt kernel, 8 heads of
-// 128 unless said otherwise: 0.7 (60 tokens x 200 keys): 8.5 and 15.1 us, 1.7 (2 x 16
-// x 1000): 13.5 and 17.5, 3.4 (8 x 16 x 500): 15.0 and 19.3, 4.1 (20 x 4000): 19.5 and
-// 25.1, 5.0 (4 ragged x 17 x 1214, D = 64): 12.0 and 13.7, 5.2 (5 x 11 x 3370, 16
-// heads over 2): 19.2 and 26.7, 6.3 (4 x 60 x 500): 23.7 and 21.2, 6.7 (8 x 32 x 500):
-// 23.8 and 20.0.
+// 128 unless said otherwise: 0.7 (60 tokens x 200 keys): 8.3 and 12.8 us, 1.7 (2 x 16
+// x 1000): 13.5 and 17.8, 3.4 (8 x 16 x 500): 15.3 and 17.5, 4.1 (20 x 4000): 20.4 and
+// 25.6, 5.0 (4 ragged x 17 x 1214, D = 64): 12.2 and 13.8, 5.2 (5 ragged x 11 x 3370,
+// 16 heads over 2): 13.4 and 26.0, 6.3 (4 x 60 x 500): 23.8 and 19.0, 6.7 (8 x 32 x
+// 500): 24.8 and 18.0.
 constexpr int kSmallRows = 240;
 constexpr int kSmallSteps = 6;
 bool small_work(const KvAttentionArgs& p, int group, int sms) {

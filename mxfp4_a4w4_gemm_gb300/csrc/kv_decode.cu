@@ -15,10 +15,10 @@
 // the copy brought, which is more than that memory passes in the time.
 //
 // What bounds it then are the instructions that decode, some 650 a step of 32
-// tokens and 8 rows at D = 128: 64 ragged requests of up to 8192 keys 69 us (4.1
+// tokens and 8 rows at D = 128: 64 ragged requests of up to 8192 keys 70 us (4.1
 // TB/s), 2 x 131000 keys x 16 rows 56 us (2.5 TB/s; a step of 16 rows has a fifth
 // more instructions than one of 8, but 255 registers leave 8 warps to hide each
-// other's latencies), one request of 1000 keys 8.7 us, most of it latency: launch,
+// other's latencies), one request of 1000 keys 8.4 us, most of it latency: launch,
 // lengths, page numbers and cells one after the other, then the joins.
 //
 // Keys and values are the M side, query rows the N side (8 per tile), so that
@@ -27,7 +27,8 @@
 //   O^T[dim, r]  += V^T[dim, token] P^T
 // * Keys: a thread's fragments are 8 consecutive dimensions of one token per
 //   32-block, one word.  Each block's product is taken with the bare codes and
-//   multiplied by the block's scale in fp32: exact for every scale.
+//   multiplied by the block's scale in fp32: exact for every scale below 2^104,
+//   beyond which the sums may overflow.
 // * Queries become FP16 times a power of two per row that puts the row's
 //   largest element at 2^14: exact for elements down to 2^-28 of it.
 // * Values need pairs of tokens in one word: two words of codes of neighbouring
@@ -64,8 +65,8 @@ constexpr int kStep = 32;                     // tokens of a step
 constexpr uint32_t kLeast = 1;
 constexpr int kFew = 4;
 // What a unit costs beside its steps, in steps: so many places of the line before its
-// first step hold no work.  1, 2, 3: 64 ragged requests x 8192 keys 71.9, 69.4, 70.4
-// us (0: 12 us more), 24 ragged x 5 tokens x 3001 20.6, 20.0, 20.4.
+// first step hold no work.  1, 2, 3: 64 ragged requests x 8192 keys 71.9, 69.9, 71.5
+// us (0: 12 us more), 24 ragged x 5 tokens x 3001 21.0, 20.6, 20.9.
 constexpr int kUnitCost = 2;
 constexpr int kWhole = 64;                    // places of the longest unit that a CTA may take whole
 constexpr int kMaxParts = 256;                // CTAs of a launch, and so parts of a cut unit
@@ -73,8 +74,9 @@ constexpr int kMaxParts = 256;                // CTAs of a launch, and so parts 
 template <int D, int NT>
 struct DecCfg {
   using Ch = KvChunk<D>;
-  // As many warps as the registers allow.  8, 12, 14, 16 warps, 64 ragged requests x 8192 keys, D = 128, 8 rows:
-  // 79.8, 74.3, 80.3, 71.1 us.  The second tile of 8 rows takes up to 255 registers at D = 128, and 12 warps spill.
+  // As many warps as the registers allow, nearly: at D = 128 the compiler reports 52 bytes of spill stores and 104 of
+  // loads (8 rows, 128 registers) and 12 and 28 (16 rows, 255); at D = 64 none.  8, 12, 14, 16 warps, 64 ragged requests
+  // x 8192 keys, D = 128, 8 rows: 79.8, 74.3, 80.3, 71.1 us; 16 rows with 12 warps 75.6 us where 8 took 57.4 (2 x 131000).
   static constexpr int WARPS = NT == 1 ? 16 : D == 64 ? 12 : 8;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int ROWS = 8 * NT;
@@ -815,8 +817,8 @@ int launch_one(const KvAttentionArgs& p, int grid, cudaStream_t st) {
 int launch_kv_decode(const KvAttentionArgs& p, int D, cudaStream_t st, int sms) {
   const int rows = p.max_q * (p.Hq / p.Hkv);
   // 16 rows at a time, but an odd number of 8-row blocks would waste half of one.  In blocks of 8 and of 16: 24 ragged
-  // requests x 20 rows 20.0 and 21.6 us (D = 64), 4 x 16384 keys x 24 rows 53.1 and 52.3 (D = 128), 2 x 131000 keys x
-  // 16 rows 59.2 and 55.5 (D = 128), 40.9 and 34.5 (D = 64)
+  // requests x 20 rows 20.5 and 22.5 us (D = 64), 4 x 16384 keys x 24 rows 54.1 and 55.9 (D = 128), 2 x 131000 keys x
+  // 16 rows 59.2 and 55.6 (D = 128), 43.0 and 35.8 (D = 64)
   const bool two = (rows + 7) / 8 % 2 == 0;
   // as many CTAs as there can be work for, one per SM at most
   const double units = static_cast<double>(p.B) * p.Hkv * ((rows + (two ? 15 : 7)) / (two ? 16 : 8));

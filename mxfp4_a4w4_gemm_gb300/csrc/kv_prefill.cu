@@ -25,7 +25,7 @@
 // has grown by more than 2^8, P staying below 2^8 meanwhile.
 //
 // A step does 512 R D flops for R rows and brings 136 D bytes: operations are the
-// floor.  4096 tokens x 16384 keys, 32 heads over 8 of 128: 679 us, 1417 TFLOP/s
+// floor.  4096 tokens x 16384 keys, 32 heads over 8 of 128: 683 us, 1408 TFLOP/s
 // (1911 measured for a plain BF16 product).  A step takes 1.8 us, of which the
 // products 58%; the rest is the chain scores -> softmax -> P of either tile, slowed by
 // the decoders, with which it shares the issue slots (64% of them taken).  Short
@@ -50,18 +50,17 @@ namespace {
 
 constexpr int kKeys = 128;                    // keys of a step
 constexpr int kRows = 256;                    // rows of a unit
-// Steps of a worker, at least.  1, 2, 4: 128 tokens x 1024 keys 39.7, 32.1, 32.9 us,
-// 128 x 128 keys 13.6, 13.9, 22.4; 2 and 4: 8 ragged x 100 x 1000 21.9 and 33.8 (all
-// shorter by now: parts are joined faster).
+// Steps of a worker, at least.  2 and 4: 128 tokens x 128 keys 12.0 and 20.4 us, 8 ragged
+// x 100 x 1000 19.6 and 30.4; 1 is like 2 (11.6, 19.7).
 constexpr uint32_t kLeastSteps = 2;
 // What a part adds to a join, in steps (128 KB through one SM).  A unit of n steps in runs of s takes s + 0.7 n / s
-// steps, so runs have sqrt(0.7 n) steps at least.  0, 0.4, 0.7, 1.2: 64 tokens x 8192 keys 49.9, 44.7, 39.6, 41.5 us;
+// steps, so runs have sqrt(0.7 n) steps at least.  0, 0.4, 0.7, 1.2: 64 tokens x 8192 keys 48.0, 45.2, 37.9, 42.2 us;
 // where there is work for more than that (128 x 8192, 50 x 50000) it makes no difference.
 constexpr float kJoinCost = 0.7f;
 // What a unit costs beside its steps (queries, output), in steps: so many places of
 // the line before its first step hold no work.  1, 2, 3: 12 ragged prompts x 700
-// tokens 35.6, 32.3, 32.9 us, 4 x 512 x 512 42.3, 39.4, 41.7, 3 ragged x 3205 47.0,
-// 39.0, 39.7 (0, with slower joins: 12 ragged prompts 46.8 where 2 took 39.0).
+// tokens 38.3, 33.8, 35.3 us, 4 x 512 x 512 39.1, 36.9, 38.4, 3 ragged x 3205 52.1,
+// 41.6, 41.1 (0, with slower joins: 12 ragged prompts 46.8 where 2 took 39.0).
 constexpr int kUnitCost = 2;
 constexpr int kMaxCtas = 512;
 // Keys that a unit's first row sees, up to which P has two terms: a step's, so that the
@@ -76,7 +75,8 @@ struct PreCfg {
   using Ch = KvChunk<D>;
   static constexpr int DEC_WARPS = 8;
   static constexpr int THREADS = 32 * (8 + DEC_WARPS + 4);         // five warpgroups, the last one half used
-  // registers a thread, by warpgroup: softmax, decoders, the rest; together what the CTA was launched with
+  // registers a thread, by warpgroup: softmax, decoders, the rest; together what the CTA was launched with.  The compiler
+  // reports 324 bytes of spill stores and 488 of loads at D = 128, 332 and 476 at D = 64 (all roles together)
   static constexpr int REGS = 96, REGS_SOFTMAX = 160, REGS_DECODE = 56, REGS_REST = 48;
   static_assert(256 * REGS_SOFTMAX + 256 * REGS_DECODE + 128 * REGS_REST <= THREADS * REGS, "register split");
   static constexpr int ATOM = 128 * 128;                         // 128 rows x 64 BF16, 128-byte swizzle
