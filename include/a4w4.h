@@ -173,6 +173,38 @@ int a4w4_moe_sort(const int32_t* topk_ids, int T, int topk, int E, int block_m,
                   int32_t* sorted_rows, int32_t* block_expert, int32_t* num_blocks,
                   void* ws, size_t ws_bytes, void* stream);
 
+/* Experts of each token and their weights from a router's logits, as a4w4_moe_sort
+ * and a4w4_moe_gemm2 take them (no counterpart on the source pages, which begin
+ * with the routed rows).
+ *   logits   row t holds E values at element t * stride: float (A4W4_F32) or BF16
+ *            (A4W4_BF16), aligned to its elements; stride >= E when T > 1
+ *   score    s = softmax over the E logits, or sigmoid of each
+ *   bias [E] float or NULL; c = s + bias decides who is chosen, s alone is the weight
+ *   groups   of E / groups consecutive experts; the strength of a group is the sum
+ *            of its group_top (1 or 2) largest c, and the top_groups strongest take
+ *            part.  groups = 1: no groups (group_top, top_groups are 1 or any others
+ *            that the limits allow)
+ *   topk_ids [T, topk], topk_weights [T, topk]  the topk largest c, largest first;
+ *            weights s * scale, or with renormalise = 1 s / (sum of the topk s) * scale
+ *   num_tokens [1] or NULL: on the device, rows from *num_tokens on get ids -1 and
+ *            weights 0 (rows of padding of a captured step; the sorts leave them out,
+ *            and what a4w4_moe_gemm2 writes to those rows of Y is not defined)
+ * Ties go to the lower index.  What is chosen, and the order, are those of the exact
+ * c (to about 2^-50 of the largest score): fp32 first, 64 bits for the rows whose
+ * order it leaves open (near ties of scores with a bias or of group strengths; some
+ * 1% of rows, and a few microseconds for them).  A NaN logit counts as -infinity, a
+ * logit of +infinity as the largest float, a NaN bias as -infinity; a row whose logits
+ * are all -infinity has scores 0, and weights whose sum is 0 are 0.  The weights are
+ * fp32 to about 2^-21.
+ * 1 <= E <= 2048, groups <= 32, E % groups == 0, two experts to a group at least
+ * where there are several, 1 <= topk <= 32, topk <= top_groups * E / groups, scale
+ * finite, T >= 0, T * topk <= 2^30. */
+enum { A4W4_F32 = 0, A4W4_BF16 = 1 };
+enum { A4W4_MOE_SCORE_SOFTMAX = 0, A4W4_MOE_SCORE_SIGMOID = 1 };
+int a4w4_moe_route(const void* logits, int logits_type, long long stride, const int32_t* num_tokens, int T, int E,
+                   int score, const float* bias, int groups, int group_top, int top_groups, int topk, int renormalise,
+                   float scale, int32_t* topk_ids, float* topk_weights, void* stream);
+
 /* The same sort, with the auxiliary gather/scatter arrays, in one launch for
  * up to 2048 routed rows and two beyond.
  * "[HIP] [CK] [FlyDSL] [Kernel] Extend MXFP4 GEMM1 replacement to A4W4",
@@ -359,6 +391,44 @@ int a4w4_kv_plan(const int32_t* past_lens, const int32_t* new_lens, int B, int p
 int a4w4_kv_append(const void* k_bf16, long long k_stride, const void* v_bf16, long long v_stride,
                    const int32_t* slot_map, int T, int Hkv, int D, void* cache, int num_pages, int page_size,
                    void* stream);
+
+/* Norms of query and key heads and their rotation by position, in one pass.
+ * For a head x of D dimensions (BF16):
+ *   y = x / sqrt(mean(x^2) + eps) * w      (w = q_weight or k_weight, float [D],
+ *                                           16-byte aligned; NULL: y = x)
+ *   the first rot_dim dimensions turn by the angles a_i = position * inv_freq[i],
+ *   i < rot_dim / 2: pairs (y[i], y[i + rot_dim/2]), or with interleaved = 1 the
+ *   neighbours (y[2i], y[2i+1]):  (u, v) -> (u cos a - v sin a, v cos a + u sin a)
+ * and the result is rounded to BF16 once.  Token t's Hq heads of queries start at
+ * element t * q_stride and are contiguous, its Hkv heads of keys likewise, and the
+ * results (all 16-byte aligned, strides multiples of 8 and at least the row when
+ * T > 1; all may be slices of one fused projection).  A result may take the place of
+ * its input (the same address and stride); else they must not overlap.
+ *   positions [T] int32; inv_freq [rot_dim / 2] float, finite, below 2^24 in
+ *   magnitude.  Angles are reduced exactly (to 2^-33 turns) before they are rounded.
+ * D 64 or 128, rot_dim a multiple of 16, 0 (norms only; positions and inv_freq may be
+ * NULL) to D; Hq, Hkv >= 0 (0: no such heads, its pointers may be NULL); eps finite
+ * and > 0 where there is a norm; T >= 0. */
+int a4w4_qk_norm_rope(const void* q_bf16, long long q_stride, const void* k_bf16, long long k_stride,
+                      const int32_t* positions, int T, int Hq, int Hkv, int D, const float* q_weight,
+                      const float* k_weight, float eps, const float* inv_freq, int rot_dim, int interleaved,
+                      void* q_out_bf16, long long q_out_stride, void* k_out_bf16, long long k_out_stride,
+                      void* stream);
+
+/* The same for the queries, with the normed and rotated keys and the values
+ * quantised into the cache: a4w4_qk_norm_rope and a4w4_kv_append in one pass, with one
+ * rounding fewer: keys are quantised from the unrounded result (their codes and
+ * scales are those of the exact value; where fp32 leaves open which, 64 bits decide),
+ * values as a4w4_kv_append does.  Values are rows like the keys.  A token whose slot is
+ * outside [0, num_pages * page_size) is skipped: neither its cells nor its row of
+ * q_out are written.  Two tokens with one slot leave either one's bytes.  positions
+ * and slot_map are what a4w4_kv_plan writes.  Hq may be 0, Hkv not; the rest as above
+ * and as in a4w4_kv_append. */
+int a4w4_kv_append_rope(const void* q_bf16, long long q_stride, const void* k_bf16, long long k_stride,
+                        const void* v_bf16, long long v_stride, const int32_t* positions, const int32_t* slot_map,
+                        int T, int Hq, int Hkv, int D, const float* q_weight, const float* k_weight, float eps,
+                        const float* inv_freq, int rot_dim, int interleaved, void* q_out_bf16, long long q_out_stride,
+                        void* cache, int num_pages, int page_size, void* stream);
 
 /* The BF16 values (exact) of the cache rows at T slots: k_out, v_out [T, Hkv, D],
  * zeros where the slot is outside [0, num_pages * page_size).  For handing a

@@ -35,6 +35,8 @@ SIGNATURES = {
     "a4w4_moe_max_blocks": (_c_int, [_c_int, _c_int, _c_int, _c_int]),
     "a4w4_moe_sort_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int]),
     "a4w4_moe_sort": (_c_int, [_i32p, _c_int, _c_int, _c_int, _c_int, _i32p, _i32p, _i32p, _vp, _c_size, _vp]),
+    "a4w4_moe_route": (_c_int, [_vp, _c_int, _c_ll, _i32p, _c_int, _c_int, _c_int, _vp, _c_int, _c_int, _c_int, _c_int,
+                                _c_int, ctypes.c_float, _i32p, _vp, _vp]),
     "a4w4_moe_sort_aux_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int]),
     "a4w4_moe_sort_aux": (_c_int, [_i32p, _c_int, _c_int, _c_int, _c_int, _i32p, _i32p, _i32p, _i32p, _i32p, _vp,
                                    _c_size, _vp]),
@@ -53,6 +55,11 @@ SIGNATURES = {
     "a4w4_kv_plan": (_c_int, [_i32p, _i32p, _c_int, _c_int, _i32p, _c_int, _i32p, _c_int, _i32p, _i32p, _i32p, _i32p,
                               _i32p, _i32p, _c_int, _i32p, _vp]),
     "a4w4_kv_append": (_c_int, [_vp, _c_ll, _vp, _c_ll, _i32p, _c_int, _c_int, _c_int, _vp, _c_int, _c_int, _vp]),
+    "a4w4_qk_norm_rope": (_c_int, [_vp, _c_ll, _vp, _c_ll, _i32p, _c_int, _c_int, _c_int, _c_int, _vp, _vp,
+                                   ctypes.c_float, _vp, _c_int, _c_int, _vp, _c_ll, _vp, _c_ll, _vp]),
+    "a4w4_kv_append_rope": (_c_int, [_vp, _c_ll, _vp, _c_ll, _vp, _c_ll, _i32p, _i32p, _c_int, _c_int, _c_int, _c_int,
+                                     _vp, _vp, ctypes.c_float, _vp, _c_int, _c_int, _vp, _c_ll, _vp, _c_int, _c_int,
+                                     _vp]),
     "a4w4_kv_read": (_c_int, [_vp, _c_int, _c_int, _i32p, _c_int, _c_int, _c_int, _vp, _vp, _vp]),
     "a4w4_kv_attention_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_int]),
     "a4w4_kv_attention": (_c_int, [_vp, _c_ll, _i32p, _c_int, _c_int, _c_int, _i32p, _i32p, _c_int, _vp, _c_int,
@@ -72,6 +79,8 @@ DEBUG_SIGNATURES = {
 }
 
 A4W4_GEMM_WEIGHT_PREFETCH = 1
+A4W4_F32, A4W4_BF16 = 0, 1
+A4W4_MOE_SCORE_SOFTMAX, A4W4_MOE_SCORE_SIGMOID = 0, 1
 A4W4_MOE_ACT_SWIGLU, A4W4_MOE_ACT_SILU = 0, 1
 A4W4_MOE_OUT_ROWS, A4W4_MOE_OUT_TILES = 0, 1
 
@@ -237,6 +246,24 @@ def a4w4_moe_sort(topk_ids, T, topk, E, block_m, sorted_rows, block_expert, num_
                                                 _stream(stream)))
 
 
+def _logits_ptr(x, stride):
+    """Rows of router logits, `stride` elements apart: only the rows themselves must be contiguous."""
+    if x is None or isinstance(x, int):
+        return x
+    if x.dim() != 2 or (x.size(1) > 1 and x.stride(1) != 1) or (x.size(0) > 1 and x.stride(0) != stride):
+        raise ValueError("logits must be a [T, E] tensor with contiguous rows and the given row stride")
+    return x.data_ptr()
+
+
+def a4w4_moe_route(logits, logits_type, stride, num_tokens, T, E, score, bias, groups, group_top, top_groups, topk,
+                   renormalise, scale, topk_ids, topk_weights, stream=None):
+    """logits: a [T, E] view with a row stride (in elements), float32 (A4W4_F32) or bfloat16 (A4W4_BF16)."""
+    _check("a4w4_moe_route",
+           lib().a4w4_moe_route(_logits_ptr(logits, stride), logits_type, stride, _ptr(num_tokens), T, E, score,
+                                _ptr(bias), groups, group_top, top_groups, topk, renormalise, scale, _ptr(topk_ids),
+                                _ptr(topk_weights), _stream(stream)))
+
+
 def a4w4_moe_sort_aux_workspace_bytes(T, topk, E):
     return lib().a4w4_moe_sort_aux_workspace_bytes(T, topk, E)
 
@@ -315,6 +342,28 @@ def a4w4_kv_append(k, k_stride, v, v_stride, slot_map, T, Hkv, D, cache, num_pag
     _check("a4w4_kv_append", lib().a4w4_kv_append(_rows_ptr(k, k_stride), k_stride, _rows_ptr(v, v_stride), v_stride,
                                                   _ptr(slot_map), T, Hkv, D, _ptr(cache), num_pages, page_size,
                                                   _stream(stream)))
+
+
+def a4w4_qk_norm_rope(q, q_stride, k, k_stride, positions, T, Hq, Hkv, D, q_weight, k_weight, eps, inv_freq, rot_dim,
+                      interleaved, q_out, q_out_stride, k_out, k_out_stride, stream=None):
+    """q, k and the results may be slices of one fused projection: [T, heads, D] views with a row stride (in elements)."""
+    _check("a4w4_qk_norm_rope",
+           lib().a4w4_qk_norm_rope(_rows_ptr(q, q_stride), q_stride, _rows_ptr(k, k_stride), k_stride, _ptr(positions),
+                                   T, Hq, Hkv, D, _ptr(q_weight), _ptr(k_weight), eps, _ptr(inv_freq), rot_dim,
+                                   interleaved, _rows_ptr(q_out, q_out_stride), q_out_stride,
+                                   _rows_ptr(k_out, k_out_stride), k_out_stride, _stream(stream)))
+
+
+def a4w4_kv_append_rope(q, q_stride, k, k_stride, v, v_stride, positions, slot_map, T, Hq, Hkv, D, q_weight, k_weight,
+                        eps, inv_freq, rot_dim, interleaved, q_out, q_out_stride, cache, num_pages, page_size,
+                        stream=None):
+    """q, k, v and q_out may be slices of one fused projection: [T, heads, D] views with a row stride (in elements)."""
+    _check("a4w4_kv_append_rope",
+           lib().a4w4_kv_append_rope(_rows_ptr(q, q_stride), q_stride, _rows_ptr(k, k_stride), k_stride,
+                                     _rows_ptr(v, v_stride), v_stride, _ptr(positions), _ptr(slot_map), T, Hq, Hkv, D,
+                                     _ptr(q_weight), _ptr(k_weight), eps, _ptr(inv_freq), rot_dim, interleaved,
+                                     _rows_ptr(q_out, q_out_stride), q_out_stride, _ptr(cache), num_pages, page_size,
+                                     _stream(stream)))
 
 
 def a4w4_kv_read(cache, num_pages, page_size, slot_map, T, Hkv, D, k_out, v_out, stream=None):

@@ -80,6 +80,41 @@ bool row_stride_ok(long long stride, int rows, int H, int D) {
   return stride % 8 == 0 && (rows <= 1 || stride >= static_cast<long long>(H) * D);
 }
 
+// Norms and rotation of heads: arguments that the two entry points share, checked and filled in.
+// inv_freq and positions are looked at where something turns only.
+bool rope_args(a4w4::RopeArgs& r, const void* q, long long q_stride, const void* k, long long k_stride,
+               const int32_t* positions, int T, int Hq, int Hkv, int D, const float* q_weight, const float* k_weight,
+               float eps, const float* inv_freq, int rot_dim, int interleaved, void* q_out, long long q_out_stride) {
+  if (T < 0 || Hq < 0 || Hkv < 0 || Hq > 65535 || Hkv > 65535 || (D != 64 && D != 128)) return false;
+  if (rot_dim < 0 || rot_dim > D || rot_dim % 16 != 0 || (interleaved != 0 && interleaved != 1)) return false;
+  if ((q_weight != nullptr && !aligned16(q_weight)) || (k_weight != nullptr && !aligned16(k_weight))) return false;
+  if ((q_weight != nullptr || k_weight != nullptr) && (!(eps > 0.f) || !(eps <= FLT_MAX))) return false;
+  if (Hq > 0 && (!row_stride_ok(q_stride, T, Hq, D) || !row_stride_ok(q_out_stride, T, Hq, D))) return false;
+  if (Hkv > 0 && !row_stride_ok(k_stride, T, Hkv, D)) return false;
+  if (T > 0) {
+    if (Hq > 0 && (!aligned16(q) || !aligned16(q_out))) return false;
+    if (Hkv > 0 && !aligned16(k)) return false;
+    if (rot_dim > 0 && (!aligned4(inv_freq) || !aligned4(positions))) return false;
+  }
+  r.q = static_cast<const uint16_t*>(q);
+  r.q_stride = q_stride;
+  r.k = static_cast<const uint16_t*>(k);
+  r.k_stride = k_stride;
+  r.positions = positions;
+  r.T = T; r.Hq = Hq; r.Hkv = Hkv;
+  r.q_weight = q_weight;
+  r.k_weight = k_weight;
+  r.eps = eps;
+  r.inv_freq = inv_freq;
+  r.rot = rot_dim;
+  r.interleaved = interleaved;
+  r.q_out = static_cast<uint16_t*>(q_out);
+  r.q_out_stride = q_out_stride;
+  return true;
+}
+
+int page_log2(int ps) { return ps == 16 ? 4 : ps == 32 ? 5 : ps == 64 ? 6 : 7; }
+
 cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
 size_t padded_k(int K) { return static_cast<size_t>((K + 255) / 256) * 256; }
@@ -287,6 +322,41 @@ int a4w4_moe_sort_aux(const int32_t* topk_ids, int T, int topk, int E, int block
   return rc == -1 ? A4W4_ERR_ARG : rc;
 }
 
+int a4w4_moe_route(const void* logits, int logits_type, long long stride, const int32_t* num_tokens, int T, int E,
+                   int score, const float* bias, int groups, int group_top, int top_groups, int topk, int renormalise,
+                   float scale, int32_t* topk_ids, float* topk_weights, void* stream) {
+  if (logits_type != A4W4_F32 && logits_type != A4W4_BF16) return A4W4_ERR_ARG;
+  if (score != A4W4_MOE_SCORE_SOFTMAX && score != A4W4_MOE_SCORE_SIGMOID) return A4W4_ERR_ARG;
+  if (T < 0 || E <= 0 || E > a4w4::kRouteMaxExperts || (T > 1 && stride < E)) return A4W4_ERR_ARG;
+  if (groups <= 0 || groups > 32 || E % groups != 0 || top_groups <= 0 || top_groups > groups ||
+      (group_top != 1 && group_top != 2))
+    return A4W4_ERR_ARG;
+  if (groups > 1 && E / groups < 2) return A4W4_ERR_ARG;
+  if (topk <= 0 || topk > 32 || topk > E / groups * top_groups) return A4W4_ERR_ARG;
+  if (renormalise != 0 && renormalise != 1) return A4W4_ERR_ARG;
+  if (!(scale >= -FLT_MAX) || !(scale <= FLT_MAX)) return A4W4_ERR_ARG;
+  if (static_cast<long long>(T) * topk > (1ll << 30)) return A4W4_ERR_ARG;
+  if ((bias != nullptr && !aligned4(bias)) || (num_tokens != nullptr && !aligned4(num_tokens))) return A4W4_ERR_ARG;
+  if (T > 0 && (!aligned4(topk_ids) || !aligned4(topk_weights) || logits == nullptr ||
+                (reinterpret_cast<uintptr_t>(logits) & (logits_type == A4W4_BF16 ? 1u : 3u)) != 0))
+    return A4W4_ERR_ARG;
+  const int sms = current_device_sms();
+  if (sms < 0) return sms;
+  if (T == 0) return A4W4_OK;
+  a4w4::RouteArgs p{};
+  p.logits = logits;
+  p.stride = stride;
+  p.count = num_tokens;
+  p.T = T; p.E = E;
+  p.bias = bias;
+  p.softmax = score == A4W4_MOE_SCORE_SOFTMAX;
+  p.groups = groups; p.group_top = group_top; p.top_groups = top_groups; p.topk = topk; p.renorm = renormalise;
+  p.scale = scale;
+  p.ids = topk_ids;
+  p.weights = topk_weights;
+  return a4w4::launch_moe_route(p, logits_type == A4W4_BF16, as_stream(stream));
+}
+
 size_t a4w4_moe_gemm1_workspace_bytes(int T, int D) {
   if (T <= 0 || D <= 0) return 0;
   return static_cast<size_t>(T) * (D / 2) + static_cast<size_t>(T) * (D / 32);
@@ -401,6 +471,48 @@ int a4w4_kv_read(const void* cache, int num_pages, int page_size, const int32_t*
   if (T == 0) return A4W4_OK;
   return a4w4::launch_kv_read(cache, num_pages, page_size, slot_map, T, Hkv, D, k_out_bf16, v_out_bf16,
                               as_stream(stream));
+}
+
+int a4w4_qk_norm_rope(const void* q_bf16, long long q_stride, const void* k_bf16, long long k_stride,
+                      const int32_t* positions, int T, int Hq, int Hkv, int D, const float* q_weight,
+                      const float* k_weight, float eps, const float* inv_freq, int rot_dim, int interleaved,
+                      void* q_out_bf16, long long q_out_stride, void* k_out_bf16, long long k_out_stride,
+                      void* stream) {
+  a4w4::RopeArgs r{};
+  if (!rope_args(r, q_bf16, q_stride, k_bf16, k_stride, positions, T, Hq, Hkv, D, q_weight, k_weight, eps, inv_freq,
+                 rot_dim, interleaved, q_out_bf16, q_out_stride))
+    return A4W4_ERR_ARG;
+  if (Hkv > 0 && (!row_stride_ok(k_out_stride, T, Hkv, D) || (T > 0 && !aligned16(k_out_bf16)))) return A4W4_ERR_ARG;
+  const int sms = current_device_sms();
+  if (sms < 0) return sms;
+  if (T == 0 || Hq + Hkv == 0) return A4W4_OK;
+  r.k_out = static_cast<uint16_t*>(k_out_bf16);
+  r.k_out_stride = k_out_stride;
+  return a4w4::launch_kv_rope(r, D, as_stream(stream), sms);
+}
+
+int a4w4_kv_append_rope(const void* q_bf16, long long q_stride, const void* k_bf16, long long k_stride,
+                        const void* v_bf16, long long v_stride, const int32_t* positions, const int32_t* slot_map,
+                        int T, int Hq, int Hkv, int D, const float* q_weight, const float* k_weight, float eps,
+                        const float* inv_freq, int rot_dim, int interleaved, void* q_out_bf16, long long q_out_stride,
+                        void* cache, int num_pages, int page_size, void* stream) {
+  a4w4::RopeArgs r{};
+  if (!rope_args(r, q_bf16, q_stride, k_bf16, k_stride, positions, T, Hq, Hkv, D, q_weight, k_weight, eps, inv_freq,
+                 rot_dim, interleaved, q_out_bf16, q_out_stride))
+    return A4W4_ERR_ARG;
+  if (num_pages <= 0 || !kv_shape_ok(num_pages, page_size, Hkv, D) || !row_stride_ok(v_stride, T, Hkv, D))
+    return A4W4_ERR_ARG;
+  if (!aligned16(cache) || (T > 0 && (!aligned16(v_bf16) || !aligned4(slot_map)))) return A4W4_ERR_ARG;
+  const int sms = current_device_sms();
+  if (sms < 0) return sms;
+  if (T == 0) return A4W4_OK;
+  r.v = static_cast<const uint16_t*>(v_bf16);
+  r.v_stride = v_stride;
+  r.slot_map = slot_map;
+  r.cache = static_cast<uint8_t*>(cache);
+  r.slots = num_pages * page_size;
+  r.page_lg = page_log2(page_size);
+  return a4w4::launch_kv_rope(r, D, as_stream(stream), sms);
 }
 
 size_t a4w4_kv_attention_workspace_bytes(int B, int max_q, int Hq, int Hkv, int D) {

@@ -139,6 +139,45 @@ int launch_moe_sort_aux(const int32_t* ids, int T, int topk, int E, int bm, int3
                         void* ws, cudaStream_t st, int sms, unsigned long long wait_ns, unsigned int* status);
 size_t moe_sort_aux_ws_bytes(int T, int topk, int E, int sms);
 
+// Routing of tokens to experts (route.cu).
+constexpr int kRouteMaxExperts = 2048;
+struct RouteArgs {
+  const void* logits;           // row t at t * stride
+  long long stride;
+  const int32_t* count;         // rows from *count on get no experts; nullptr: none
+  int T, E;
+  const float* bias;            // [E] or nullptr
+  int softmax, groups, group_top, top_groups, topk, renorm;
+  float scale;
+  int32_t* ids;                 // [T, topk]
+  float* weights;               // [T, topk]
+  // set by the launcher: rows can be read four values at a time; ceil(2^32 / (E / groups));
+  // lanes per group, and shared floats per token
+  int vectors;
+  unsigned int per_recip;
+  int skew, val_stride;
+};
+int launch_moe_route(RouteArgs p, int bf16, cudaStream_t st);
+
+// Norms and rotation of heads, to rows or to the cache (rope.cu).
+struct RopeArgs {
+  const uint16_t *q, *k, *v;
+  long long q_stride, k_stride, v_stride;
+  const int32_t *positions, *slot_map;
+  int T, Hq, Hkv;
+  const float *q_weight, *k_weight;      // [D] or nullptr: no norm
+  float eps;
+  const float* inv_freq;                 // [rot / 2]
+  int rot, interleaved;
+  uint16_t *q_out, *k_out;
+  long long q_out_stride, k_out_stride;
+  uint8_t* cache;                        // nullptr: keys go to k_out
+  int slots, page_lg;
+  int split;                             // warps per token (set by the launcher)
+};
+// -1: more work than it counts.
+int launch_kv_rope(RopeArgs p, int D, cudaStream_t st, int sms);
+
 // Paged MXFP4 key/value cache (kv.cu) and attention over it (kv_attention.cu).
 int launch_kv_plan(const int32_t* past_lens, const int32_t* new_lens, int B, int page_size, int32_t* block_table,
                    int max_pages, int32_t* free_ring, int ring_size, const int32_t* ring_state,
