@@ -132,6 +132,35 @@ int a4w4_gemm_a16w4(const void* A_bf16, int M, int K, const void* Wq, const void
                     void* C_bf16, unsigned int flags, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* 8-bit GEMM with a scale for each block of 128:  C[M, N] (BF16) = A[M, K] x W[N, K]^T
+ * (no counterpart on the source pages: the projections that a model with 4-bit experts
+ * keeps in 8 bits).
+ *   Weights: E4M3 codes with a float scale for each 128 x 128 block, Ws [N/128, K/128].
+ *   Activations: BF16, quantised here to E4M3 with a power-of-two scale for each row and
+ *   128 k's: 2^e with the smallest e >= -126 such that the block's largest magnitude is
+ *   at most 448 * 2^e; the code is x * 2^-e (exact) rounded to nearest, ties to even.  An
+ *   infinity or NaN makes its block's scale, and so its row of C, NaN.
+ *   C[m, n] = sum over blocks b of 2^e[m,b] * Ws[n/128, b] * (sum over b's k's of the
+ *   codes' products), every sum in fp32, in a fixed order: bitwise deterministic.
+ * N % 128 == 0, K % 128 == 0, M >= 1; rows >= M of C are never touched.
+ *
+ * Weight tiles: tile (nt, kt) = rows 128 nt .., k's 128 kt .. at byte (nt * (K/128) + kt) *
+ * 16384; byte b of row r at (r/8)*1024 + (r%8)*128 + ((b/16) ^ (r%8))*16 + b%16.
+ * a4w4_shuffle_w8_weight lays out a checkpoint's codes [N, K] (its scales are used as they
+ * are; W8 is not W_e4m3); a4w4_prepare_w8_weight quantises BF16 weights, Ws = largest
+ * magnitude / 448, code = w / Ws rounded to nearest. */
+size_t a4w4_w8_weight_bytes(int N, int K);   /* N * K */
+int a4w4_prepare_w8_weight(const void* W_bf16, int N, int K, void* W8, float* Ws, void* stream);
+int a4w4_shuffle_w8_weight(const void* W_e4m3, int N, int K, void* W8, void* stream);
+/* Larger M quantises the activations once into tiles in `workspace` (at least
+ * a4w4_gemm_w8a8_workspace_bytes(M, N, K), 16-byte aligned, overwritten before it is
+ * read); where that size is 0 it may be NULL.  flags: A4W4_GEMM_WEIGHT_PREFETCH as for
+ * a4w4_gemm_ex (of W8 alone). */
+size_t a4w4_gemm_w8a8_workspace_bytes(int M, int N, int K);
+int a4w4_gemm_w8a8(const void* A_bf16, int M, int K, const void* W8, const float* Ws, int N, void* C_bf16,
+                   void* workspace, size_t ws_bytes, unsigned int flags, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Standalone MXFP4 quantisation (plain layout).
  * "[gfx1250] Fuse A4W4 stage1 FP4 quantization", Summary (the standalone quant
  * kept as the fallback path).

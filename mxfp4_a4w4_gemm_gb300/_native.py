@@ -28,6 +28,11 @@ SIGNATURES = {
     "a4w4_gemm": (_c_int, [_vp, _c_int, _c_int, _vp, _vp, _c_int, _vp, _vp, _c_size, _vp]),
     "a4w4_gemm_ex": (_c_int, [_vp, _c_int, _c_int, _vp, _vp, _c_int, _vp, _vp, _c_size, ctypes.c_uint, _vp]),
     "a4w4_gemm_a16w4": (_c_int, [_vp, _c_int, _c_int, _vp, _vp, _c_int, _vp, ctypes.c_uint, _vp]),
+    "a4w4_w8_weight_bytes": (_c_size, [_c_int, _c_int]),
+    "a4w4_prepare_w8_weight": (_c_int, [_vp, _c_int, _c_int, _vp, _vp, _vp]),
+    "a4w4_shuffle_w8_weight": (_c_int, [_vp, _c_int, _c_int, _vp, _vp]),
+    "a4w4_gemm_w8a8_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int]),
+    "a4w4_gemm_w8a8": (_c_int, [_vp, _c_int, _c_int, _vp, _vp, _c_int, _vp, _vp, _c_size, ctypes.c_uint, _vp]),
     "a4w4_mxfp4_quant": (_c_int, [_vp, _c_int, _c_int, _vp, _vp, _vp]),
     "a4w4_moe_w1_codes_bytes": (_c_size, [_c_int, _c_int, _c_int]),
     "a4w4_moe_w1_scales_bytes": (_c_size, [_c_int, _c_int, _c_int]),
@@ -213,6 +218,28 @@ def a4w4_gemm_ex(A, M, K, Wq, Ws, N, C, workspace=None, ws_bytes=0, flags=0, str
 def a4w4_gemm_a16w4(A, M, K, Wq, Ws, N, C, flags=0, stream=None):
     _check("a4w4_gemm_a16w4", lib().a4w4_gemm_a16w4(_ptr(A), M, K, _ptr(Wq), _ptr(Ws), N, _ptr(C), flags,
                                                     _stream(stream)))
+
+
+def a4w4_w8_weight_bytes(N, K):
+    return lib().a4w4_w8_weight_bytes(N, K)
+
+
+def a4w4_prepare_w8_weight(W, N, K, W8, Ws, stream=None):
+    _check("a4w4_prepare_w8_weight",
+           lib().a4w4_prepare_w8_weight(_ptr(W), N, K, _ptr(W8), _ptr(Ws), _stream(stream)))
+
+
+def a4w4_shuffle_w8_weight(W, N, K, W8, stream=None):
+    _check("a4w4_shuffle_w8_weight", lib().a4w4_shuffle_w8_weight(_ptr(W), N, K, _ptr(W8), _stream(stream)))
+
+
+def a4w4_gemm_w8a8_workspace_bytes(M, N, K):
+    return lib().a4w4_gemm_w8a8_workspace_bytes(M, N, K)
+
+
+def a4w4_gemm_w8a8(A, M, K, W8, Ws, N, C, workspace=None, ws_bytes=0, flags=0, stream=None):
+    _check("a4w4_gemm_w8a8", lib().a4w4_gemm_w8a8(_ptr(A), M, K, _ptr(W8), _ptr(Ws), N, _ptr(C), _ptr(workspace),
+                                                   ws_bytes, flags, _stream(stream)))
 
 
 def a4w4_mxfp4_quant(X, rows, cols, q, scales, stream=None):

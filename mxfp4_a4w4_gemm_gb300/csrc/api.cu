@@ -245,6 +245,48 @@ int a4w4_gemm_a16w4(const void* A_bf16, int M, int K, const void* Wq, const void
                             (flags & A4W4_GEMM_WEIGHT_PREFETCH) ? 1 : 0);
 }
 
+size_t a4w4_w8_weight_bytes(int N, int K) {
+  if (N <= 0 || K <= 0) return 0;
+  return static_cast<size_t>(N) * K;
+}
+
+int a4w4_prepare_w8_weight(const void* W_bf16, int N, int K, void* W8, float* Ws, void* stream) {
+  if (N <= 0 || K <= 0 || N % 128 != 0 || K % 128 != 0) return A4W4_ERR_ARG;
+  if (!aligned16(W_bf16) || !aligned16(W8) || !aligned4(Ws)) return A4W4_ERR_ARG;
+  const int sms = current_device_sms();
+  if (sms < 0) return sms;
+  return a4w4::launch_prepare_w8(W_bf16, N, K, W8, Ws, as_stream(stream));
+}
+
+int a4w4_shuffle_w8_weight(const void* W_e4m3, int N, int K, void* W8, void* stream) {
+  if (N <= 0 || K <= 0 || N % 128 != 0 || K % 128 != 0) return A4W4_ERR_ARG;
+  if (!aligned16(W_e4m3) || !aligned16(W8) || W_e4m3 == W8) return A4W4_ERR_ARG;
+  const int sms = current_device_sms();
+  if (sms < 0) return sms;
+  return a4w4::launch_shuffle_w8(W_e4m3, N, K, W8, as_stream(stream), sms);
+}
+
+size_t a4w4_gemm_w8a8_workspace_bytes(int M, int N, int K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return a4w4::plan_w8a8(M, N, K, sizing_sms()).ws_bytes;
+}
+
+int a4w4_gemm_w8a8(const void* A_bf16, int M, int K, const void* W8, const float* Ws, int N, void* C_bf16,
+                   void* workspace, size_t ws_bytes, unsigned int flags, void* stream) {
+  if (M <= 0 || N <= 0 || K <= 0 || N % 128 != 0 || K % 128 != 0) return A4W4_ERR_ARG;
+  if (!aligned16(A_bf16) || !aligned16(W8) || !aligned4(Ws) || !aligned16(C_bf16)) return A4W4_ERR_ARG;
+  if ((flags & ~static_cast<unsigned int>(A4W4_GEMM_WEIGHT_PREFETCH)) != 0) return A4W4_ERR_ARG;
+  const int sms = current_device_sms();
+  if (sms < 0) return sms;
+  const a4w4::W8Plan plan = a4w4::plan_w8a8(M, N, K, sms);
+  if (plan.ws_bytes > 0 && (ws_bytes < plan.ws_bytes || !aligned16(workspace))) return A4W4_ERR_WORKSPACE;
+  unsigned int* status = status_ptr();
+  if (status == nullptr) return A4W4_ERR_LAUNCH;
+  return a4w4::launch_w8a8(plan, A_bf16, M, K, W8, Ws, N, C_bf16, workspace, as_stream(stream),
+                           g_wait_ns.load(std::memory_order_relaxed), status,
+                           (flags & A4W4_GEMM_WEIGHT_PREFETCH) ? 1 : 0, sms);
+}
+
 int a4w4_mxfp4_quant(const void* X_bf16, int rows, int cols, void* q, void* scales, void* stream) {
   if (rows <= 0 || cols <= 0 || cols % 32 != 0) return A4W4_ERR_ARG;
   if (!aligned16(X_bf16) || !aligned16(q) || scales == nullptr) return A4W4_ERR_ARG;

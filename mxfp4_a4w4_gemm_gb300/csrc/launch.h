@@ -178,6 +178,21 @@ struct RopeArgs {
 // -1: more work than it counts.
 int launch_kv_rope(RopeArgs p, int D, cudaStream_t st, int sms);
 
+// 8-bit block-scaled product (w8a8.cu).
+struct W8Plan {
+  int large;          // 1: 128 x 256 tiles, activations quantised once; 0: weight rows on the matrix unit's M side
+  int nx;             // tokens per thread block (not large)
+  int x_tiles, w_tiles, splits;
+  int kt;             // 128-wide blocks of K
+  int half_tiles;     // large: tiles of the last partial wave, run as halves
+  size_t ws_bytes;
+};
+W8Plan plan_w8a8(int M, int N, int K, int sms);
+int launch_w8a8(const W8Plan& plan, const void* A, int M, int K, const void* W8, const float* Ws, int N, void* C,
+                void* ws, cudaStream_t st, unsigned long long wait_ns, unsigned int* status, int prefetch_w, int sms);
+int launch_prepare_w8(const void* w_bf16, int N, int K, void* w8, float* ws, cudaStream_t st);
+int launch_shuffle_w8(const void* w_e4m3, int N, int K, void* w8, cudaStream_t st, int sms);
+
 // Paged MXFP4 key/value cache (kv.cu) and attention over it (kv_attention.cu).
 int launch_kv_plan(const int32_t* past_lens, const int32_t* new_lens, int B, int page_size, int32_t* block_table,
                    int max_pages, int32_t* free_ring, int ring_size, const int32_t* ring_state,

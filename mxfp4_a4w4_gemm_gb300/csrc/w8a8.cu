@@ -1,0 +1,856 @@
+// w8a8.cu -- 8-bit product with a scale for each block of 128 (include/a4w4.h,
+// a4w4_gemm_w8a8): BF16 activations quantised to E4M3 with a power-of-two scale per
+// row and 128 k's, E4M3 weights with a float scale per 128 x 128 block, BF16 output.
+//
+//   C[m, n] = sum over b of  2^e[m,b] ws[n/128, b]  sum over k in block b of a~[m,k] w[n,k]
+//
+// The inner sums are tcgen05.mma.kind::f8f6f4 products of 128 k's (four MMAs of K = 32)
+// into a fresh TMEM accumulator; since the weights' scales are any floats, each block's
+// sum is read back, scaled and added in fp32 registers while the next block's MMAs run
+// into the other accumulator.  Two kernels:
+//
+//   small  few tokens: 128 weight rows are the MMA's M side, 16, 32 or 64 tokens its N
+//          side, K split over the thread blocks of a cluster; activations are quantised
+//          in the kernel.  Bound by the weights' bytes.
+//   large  128 tokens x 256 weight rows per tile, one persistent thread block per SM,
+//          activations quantised once beforehand into tiles in the workspace.
+#include <cfloat>
+
+#include "device.cuh"
+#include "launch.h"
+
+namespace a4w4 {
+
+namespace {
+
+constexpr int kTile = 16384;                       // 128 rows x 128 bytes
+constexpr int kActTile = kTile + 512;              // activation tile: codes, then 128 row scales
+
+// ---------------------------------------------------------------------------
+// E4M3
+
+// 16 floats, already scaled -> 16 codes (round to nearest even, saturating).
+__device__ __forceinline__ uint4 cvt_e4m3x16(const float* y) {
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(w[q]) : "f"(y[4 * q]), "f"(y[4 * q + 1]), "f"(y[4 * q + 2]), "f"(y[4 * q + 3]));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ uint32_t max_abs_of(const uint4& a, const uint4& b) {
+  const uint32_t m = max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(a.x, a.y), max_abs_bf16x2(a.z, a.w)),
+                                    max_abs_bf16x2(max_abs_bf16x2(b.x, b.y), max_abs_bf16x2(b.z, b.w)));
+  return m & 0x7FFF7FFFu;
+}
+
+__device__ __forceinline__ void unpack16(const uint4& a, const uint4& b, float f, float* y) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    y[2 * u] = __uint_as_float(w[u] << 16) * f;
+    y[2 * u + 1] = __uint_as_float(w[u] & 0xFFFF0000u) * f;
+  }
+}
+
+// One row's block of 128 over eight neighbouring lanes (16 BF16 each, a and b):
+// amax 2^-e <= 448 with the smallest such e >= -126; codes of x 2^-e and the scale 2^e.
+// E4M3 is a floating type, so a power of two costs no precision against amax / 448, and
+// the scaling is exact.  An infinity or NaN in the block makes the scale NaN.
+__device__ __forceinline__ uint4 quant128(const uint4& a, const uint4& b, float* scale) {
+  uint32_t m = max_abs_of(a, b);
+  uint32_t amax = max(m & 0xFFFFu, m >> 16);
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+  // amax = 1.f 2^(E - 127), 448 = 1.75 2^8
+  const int e = max(static_cast<int>(amax >> 7) - 135 + ((amax & 0x7Fu) > 0x60u ? 1 : 0), -126);
+  float y[16];
+  unpack16(a, b, __uint_as_float(static_cast<uint32_t>(127 - e) << 23), y);
+  *scale = (amax >> 7) == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+  return cvt_e4m3x16(y);
+}
+
+// Place of 16-byte piece c of row r in a tile of 128-byte rows, 128-byte swizzle.
+__device__ __forceinline__ uint32_t tile_piece(int r, int c) {
+  return static_cast<uint32_t>((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
+}
+
+// Checkpoint codes [N, K] -> tiles (nt, kt) at (nt * KT + kt) * 16384.  One 16-byte piece a thread.
+__global__ void __launch_bounds__(256) w8_shuffle_kernel(const uint8_t* __restrict__ w, int K, int KT, long long pieces,
+                                                         uint8_t* __restrict__ w8) {
+  griddep_wait();
+  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+  const int per_row = K / 16;
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < pieces; i += stride) {
+    const long long n = i / per_row;
+    const int c = static_cast<int>(i - n * per_row);
+    const uint4 v = ld_global_nc_v4(w + i * 16);
+    const long long tile = (n >> 7) * KT + (c >> 3);
+    *reinterpret_cast<uint4*>(w8 + tile * kTile + tile_piece(static_cast<int>(n & 127), c & 7)) = v;
+  }
+}
+
+// BF16 weights: one thread block per 128 x 128 block: scale amax / 448, codes of w / scale.
+__global__ void __launch_bounds__(256) w8_prepare_kernel(const uint16_t* __restrict__ w, int K, int KT,
+                                                         uint8_t* __restrict__ w8, float* __restrict__ ws) {
+  __shared__ uint32_t s_max[8];
+  griddep_wait();
+  const long long tile = blockIdx.x;
+  const long long nt = tile / KT;
+  const int kt = static_cast<int>(tile - nt * KT);
+  uint4 v[4][2];
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 32 + (threadIdx.x >> 3), c = threadIdx.x & 7;
+    const uint16_t* src = w + (nt * 128 + r) * K + kt * 128 + c * 16;
+    v[i][0] = ld_global_nc_v4(src);
+    v[i][1] = ld_global_nc_v4(src + 8);
+    const uint32_t x = max_abs_of(v[i][0], v[i][1]);
+    m = max(m, max(x & 0xFFFFu, x >> 16));
+  }
+  m = __reduce_max_sync(0xFFFFFFFFu, m);
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, s_max[i]);
+  const float scale = __fdiv_rn(__uint_as_float(m << 16), 448.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 32 + (threadIdx.x >> 3), c = threadIdx.x & 7;
+    float y[16];
+    unpack16(v[i][0], v[i][1], 1.f, y);
+#pragma unroll
+    for (int u = 0; u < 16; ++u) y[u] = scale > 0.f ? __fdiv_rn(y[u], scale) : 0.f;
+    *reinterpret_cast<uint4*>(w8 + tile * kTile + tile_piece(r, c)) = cvt_e4m3x16(y);
+  }
+  if (threadIdx.x == 0) ws[tile] = scale;
+}
+
+// Activations -> tiles (x, kt) of 128 rows at (x * KT + kt) * kActTile; rows from M on are zero.
+// Eight lanes a block of 128, so a warp reads 1 KB of one row.
+__global__ void __launch_bounds__(256) w8_quant_tiles_kernel(const uint16_t* __restrict__ a, int M, int K, int KT,
+                                                             long long blocks, uint8_t* __restrict__ aq) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const long long blk = i >> 3;
+  const int c = static_cast<int>(i & 7);
+  const long long row = blk / KT;
+  const int kt = static_cast<int>(blk - row * KT);
+  uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
+  if (blk < blocks && row < M) {
+    const uint16_t* src = a + row * K + kt * 128 + c * 16;
+    v0 = ld_global_nc_v4(src);
+    v1 = ld_global_nc_v4(src + 8);
+  }
+  float scale;
+  const uint4 code = quant128(v0, v1, &scale);
+  if (blk >= blocks) return;
+  const int r = static_cast<int>(row & 127);
+  uint8_t* tile = aq + ((row >> 7) * KT + kt) * kActTile;
+  *reinterpret_cast<uint4*>(tile + tile_piece(r, c)) = code;
+  if (c == 0) *reinterpret_cast<float*>(tile + kTile + 4 * r) = row < M ? scale : 0.f;
+}
+
+// ---------------------------------------------------------------------------
+// Tensor core
+
+// E4M3 x E4M3, both K-major, fp32 D, M = 128, K = 32: formats 0 at bits 7 and 10.
+__device__ __forceinline__ uint32_t idesc_e4m3(uint32_t n) { return (1u << 4) | ((n >> 3) << 17) | ((128u >> 4) << 24); }
+
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// 32 or 16 consecutive fp32 columns of this thread's TMEM lane, not waited for.
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ unsigned long long pack2(uint32_t lo, uint32_t hi) {
+  unsigned long long d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float lo2(unsigned long long v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi2(unsigned long long v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+
+__device__ __forceinline__ uint32_t bf16x2_of(unsigned long long v) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo2(v), hi2(v));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// ---------------------------------------------------------------------------
+// Large
+
+struct W8LargeArgs {
+  const uint8_t* Aq;        // activation tiles
+  const uint8_t* W8;        // weight tiles
+  const float* Ws;          // [N / 128, KT]
+  uint16_t* C;              // [M, N] BF16
+  int M, N, KT;
+  int wide;                 // tiles of 256 weight rows per tile of tokens
+  int full_units;           // tiles 0 .. full_units - 1 (x-major) run whole
+  int split_units;          // then this many halves of the other wide tiles
+  int units;                // and the narrow tiles at the end of an odd N / 128
+  unsigned long long wait_ns;
+  unsigned int* status;
+};
+
+struct W8L {
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int STAGES = 4;
+  static constexpr int STAGE = 3 * kTile;
+  static constexpr int STG_PITCH = 80;                 // 32 BF16 columns and 16 bytes: 16-byte rows on different banks
+  static constexpr int OFF_STG = STAGES * STAGE;
+  static constexpr int OFF_BAR = OFF_STG + EPI_WARPS * 32 * STG_PITCH;
+  static constexpr int NBAR = 2 * STAGES + 5;          // full, empty; accumulators' full and empty; drain
+  static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
+  static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;
+  static_assert(SMEM_BYTES <= 232448, "shared memory");
+};
+
+struct W8Unit { int x, w, n; };                        // token tile, first 128-row weight tile, how many of them
+
+__device__ __forceinline__ W8Unit w8_unit(const W8LargeArgs& p, int u) {
+  if (u < p.full_units) return {u / p.wide, 2 * (u % p.wide), 2};
+  u -= p.full_units;
+  if (u < p.split_units) {
+    const int tile = p.full_units + (u >> 1);
+    return {tile / p.wide, 2 * (tile % p.wide) + (u & 1), 1};
+  }
+  return {u - p.split_units, 2 * p.wide, 1};
+}
+
+// One unit's blocks of K: COLS columns of this thread's row.  False: a wait gave up.
+template <int COLS>
+__device__ __forceinline__ bool w8_promote(const W8LargeArgs& p, uint32_t tmem, uint32_t acc_full, uint32_t acc_empty,
+                                           const uint8_t* row_scale, const float* block_scale, int& g,
+                                           unsigned long long* acc, volatile int* abort_flag) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < COLS / 2; ++i) acc[i] = 0ull;
+  float sa = *reinterpret_cast<const float*>(row_scale), sw = block_scale[0];
+  for (int kt = 0; kt < p.KT; ++kt, ++g) {
+    const uint32_t s = __float_as_uint(sa * sw);       // exact: sa is a power of two
+    const unsigned long long s2 = pack2(s, s);
+    if (kt + 1 < p.KT) {
+      sa = *reinterpret_cast<const float*>(row_scale + static_cast<long long>(kt + 1) * kActTile);
+      sw = block_scale[kt + 1];
+    }
+    const int b = g & 1;
+    if (!mbar_wait(acc_full + 8u * b, static_cast<uint32_t>(g >> 1) & 1u, abort_flag, p.wait_ns, p.status)) return false;
+    __syncwarp();
+    tc_fence_after();
+#pragma unroll
+    for (int c = 0; c < COLS; c += 32) {
+      uint32_t t[32];
+      tmem_ld32_issue(tmem + b * 256 + c, t);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[c / 2 + i] = fma2(pack2(t[2 * i], t[2 * i + 1]), s2, acc[c / 2 + i]);
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(acc_empty + 8u * b);
+  }
+  return true;
+}
+
+template <int COLS>
+__device__ __forceinline__ void w8_store(const W8LargeArgs& p, const unsigned long long* acc, uint8_t* stg, int row0, int col0) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < COLS; c += 32) {
+    uint4* mine = reinterpret_cast<uint4*>(stg + lane * W8L::STG_PITCH);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      mine[i] = make_uint4(bf16x2_of(acc[c / 2 + 4 * i]), bf16x2_of(acc[c / 2 + 4 * i + 1]),
+                           bf16x2_of(acc[c / 2 + 4 * i + 2]), bf16x2_of(acc[c / 2 + 4 * i + 3]));
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2), seg = lane & 3;
+      const uint4 v = *reinterpret_cast<const uint4*>(stg + r * W8L::STG_PITCH + seg * 16);
+      if (row0 + r < p.M)
+        *reinterpret_cast<uint4*>(p.C + static_cast<long long>(row0 + r) * p.N + col0 + c + seg * 8) = v;
+    }
+    __syncwarp();
+  }
+}
+
+//   warp 0      producer: per block of K one activation tile and two (one) weight tiles;
+//   warp 1      TMEM owner and MMA issuer: two accumulators of 256 columns in turn;
+//   warps 2-9   two per TMEM lane quadrant, a thread per token row and half of the
+//               columns: scale and add each block's sums, then BF16 rows.
+__global__ void __launch_bounds__(W8L::THREADS, 1) a4w4_w8a8_large_kernel(const W8LargeArgs p) {
+  using Cf = W8L;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = gridDim.x;
+  const unsigned long long drain_ns = p.wait_ns > 100000000ull ? p.wait_ns : 100000000ull;
+
+  const uint32_t full = base + Cf::OFF_BAR, empty = full + 8u * Cf::STAGES;
+  const uint32_t acc_full = empty + 8u * Cf::STAGES, acc_empty = acc_full + 16u, drain = acc_empty + 16u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cf::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cf::OFF_MISC + 8);
+  volatile int* never = reinterpret_cast<volatile int*>(smem + Cf::OFF_MISC + 16);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2 * Cf::STAGES + 2; ++s) mbar_init(full + 8u * s, 1);   // full, empty, acc_full
+    mbar_init(acc_empty, Cf::EPI_WARPS);
+    mbar_init(acc_empty + 8u, Cf::EPI_WARPS);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *never = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();                                       // the activation tiles come from the kernel before
+  griddep_launch_dependents();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_last();         // operands are read again by other tiles, from L2
+      int g = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; u < p.units && ok; u += G) {
+        const W8Unit t = w8_unit(p, u);
+        const uint8_t* a = p.Aq + static_cast<long long>(t.x) * p.KT * kActTile;
+        const uint8_t* w = p.W8 + static_cast<long long>(t.w) * p.KT * kTile;
+        for (int kt = 0; kt < p.KT; ++kt, ++g) {
+          const int s = g % Cf::STAGES;
+          if (!mbar_wait(empty + 8u * s, ((g / Cf::STAGES) & 1) ^ 1u, abort_flag, p.wait_ns, p.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = full + 8u * s, dst = base + s * Cf::STAGE;
+          mbar_arrive_expect_tx(fb, (1 + t.n) * kTile);
+          bulk_g2s(dst, a + static_cast<long long>(kt) * kActTile, kTile, fb, pol);
+          bulk_g2s(dst + kTile, w + static_cast<long long>(kt) * kTile, kTile, fb, pol);
+          if (t.n == 2) bulk_g2s(dst + 2 * kTile, w + static_cast<long long>(p.KT + kt) * kTile, kTile, fb, pol);
+        }
+      }
+      // every copy issued lands before the shared memory is released
+      for (int j = (g > Cf::STAGES ? g - Cf::STAGES : 0); j < g; ++j)
+        mbar_wait(full + 8u * (j % Cf::STAGES), (j / Cf::STAGES) & 1u, never, drain_ns, p.status);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint64_t adesc0 = sdesc_sw128(base), bdesc0 = sdesc_sw128(base + kTile);
+      int g = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; u < p.units && ok; u += G) {
+        const uint32_t idesc = idesc_e4m3(128u * w8_unit(p, u).n);
+        for (int kt = 0; kt < p.KT; ++kt, ++g) {
+          const int s = g % Cf::STAGES, b = g & 1;
+          // the accumulator's sums of two blocks ago have been read
+          if ((g >= 2 && !mbar_wait(acc_empty + 8u * b, static_cast<uint32_t>((g >> 1) - 1) & 1u, abort_flag, p.wait_ns, p.status)) ||
+              !mbar_wait(full + 8u * s, (g / Cf::STAGES) & 1u, abort_flag, p.wait_ns, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = adesc0 + ((s * Cf::STAGE) >> 4), bd = bdesc0 + ((s * Cf::STAGE) >> 4);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) mma_e4m3(tmem + b * 256, ad + 2 * ks, bd + 2 * ks, idesc, ks > 0 ? 1u : 0u);
+          mma_commit(empty + 8u * s);
+          mma_commit(acc_full + 8u * b);
+        }
+      }
+      // TMEM is released only after every MMA issued has completed
+      mma_commit(drain);
+      mbar_wait(drain, 0, never, drain_ns, p.status);
+    }
+  } else {
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    uint8_t* stg = smem + Cf::OFF_STG + (warp - 2) * 32 * Cf::STG_PITCH;
+    unsigned long long acc[64];
+    int g = 0;
+    for (int u = blockIdx.x; u < p.units; u += G) {
+      const W8Unit t = w8_unit(p, u);
+      const uint8_t* sa = p.Aq + static_cast<long long>(t.x) * p.KT * kActTile + kTile + 4 * (q * 32 + lane);
+      const int row0 = t.x * 128 + q * 32;
+      if (t.n == 2) {
+        if (!w8_promote<128>(p, tq + half * 128, acc_full, acc_empty, sa,
+                             p.Ws + static_cast<long long>(t.w + half) * p.KT, g, acc, abort_flag))
+          break;
+        w8_store<128>(p, acc, stg, row0, (t.w + half) * 128);
+      } else {
+        if (!w8_promote<64>(p, tq + half * 64, acc_full, acc_empty, sa, p.Ws + static_cast<long long>(t.w) * p.KT, g,
+                            acc, abort_flag))
+          break;
+        w8_store<64>(p, acc, stg, row0, t.w * 128 + half * 64);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Small
+
+struct W8SmallArgs {
+  const uint16_t* A;        // [M, K] BF16
+  const uint8_t* W8;
+  const float* Ws;
+  uint16_t* C;
+  int M, N, K, KT, splits;
+  int prefetch_w;           // 1: weights may be read before the previous grid on the stream completes
+  unsigned long long wait_ns;
+  unsigned int* status;
+};
+
+template <int NX>
+struct W8S {
+  static constexpr int RING = 4;                       // tiles in flight, of weights and of activations
+  static constexpr int THREADS = 64 + 128 + 128;       // two single warps, producers, promoters
+  static constexpr int X_STAGE = NX * 128;
+  static constexpr int OFF_X = RING * kTile;
+  static constexpr int OFF_SCALE = OFF_X + RING * X_STAGE;
+  static constexpr int OFF_BAR = OFF_SCALE + RING * NX * 4;
+  static constexpr int NBAR = 2 * RING + 8;            // full_w, empty_w; full_x, empty_x; acc full x 2, empty x 2; red; drain
+  static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
+  static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;
+  static constexpr int ACC_COLS = NX;
+  static constexpr int TMEM_COLS = 2 * NX <= 32 ? 32 : 2 * NX <= 64 ? 64 : 128;
+  // After the last block the rings' bytes serve the reduction: this block's partial sums,
+  // then up to 16 senders' shares of this block's slice ((G + S) groups of 16 bytes, G = 32 NX)
+  static constexpr int OFF_PUSH = NX * 512;
+  static_assert(OFF_PUSH + NX * 512 + 256 <= OFF_SCALE, "the reduction fits the rings");
+  static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "two thread blocks on an SM");
+};
+
+//   warp 0      weight producer;
+//   warp 1      TMEM owner and MMA issuer (two accumulators of NX columns in turn);
+//   warps 2-5   activations: rounds of up to RING blocks of K, eight lanes per row and block;
+//   warps 6-9   a thread per weight row: scale and add each block's NX sums.
+// Then all of warps 2-9 reduce over the cluster: slice r of the 128 x NX sums belongs to
+// rank r, everyone sends its share there, the owner adds in rank order.
+template <int NX>
+__global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(const W8SmallArgs p) {
+  using Cf = W8S<NX>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w_tile = blockIdx.x, split = blockIdx.z;
+  const int kt0 = static_cast<int>(static_cast<long long>(split) * p.KT / p.splits);
+  const int kt1 = static_cast<int>(static_cast<long long>(split + 1) * p.KT / p.splits);
+  const int nk = kt1 - kt0;
+  const int m0 = blockIdx.y * NX;
+  const int mvalid = min(NX, p.M - m0);
+  const unsigned long long drain_ns = p.wait_ns > 100000000ull ? p.wait_ns : 100000000ull;
+
+  const uint32_t full_w = base + Cf::OFF_BAR, empty_w = full_w + 8u * Cf::RING;
+  const uint32_t full_x = empty_w + 8u * Cf::RING, empty_x = full_x + 8u;
+  const uint32_t acc_full = empty_x + 8u, acc_empty = acc_full + 16u;
+  const uint32_t red_bar = acc_empty + 16u, drain = red_bar + 8u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cf::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cf::OFF_MISC + 8);
+  volatile int* never = reinterpret_cast<volatile int*>(smem + Cf::OFF_MISC + 16);
+  volatile int* owner_ready = reinterpret_cast<volatile int*>(smem + Cf::OFF_MISC + 24);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2 * Cf::RING; ++s) mbar_init(full_w + 8u * s, 1);
+    mbar_init(full_x, 128);
+    mbar_init(empty_x, 1 + 4);                         // the MMAs' commit, and the promoters, who read the scales
+    mbar_init(acc_full, 1);
+    mbar_init(acc_full + 8u, 1);
+    mbar_init(acc_empty, 4);
+    mbar_init(acc_empty + 8u, 4);
+    mbar_init(red_bar, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *never = 0;
+    *owner_ready = 0;
+    fence_barrier_init();
+    if (p.splits > 1) {
+      const int S = p.splits, G = mvalid * 32, rank = static_cast<int>(cluster_ctarank());
+      const int g0 = static_cast<int>(static_cast<long long>(rank) * G / S);
+      const int g1 = static_cast<int>(static_cast<long long>(rank + 1) * G / S);
+      mbar_arrive_expect_tx(red_bar, static_cast<uint32_t>(S * (g1 - g0) * 16));
+    }
+  }
+  // rows of tokens that do not exist: codes and scales zero, never written again
+  for (int i = threadIdx.x; i < (Cf::OFF_BAR - Cf::OFF_X) / 16; i += Cf::THREADS)
+    reinterpret_cast<uint4*>(smem + Cf::OFF_X)[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), Cf::TMEM_COLS);
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  griddep_launch_dependents();                         // (the next grid waits for the whole of this one)
+  if (warp == 0) {
+    if (lane == 0) {
+      if (!p.prefetch_w) griddep_wait();
+      const uint64_t pol = policy_evict_first();       // every weight byte is read once (per tile of tokens)
+      const uint8_t* w = p.W8 + (static_cast<long long>(w_tile) * p.KT + kt0) * kTile;
+      int i = 0;
+      for (; i < nk; ++i) {
+        const int s = i % Cf::RING;
+        if (!mbar_wait(empty_w + 8u * s, ((i / Cf::RING) & 1) ^ 1u, abort_flag, p.wait_ns, p.status)) break;
+        mbar_arrive_expect_tx(full_w + 8u * s, kTile);
+        bulk_g2s(base + s * kTile, w + static_cast<long long>(i) * kTile, kTile, full_w + 8u * s, pol);
+      }
+      for (int j = (i > Cf::RING ? i - Cf::RING : 0); j < i; ++j)
+        mbar_wait(full_w + 8u * (j % Cf::RING), (j / Cf::RING) & 1u, never, drain_ns, p.status);
+    }
+    __syncwarp();
+    griddep_wait();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint64_t adesc0 = sdesc_sw128(base), bdesc0 = sdesc_sw128(base + Cf::OFF_X);
+      const uint32_t idesc = idesc_e4m3(NX);
+      bool ok = true;
+      for (int i = 0; i < nk && ok; ++i) {
+        const int s = i % Cf::RING, b = i & 1;
+        if (s == 0) ok = mbar_wait(full_x, static_cast<uint32_t>(i / Cf::RING) & 1u, abort_flag, p.wait_ns, p.status);
+        ok = ok && (i < 2 || mbar_wait(acc_empty + 8u * b, static_cast<uint32_t>((i >> 1) - 1) & 1u, abort_flag, p.wait_ns, p.status));
+        ok = ok && mbar_wait(full_w + 8u * s, (i / Cf::RING) & 1u, abort_flag, p.wait_ns, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t ad = adesc0 + ((s * kTile) >> 4), bd = bdesc0 + ((s * Cf::X_STAGE) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_e4m3(tmem + b * Cf::ACC_COLS, ad + 2 * ks, bd + 2 * ks, idesc, ks > 0 ? 1u : 0u);
+        mma_commit(empty_w + 8u * s);
+        if (s == Cf::RING - 1) mma_commit(empty_x);
+        mma_commit(acc_full + 8u * b);
+      }
+      mma_commit(drain);
+      mbar_wait(drain, 0, never, drain_ns, p.status);
+    }
+    __syncwarp();
+    griddep_wait();
+  } else {
+    griddep_wait();                                    // A is written by the previous grid
+    int ready = nk > 0;
+    if (warp < 6) {
+      // ---------------- activations ----------------
+      const int pt = threadIdx.x - 64, c = pt & 7;
+      constexpr int CH = 4;                            // blocks of 128 in flight per eight lanes
+      float* s_scale = reinterpret_cast<float*>(smem + Cf::OFF_SCALE);
+      bool stop = false;
+      for (int r0 = 0, rnd = 0; r0 < nk && !stop; r0 += Cf::RING, ++rnd) {
+        const int total = min(nk - r0, Cf::RING) * mvalid;
+        bool waited = rnd == 0;
+        for (int t0 = pt >> 3; t0 < total + (pt >> 3) && !stop; t0 += 16 * CH) {   // (warps stay whole)
+          uint4 v[CH][2];
+#pragma unroll
+          for (int h = 0; h < CH; ++h) {
+            const int t = t0 + 16 * h, j = t / mvalid, r = t - j * mvalid;
+            v[h][0] = v[h][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (t < total) {
+              const uint16_t* src = p.A + static_cast<long long>(m0 + r) * p.K + (kt0 + r0 + j) * 128 + c * 16;
+              v[h][0] = ld_global_nc_v4(src);
+              v[h][1] = ld_global_nc_v4(src + 8);
+            }
+          }
+          if (!waited) {                               // the round's places are free again
+            waited = true;
+            if (!mbar_wait(empty_x, static_cast<uint32_t>(rnd - 1) & 1u, abort_flag, p.wait_ns, p.status)) stop = true;
+          }
+          if (__any_sync(0xFFFFFFFFu, stop)) {
+            stop = true;
+            break;
+          }
+#pragma unroll
+          for (int h = 0; h < CH; ++h) {
+            const int t = t0 + 16 * h, j = t / mvalid, r = t - j * mvalid;
+            float scale;
+            const uint4 code = quant128(v[h][0], v[h][1], &scale);
+            if (t < total) {
+              *reinterpret_cast<uint4*>(smem + Cf::OFF_X + j * Cf::X_STAGE + tile_piece(r, c)) = code;
+              if (c == 0) s_scale[j * NX + r] = scale;
+            }
+          }
+        }
+        if (!stop) {
+          fence_proxy_async_smem();
+          mbar_arrive(full_x);
+        }
+      }
+      ready = ready && !stop;
+    } else {
+      // ---------------- promotion ----------------
+      const int q = warp & 3;
+      const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
+      const float* block_scale = p.Ws + static_cast<long long>(w_tile) * p.KT + kt0;
+      unsigned long long acc[NX / 2];
+#pragma unroll
+      for (int i = 0; i < NX / 2; ++i) acc[i] = 0ull;
+      for (int i = 0; i < nk; ++i) {
+        const int s = i % Cf::RING, b = i & 1;
+        const uint32_t sw = __float_as_uint(block_scale[i]);
+        const unsigned long long sw2 = pack2(sw, sw);
+        // the scales' writes are seen through the producers' own barrier
+        if ((s == 0 && !mbar_wait(full_x, static_cast<uint32_t>(i / Cf::RING) & 1u, abort_flag, p.wait_ns, p.status)) ||
+            !mbar_wait(acc_full + 8u * b, static_cast<uint32_t>(i >> 1) & 1u, abort_flag, p.wait_ns, p.status)) {
+          ready = 0;
+          break;
+        }
+        __syncwarp();
+        tc_fence_after();
+        const ulonglong2* sa = reinterpret_cast<const ulonglong2*>(smem + Cf::OFF_SCALE + s * NX * 4);
+#pragma unroll
+        for (int c = 0; c < NX; c += 16) {
+          float t[16];
+          tmem_ld16(tq + b * Cf::ACC_COLS + c, t);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const ulonglong2 s2 = sa[c / 4 + u];       // four tokens' scales
+            acc[c / 2 + 2 * u] = fma2(pack2(__float_as_uint(t[4 * u]), __float_as_uint(t[4 * u + 1])), mul2(s2.x, sw2),
+                                      acc[c / 2 + 2 * u]);
+            acc[c / 2 + 2 * u + 1] = fma2(pack2(__float_as_uint(t[4 * u + 2]), __float_as_uint(t[4 * u + 3])),
+                                          mul2(s2.y, sw2), acc[c / 2 + 2 * u + 1]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(acc_empty + 8u * b);
+          if (s == Cf::RING - 1) mbar_arrive(empty_x);
+        }
+      }
+      ready = __all_sync(0xFFFFFFFFu, ready);
+      // weight row q * 32 + lane of every token: partial [token][weight row] over the drained ring,
+      // or, where nothing is to be reduced, BF16 (a warp writes 64 bytes of a token's row)
+      const int lrow = q * 32 + lane;
+      if (ready && p.splits == 1) {
+#pragma unroll
+        for (int i = 0; i < NX; ++i)
+          if (i < mvalid)
+            p.C[static_cast<long long>(m0 + i) * p.N + w_tile * 128 + lrow] =
+                __bfloat16_as_ushort(__float2bfloat16_rn(i & 1 ? hi2(acc[i / 2]) : lo2(acc[i / 2])));
+      } else if (ready) {
+        float* red = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int i = 0; i < NX; ++i)
+          if (i < mvalid) red[i * 128 + lrow] = i & 1 ? hi2(acc[i / 2]) : lo2(acc[i / 2]);
+      }
+    }
+    if (p.splits > 1 && !ready) *abort_flag = 1;       // this block's sums are not whole
+  }
+
+  if (p.splits > 1) {
+    // every block of the cluster is through with its rings (which the shares now land in)
+    __syncthreads();
+    cluster_sync_all();
+    if (warp >= 2) {
+      constexpr int P = 256;
+      const int et = threadIdx.x - 64;
+      const int S = p.splits, G = mvalid * 32, slot = (G + S - 1) / S;
+      const uint32_t rank = cluster_ctarank();
+      const float4* red4 = reinterpret_cast<const float4*>(smem);
+      // group g (four weight rows of a token) belongs to o = max{o : floor(o G / S) <= g}; sent
+      // whatever happened before, so that every owner's byte count completes
+      for (int g = et; g < G; g += P) {
+        const int o = static_cast<int>((static_cast<long long>(g + 1) * S - 1) / G);
+        const int og0 = static_cast<int>(static_cast<long long>(o) * G / S);
+        const uint32_t dst = cluster_map_shared(
+            base + Cf::OFF_PUSH + static_cast<uint32_t>((static_cast<int>(rank) * slot + (g - og0)) * 16), static_cast<uint32_t>(o));
+        st_async_v4(dst, red4[g], cluster_map_shared(red_bar, static_cast<uint32_t>(o)));
+      }
+      if (et == 0) {
+        const unsigned long long lim = 32ull * drain_ns;
+        *owner_ready = mbar_wait_cluster(red_bar, 0, lim, p.status) && !*abort_flag ? 1 : 0;
+      }
+      named_bar_sync(3, P);
+      if (*owner_ready) {
+        const int g0 = static_cast<int>(static_cast<long long>(rank) * G / S);
+        const int g1 = static_cast<int>(static_cast<long long>(rank + 1) * G / S);
+        const float4* push = reinterpret_cast<const float4*>(smem + Cf::OFF_PUSH);
+        for (int g = g0 + et; g < g1; g += P) {
+          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int c = 0; c < S; ++c) {
+            const float4 v = push[c * slot + (g - g0)];
+            sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
+          }
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x, sum.y), hi = __floats2bfloat162_rn(sum.z, sum.w);
+          uint2 o;
+          o.x = *reinterpret_cast<const uint32_t*>(&lo);
+          o.y = *reinterpret_cast<const uint32_t*>(&hi);
+          *reinterpret_cast<uint2*>(p.C + static_cast<long long>(m0 + (g >> 5)) * p.N + w_tile * 128 + (g & 31) * 4) = o;
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, Cf::TMEM_COLS);
+  }
+}
+
+template <int NX>
+int launch_small_nx(const W8SmallArgs& a, dim3 grid, cudaStream_t st) {
+  using Cf = W8S<NX>;
+  auto kern = a4w4_w8a8_small_kernel<NX>;
+  static std::atomic<unsigned long long> attr_devs{0};   // bit d: attributes set on device d
+  if (ensure_func_attrs(attr_devs, [&] {
+        // clusters of up to 16 thread blocks (more than the portable 8)
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM_BYTES) == cudaSuccess &&
+               cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+      }) != 0)
+    return -4;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(Cf::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = Cf::SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = 1;
+  attrs[1].val.clusterDim.y = 1;
+  attrs[1].val.clusterDim.z = static_cast<unsigned>(a.splits);
+  cfg.attrs = attrs;
+  cfg.numAttrs = a.splits > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return -4;
+  return cudaGetLastError() == cudaSuccess ? 0 : -4;
+}
+
+}  // namespace
+
+W8Plan plan_w8a8(int M, int N, int K, int sms) {
+  W8Plan pl{};
+  pl.kt = K / 128;
+  pl.w_tiles = N / 128;
+  const int small_nx = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  pl.large = M > 128;
+  if (pl.large) {
+    pl.x_tiles = (M + 127) / 128;
+    const long long tiles = static_cast<long long>(pl.x_tiles) * (pl.w_tiles / 2), rest = tiles % sms;
+    // the last, partial wave's tiles run as halves where they then still are one wave
+    pl.half_tiles = 2 * rest <= sms ? static_cast<int>(rest) : 0;
+    pl.ws_bytes = static_cast<size_t>(pl.x_tiles) * pl.kt * kActTile;
+    return pl;
+  }
+  pl.nx = small_nx;
+  pl.x_tiles = (M + pl.nx - 1) / pl.nx;
+  const int blocks = pl.w_tiles * pl.x_tiles;
+  pl.splits = 2 * sms / (blocks > 0 ? blocks : 1);      // two thread blocks on every SM
+  if (pl.splits > 16) pl.splits = 16;
+  if (pl.splits > pl.kt) pl.splits = pl.kt;
+  if (pl.splits < 1) pl.splits = 1;
+  return pl;
+}
+
+int launch_w8a8(const W8Plan& pl, const void* A, int M, int K, const void* W8, const float* Ws, int N, void* C,
+                void* ws, cudaStream_t st, unsigned long long wait_ns, unsigned int* status, int prefetch_w, int sms) {
+  if (!pl.large) {
+    W8SmallArgs a{};
+    a.A = static_cast<const uint16_t*>(A);
+    a.W8 = static_cast<const uint8_t*>(W8);
+    a.Ws = Ws;
+    a.C = static_cast<uint16_t*>(C);
+    a.M = M; a.N = N; a.K = K; a.KT = pl.kt; a.splits = pl.splits;
+    a.prefetch_w = prefetch_w;
+    a.wait_ns = wait_ns;
+    a.status = status;
+    const dim3 grid(pl.w_tiles, pl.x_tiles, pl.splits);
+    return pl.nx == 16 ? launch_small_nx<16>(a, grid, st) : pl.nx == 32 ? launch_small_nx<32>(a, grid, st)
+                                                                       : launch_small_nx<64>(a, grid, st);
+  }
+  const long long blocks = static_cast<long long>(pl.x_tiles) * 128 * pl.kt;
+  const long long grid = (blocks * 8 + 255) / 256;
+  if (grid > INT32_MAX) return -1;
+  int rc = launch_pdl(w8_quant_tiles_kernel, static_cast<int>(grid), 256, st, static_cast<const uint16_t*>(A), M, K,
+                      pl.kt, blocks, static_cast<uint8_t*>(ws));
+  if (rc != 0) return rc;
+  static std::atomic<unsigned long long> attr_devs{0};   // bit d: attribute set on device d
+  if (ensure_func_attrs(attr_devs, [&] {
+        return cudaFuncSetAttribute(a4w4_w8a8_large_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    W8L::SMEM_BYTES) == cudaSuccess;
+      }) != 0)
+    return -4;
+  W8LargeArgs a{};
+  a.Aq = static_cast<const uint8_t*>(ws);
+  a.W8 = static_cast<const uint8_t*>(W8);
+  a.Ws = Ws;
+  a.C = static_cast<uint16_t*>(C);
+  a.M = M; a.N = N; a.KT = pl.kt;
+  a.wide = pl.w_tiles / 2;
+  const long long tiles = static_cast<long long>(pl.x_tiles) * a.wide;
+  const long long units = tiles + pl.half_tiles + (pl.w_tiles % 2 ? pl.x_tiles : 0);
+  if (units > INT32_MAX) return -1;
+  a.full_units = static_cast<int>(tiles) - pl.half_tiles;
+  a.split_units = 2 * pl.half_tiles;
+  a.units = static_cast<int>(units);
+  a.wait_ns = wait_ns;
+  a.status = status;
+  return launch_pdl_smem(a4w4_w8a8_large_kernel, a.units < sms ? a.units : sms, W8L::THREADS, W8L::SMEM_BYTES, st, a);
+}
+
+int launch_prepare_w8(const void* w_bf16, int N, int K, void* w8, float* ws, cudaStream_t st) {
+  const long long tiles = static_cast<long long>(N / 128) * (K / 128);
+  if (tiles > INT32_MAX) return -1;
+  return launch_pdl(w8_prepare_kernel, static_cast<int>(tiles), 256, st, static_cast<const uint16_t*>(w_bf16), K, K / 128,
+                    static_cast<uint8_t*>(w8), ws);
+}
+
+int launch_shuffle_w8(const void* w_e4m3, int N, int K, void* w8, cudaStream_t st, int sms) {
+  const long long pieces = static_cast<long long>(N) * (K / 16);
+  const long long most = static_cast<long long>(sms) * 8, want = (pieces + 255) / 256;
+  return launch_pdl(w8_shuffle_kernel, static_cast<int>(want < most ? want : most), 256, st,
+                    static_cast<const uint8_t*>(w_e4m3), K, K / 128, pieces, static_cast<uint8_t*>(w8));
+}
+
+}  // namespace a4w4
