@@ -85,7 +85,7 @@ bool row_stride_ok(long long stride, int rows, int H, int D) {
 bool rope_args(a4w4::RopeArgs& r, const void* q, long long q_stride, const void* k, long long k_stride,
                const int32_t* positions, int T, int Hq, int Hkv, int D, const float* q_weight, const float* k_weight,
                float eps, const float* inv_freq, int rot_dim, int interleaved, void* q_out, long long q_out_stride) {
-  if (T < 0 || Hq < 0 || Hkv < 0 || Hq > 65535 || Hkv > 65535 || (D != 64 && D != 128)) return false;
+  if (T < 0 || Hq < 0 || Hkv < 0 || Hq > 4096 || Hkv > 4096 || Hq + 2 * Hkv > 4096 || (D != 64 && D != 128)) return false;
   if (rot_dim < 0 || rot_dim > D || rot_dim % 16 != 0 || (interleaved != 0 && interleaved != 1)) return false;
   if ((q_weight != nullptr && !aligned16(q_weight)) || (k_weight != nullptr && !aligned16(k_weight))) return false;
   if ((q_weight != nullptr || k_weight != nullptr) && (!(eps > 0.f) || !(eps <= FLT_MAX))) return false;
@@ -528,6 +528,9 @@ int a4w4_qk_norm_rope(const void* q_bf16, long long q_stride, const void* k_bf16
   const int sms = current_device_sms();
   if (sms < 0) return sms;
   if (T == 0 || Hq + Hkv == 0) return A4W4_OK;
+  r.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+  r.status = status_ptr();
+  if (r.status == nullptr) return A4W4_ERR_LAUNCH;
   r.k_out = static_cast<uint16_t*>(k_out_bf16);
   r.k_out_stride = k_out_stride;
   return a4w4::launch_kv_rope(r, D, as_stream(stream), sms);
@@ -548,6 +551,9 @@ int a4w4_kv_append_rope(const void* q_bf16, long long q_stride, const void* k_bf
   const int sms = current_device_sms();
   if (sms < 0) return sms;
   if (T == 0) return A4W4_OK;
+  r.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+  r.status = status_ptr();
+  if (r.status == nullptr) return A4W4_ERR_LAUNCH;
   r.v = static_cast<const uint16_t*>(v_bf16);
   r.v_stride = v_stride;
   r.slot_map = slot_map;

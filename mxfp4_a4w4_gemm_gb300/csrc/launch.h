@@ -151,9 +151,9 @@ struct RouteArgs {
   float scale;
   int32_t* ids;                 // [T, topk]
   float* weights;               // [T, topk]
-  // set by the launcher: rows can be read four values at a time; ceil(2^32 / (E / groups));
+  // set by the launcher: rows, the bias can be read four values at a time; ceil(2^32 / (E / groups));
   // lanes per group, and shared floats per token
-  int vectors;
+  int vectors, bias_vectors;
   unsigned int per_recip;
   int skew, val_stride;
 };
@@ -173,7 +173,11 @@ struct RopeArgs {
   long long q_out_stride, k_out_stride;
   uint8_t* cache;                        // nullptr: keys go to k_out
   int slots, page_lg;
-  int split;                             // warps per token (set by the launcher)
+  unsigned long long wait_ns;
+  unsigned int* status;
+  // set by the launcher: parts of a token, each a block's; units (256 / D heads) of a part, of queries
+  // and of keys; bytes of a part's heads
+  int split, part_q, part_kv, stage_bytes;
 };
 // -1: more work than it counts.
 int launch_kv_rope(RopeArgs p, int D, cudaStream_t st, int sms);

@@ -2,16 +2,18 @@
 // (a4w4_qk_norm_rope), or with the keys and the values to the paged MXFP4 cache
 // (a4w4_kv_append_rope).  Formulas: include/a4w4.h.
 //
-// A thread holds eight consecutive dimensions of a head (16 bytes), D / 8 threads
-// a head, a warp 256 / D heads of one token at a time.  With y = r w x (r the
-// reciprocal of the root mean square, w the norm's weight) dimension i and its
-// partner p of a pair become r (A_i x_i + B_i x_p), A_i = w_i cos, B_i = +-w_p sin:
-// sixteen coefficients in registers for all heads of a token, and four shuffles of
-// packed BF16 where the partner is another thread's.
+// A thread block takes one token (or, of few tokens, a part of one).  A thread holds
+// eight dimensions of a head (16 bytes), D / 8 threads a head, a warp 256 / D heads (a
+// unit) at a time.  With y = r w x (r the reciprocal of the root mean square, w
+// the norm's weight) dimension i and its partner p of a pair become r (A_i x_i + B_i x_p),
+// A_i = w_i cos, B_i = +-w_p sin: the token's coefficients are formed once, in shared
+// memory, while its heads are on their way to registers.
 //
 // Angles: position times frequency as turns, in 64-bit integers modulo one turn
 // (F = f / 2 pi as a 64-bit binary fraction, position * F wraps): exact to 2^-33
 // turns at position 2^31, so that 32 bits are enough for what is left.
+#include <atomic>
+
 #include "device.cuh"
 #include "kv.cuh"
 #include "launch.h"
@@ -21,6 +23,12 @@ namespace a4w4 {
 namespace {
 
 constexpr int kRopeWarps = 4;
+// Blocks on an SM.  More of them do not pay for the registers that they take from each other:
+// 8191 x 40 heads of 128 with 5 31.1 us, 6 33.0, 7 36.9; to the cache (and read) with 4 54.4, 5 68.9.
+template <bool CACHE>
+constexpr int kRopeBlocks = CACHE ? 4 : 5;
+constexpr int kRopeBatch = 4;          // units whose norms go through one reduction
+constexpr int kRopeUnits = 32;         // of a part of a token: 16 KB a stage
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 // f / (2 pi) modulo 1 as a 64-bit binary fraction: the 24-bit significand times
@@ -47,93 +55,175 @@ __device__ __forceinline__ unsigned long long turns_per_position(float f) {
   return b >> 31 ? 0ull - F : F;
 }
 
-struct Pair { float c, s; };
+using Two = unsigned long long;         // two floats, for instructions that take pairs
+__device__ __forceinline__ Two two(float lo, float hi) {
+  Two d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ Two two_of_bf16(uint32_t w) {
+  return two(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float lo_of(Two v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi_of(Two v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ Two swapped(Two v) { return two(hi_of(v), lo_of(v)); }
 
-// E2M1 codes 0..7 of |y|, ties to the even code, in 64 bits.
+// E2M1 code (with its sign) of a 64-bit value: rounded towards zero to fp32, with the last bit set
+// where something was lost, which no border of E2M1 has.
 __device__ __forceinline__ uint32_t e2m1_of(double y) {
-  return (y > 0.25) + (y >= 0.75) + (y > 1.25) + (y >= 1.75) + (y > 2.5) + (y >= 3.5) + (y > 5.0);
+  float f = __double2float_rz(y);
+  if (static_cast<double>(f) != y) f = __uint_as_float(__float_as_uint(f) | 1u);
+  return cvt_e2m1x8(f, f, f, f, f, f, f, f) & 15u;
 }
 
-// One warp's share of a token.
+__device__ __forceinline__ float bf16_of(const uint4& x, int u) {
+  const uint32_t w = u < 4 ? (u < 2 ? x.x : x.y) : (u < 6 ? x.z : x.w);
+  return __uint_as_float(u & 1 ? w & 0xFFFF0000u : w << 16);
+}
+
+// Sum of the squares of a thread's eight dimensions (five roundings).
+__device__ __forceinline__ float squares_of(const uint4& v) {
+  const Two a = two_of_bf16(v.x), b = two_of_bf16(v.y), c = two_of_bf16(v.z), d = two_of_bf16(v.w);
+  const Two s = fma2(a, a, fma2(b, b, fma2(c, c, mul2(d, d))));
+  return lo_of(s) + hi_of(s);
+}
+
+// What follows runs seldom.  It stands apart and takes values: a member function that is called
+// would keep its object in memory, which the loops would then read again and again.
+
+// Reciprocal of the root mean square of a head (LPH threads) in 64 bits.
+template <int LPH>
+__device__ __noinline__ double norm_64(uint4 x, float eps) {
+  double ssq = 0.0;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const double a = bf16_of(x, u);
+    ssq = fma(a, a, ssq);
+  }
+  // the warp as a whole is here
+#pragma unroll
+  for (int o = LPH / 2; o > 0; o >>= 1) ssq += __shfl_xor_sync(kAll, ssq, o);
+  return rsqrt(ssq * (1.0 / (8 * LPH)) + static_cast<double>(eps));
+}
+
+// The values of a unit of keys that fp32 leaves open (a bit each in `open`) in 64 bits: their
+// codes in `code` with the scale 1 / unit, or, where `unit` is negative, whether one of them
+// reaches -unit in magnitude.  turns: per position, of each pair; eps 0: no norm.  One value
+// costs its warp some 3 us, for the latency of the few 64-bit units.
 template <int D>
-struct RopeWarp {
-  static constexpr int LPH = D / 8, HPW = 32 / LPH;      // threads per head, heads at a time
+__device__ __noinline__ uint32_t keys_64(const float* w, const unsigned long long* turns, float eps, int rot, int pairs,
+                                         int position, uint4 x, uint4 y, uint32_t open, uint32_t code, double unit) {
+  constexpr int LPH = D / 8;
+  const int d0 = 8 * ((threadIdx.x & 31) % LPH), half = rot / 2;
+  const bool second = !pairs && d0 >= half;
+  const double r = eps > 0.f ? norm_64<LPH>(x, eps) : 1.0;
+  uint32_t reached = 0u;
+#pragma unroll 1
+  for (; open != 0u; open &= open - 1u) {
+    const int u = __ffs(open) - 1, d = d0 + u;
+    double o = bf16_of(x, u) * static_cast<double>(w[d]);
+    if (d0 < rot) {
+      const int other = pairs ? d ^ 1 : second ? d - half : d + half;
+      const unsigned long long turn = static_cast<unsigned long long>(static_cast<long long>(position)) *
+                                      turns[pairs ? d / 2 : second ? other : d];
+      double s, c;
+      sincospi(static_cast<double>(static_cast<long long>(turn)) * 0x1p-63, &s, &c);
+      const double par = bf16_of(y, u) * static_cast<double>(w[other]);
+      o = o * c + par * ((pairs ? (u & 1) != 0 : second) ? s : -s);
+    }
+    o *= r;
+    reached |= fabs(o) >= -unit;
+    code = (code & ~(15u << (4 * u))) | e2m1_of(o * unit) << (4 * u);
+  }
+  return unit < 0.0 ? reached : code;
+}
+
+// A token's coefficients, of queries and of keys.
+template <int D>
+struct RopeCoef {
+  float a[2][D], b[2][D];
+};
+
+// What forms them: thread i of a block's first D / 2 has pair i; where fewer pairs turn,
+// two dimensions that stay.
+template <int D, bool PAIRS>
+struct RopePair {
+  bool mine, turns;
+  int u, w;                                              // dimensions
+  unsigned long long per_position;
+
+  __device__ __forceinline__ explicit RopePair(const RopeArgs& p) {
+    const int i = threadIdx.x, half = p.rot / 2;
+    mine = i < D / 2;
+    turns = i < half;
+    u = !PAIRS && turns ? i : 2 * i;
+    w = !PAIRS && turns ? i + half : 2 * i + 1;
+    per_position = turns ? turns_per_position(p.inv_freq[i]) : 0ull;
+  }
+  __device__ __forceinline__ void form(int position, const float (*weight)[D], RopeCoef<D>& out) const {
+    if (!mine) return;
+    float c = 1.f, s = 0.f;
+    if (turns) {
+      const unsigned long long turn = static_cast<unsigned long long>(static_cast<long long>(position)) * per_position;
+      // the upper half as a signed fraction of half a turn, [-1, 1): the nearest that has 24
+      // bits, and what is left to first order, so that sine and cosine are good to two of their
+      // own last bits
+      const int32_t x = static_cast<int32_t>(turn >> 32);
+      const int64_t high = (static_cast<int64_t>(x) + 128) & ~int64_t{255};
+      float c0, s0;
+      sincospif(static_cast<float>(high) * 0x1p-31f, &s0, &c0);
+      const float rest = static_cast<float>(static_cast<int32_t>(x - high)) * 0x1.921fb6p-30f;
+      c = fmaf(-rest, s0, c0);
+      s = fmaf(rest, c0, s0);
+    }
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind) {
+      const float wu = weight[kind][u], ww = weight[kind][w];
+      out.a[kind][u] = wu * c;
+      out.b[kind][u] = -ww * s;
+      out.a[kind][w] = ww * c;
+      out.b[kind][w] = wu * s;
+    }
+  }
+};
+
+// Keys and values to the cache: a thread holds eight consecutive dimensions of a head, and a
+// partner's eight come from another thread where halves are paired.
+template <int D>
+struct RopeCells {
+  static constexpr int LPH = D / 8, HPW = 32 / LPH;      // threads per head, heads of a unit
   const RopeArgs& p;
   const int lane, d0, sub;                               // first dimension of this thread, head of the HPW
-  const long long t;
-  const Pair* s_pair;                                    // cos, sin of each pair's angle
   int partner;                                           // thread with the pairs' other halves (half split)
   bool rotated, second;                                  // whether d0 .. d0 + 7 turn; are second halves of their pairs
 
-  __device__ __forceinline__ RopeWarp(const RopeArgs& args, long long token, const Pair* pairs)
-      : p(args), lane(threadIdx.x & 31), d0(8 * (lane % LPH)), sub(lane / LPH), t(token), s_pair(pairs) {
+  __device__ __forceinline__ explicit RopeCells(const RopeArgs& args)
+      : p(args), lane(threadIdx.x & 31), d0(8 * (lane % LPH)), sub(lane / LPH) {
     const int half = p.rot / 2;
     rotated = d0 < p.rot;
     second = !p.interleaved && d0 >= half;
     partner = !rotated || p.interleaved ? lane : second ? lane - half / 8 : lane + half / 8;
   }
 
-  // Pair of dimension d0 + u.
-  __device__ __forceinline__ int pair_of(int u) const {
-    return p.interleaved ? (d0 + u) / 2 : second ? d0 + u - p.rot / 2 : d0 + u;
-  }
-
-  // A, B and the largest |w| of this thread's dimensions and of their partners'.
-  __device__ __forceinline__ void coefficients(const float* w, float* A, float* B, float* wmax, float* pmax) const {
-    *wmax = *pmax = 1.f;
-    float own[8];
-#pragma unroll
-    for (int u = 0; u < 8; u += 4) {
-      const float4 v = w != nullptr ? *reinterpret_cast<const float4*>(w + d0 + u) : make_float4(1.f, 1.f, 1.f, 1.f);
-      own[u] = v.x; own[u + 1] = v.y; own[u + 2] = v.z; own[u + 3] = v.w;
-    }
-    const int other = second ? d0 - p.rot / 2 : d0 + p.rot / 2;       // half split only
-    float pm = 0.f, om = 0.f;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      float c = 1.f, s = 0.f, wp = 0.f;
-      if (rotated) {
-        const Pair a = s_pair[pair_of(u)];
-        c = a.c;
-        s = (p.interleaved ? (u & 1) != 0 : second) ? a.s : -a.s;
-        wp = p.interleaved ? own[u ^ 1] : w != nullptr ? w[other + u] : 1.f;
-      }
-      A[u] = own[u] * c;
-      B[u] = wp * s;
-      om = fmaxf(om, fabsf(own[u]));
-      pm = fmaxf(pm, fabsf(wp));
-    }
-    *wmax = om;
-    *pmax = pm;
-  }
-
-  // Reciprocal of the root mean square of a head (over the LPH threads that hold it).
+  // Reciprocal of the root mean square of a head (over the LPH threads that hold it), to 2^-21.5:
+  // eight roundings of the sum, halved, and those of the last step.
   __device__ __forceinline__ float norm(const uint4& x) const {
-    float ssq = 0.f;
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const float a = __uint_as_float(w[u] << 16), b = __uint_as_float(w[u] & 0xFFFF0000u);
-      ssq = fmaf(a, a, fmaf(b, b, ssq));
-    }
+    float ssq = squares_of(x);
 #pragma unroll
     for (int o = LPH / 2; o > 0; o >>= 1) ssq += __shfl_xor_sync(kAll, ssq, o);
-    if (!(ssq < 1e38f)) return static_cast<float>(norm_64(x));   // the squares may have passed fp32's range
-    return rsqrtf(ssq * (1.f / D) + p.eps);
-  }
-  // (a head's threads come here together)
-  __device__ __noinline__ double norm_64(const uint4& x) const {
-    const unsigned mask = LPH == 32 ? kAll : ((1u << LPH) - 1u) << (sub * LPH);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    double ssq = 0.0;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const double a = __uint_as_float(w[u] << 16), b = __uint_as_float(w[u] & 0xFFFF0000u);
-      ssq += a * a + b * b;
-    }
-#pragma unroll
-    for (int o = LPH / 2; o > 0; o >>= 1) ssq += __shfl_xor_sync(mask, ssq, o);
-    return 1.0 / sqrt(ssq / D + static_cast<double>(p.eps));
+    if (__any_sync(kAll, !(ssq < 1e38f))) return static_cast<float>(norm_64<LPH>(x, p.eps));   // the squares may have passed fp32's range
+    const float v = fmaf(ssq, 1.f / D, p.eps), r = rsqrtf(v);
+    return fmaf(0.5f * r, fmaf(-v * r, r, 1.f), r);
   }
 
   __device__ __forceinline__ uint4 partners(const uint4& x) const {
@@ -148,69 +238,27 @@ struct RopeWarp {
     return rotated ? y : make_uint4(0u, 0u, 0u, 0u);      // what stays as it is takes nothing from a neighbour
   }
 
-  __device__ __forceinline__ void rotate(const uint4& x, const uint4& y, const float* A, const float* B, float r,
-                                         float* out) const {
+  // o = r (A x + B y), and what |o| may be off by: `off` r (|A x| + |B y|).
+  __device__ __forceinline__ void rotate(const RopeCoef<D>& coef, const uint4& x, const uint4& y, float r, float* o,
+                                         float* sum) const {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      out[2 * u] = r * fmaf(A[2 * u], __uint_as_float(w[u] << 16), B[2 * u] * __uint_as_float(v[u] << 16));
-      out[2 * u + 1] = r * fmaf(A[2 * u + 1], __uint_as_float(w[u] & 0xFFFF0000u),
-                                B[2 * u + 1] * __uint_as_float(v[u] & 0xFFFF0000u));
-    }
-  }
-
-  // Heads first, first + step, ... (in units of HPW) of H heads in x: to BF16 rows.
-  __device__ __forceinline__ void to_rows(const uint16_t* x, uint16_t* out, int H, const float* w, int first, int step) const {
-    if (first * HPW >= H) return;
-    float A[8], B[8], wm, pm;
-    coefficients(w, A, B, &wm, &pm);
-    for (int g = first; g * HPW < H; g += step) {
-      const int h = g * HPW + sub;
-      const bool in = h < H;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (in) v = *reinterpret_cast<const uint4*>(x + h * D + d0);
-      const float r = w != nullptr ? norm(v) : 1.f;
-      const uint4 y = partners(v);
-      float o[8];
-      rotate(v, y, A, B, r, o);
-      if (in)
-        *reinterpret_cast<uint4*>(out + h * D + d0) =
-            make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
-    }
-  }
-
-  // Codes and scale of a key head in 64 bits.
-  __device__ __noinline__ uint32_t key_cells_64(const uint4& x, const uint4& y, const float* w, int position,
-                                                uint32_t* code) const {
-    const double r = w != nullptr ? norm_64(x) : 1.0;
-    const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
-    double o[8], amax = 0.0;
-    for (int u = 0; u < 8; ++u) {
-      const double own = __uint_as_float(u & 1 ? a[u / 2] & 0xFFFF0000u : a[u / 2] << 16) * (w != nullptr ? w[d0 + u] : 1.0);
-      o[u] = own;
-      if (rotated) {
-        const int other = p.interleaved ? d0 + (u ^ 1) : second ? d0 + u - p.rot / 2 : d0 + u + p.rot / 2;
-        const double par = __uint_as_float(u & 1 ? b[u / 2] & 0xFFFF0000u : b[u / 2] << 16) * (w != nullptr ? w[other] : 1.0);
-        const unsigned long long turn = static_cast<unsigned long long>(static_cast<long long>(position)) *
-                                        turns_per_position(p.inv_freq[pair_of(u)]);
-        double s, c;
-        sincospi(static_cast<double>(static_cast<long long>(turn)) * 0x1p-63, &s, &c);
-        o[u] = own * c + par * ((p.interleaved ? (u & 1) != 0 : second) ? s : -s);
+    for (int u = 0; u < 8; u += 4) {
+      const float4 A = *reinterpret_cast<const float4*>(coef.a[1] + d0 + u), B = *reinterpret_cast<const float4*>(coef.b[1] + d0 + u);
+      const float a[4] = {A.x, A.y, A.z, A.w}, b[4] = {B.x, B.y, B.z, B.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t wi = w[(u + i) / 2], vi = v[(u + i) / 2];
+        const float m = a[i] * __uint_as_float(i & 1 ? wi & 0xFFFF0000u : wi << 16);
+        const float n = b[i] * __uint_as_float(i & 1 ? vi & 0xFFFF0000u : vi << 16);
+        o[u + i] = r * (m + n);
+        sum[u + i] = r * (fabsf(m) + fabsf(n));
       }
-      o[u] *= r;
-      amax = fmax(amax, fabs(o[u]));
     }
-    const unsigned mask = LPH == 32 ? kAll : ((1u << LPH) - 1u) << (sub * LPH);
-    amax = fmax(amax, __shfl_xor_sync(mask, amax, 1));
-    amax = fmax(amax, __shfl_xor_sync(mask, amax, 2));
-    // 2^(e - 127), e = floor(log2 amax) - 2 + 127, at least 0 and at most what an infinity gives
-    const int ex = static_cast<int>(__double_as_longlong(amax) >> 52 & 2047) - 1023;
-    const int e = min(max(ex - 2 + 127, 0), 253);
-    const double unit = __longlong_as_double(static_cast<long long>(1023 + 127 - e) << 52);
-    uint32_t c = 0u;
-    for (int u = 0; u < 8; ++u) c |= (e2m1_of(fabs(o[u]) * unit) | (signbit(o[u]) ? 8u : 0u)) << (4 * u);
-    *code = c;
-    return static_cast<uint32_t>(e);
+  }
+
+  static __device__ __forceinline__ uint32_t codes_of(const Two* y) {
+    return cvt_e2m1x8(lo_of(y[0]), hi_of(y[0]), lo_of(y[1]), hi_of(y[1]), lo_of(y[2]), hi_of(y[2]), lo_of(y[3]), hi_of(y[3]));
   }
 
   __device__ __forceinline__ uint8_t* chunk_of(int slot, int h) const {
@@ -218,151 +266,372 @@ struct RopeWarp {
     return p.cache + kv_chunk_offset<D>(slot >> p.page_lg, h, (slot >> 4) & (chunks - 1), p.Hkv, chunks);
   }
 
-  // The keys to the cache: quantised from the fp32 value.  Each value is known to
-  // 2^-19 r (|w x| + |w_p x_p|) (2^-21.6 from the coefficients and products, 2^-20.7 from r,
-  // two roundings); where that leaves a code or the scale open, 64 bits decide.
-  __device__ __forceinline__ void keys_to_cache(const uint16_t* x, int slot, int position, int first, int step) const {
+  // Keys to the cache, quantised from the fp32 value o = r (A x + B y).  What is known of it: r to
+  // 2^-21.5 of itself, sine and cosine to 2^-21.8 of themselves, the weight's product, the two
+  // products, their sum and the last product a rounding each: in all within 2^-20.2 of
+  // r (|A x| + |B y|); without norm or rotation o is x.  Where that leaves a code or the scale
+  // open, 64 bits decide (some 5 codes of a million).
+  __device__ __forceinline__ void key_cell(const RopeCoef<D>& coef, const float* weight, const unsigned long long* turns,
+                                           const uint4& v, int n, int slot, int position) const {
     using Ch = KvChunk<D>;
-    if (first * HPW >= p.Hkv) return;
-    float A[8], B[8], wm, pm;
-    coefficients(p.k_weight, A, B, &wm, &pm);
-    for (int g = first; g * HPW < p.Hkv; g += step) {
-      const int h = g * HPW + sub;
-      const bool in = h < p.Hkv;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (in) v = *reinterpret_cast<const uint4*>(x + h * D + d0);
-      const float r = p.k_weight != nullptr ? norm(v) : 1.f;
-      const uint4 y = partners(v);
-      float o[8];
-      rotate(v, y, A, B, r, o);
-      float amax = 0.f;
+    const bool normed = p.k_weight != nullptr;
+    const float r = normed ? norm(v) : 1.f;
+    const uint4 y = partners(v);
+    float o[8], off[8];
+    rotate(coef, v, y, r, o, off);
+    const float rel = rotated || normed ? 0x1.dp-21f : 0.f;
+    float least = 0.f, most = 0.f;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) amax = fmaxf(amax, fabsf(o[u]));
-      uint32_t mx = max_abs_bf16x2(max_abs_bf16x2(v.x, v.y), max_abs_bf16x2(v.z, v.w)) & 0x7FFF7FFFu;
-      uint32_t my = max_abs_bf16x2(max_abs_bf16x2(y.x, y.y), max_abs_bf16x2(y.z, y.w)) & 0x7FFF7FFFu;
-      const float bx = fmaxf(__uint_as_float(mx << 16), __uint_as_float(mx & 0xFFFF0000u));
-      const float by = fmaxf(__uint_as_float(my << 16), __uint_as_float(my & 0xFFFF0000u));
-      const bool zero = bx == 0.f && by == 0.f;
-      float off = r * (bx * wm + by * pm) * 0x1p-19f + (zero ? 0.f : 0x1p-147f);
-      amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 1));
-      off = fmaxf(off, __shfl_xor_sync(kAll, off, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 2));
-      off = fmaxf(off, __shfl_xor_sync(kAll, off, 2));
-      const uint32_t eb = __float_as_uint(amax) >> 23;
-      uint32_t e = eb > 2u ? eb - 2u : 0u;
-      const float inv = __uint_as_float((254u - e) << 23), slack = off * inv;
-      float lo[8], hi[8];
+    for (int u = 0; u < 8; ++u) {
+      // (tiny values lose more, zeros nothing)
+      off[u] = off[u] > 0.f ? fmaf(off[u], rel, rel > 0.f ? 0x1p-147f : 0.f) : 0.f;
+      least = fmaxf(least, fabsf(o[u]) - off[u]);
+      most = fmaxf(most, fabsf(o[u]) + off[u]);
+    }
+    least = fmaxf(least, __shfl_xor_sync(kAll, least, 1));
+    most = fmaxf(most, __shfl_xor_sync(kAll, most, 1));
+    least = fmaxf(least, __shfl_xor_sync(kAll, least, 2));
+    most = fmaxf(most, __shfl_xor_sync(kAll, most, 2));
+    uint32_t eb = __float_as_uint(most) >> 23;
+    if (__any_sync(kAll, __float_as_uint(least) >> 23 != eb)) {
+      // does the largest magnitude reach the power of two that `most` has passed?
+      const float power = __uint_as_float(eb << 23);
+      uint32_t open = 0u;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        lo[u] = fmaf(o[u], inv, -slack);
-        hi[u] = fmaf(o[u], inv, slack);
-      }
-      uint32_t code = cvt_e2m1x8(lo[0], lo[1], lo[2], lo[3], lo[4], lo[5], lo[6], lo[7]);
-      const uint32_t code_hi = cvt_e2m1x8(hi[0], hi[1], hi[2], hi[3], hi[4], hi[5], hi[6], hi[7]);
-      const bool open = code != code_hi || __float_as_uint(amax - off) >> 23 != eb || __float_as_uint(amax + off) >> 23 != eb;
-      if (__any_sync(kAll, open && off > 0.f)) e = key_cells_64(v, y, p.k_weight, position, &code);
-      if (in) {
-        uint8_t* chunk = chunk_of(slot, h);
-        const int row = slot & 15;
-        *reinterpret_cast<uint32_t*>(chunk + Ch::key_word(row, d0 / 32, d0 % 32 / 8)) = code;
-        if (d0 % 32 == 0) chunk[Ch::kKeyScales + row * Ch::J + d0 / 32] = static_cast<uint8_t>(e);
-      }
+      for (int u = 0; u < 8; ++u) open |= least < power && fabsf(o[u]) + off[u] >= power ? 1u << u : 0u;
+      uint32_t reached = keys_64<D>(weight, turns, normed ? p.eps : 0.f, p.rot, p.interleaved, position, v, y, open, 0u,
+                                    -static_cast<double>(power));      // (the warp as a whole)
+      reached |= least >= power;
+      reached |= __shfl_xor_sync(kAll, reached, 1);
+      reached |= __shfl_xor_sync(kAll, reached, 2);
+      if (reached == 0u) --eb;
+    }
+    const uint32_t e = eb > 2u ? eb - 2u : 0u;
+    const float inv = __uint_as_float((254u - e) << 23);
+    const Two i2 = two(inv, inv), j2 = two(-inv, -inv);
+    Two lo[4], hi[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const Two m = mul2(two(o[2 * u], o[2 * u + 1]), i2), d = two(off[2 * u], off[2 * u + 1]);
+      lo[u] = fma2(d, j2, m);
+      hi[u] = fma2(d, i2, m);
+    }
+    uint32_t code = codes_of(lo);
+    const uint32_t diff = code ^ codes_of(hi);
+    if (__any_sync(kAll, diff != 0u)) {
+      uint32_t open = 0u;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) open |= (diff >> (4 * u) & 15u) != 0u ? 1u << u : 0u;
+      code = keys_64<D>(weight, turns, normed ? p.eps : 0.f, p.rot, p.interleaved, position, v, y, open, code, inv);
+    }
+    const int h = n * HPW + sub;
+    if (h < p.Hkv) {
+      uint8_t* chunk = chunk_of(slot, h);
+      const int row = slot & 15;
+      *reinterpret_cast<uint32_t*>(chunk + Ch::key_word(row, d0 / 32, d0 % 32 / 8)) = code;
+      if (d0 % 32 == 0) chunk[Ch::kKeyScales + row * Ch::J + d0 / 32] = static_cast<uint8_t>(e);
     }
   }
 
-  __device__ __forceinline__ void values_to_cache(const uint16_t* x, int slot, int first, int step) const {
+  __device__ __forceinline__ void value_cell(const uint4& v, int n, int slot) const {
     using Ch = KvChunk<D>;
-    for (int g = first; g * HPW < p.Hkv; g += step) {
-      const int h = g * HPW + sub;
-      const bool in = h < p.Hkv;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (in) v = *reinterpret_cast<const uint4*>(x + h * D + d0);
-      uint32_t m = max_abs_bf16x2(max_abs_bf16x2(v.x, v.y), max_abs_bf16x2(v.z, v.w));
-      m = max_abs_bf16x2(m, __shfl_xor_sync(kAll, m, 1));
-      m = max_abs_bf16x2(m, __shfl_xor_sync(kAll, m, 2)) & 0x7FFF7FFFu;
-      const uint32_t eb = max(m & 0xFFFFu, m >> 16) >> 7, e = eb > 2u ? eb - 2u : 0u;
-      const float inv = __uint_as_float((254u - e) << 23);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      float f[8];
+    uint32_t m = max_abs_bf16x2(max_abs_bf16x2(v.x, v.y), max_abs_bf16x2(v.z, v.w));
+    m = max_abs_bf16x2(m, __shfl_xor_sync(kAll, m, 1));
+    m = max_abs_bf16x2(m, __shfl_xor_sync(kAll, m, 2)) & 0x7FFF7FFFu;
+    const uint32_t eb = max(m & 0xFFFFu, m >> 16) >> 7, e = eb > 2u ? eb - 2u : 0u;
+    const float inv = __uint_as_float((254u - e) << 23);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float f[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        f[2 * u] = __uint_as_float(w[u] << 16) * inv;
-        f[2 * u + 1] = __uint_as_float(w[u] & 0xFFFF0000u) * inv;
-      }
-      const uint32_t code = cvt_e2m1x8(f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7]);
-      // Thread l has the bytes of run g = 4 (l % 2) .. + 3 at place i = l / 2; it writes four
-      // places of one run: i0 .. i0 + 3 of run `run`.
-      const int l = lane % LPH, run = D == 128 ? l / 2 : l, i0 = D == 128 ? 4 * (l & 1) : 0;
-      uint32_t word = 0u;
+    for (int u = 0; u < 4; ++u) {
+      f[2 * u] = __uint_as_float(w[u] << 16) * inv;
+      f[2 * u + 1] = __uint_as_float(w[u] & 0xFFFF0000u) * inv;
+    }
+    const uint32_t code = cvt_e2m1x8(f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7]);
+    // Thread l has the bytes of runs 4 (l % 2) .. + 3 at place i = l / 2; it writes four
+    // places of one run: i0 .. i0 + 3 of run `run`.
+    const int l = lane % LPH, run = D == 128 ? l / 2 : l, i0 = D == 128 ? 4 * (l & 1) : 0;
+    uint32_t word = 0u;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t c = __shfl_sync(kAll, code, sub * LPH + 2 * (i0 + i) + run / 4);
-        word |= (c >> (8 * (run & 3)) & 255u) << (8 * i);
-      }
-      if (in) {
-        uint8_t* chunk = chunk_of(slot, h);
-        const int row = slot & 15;
-        *reinterpret_cast<uint32_t*>(chunk + Ch::value_run(row, run) + i0) = word;
-        if (d0 % 32 == 0) chunk[Ch::kValueScales + row * Ch::J + d0 / 32] = static_cast<uint8_t>(e);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t c = __shfl_sync(kAll, code, sub * LPH + 2 * (i0 + i) + run / 4);
+      word |= (c >> (8 * (run & 3)) & 255u) << (8 * i);
+    }
+    const int h = n * HPW + sub;
+    if (h < p.Hkv) {
+      uint8_t* chunk = chunk_of(slot, h);
+      const int row = slot & 15;
+      *reinterpret_cast<uint32_t*>(chunk + Ch::value_run(row, run) + i0) = word;
+      if (d0 % 32 == 0) chunk[Ch::kValueScales + row * Ch::J + d0 / 32] = static_cast<uint8_t>(e);
     }
   }
 };
 
-// A warp takes every `split`-th unit (256 / D heads) of one token: queries, keys, values one after the other.
-template <int D, bool CACHE>
-__global__ void __launch_bounds__(32 * kRopeWarps) kv_rope_kernel(const RopeArgs p) {
-  __shared__ Pair s_pair[kRopeWarps][D / 2];
+// Heads to BF16 rows: a thread holds two runs of four dimensions of a head, which are each
+// other's partners where halves are paired, so that nothing crosses threads but the sums of
+// squares; those of four units go through one reduction.
+template <int D, bool PAIRS>
+struct RopeRows {
+  static constexpr int LPH = D / 8, HPW = 32 / LPH;
+  const RopeArgs& p;
+  const int lane, sub;
+  int da, db;                                            // first dimensions of the runs
+  bool rotated;
+  Two Aa[2], Ab[2], Ba[2], Bb[2];
+
+  __device__ __forceinline__ explicit RopeRows(const RopeArgs& args)
+      : p(args), lane(threadIdx.x & 31), sub(lane / LPH) {
+    const int j = lane % LPH, h = PAIRS ? 0 : p.rot / 8;  // threads of a head that hold two halves
+    da = j < h ? 4 * j : 8 * j;
+    db = j < h ? 4 * (j + h) : 8 * j + 4;
+    rotated = da < p.rot;
+  }
+  __device__ __forceinline__ void coefficients(const RopeCoef<D>& c, int kind) {
+    const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(c.a[kind] + da), y = *reinterpret_cast<const ulonglong2*>(c.a[kind] + db);
+    const ulonglong2 z = *reinterpret_cast<const ulonglong2*>(c.b[kind] + da), w = *reinterpret_cast<const ulonglong2*>(c.b[kind] + db);
+    Aa[0] = x.x; Aa[1] = x.y; Ab[0] = y.x; Ab[1] = y.y;
+    Ba[0] = z.x; Ba[1] = z.y; Bb[0] = w.x; Bb[1] = w.y;
+  }
+  // x: this thread's head of the unit.
+  __device__ __forceinline__ uint4 load(const uint16_t* x) const {
+    const uint2 a = *reinterpret_cast<const uint2*>(x + da), b = *reinterpret_cast<const uint2*>(x + db);
+    return make_uint4(a.x, a.y, b.x, b.y);
+  }
+  __device__ __forceinline__ float norm(const uint4& v) const {
+    float s = squares_of(v);
+#pragma unroll
+    for (int o = 1; o < LPH; o <<= 1) s += __shfl_xor_sync(kAll, s, o);
+    return __any_sync(kAll, !(s < 1e38f)) ? static_cast<float>(norm_64<LPH>(v, p.eps)) : rsqrtf(s * (1.f / D) + p.eps);
+  }
+  // The same for four units.
+  __device__ __forceinline__ void norms(const uint4* v, float* r) const {
+    const float s0 = squares_of(v[0]), s1 = squares_of(v[1]), s2 = squares_of(v[2]), s3 = squares_of(v[3]);
+    const bool odd = lane & 1, upper = lane & 2;
+    // lane l ends up with unit l % 4's sum
+    const float a = (odd ? s1 : s0) + __shfl_xor_sync(kAll, odd ? s0 : s1, 1);
+    const float b = (odd ? s3 : s2) + __shfl_xor_sync(kAll, odd ? s2 : s3, 1);
+    float s = (upper ? b : a) + __shfl_xor_sync(kAll, upper ? a : b, 2);
+#pragma unroll
+    for (int o = 4; o < LPH; o <<= 1) s += __shfl_xor_sync(kAll, s, o);
+    const float q = rsqrtf(s * (1.f / D) + p.eps);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __shfl_sync(kAll, q, (lane & ~3) | i);
+    if (__any_sync(kAll, !(s < 1e38f))) {                // the squares may have passed fp32's range
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = static_cast<float>(norm_64<LPH>(v[i], p.eps));
+    }
+  }
+  __device__ __forceinline__ void store(const uint4& v, float r, uint16_t* x) const {
+    const Two a[2] = {two_of_bf16(v.x), two_of_bf16(v.y)}, b[2] = {two_of_bf16(v.z), two_of_bf16(v.w)};
+    const bool stays = p.rot < D && !rotated;            // what stays as it is takes nothing from a neighbour
+    const Two r2 = two(r, r);
+    uint32_t o[4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      Two pa = PAIRS ? swapped(a[u]) : b[u], pb = PAIRS ? swapped(b[u]) : a[u];
+      if (stays) pa = pb = 0ull;
+      const Two x = mul2(r2, fma2(Aa[u], a[u], mul2(Ba[u], pa))), y = mul2(r2, fma2(Ab[u], b[u], mul2(Bb[u], pb)));
+      o[u] = pack_bf16(lo_of(x), hi_of(x));
+      o[2 + u] = pack_bf16(lo_of(y), hi_of(y));
+    }
+    *reinterpret_cast<uint2*>(x + da) = make_uint2(o[0], o[1]);
+    *reinterpret_cast<uint2*>(x + db) = make_uint2(o[2], o[3]);
+  }
+  // Units n .. e - 1 (this warp's), of which this thread has a head in those below m: from rows in
+  // shared memory to rows `out` (both: this thread's head of unit 0).
+  __device__ __forceinline__ void run(const uint16_t* x, uint16_t* out, const float* w, int n, int e, int m) const {
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    for (; n + 1 < e; n += kRopeBatch) {
+      uint4 v[kRopeBatch];
+#pragma unroll
+      for (int i = 0; i < kRopeBatch; ++i) v[i] = n + i < m ? load(x + (n + i) * 256) : none;
+      float r[kRopeBatch] = {1.f, 1.f, 1.f, 1.f};
+      if (w != nullptr) norms(v, r);
+#pragma unroll
+      for (int i = 0; i < kRopeBatch; ++i)
+        if (n + i < m) store(v[i], r[i], out + (n + i) * 256);
+    }
+    if (n < e) {
+      const uint4 v = n < m ? load(x + n * 256) : none;
+      const float r = w != nullptr ? norm(v) : 1.f;
+      if (n < m) store(v, r, out + n * 256);
+    }
+  }
+};
+
+// What a warp does of a part of a token: units first .. end - 1, of which this thread has a head in
+// those below `mine`.  The part's n units from u0 go to the warps in runs, warp `start` the first.
+struct RopeRun {
+  int first, end, mine;
+  __device__ __forceinline__ RopeRun(int u0, int n, int start, int heads_end) {
+    const int run = (n + kRopeWarps - 1) / kRopeWarps, w = ((threadIdx.x >> 5) - start) & (kRopeWarps - 1);
+    first = u0 + min(w * run, n);
+    end = u0 + min((w + 1) * run, n);
+    mine = min(end, heads_end);
+  }
+};
+
+// A block walks over tokens (or over one part of the heads of each: of few tokens, or of tokens
+// with very many heads).  One thread copies the next token's heads to shared memory while
+// the block works on this one's; the next token's coefficients go to the other buffer too.
+// 8191 tokens x 40 heads of 128 with norms: ROPE_TIME us.
+template <int D, bool CACHE, bool PAIRS>
+__global__ void __launch_bounds__(32 * kRopeWarps, kRopeBlocks<CACHE>) kv_rope_kernel(const RopeArgs p) {
+  extern __shared__ __align__(128) uint8_t smem[];         // two stages of heads, two sets of coefficients
+  __shared__ alignas(8) unsigned long long s_bar[2];
+  __shared__ int s_flags[2];
+  __shared__ unsigned long long s_turns[CACHE ? D / 2 : 1];   // per position, of each pair
+  __shared__ float s_weight[2][D];                       // the norms' (1 without), of queries and of keys
+  using Rows = RopeRows<D, PAIRS>;
+  constexpr int HPW = Rows::HPW;
+  const uint32_t bar = smem_u32(s_bar);
+  volatile int *abort_flag = s_flags, *never = s_flags + 1;
+  if (threadIdx.x == 0) {
+    mbar_init(bar, 1);
+    mbar_init(bar + 8u, 1);
+    s_flags[0] = s_flags[1] = 0;
+    fence_barrier_init();
+  }
+  const int part = p.split > 1 ? blockIdx.x % p.split : 0, stride = gridDim.x / p.split;
+  const int uq = (p.Hq + HPW - 1) / HPW, uk = (p.Hkv + HPW - 1) / HPW;
+  // this part's units
+  const int q0 = part * p.part_q, q1 = min(q0 + p.part_q, uq), k0 = part * p.part_kv, k1 = min(k0 + p.part_kv, uk);
+  const int nq = max(q1 - q0, 0), nk = max(k1 - k0, 0);
   griddep_wait();
   griddep_launch_dependents();
-  constexpr int HPW = RopeWarp<D>::HPW;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long item = static_cast<long long>(blockIdx.x) * kRopeWarps + warp;
-  const long long t = item / p.split;
-  const int s = static_cast<int>(item - t * p.split);
-  if (t >= p.T) return;
-  int slot = 0;
+  __syncthreads();
+
+  RopeCoef<D>* coef = reinterpret_cast<RopeCoef<D>*>(smem + 2 * p.stage_bytes);
+  const int off_k = p.part_q * 512, off_v = off_k + p.part_kv * 512;       // within a stage
+  auto issue = [&](long long t, int slot, int s) {                          // thread 0
+    const uint32_t fb = bar + 8u * s, dst = smem_u32(smem) + s * p.stage_bytes;
+    if (CACHE && static_cast<unsigned>(slot) >= static_cast<unsigned>(p.slots)) {
+      mbar_arrive(fb);                                    // nothing to be done, nothing to be fetched
+      return;
+    }
+    const int bq = (min(q1 * HPW, p.Hq) - q0 * HPW) * D * 2, bk = (min(k1 * HPW, p.Hkv) - k0 * HPW) * D * 2;
+    mbar_arrive_expect_tx(fb, (nq > 0 ? bq : 0) + (nk > 0 ? (CACHE ? 2 : 1) * bk : 0));
+    const uint64_t pol = policy_evict_first();
+    if (nq > 0) bulk_g2s(dst, p.q + t * p.q_stride + q0 * 256, bq, fb, pol);
+    if (nk > 0) bulk_g2s(dst + off_k, p.k + t * p.k_stride + k0 * 256, bk, fb, pol);
+    if (CACHE && nk > 0) bulk_g2s(dst + off_v, p.v + t * p.v_stride + k0 * 256, bk, fb, pol);
+  };
+  long long t = blockIdx.x / p.split;                     // below T
+  int slot = 0, next_slot = 0, issued = 0, done = 0;
   if (CACHE) {
     slot = p.slot_map[t];
-    if (static_cast<unsigned>(slot) >= static_cast<unsigned>(p.slots)) return;
+    next_slot = t + stride < p.T ? p.slot_map[t + stride] : -1;
   }
-  const int position = p.rot > 0 ? p.positions[t] : 0;
-  for (int i = lane; i < p.rot / 2; i += 32) {
-    const unsigned long long turn =
-        static_cast<unsigned long long>(static_cast<long long>(position)) * turns_per_position(p.inv_freq[i]);
-    // the upper half as a signed fraction of half a turn, [-1, 1)
-    const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
-    Pair a;
-    sincospif(x, &a.s, &a.c);
-    s_pair[warp][i] = a;
+  if (threadIdx.x == 0) {
+    issue(t, slot, 0);
+    if (t + stride < p.T) issue(t + stride, next_slot, 1);
+    issued = t + stride < p.T ? 2 : 1;
   }
-  __syncwarp();
-  const RopeWarp<D> rw(p, t, s_pair[warp]);
-  const int uq = (p.Hq + HPW - 1) / HPW, uk = (p.Hkv + HPW - 1) / HPW;
-  // first unit of each kind that falls to this warp
-  const int fk = ((s - uq) % p.split + p.split) % p.split, fv = ((s - uq - uk) % p.split + p.split) % p.split;
-  rw.to_rows(p.q + t * p.q_stride, p.q_out + t * p.q_out_stride, p.Hq, p.q_weight, s, p.split);
-  if (CACHE) {
-    rw.keys_to_cache(p.k + t * p.k_stride, slot, position, fk, p.split);
-    rw.values_to_cache(p.v + t * p.v_stride, slot, fv, p.split);
-  } else {
-    rw.to_rows(p.k + t * p.k_stride, p.k_out + t * p.k_out_stride, p.Hkv, p.k_weight, fk, p.split);
+  if (threadIdx.x < D) {
+    s_weight[0][threadIdx.x] = p.q_weight != nullptr ? p.q_weight[threadIdx.x] : 1.f;
+    s_weight[1][threadIdx.x] = p.k_weight != nullptr ? p.k_weight[threadIdx.x] : 1.f;
   }
+  __syncthreads();
+  Rows rows(p);
+  const RopeCells<D> cells(p);
+  const RopePair<D, PAIRS> pair(p);
+  if (CACHE && pair.turns) s_turns[threadIdx.x] = pair.per_position;
+  // queries, keys and values begin with the warp after the last one of those before
+  const int with_q = nq > 0 ? (nq - 1) / ((nq + kRopeWarps - 1) / kRopeWarps) + 1 : 0;
+  const int with_k = nk > 0 ? (nk - 1) / ((nk + kRopeWarps - 1) / kRopeWarps) + 1 : 0;
+  const RopeRun rq(q0, nq, 0, (p.Hq - rows.sub + HPW - 1) / HPW);
+  const RopeRun rk(k0, nk, with_q, (p.Hkv - rows.sub + HPW - 1) / HPW);
+  const RopeRun rv(k0, nk, with_q + with_k, (p.Hkv - rows.sub + HPW - 1) / HPW);
+  int position = p.rot > 0 ? p.positions[t] : 0;
+  pair.form(position, s_weight, coef[0]);
+  __syncthreads();
+  for (int s = 0;; s ^= 1) {
+    const bool more = t + stride < p.T;
+    const int next_position = more && p.rot > 0 ? p.positions[t + stride] : 0;
+    const int ahead_slot = CACHE && t + 2 * stride < p.T ? p.slot_map[t + 2 * stride] : -1;
+    const bool ok = mbar_wait(bar + 8u * s, (done >> 1) & 1, abort_flag, p.wait_ns, p.status);
+    __syncwarp();
+    done += ok;
+    const uint16_t* stage = reinterpret_cast<const uint16_t*>(smem + s * p.stage_bytes);
+    const RopeCoef<D>& now = coef[s];
+    if (ok && (!CACHE || static_cast<unsigned>(slot) < static_cast<unsigned>(p.slots))) {
+      if (rq.first < rq.end) {
+        rows.coefficients(now, 0);
+        rows.run(stage + rows.sub * D - q0 * 256, p.q_out + t * p.q_out_stride + rows.sub * D, p.q_weight, rq.first, rq.end,
+                 rq.mine);
+      }
+      const uint16_t *k = stage + off_k / 2 - k0 * 256, *v = stage + off_v / 2 - k0 * 256;
+      if (CACHE) {
+        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+        for (int n = rk.first; n < rk.end; ++n)
+          cells.key_cell(now, s_weight[1], s_turns, n < rk.mine ? *reinterpret_cast<const uint4*>(k + n * 256 + cells.lane * 8) : none, n, slot, position);
+        for (int n = rv.first; n < rv.end; ++n)
+          cells.value_cell(n < rv.mine ? *reinterpret_cast<const uint4*>(v + n * 256 + cells.lane * 8) : none, n, slot);
+      } else if (rk.first < rk.end) {
+        rows.coefficients(now, 1);
+        rows.run(k + rows.sub * D, p.k_out + t * p.k_out_stride + rows.sub * D, p.k_weight, rk.first, rk.end, rk.mine);
+      }
+    }
+    if (!more) break;
+    pair.form(next_position, s_weight, coef[s ^ 1]);
+    if (__syncthreads_or(!ok)) break;
+    if (threadIdx.x == 0 && t + 2 * stride < p.T) {
+      issue(t + 2 * stride, ahead_slot, s);
+      ++issued;
+    }
+    t += stride;
+    position = next_position;
+    slot = next_slot;
+    next_slot = ahead_slot;
+  }
+  // every copy issued lands before the shared memory is released
+  if (threadIdx.x == 0) {
+    const unsigned long long drain_ns = p.wait_ns > 100000000ull ? p.wait_ns : 100000000ull;
+    for (; done < issued; ++done) mbar_wait(bar + 8u * (done & 1), (done >> 1) & 1, never, drain_ns, p.status);
+  }
+}
+
+template <int D, bool CACHE, bool PAIRS>
+int launch_rope_kind(RopeArgs p, cudaStream_t st, int sms) {
+  auto kern = kv_rope_kernel<D, CACHE, PAIRS>;
+  const int smem = 2 * p.stage_bytes + 2 * static_cast<int>(sizeof(RopeCoef<D>));
+  static std::atomic<unsigned long long> attr_devs{0};   // bit d: attribute set on device d
+  if (ensure_func_attrs(attr_devs, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    2 * kRopeUnits * 512 + 2 * static_cast<int>(sizeof(RopeCoef<D>))) == cudaSuccess;
+      }) != 0)
+    return -4;
+  // as many blocks as stay on the SMs at once
+  int fit = 233472 / (smem + 2048 + 1024);                // with what the kernel and the system hold of it
+  if (fit > kRopeBlocks<CACHE>) fit = kRopeBlocks<CACHE>;
+  const long long items = static_cast<long long>(p.T) * p.split, most = static_cast<long long>(fit) * sms / p.split * p.split;
+  return launch_pdl_smem(kern, static_cast<int>(items < most ? items : most), 32 * kRopeWarps, smem, st, p);
+}
+
+template <int D, bool CACHE>
+int launch_rope_d(const RopeArgs& p, cudaStream_t st, int sms) {
+  return p.interleaved ? launch_rope_kind<D, CACHE, true>(p, st, sms) : launch_rope_kind<D, CACHE, false>(p, st, sms);
 }
 
 }  // namespace
 
 int launch_kv_rope(RopeArgs p, int D, cudaStream_t st, int sms) {
   const bool cache = p.cache != nullptr;
-  const int per = 256 / D, units = (p.Hq + per - 1) / per + (cache ? 2 : 1) * ((p.Hkv + per - 1) / per);
-  // warps enough for 16 on every SM, each with whole units
-  const long long want = (16ll * sms + p.T - 1) / p.T;
-  p.split = static_cast<int>(want < 1 ? 1 : want > units ? units : want);
-  const long long grid = (static_cast<long long>(p.T) * p.split + kRopeWarps - 1) / kRopeWarps;
-  if (grid > INT32_MAX) return -1;
-  auto kern = D == 64 ? (cache ? kv_rope_kernel<64, true> : kv_rope_kernel<64, false>)
-                      : (cache ? kv_rope_kernel<128, true> : kv_rope_kernel<128, false>);
-  return launch_pdl(kern, static_cast<int>(grid), 32 * kRopeWarps, st, p);
+  const int per = 256 / D, uq = (p.Hq + per - 1) / per, uk = (p.Hkv + per - 1) / per, kinds = cache ? 2 : 1;
+  // parts of a token: what a stage holds; of few tokens so many that there are four blocks on
+  // every SM, with a unit for each warp
+  int split = 1;
+  const auto units = [&](int n) { return (uq + n - 1) / n + kinds * ((uk + n - 1) / n); };
+  while (units(split) > kRopeUnits) ++split;
+  const long long want = (4ll * sms + p.T - 1) / p.T;
+  while (split < want && units(split) > kRopeWarps) ++split;
+  if (split > sms) return -1;
+  p.split = split;
+  p.part_q = (uq + split - 1) / split;
+  p.part_kv = (uk + split - 1) / split;
+  p.stage_bytes = units(split) * 512;
+  return D == 64 ? (cache ? launch_rope_d<64, true>(p, st, sms) : launch_rope_d<64, false>(p, st, sms))
+                 : (cache ? launch_rope_d<128, true>(p, st, sms) : launch_rope_d<128, false>(p, st, sms));
 }
 
 }  // namespace a4w4

@@ -16,6 +16,7 @@
 #include <cfloat>
 
 #include "device.cuh"
+#include "kv.cuh"
 #include "launch.h"
 
 namespace a4w4 {
@@ -34,9 +35,10 @@ __device__ __forceinline__ float from_ordered(uint32_t u) {
   return __uint_as_float(u ^ ((u >> 31) - 1u | 0x80000000u));
 }
 
-// What a logit counts as: NaN as -infinity, +infinity as the largest float, -0 as 0.
-__device__ __forceinline__ float clean_logit(float x) { return x != x ? -INFINITY : fminf(x, FLT_MAX) + 0.f; }
-__device__ __forceinline__ float clean_bias(float b) { return b != b ? -INFINITY : b + 0.f; }
+// What a logit counts as: NaN as -infinity, +infinity as the largest float, -0 as 0.  (Of a NaN
+// and a number fmaxf gives the number.)
+__device__ __forceinline__ float clean_logit(float x) { return fminf(fmaxf(x, -INFINITY), FLT_MAX) + 0.f; }
+__device__ __forceinline__ float clean_bias(float b) { return fmaxf(b, -INFINITY) + 0.f; }
 
 template <bool BF16>
 __device__ __forceinline__ float logit(const RouteArgs& p, int t, int e) {
@@ -46,9 +48,17 @@ __device__ __forceinline__ float logit(const RouteArgs& p, int t, int e) {
 }
 __device__ __forceinline__ float bias_of(const RouteArgs& p, int e) { return clean_bias(p.bias[e]); }
 
+// To 2^-21.7 of itself (weights: chosen experts only).
 __device__ __forceinline__ float sigmoid(float x) {
   // exp of what is not positive: no overflow, and small scores keep their bits
   const float z = expf(-fabsf(x)), r = __frcp_rn(1.f + z);
+  return x >= 0.f ? r : z * r;
+}
+// The same in fewer instructions, to 2^-21.7 and |x| 2^-23.4 of itself where x < 0: for comparing.
+__device__ __forceinline__ float sigmoid_near(float x) {
+  const float z = ex2(-1.4426950408889634f * fabsf(x));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + z));
   return x >= 0.f ? r : z * r;
 }
 __device__ __forceinline__ double sigmoid_64(double x) { return 1.0 / (1.0 + exp(-x)); }
@@ -69,18 +79,18 @@ __device__ __forceinline__ double warp_sum_64(double v) {
   return v;
 }
 
-// The k-th largest (k = 0: the largest) of the lanes' values.
-__device__ __forceinline__ uint32_t warp_kth(uint32_t v, int k, int lane) {
+// The k-th largest (k = 1: the largest) of the lanes' values: the largest one that k lanes reach.
+// Fewer trips than sorting over the warp: T = 1 x 896 experts SORT_TIME us.
+__device__ __forceinline__ uint32_t warp_kth(uint32_t v, int k, uint32_t* s_lane, int lane) {
+  s_lane[lane] = v;
+  __syncwarp();
+  int reached = 0;
 #pragma unroll
-  for (int size = 2; size <= 32; size <<= 1) {
-#pragma unroll
-    for (int o = size >> 1; o > 0; o >>= 1) {
-      const uint32_t u = __shfl_xor_sync(kAll, v, o);
-      // descending runs where the size bit of the lane is clear
-      v = ((lane & o) == 0) == ((lane & size) == 0) ? max(u, v) : min(u, v);
-    }
+  for (int j = 0; j < 8; ++j) {
+    const uint4 u = reinterpret_cast<const uint4*>(s_lane)[j];
+    reached += (u.x >= v) + (u.y >= v) + (u.z >= v) + (u.w >= v);
   }
-  return __shfl_sync(kAll, v, k);
+  return __reduce_max_sync(kAll, reached >= k ? v : 0u);
 }
 
 // A group's strength, from its two largest.  (Opposite infinities of a bias: as if it had none.)
@@ -114,35 +124,39 @@ __device__ __forceinline__ uint32_t best_groups(const RouteArgs& p, Real mine, i
 }
 
 // The whole choice in 64 bits.  Lane r < topk gets the r-th expert.  Rare (see
-// above), or rows with more than kCand keys that tie: bound by the few 64-bit
-// units of an SM, 896 experts about 10 us.
+// above), or rows with more than kCand keys that tie.  Bound by the few 64-bit units of
+// an SM and their latency, so that four exponentials are kept in flight.
 template <bool BF16>
 __device__ __noinline__ int route_in_64(const RouteArgs& p, int t, int lane) {
-  const int E = p.E, per = E / p.groups;
-  double top = -INFINITY, sum = 0.0;
+  const int E = p.E, per = E / p.groups, n = (E - lane + 31) / 32;
+  double c[kRouteMaxExperts / 32];                    // of expert lane + 32 i; NaN: not to be chosen
   if (p.softmax) {
     float m = -INFINITY;
     for (int e = lane; e < E; e += 32) m = fmaxf(m, logit<BF16>(p, t, e));
     m = warp_max(m);
-    top = m == -INFINITY ? 0.0 : static_cast<double>(m);
-    for (int e = lane; e < E; e += 32) sum += exp(static_cast<double>(logit<BF16>(p, t, e)) - top);
+    const double top = m == -INFINITY ? 0.0 : static_cast<double>(m);
+    double sum = 0.0;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      c[i] = exp(static_cast<double>(logit<BF16>(p, t, lane + 32 * i)) - top);
+      sum += c[i];
+    }
     sum = warp_sum_64(sum);
+    const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
+    for (int i = 0; i < n; ++i) c[i] *= inv;
+  } else {
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) c[i] = sigmoid_64(logit<BF16>(p, t, lane + 32 * i));
   }
-  const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
-  auto score = [&](int e) {
-    const double x = logit<BF16>(p, t, e);
-    const double s = p.softmax ? exp(x - top) * inv : sigmoid_64(x);
-    return p.bias == nullptr ? s : s + static_cast<double>(bias_of(p, e));
-  };
-  uint32_t kept = 1u;
+  if (p.bias != nullptr)
+    for (int i = 0; i < n; ++i) c[i] += static_cast<double>(bias_of(p, lane + 32 * i));
   if (p.groups > 1) {
     double mine = 0.0;
     for (int g = 0; g < p.groups; ++g) {
-      double a = -INFINITY, b = -INFINITY;          // the two largest
-      for (int e = g * per + lane; e < (g + 1) * per; e += 32) {
-        const double c = score(e);
-        b = fmax(b, fmin(a, c));
-        a = fmax(a, c);
+      double a = -INFINITY, b = -INFINITY;            // the two largest
+      for (int i = (g * per - lane + 31) / 32; i < n && lane + 32 * i < (g + 1) * per; ++i) {
+        b = fmax(b, fmin(a, c[i]));
+        a = fmax(a, c[i]);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
@@ -152,17 +166,13 @@ __device__ __noinline__ int route_in_64(const RouteArgs& p, int t, int lane) {
       }
       if (lane == g) mine = strength_of(p, a, b);
     }
-    kept = best_groups<double>(p, mine, lane, 0.0, nullptr);
+    const uint32_t kept = best_groups<double>(p, mine, lane, 0.0, nullptr);
+    for (int i = 0; i < n; ++i)
+      if ((kept >> ((lane + 32 * i) / per) & 1u) == 0u) c[i] = NAN;
   }
-  double c[kRouteMaxExperts / 32];
-  const int n = (E - lane + 31) / 32;
-  for (int i = 0; i < n; ++i) {
-    const int e = lane + 32 * i;
-    // NaN: not to be chosen
-    c[i] = (kept >> (p.groups > 1 ? e / per : 0) & 1u) == 0u ? NAN
-           : p.bias == nullptr                               ? static_cast<double>(logit<BF16>(p, t, e))
-                                                             : score(e);
-  }
+  if (p.bias == nullptr)                               // the logits' own order: scores may have run into 0 or 1
+    for (int i = 0; i < n; ++i)
+      if (c[i] == c[i]) c[i] = logit<BF16>(p, t, lane + 32 * i);
   int id = 0;
   for (int k = 0; k < p.topk; ++k) {
     double best = 0.0;
@@ -190,31 +200,25 @@ __device__ __noinline__ int route_in_64(const RouteArgs& p, int t, int lane) {
 
 // NV: keys per lane, four consecutive experts each (expert 4 (32 i + lane) + u).
 template <int NV, bool BF16>
-__global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(const RouteArgs p) {
-  __shared__ unsigned long long s_key[kRouteWarps][kCand];
+__global__ void __launch_bounds__(32 * kRouteWarps, NV <= 32 ? 7 : 3) moe_route_kernel(const RouteArgs p) {
+  __shared__ alignas(16) unsigned long long s_key[kRouteWarps][kCand + 4];
   __shared__ uint16_t s_at[kRouteWarps][kCand];
   __shared__ unsigned long long s_top[kRouteWarps][34];   // the best in order, one more than can be asked for
+  __shared__ alignas(16) uint32_t s_lane[kRouteWarps][32];
   extern __shared__ float s_val[];                          // with groups: [kRouteWarps][E + groups * 32]
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x * kRouteWarps + warp, E = p.E, topk = p.topk;
   if (t >= p.T) return;
-  int32_t* ids = p.ids + static_cast<long long>(t) * topk;
-  float* weights = p.weights + static_cast<long long>(t) * topk;
-  if (p.count != nullptr && t >= *p.count) {
-    if (lane < topk) {
-      ids[lane] = -1;
-      weights[lane] = 0.f;
-    }
-    return;
-  }
+  const int count = p.count != nullptr ? *p.count : p.T;    // (looked at when the logits are on their way)
 
   float x[NV];
 #pragma unroll
   for (int i = 0; i < NV; i += 4) {
     const int e = 4 * (i / 4 * 32 + lane);
     const long long at = t * p.stride + e;
+    x[i] = x[i + 1] = x[i + 2] = x[i + 3] = -INFINITY;
     if (p.vectors) {                                  // E and the rows' starts are multiples of four values
       if (e < E) {
         if (BF16) {
@@ -233,9 +237,18 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(const Route
           x[i + u] = BF16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p.logits)[at + u]) << 16)
                           : static_cast<const float*>(p.logits)[at + u];
     }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) x[i + u] = e + u < E ? clean_logit(x[i + u]) : -INFINITY;
   }
+  int32_t* ids = p.ids + static_cast<long long>(t) * topk;
+  float* weights = p.weights + static_cast<long long>(t) * topk;
+  if (t >= count) {
+    if (lane < topk) {
+      ids[lane] = -1;
+      weights[lane] = 0.f;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) x[i] = clean_logit(x[i]);
 
   // scores where they are compared; `margin` bounds how far apart two of them may be and still change places
   const bool by_score = p.bias != nullptr, by_sum = p.groups > 1 && (by_score || p.group_top == 2);
@@ -253,23 +266,45 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(const Route
       inv = z > 0.f ? 1.f / z : 0.f;
       margin = inv * 0x1p-18f;      // the sum's 23 roundings, and the exponentials'
     } else {
-      margin = sigmoid(top) * 0x1p-20f;
+      margin = sigmoid(top) * (0x1p-19f + fmaxf(-top, 0.f) * 0x1p-21f);
+      if (top >= 0.f) margin *= 0.5f;
+      if (top == -INFINITY) margin = 0.f;
     }
-    margin += 0x1p-146f;            // scores so small that they have lost bits
+    margin += 0x1p-120f;            // scores so small that they have lost bits
   }
   uint32_t key[NV];
+  if (by_score || by_sum) {
+    float* val = s_val + warp * p.val_stride;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = 4 * (i / 4 * 32 + lane) + (i & 3);
-    float c = x[i];
-    if (by_score || by_sum) {
-      const float s = p.softmax ? expf(x[i] - top) * inv : sigmoid(x[i]);
-      c = by_score && e < E ? s + bias_of(p, e) : s;
+    for (int i = 0; i < NV; i += 4) {
+      const int e = 4 * (i / 4 * 32 + lane);
+      float b[4] = {0.f, 0.f, 0.f, 0.f};
+      if (by_score) {
+        if (p.bias_vectors) {
+          if (e < E) {
+            const float4 w = *reinterpret_cast<const float4*>(p.bias + e);
+            b[0] = clean_bias(w.x); b[1] = clean_bias(w.y); b[2] = clean_bias(w.z); b[3] = clean_bias(w.w);
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (e + u < E) b[u] = bias_of(p, e + u);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float c = (p.softmax ? expf(x[i + u] - top) * inv : sigmoid_near(x[i + u])) + b[u];
+        key[i + u] = e + u < E ? ordered(by_score ? c : x[i + u]) : 0u;
+        if (by_sum && e + u < E) val[e + u + __umulhi(static_cast<unsigned>(e + u), p.per_recip) * p.skew] = c;
+      }
     }
-    key[i] = e < E ? ordered(by_score ? c : x[i]) : 0u;
-    if (p.groups > 1 && e < E) {
-      const int g = __umulhi(static_cast<unsigned>(e), p.per_recip);
-      s_val[warp * p.val_stride + e + g * p.skew] = c;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = 4 * (i / 4 * 32 + lane) + (i & 3);
+      key[i] = e < E ? ordered(x[i]) : 0u;
+      if (p.groups > 1 && e < E)
+        s_val[warp * p.val_stride + e + __umulhi(static_cast<unsigned>(e), p.per_recip) * p.skew] = x[i];
     }
   }
 
@@ -296,7 +331,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(const Route
     // logits are compared as they are; of a sum of two the error is twice a score's and the roundings of c and of the sum
     float most = fmaxf(fabsf(a), p.group_top == 2 ? fabsf(b) : 0.f);
     most = warp_max(most < INFINITY ? most : 0.f);
-    uint32_t kept = best_groups<float>(p, strength, lane, 2.f * margin + most * 0x1p-21f, by_sum ? &in_64 : nullptr);
+    const uint32_t kept = best_groups<float>(p, strength, lane, 2.f * margin + most * 0x1p-21f, by_sum ? &in_64 : nullptr);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = 4 * (i / 4 * 32 + lane) + (i & 3);
@@ -306,15 +341,15 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(const Route
   }
 
   int id = 0;
+  float xi = -INFINITY;                               // lane r < topk: the r-th expert and its logit
   if (!in_64) {
     uint32_t most = 0u;
 #pragma unroll
     for (int i = 0; i < NV; ++i) most = max(most, key[i]);
-    uint32_t floor_key = max(warp_kth(most, topk - 1, lane), 1u);
+    uint32_t floor_key = max(warp_kth(most, topk, s_lane[warp], lane), 1u);
     const float f = from_ordered(floor_key);
-    if (by_score && fabsf(f) < INFINITY) {           // (absent: NaN)
+    if (by_score && fabsf(f) < INFINITY)             // (no such key: NaN)
       floor_key = max(ordered(f - (margin + fabsf(f) * 0x1p-22f)), 1u);
-    }
     int mine = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) mine += key[i] >= floor_key;
@@ -337,23 +372,30 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(const Route
           cand[before++] = static_cast<unsigned long long>(key[i]) << 32 | (kAll - e);   // of equals the lower comes first
         }
       }
+      if (lane < 4) cand[n + lane] = 0ull;            // below every key: the ranks are counted four at a time
       __syncwarp();
       for (int i = lane; i < n; i += 32) {
         const unsigned long long c = cand[i];
         int rank = 0;
-        for (int j = 0; j < n; ++j) rank += cand[j] > c;
+#pragma unroll 2
+        for (int j = 0; j < n; j += 4) {
+          const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(cand + j);
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(cand + j + 2);
+          rank += (u.x > c) + (u.y > c) + (v.x > c) + (v.y > c);
+        }
         if (rank <= topk) best[rank] = c;
       }
       __syncwarp();
       const unsigned long long c = best[lane < n && lane < topk ? lane : 0];
       id = static_cast<int>(kAll - static_cast<uint32_t>(c));
+      xi = by_score ? logit<BF16>(p, t, id) : from_ordered(static_cast<uint32_t>(c >> 32));
       bool near = false;
       if (by_score && lane < topk && lane + 1 < n) {
         const unsigned long long d = best[lane + 1];
         const float vc = from_ordered(static_cast<uint32_t>(c >> 32)), vd = from_ordered(static_cast<uint32_t>(d >> 32));
         if (!(vc - vd > margin + fmaxf(fabsf(vc), fabsf(vd)) * 0x1p-22f) && (vc != vd || fabsf(vc) < INFINITY)) {
           const int other = static_cast<int>(kAll - static_cast<uint32_t>(d));
-          near = logit<BF16>(p, t, id) != logit<BF16>(p, t, other) || bias_of(p, id) != bias_of(p, other);
+          near = xi != logit<BF16>(p, t, other) || bias_of(p, id) != bias_of(p, other);
         }
       }
       if (__any_sync(kAll, near)) {
@@ -377,18 +419,22 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(const Route
           }
           __syncwarp();
           id = static_cast<int>(best[lane < topk ? lane : 0]);
+          xi = logit<BF16>(p, t, id);
         }
       }
     }
   }
-  if (in_64) id = route_in_64<BF16>(p, t, lane);
+  if (in_64) {
+    id = route_in_64<BF16>(p, t, lane);
+    xi = logit<BF16>(p, t, id);
+  }
 
   // weights: scores of the chosen ones, with the largest of them brought near 1 where they are divided by their sum
   const bool mine = lane < topk;
-  const float xi = mine ? logit<BF16>(p, t, id) : -INFINITY;
+  if (!mine) xi = -INFINITY;
   float w;
   if (p.renorm) {
-    const float m = warp_max(xi);
+    const float m = by_score ? warp_max(xi) : __shfl_sync(kAll, xi, 0);
     if (m == -INFINITY) {
       w = 0.f;                                        // nothing to share
     } else {
@@ -428,6 +474,7 @@ int launch_moe_route(RouteArgs p, int bf16, cudaStream_t st) {
   const int per = p.E / p.groups;
   // 16 bytes (8 in BF16) at a time
   p.vectors = p.E % 4 == 0 && p.stride % 4 == 0 && reinterpret_cast<uintptr_t>(p.logits) % (bf16 ? 8 : 16) == 0;
+  p.bias_vectors = p.E % 4 == 0 && reinterpret_cast<uintptr_t>(p.bias) % 16 == 0;
   p.per_recip = p.groups > 1 ? static_cast<unsigned>((0x100000000ull + per - 1) / per) : 0u;   // per >= 2
   p.skew = 1;
   while (2 * p.skew * p.groups <= 32) p.skew *= 2;
