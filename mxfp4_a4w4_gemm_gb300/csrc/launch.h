@@ -189,6 +189,7 @@ struct W8Plan {
   int x_tiles, w_tiles, splits;
   int kt;             // 128-wide blocks of K
   int half_tiles;     // large: tiles of the last partial wave, run as halves
+  int cluster;        // large: thread blocks that share their weight tiles (1 or 2)
   size_t ws_bytes;
 };
 W8Plan plan_w8a8(int M, int N, int K, int sms);

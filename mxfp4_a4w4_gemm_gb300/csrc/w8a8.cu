@@ -173,20 +173,36 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64
       :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-// 32 or 16 consecutive fp32 columns of this thread's TMEM lane, not waited for.
-__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t* r) {
+// 64 consecutive fp32 columns of this thread's TMEM lane, in one load.
+__device__ __forceinline__ void tmem_ld64_now(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
-      "%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,"
+      "%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,"
+      "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63"
+      "}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
       : "r"(taddr));
+  // the registers are named so that nothing uses them earlier
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31]), "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]),
+                 "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]), "+r"(r[40]), "+r"(r[41]), "+r"(r[42]),
+                 "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]), "+r"(r[48]), "+r"(r[49]),
+                 "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]), "+r"(r[56]),
+                 "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63])
+               :: "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
 __device__ __forceinline__ unsigned long long pack2(uint32_t lo, uint32_t hi) {
   unsigned long long d;
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
@@ -228,8 +244,12 @@ struct W8LargeArgs {
 };
 
 struct W8L {
-  static constexpr int EPI_WARPS = 8;
-  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int EPI_WARPS = 8, EPI_FIRST = 4;   // the first warpgroup: producer, MMA issuer, two that only help out
+  static constexpr int THREADS = 32 * (EPI_FIRST + EPI_WARPS);
+  // a thread of the epilogue holds 128 sums and 64 columns: the registers of the launch (384 x
+  // 168) go to the two warpgroups that need them (128 x 40 + 256 x 232)
+  static constexpr int REGS_FEW = 40, REGS_MANY = 232;
+  static_assert(128 * REGS_FEW + 32 * EPI_WARPS * REGS_MANY <= THREADS * 168, "registers");
   static constexpr int STAGES = 4;
   static constexpr int STAGE = 3 * kTile;
   static constexpr int STG_PITCH = 80;                 // 32 BF16 columns and 16 bytes: 16-byte rows on different banks
@@ -273,17 +293,21 @@ __device__ __forceinline__ bool w8_promote(const W8LargeArgs& p, uint32_t tmem, 
     if (!mbar_wait(acc_full + 8u * b, static_cast<uint32_t>(g >> 1) & 1u, abort_flag, p.wait_ns, p.status)) return false;
     __syncwarp();
     tc_fence_after();
+    // few and large loads: the two warps of a scheduler load and add in turn
+    static_assert(COLS % 64 == 0, "columns");
+    constexpr int W = 64;
 #pragma unroll
-    for (int c = 0; c < COLS; c += 32) {
-      uint32_t t[32];
-      tmem_ld32_issue(tmem + b * 256 + c, t);
-      tmem_wait_ld();
+    for (int c = 0; c < COLS; c += W) {
+      uint32_t t[W];
+      tmem_ld64_now(tmem + b * 256 + c, t);
+      if (c + W == COLS) {                               // everything is read: the accumulator may be written again
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty + 8u * b);
+      }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[c / 2 + i] = fma2(pack2(t[2 * i], t[2 * i + 1]), s2, acc[c / 2 + i]);
+      for (int i = 0; i < W / 2; ++i) acc[c / 2 + i] = fma2(pack2(t[2 * i], t[2 * i + 1]), s2, acc[c / 2 + i]);
     }
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(acc_empty + 8u * b);
   }
   return true;
 }
@@ -312,7 +336,7 @@ __device__ __forceinline__ void w8_store(const W8LargeArgs& p, const unsigned lo
 
 //   warp 0      producer: per block of K one activation tile and two (one) weight tiles;
 //   warp 1      TMEM owner and MMA issuer: two accumulators of 256 columns in turn;
-//   warps 2-9   two per TMEM lane quadrant, a thread per token row and half of the
+//   warps 4-11  two per TMEM lane quadrant, a thread per token row and half of the
 //               columns: scale and add each block's sums, then BF16 rows.
 __global__ void __launch_bounds__(W8L::THREADS, 1) a4w4_w8a8_large_kernel(const W8LargeArgs p) {
   using Cf = W8L;
@@ -349,63 +373,67 @@ __global__ void __launch_bounds__(W8L::THREADS, 1) a4w4_w8a8_large_kernel(const 
   griddep_wait();                                       // the activation tiles come from the kernel before
   griddep_launch_dependents();
 
-  if (warp == 0) {
-    if (lane == 0) {
-      const uint64_t pol = policy_evict_last();         // operands are read again by other tiles, from L2
-      int g = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; u < p.units && ok; u += G) {
-        const W8Unit t = w8_unit(p, u);
-        const uint8_t* a = p.Aq + static_cast<long long>(t.x) * p.KT * kActTile;
-        const uint8_t* w = p.W8 + static_cast<long long>(t.w) * p.KT * kTile;
-        for (int kt = 0; kt < p.KT; ++kt, ++g) {
-          const int s = g % Cf::STAGES;
-          if (!mbar_wait(empty + 8u * s, ((g / Cf::STAGES) & 1) ^ 1u, abort_flag, p.wait_ns, p.status)) {
-            ok = false;
-            break;
+  if (warp < Cf::EPI_FIRST) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(Cf::REGS_FEW));
+    if (warp == 0) {
+      if (lane == 0) {
+        const uint64_t pol = policy_evict_last();         // operands are read again by other tiles, from L2
+        int g = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; u < p.units && ok; u += G) {
+          const W8Unit t = w8_unit(p, u);
+          const uint8_t* a = p.Aq + static_cast<long long>(t.x) * p.KT * kActTile;
+          const uint8_t* w = p.W8 + static_cast<long long>(t.w) * p.KT * kTile;
+          for (int kt = 0; kt < p.KT; ++kt, ++g) {
+            const int s = g % Cf::STAGES;
+            if (!mbar_wait(empty + 8u * s, ((g / Cf::STAGES) & 1) ^ 1u, abort_flag, p.wait_ns, p.status)) {
+              ok = false;
+              break;
+            }
+            const uint32_t fb = full + 8u * s, dst = base + s * Cf::STAGE;
+            mbar_arrive_expect_tx(fb, (1 + t.n) * kTile);
+            bulk_g2s(dst, a + static_cast<long long>(kt) * kActTile, kTile, fb, pol);
+            bulk_g2s(dst + kTile, w + static_cast<long long>(kt) * kTile, kTile, fb, pol);
+            if (t.n == 2) bulk_g2s(dst + 2 * kTile, w + static_cast<long long>(p.KT + kt) * kTile, kTile, fb, pol);
           }
-          const uint32_t fb = full + 8u * s, dst = base + s * Cf::STAGE;
-          mbar_arrive_expect_tx(fb, (1 + t.n) * kTile);
-          bulk_g2s(dst, a + static_cast<long long>(kt) * kActTile, kTile, fb, pol);
-          bulk_g2s(dst + kTile, w + static_cast<long long>(kt) * kTile, kTile, fb, pol);
-          if (t.n == 2) bulk_g2s(dst + 2 * kTile, w + static_cast<long long>(p.KT + kt) * kTile, kTile, fb, pol);
         }
+        // every copy issued lands before the shared memory is released
+        for (int j = (g > Cf::STAGES ? g - Cf::STAGES : 0); j < g; ++j)
+          mbar_wait(full + 8u * (j % Cf::STAGES), (j / Cf::STAGES) & 1u, never, drain_ns, p.status);
       }
-      // every copy issued lands before the shared memory is released
-      for (int j = (g > Cf::STAGES ? g - Cf::STAGES : 0); j < g; ++j)
-        mbar_wait(full + 8u * (j % Cf::STAGES), (j / Cf::STAGES) & 1u, never, drain_ns, p.status);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      const uint64_t adesc0 = sdesc_sw128(base), bdesc0 = sdesc_sw128(base + kTile);
-      int g = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; u < p.units && ok; u += G) {
-        const uint32_t idesc = idesc_e4m3(128u * w8_unit(p, u).n);
-        for (int kt = 0; kt < p.KT; ++kt, ++g) {
-          const int s = g % Cf::STAGES, b = g & 1;
-          // the accumulator's sums of two blocks ago have been read
-          if ((g >= 2 && !mbar_wait(acc_empty + 8u * b, static_cast<uint32_t>((g >> 1) - 1) & 1u, abort_flag, p.wait_ns, p.status)) ||
-              !mbar_wait(full + 8u * s, (g / Cf::STAGES) & 1u, abort_flag, p.wait_ns, p.status)) {
-            ok = false;
-            break;
+    } else if (warp == 1) {
+      if (lane == 0) {
+        const uint64_t adesc0 = sdesc_sw128(base), bdesc0 = sdesc_sw128(base + kTile);
+        int g = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; u < p.units && ok; u += G) {
+          const uint32_t idesc = idesc_e4m3(128u * w8_unit(p, u).n);
+          for (int kt = 0; kt < p.KT; ++kt, ++g) {
+            const int s = g % Cf::STAGES, b = g & 1;
+            // the accumulator's sums of two blocks ago have been read
+            if ((g >= 2 && !mbar_wait(acc_empty + 8u * b, static_cast<uint32_t>((g >> 1) - 1) & 1u, abort_flag, p.wait_ns, p.status)) ||
+                !mbar_wait(full + 8u * s, (g / Cf::STAGES) & 1u, abort_flag, p.wait_ns, p.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t ad = adesc0 + ((s * Cf::STAGE) >> 4), bd = bdesc0 + ((s * Cf::STAGE) >> 4);
+  #pragma unroll
+            for (int ks = 0; ks < 4; ++ks) mma_e4m3(tmem + b * 256, ad + 2 * ks, bd + 2 * ks, idesc, ks > 0 ? 1u : 0u);
+            mma_commit(empty + 8u * s);
+            mma_commit(acc_full + 8u * b);
           }
-          tc_fence_after();
-          const uint64_t ad = adesc0 + ((s * Cf::STAGE) >> 4), bd = bdesc0 + ((s * Cf::STAGE) >> 4);
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks) mma_e4m3(tmem + b * 256, ad + 2 * ks, bd + 2 * ks, idesc, ks > 0 ? 1u : 0u);
-          mma_commit(empty + 8u * s);
-          mma_commit(acc_full + 8u * b);
         }
+        // TMEM is released only after every MMA issued has completed
+        mma_commit(drain);
+        mbar_wait(drain, 0, never, drain_ns, p.status);
       }
-      // TMEM is released only after every MMA issued has completed
-      mma_commit(drain);
-      mbar_wait(drain, 0, never, drain_ns, p.status);
     }
   } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(Cf::REGS_MANY));
+    const int q = warp & 3, half = (warp - Cf::EPI_FIRST) >> 2;
     const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    uint8_t* stg = smem + Cf::OFF_STG + (warp - 2) * 32 * Cf::STG_PITCH;
+    uint8_t* stg = smem + Cf::OFF_STG + (warp - Cf::EPI_FIRST) * 32 * Cf::STG_PITCH;
     unsigned long long acc[64];
     int g = 0;
     for (int u = blockIdx.x; u < p.units; u += G) {
