@@ -9,7 +9,7 @@
 // sum is read back, scaled and added in fp32 registers while the next block's MMAs run
 // into the other accumulator.  Two kernels:
 //
-//   small  few tokens: 128 weight rows are the MMA's M side, 16, 32 or 64 tokens its N
+//   small  few tokens: 128 weight rows are the MMA's M side, 16 or 32 tokens its N
 //          side, K split over the thread blocks of a cluster; activations are quantised
 //          in the kernel.  Bound by the weights' bytes.
 //   large  128 tokens x 256 weight rows per tile, one persistent thread block per SM,
@@ -163,6 +163,17 @@ __global__ void __launch_bounds__(256) w8_quant_tiles_kernel(const uint16_t* __r
 
 // E4M3 x E4M3, both K-major, fp32 D, M = 128, K = 32: formats 0 at bits 7 and 10.
 __device__ __forceinline__ uint32_t idesc_e4m3(uint32_t n) { return (1u << 4) | ((n >> 3) << 17) | ((128u >> 4) << 24); }
+
+// One thread of a whole warp, in a form that the compiler knows to be one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
 
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                          uint32_t accumulate) {
@@ -402,26 +413,33 @@ __global__ void __launch_bounds__(W8L::THREADS, 1) a4w4_w8a8_large_kernel(const 
           mbar_wait(full + 8u * (j % Cf::STAGES), (j / Cf::STAGES) & 1u, never, drain_ns, p.status);
       }
     } else if (warp == 1) {
-      if (lane == 0) {
+      // (One thread's path from "read" to the next MMAs is part of every block of K: it waits for
+      // the operands first, for the accumulator last, and commits the accumulator first.)
+      if (elect_one()) {
         const uint64_t adesc0 = sdesc_sw128(base), bdesc0 = sdesc_sw128(base + kTile);
-        int g = 0;
+        int s = 0, g = 0;
+        uint32_t ph = 0;
         bool ok = true;
         for (int u = blockIdx.x; u < p.units && ok; u += G) {
           const uint32_t idesc = idesc_e4m3(128u * w8_unit(p, u).n);
           for (int kt = 0; kt < p.KT; ++kt, ++g) {
-            const int s = g % Cf::STAGES, b = g & 1;
-            // the accumulator's sums of two blocks ago have been read
-            if ((g >= 2 && !mbar_wait(acc_empty + 8u * b, static_cast<uint32_t>((g >> 1) - 1) & 1u, abort_flag, p.wait_ns, p.status)) ||
-                !mbar_wait(full + 8u * s, (g / Cf::STAGES) & 1u, abort_flag, p.wait_ns, p.status)) {
+            const uint32_t b = g & 1, af = acc_full + 8u * b, d = tmem + b * 256, off = static_cast<uint32_t>(s * Cf::STAGE) >> 4;
+            const uint64_t ad = adesc0 + off, bd = bdesc0 + off;
+            if (!mbar_wait(full + 8u * s, ph, abort_flag, p.wait_ns, p.status) ||
+                // the accumulator's sums of two blocks ago have been read
+                (g >= 2 && !mbar_wait(af + 16u, static_cast<uint32_t>((g >> 1) - 1) & 1u, abort_flag, p.wait_ns, p.status))) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint64_t ad = adesc0 + ((s * Cf::STAGE) >> 4), bd = bdesc0 + ((s * Cf::STAGE) >> 4);
-  #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) mma_e4m3(tmem + b * 256, ad + 2 * ks, bd + 2 * ks, idesc, ks > 0 ? 1u : 0u);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) mma_e4m3(d, ad + 2 * ks, bd + 2 * ks, idesc, ks > 0 ? 1u : 0u);
+            mma_commit(af);
             mma_commit(empty + 8u * s);
-            mma_commit(acc_full + 8u * b);
+            if (++s == Cf::STAGES) {
+              s = 0;
+              ph ^= 1u;
+            }
           }
         }
         // TMEM is released only after every MMA issued has completed
@@ -489,7 +507,7 @@ struct W8S {
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;
   static constexpr int ACC_COLS = NX;
-  static constexpr int TMEM_COLS = 2 * NX <= 32 ? 32 : 2 * NX <= 64 ? 64 : 128;
+  static constexpr int TMEM_COLS = 2 * NX;
   // After the last block the rings' bytes serve the reduction: this block's partial sums,
   // then up to 16 senders' shares of this block's slice ((G + S) groups of 16 bytes, G = 32 NX)
   static constexpr int OFF_PUSH = NX * 512;
@@ -801,8 +819,7 @@ W8Plan plan_w8a8(int M, int N, int K, int sms) {
   W8Plan pl{};
   pl.kt = K / 128;
   pl.w_tiles = N / 128;
-  const int small_nx = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-  pl.large = M > 128;
+  pl.large = M > 32;
   if (pl.large) {
     pl.x_tiles = (M + 127) / 128;
     const long long tiles = static_cast<long long>(pl.x_tiles) * (pl.w_tiles / 2), rest = tiles % sms;
@@ -811,7 +828,7 @@ W8Plan plan_w8a8(int M, int N, int K, int sms) {
     pl.ws_bytes = static_cast<size_t>(pl.x_tiles) * pl.kt * kActTile;
     return pl;
   }
-  pl.nx = small_nx;
+  pl.nx = M <= 16 ? 16 : 32;
   pl.x_tiles = (M + pl.nx - 1) / pl.nx;
   const int blocks = pl.w_tiles * pl.x_tiles;
   pl.splits = 2 * sms / (blocks > 0 ? blocks : 1);      // two thread blocks on every SM
@@ -834,8 +851,7 @@ int launch_w8a8(const W8Plan& pl, const void* A, int M, int K, const void* W8, c
     a.wait_ns = wait_ns;
     a.status = status;
     const dim3 grid(pl.w_tiles, pl.x_tiles, pl.splits);
-    return pl.nx == 16 ? launch_small_nx<16>(a, grid, st) : pl.nx == 32 ? launch_small_nx<32>(a, grid, st)
-                                                                       : launch_small_nx<64>(a, grid, st);
+    return pl.nx == 16 ? launch_small_nx<16>(a, grid, st) : launch_small_nx<32>(a, grid, st);
   }
   const long long blocks = static_cast<long long>(pl.x_tiles) * 128 * pl.kt;
   const long long grid = (blocks * 8 + 255) / 256;
