@@ -34,9 +34,12 @@ Modules:
   moe    -- routed-row sort, the grouped GEMM1 + SwiGLU (or SiLU) + MXFP4
             requant, and GEMM2 (down projection, top-k weighted sum)
   kv     -- the paged key/value cache: step plan, cache bytes, attention
+  w8a8   -- the 8-bit product with a scale for each block of 128
+  rope   -- norms of query and key heads and their rotation by position
+  route  -- routing of tokens to experts
 
 Parity status of every function is pinned by ``tests/test_oracle_*.py``
 (-m "not gpu"); none is "parity unpinned".
 """
 
-from . import mxfp4, gemm, moe, kv  # noqa: F401
+from . import mxfp4, gemm, moe, kv, w8a8, rope, route  # noqa: F401
