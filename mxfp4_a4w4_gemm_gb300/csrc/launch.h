@@ -152,10 +152,10 @@ struct RouteArgs {
   int32_t* ids;                 // [T, topk]
   float* weights;               // [T, topk]
   // set by the launcher: rows, the bias can be read four values at a time; ceil(2^32 / (E / groups));
-  // lanes per group, and shared floats per token
+  // lanes per group; ceil(E / 4)
   int vectors, bias_vectors;
   unsigned int per_recip;
-  int skew, val_stride;
+  int group_lanes, row_quads;
 };
 int launch_moe_route(RouteArgs p, int bf16, cudaStream_t st);
 

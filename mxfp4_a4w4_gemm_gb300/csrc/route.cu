@@ -1,18 +1,23 @@
 // route.cu -- routing of tokens to experts: scores, groups, top-k, weights
 // (include/a4w4.h, a4w4_moe_route).
 //
-// A warp takes one token.  Its E logits stay in registers as 32-bit keys whose
-// unsigned order is the order of what is compared (the logits themselves where
-// there is no bias: both score functions are increasing; score + bias
-// otherwise).  The k-th largest of the 32 lanes' maxima is a lower bound of the
-// k-th largest key, so only the few keys at or above it (22 of 896 for k = 16)
-// go to shared memory, where each one's rank is the number of keys above it: no
-// sort and no k passes over the row.
+// A warp takes one token.  Its E logits become 32-bit keys in shared memory whose
+// unsigned order is the order of what is compared (the logits themselves where there is
+// no bias: both score functions are increasing; score + bias otherwise).  The k-th
+// largest of the 32 lanes' maxima is a lower bound of the k-th largest key, so only the
+// few keys at or above it (22 of 896 for k = 16) are looked at again: each one's rank is
+// the number of keys above it, no sort and no k passes over the row.
 //
-// Choosing as exact scores would: score + bias is known to about 2^-21 of the
+// Every loop over the row is short in code: with the keys in registers, and so the
+// loops written out, a third of the time went to fetching instructions (4096 x 896
+// 13.4 us, as it stands ROUTE_TIME).
+//
+// Choosing as exact scores would: score + bias is known to about 2^-20 of the
 // largest score.  Where two neighbours of the chosen order (or a kept and a
-// dropped group) are nearer than that and do not come from the same inputs, 64
-// bits decide: for the candidates alone (sigmoid), or for the row.
+// dropped group) are nearer than that and do not come from the same inputs, the
+// candidates are compared again as sums of two floats (2^-44), and what then still is
+// open, or groups, the row over in 64 bits, of which an SM has few units (some 90 us
+// for 896 experts: of the rows met in practice none).
 #include <cfloat>
 
 #include "device.cuh"
@@ -93,6 +98,70 @@ __device__ __forceinline__ uint32_t warp_kth(uint32_t v, int k, uint32_t* s_lane
   return __reduce_max_sync(kAll, reached >= k ? v : 0u);
 }
 
+// ---------------------------------------------------------------------------
+// Unevaluated sums of two floats (the error-free sums of Knuth and Dekker, products by fma):
+// 2^-46 of the value and more for some ten fp32 instructions, where 64-bit ones wait 100 cycles
+// for each other.
+struct Pair { float h, l; };
+__device__ __forceinline__ Pair fast_two_sum(float a, float b) {      // |a| >= |b|
+  const float s = a + b;
+  return {s, b - (s - a)};
+}
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  const Pair s = two_sum(a.h, b.h);
+  return fast_two_sum(s.h, s.l + (a.l + b.l));
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+  const float p = a.h * b.h;
+  return fast_two_sum(p, fmaf(a.h, b.l, fmaf(a.l, b.h, fmaf(a.h, b.h, -p))));
+}
+__device__ __forceinline__ Pair reciprocal(Pair s) {
+  const float r = 1.f / s.h;
+  return fast_two_sum(r, r * (fmaf(-s.h, r, 1.f) - s.l * r));
+}
+__device__ __forceinline__ constexpr Pair as_pair(double v) {
+  return {static_cast<float>(v), static_cast<float>(v - static_cast<double>(static_cast<float>(v)))};
+}
+// exp(d), d <= 0: d = n ln 2 + r, |r| <= 0.35, Taylor's series; 0 below 2^-120.
+__device__ __forceinline__ Pair exp_pair(Pair d) {
+  constexpr double kLn2 = 0.69314718055994530942;
+  constexpr float kA = 0x1.62e4p-1f;                 // 16 bits: n times it is exact
+  constexpr Pair kB = as_pair(kLn2 - static_cast<double>(kA));
+  if (!(d.h > -83.f)) return {0.f, 0.f};
+  const float n = rintf(d.h * 1.44269504f), p = n * kB.h;
+  const Pair r = add(add(two_sum(d.h, -n * kA), {d.l, 0.f}), {-p, -fmaf(n, kB.l, fmaf(n, kB.h, -p))});
+  constexpr double c8 = 1.0 / 40320, c9 = c8 / 9, c10 = c9 / 10, c11 = c10 / 11, c12 = c11 / 12;
+  const float q = fmaf(r.h, fmaf(r.h, fmaf(r.h, fmaf(r.h, float(c12), float(c11)), float(c10)), float(c9)), float(c8));
+  Pair e = add(as_pair(1.0 / 5040), mul(r, {q, 0.f}));
+  e = add(as_pair(1.0 / 720), mul(r, e));
+  e = add(as_pair(1.0 / 120), mul(r, e));
+  e = add(as_pair(1.0 / 24), mul(r, e));
+  e = add(as_pair(1.0 / 6), mul(r, e));
+  e = add({0.5f, 0.f}, mul(r, e));
+  e = add({1.f, 0.f}, mul(r, e));
+  e = add({1.f, 0.f}, mul(r, e));
+  const float scale = pow2i_normal(static_cast<int>(n));
+  return {e.h * scale, e.l * scale};
+}
+__device__ __forceinline__ Pair sigmoid_pair(float x) {
+  const Pair z = exp_pair({-fabsf(x), 0.f}), r = reciprocal(add({1.f, 0.f}, z));
+  return x >= 0.f ? r : mul(z, r);
+}
+__device__ __forceinline__ Pair warp_sum(Pair v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = add(v, {__shfl_xor_sync(kAll, v.h, o), __shfl_xor_sync(kAll, v.l, o)});
+  return v;
+}
+// A key of the same order.  (Infinite biases: nothing is left of the smaller term.)
+__device__ __forceinline__ unsigned long long ordered(Pair v) {
+  if (!(fabsf(v.h) < INFINITY)) v.l = 0.f;
+  return static_cast<unsigned long long>(ordered(v.h + 0.f)) << 32 | ordered(v.l + 0.f);
+}
+
 // A group's strength, from its two largest.  (Opposite infinities of a bias: as if it had none.)
 template <typename Real>
 __device__ __forceinline__ Real strength_of(const RouteArgs& p, Real a, Real b) {
@@ -123,9 +192,9 @@ __device__ __forceinline__ uint32_t best_groups(const RouteArgs& p, Real mine, i
   return mask;
 }
 
-// The whole choice in 64 bits.  Lane r < topk gets the r-th expert.  Rare (see
-// above), or rows with more than kCand keys that tie.  Bound by the few 64-bit units of
-// an SM and their latency, so that four exponentials are kept in flight.
+// The whole choice in 64 bits.  Lane r < topk gets the r-th expert.  For what the rest leaves
+// open (see above), and rows with more than kCand keys that tie.  Bound by the few 64-bit
+// units of an SM and their latency, so that four exponentials are kept in flight.
 template <bool BF16>
 __device__ __noinline__ int route_in_64(const RouteArgs& p, int t, int lane) {
   const int E = p.E, per = E / p.groups, n = (E - lane + 31) / 32;
@@ -198,44 +267,83 @@ __device__ __noinline__ int route_in_64(const RouteArgs& p, int t, int lane) {
   return id;
 }
 
-// NV: keys per lane, four consecutive experts each (expert 4 (32 i + lane) + u).
-template <int NV, bool BF16>
-__global__ void __launch_bounds__(32 * kRouteWarps, NV <= 32 ? 7 : 3) moe_route_kernel(const RouteArgs p) {
+// Four logits of a row from expert e on, as they count; -infinity behind the last.
+template <bool BF16>
+__device__ __forceinline__ float4 four_logits(const RouteArgs& p, long long row, int e) {
+  float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  const long long at = row + e;
+  if (p.vectors) {                                    // E and the rows' starts are multiples of four values
+    if (e < p.E) {
+      if (BF16) {
+        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.logits) + at);
+        x[0] = __uint_as_float(w.x << 16); x[1] = __uint_as_float(w.x & 0xFFFF0000u);
+        x[2] = __uint_as_float(w.y << 16); x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+      } else {
+        const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(p.logits) + at);
+        x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (e + u < p.E)
+        x[u] = BF16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p.logits)[at + u]) << 16)
+                    : static_cast<const float*>(p.logits)[at + u];
+  }
+  return make_float4(clean_logit(x[0]), clean_logit(x[1]), clean_logit(x[2]), clean_logit(x[3]));
+}
+__device__ __forceinline__ float4 four_biases(const RouteArgs& p, int e) {
+  if (p.bias_vectors) {
+    const float4 w = e < p.E ? *reinterpret_cast<const float4*>(p.bias + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+    return make_float4(clean_bias(w.x), clean_bias(w.y), clean_bias(w.z), clean_bias(w.w));
+  }
+  float b[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (e + u < p.E) b[u] = bias_of(p, e + u);
+  return make_float4(b[0], b[1], b[2], b[3]);
+}
+// Keys of experts e .. e + 3; 0 behind the last, below every other.
+__device__ __forceinline__ uint4 four_keys(float4 c, int e, int E) {
+  return make_uint4(ordered(c.x), e + 1 < E ? ordered(c.y) : 0u, e + 2 < E ? ordered(c.z) : 0u, e + 3 < E ? ordered(c.w) : 0u);
+}
+__device__ __forceinline__ float4 four_sums(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+
+template <bool BF16>
+__global__ void __launch_bounds__(32 * kRouteWarps, 8) moe_route_kernel(const RouteArgs p) {
   __shared__ alignas(16) unsigned long long s_key[kRouteWarps][kCand + 4];
   __shared__ uint16_t s_at[kRouteWarps][kCand];
   __shared__ unsigned long long s_top[kRouteWarps][34];   // the best in order, one more than can be asked for
   __shared__ alignas(16) uint32_t s_lane[kRouteWarps][32];
-  extern __shared__ float s_val[];                          // with groups: [kRouteWarps][E + groups * 32]
+  extern __shared__ uint4 s_row[];                          // [kRouteWarps][row_quads]: the row's keys (or logits)
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x * kRouteWarps + warp, E = p.E, topk = p.topk;
   if (t >= p.T) return;
   const int count = p.count != nullptr ? *p.count : p.T;    // (looked at when the logits are on their way)
+  const long long row = t * p.stride;
+  uint4* quad = s_row + warp * p.row_quads;             // quad q: experts 4 q .. + 3, of lane q % 32
+  const uint32_t* keys = reinterpret_cast<const uint32_t*>(quad);
 
-  float x[NV];
-#pragma unroll
-  for (int i = 0; i < NV; i += 4) {
-    const int e = 4 * (i / 4 * 32 + lane);
-    const long long at = t * p.stride + e;
-    x[i] = x[i + 1] = x[i + 2] = x[i + 3] = -INFINITY;
-    if (p.vectors) {                                  // E and the rows' starts are multiples of four values
-      if (e < E) {
-        if (BF16) {
-          const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.logits) + at);
-          x[i] = __uint_as_float(w.x << 16); x[i + 1] = __uint_as_float(w.x & 0xFFFF0000u);
-          x[i + 2] = __uint_as_float(w.y << 16); x[i + 3] = __uint_as_float(w.y & 0xFFFF0000u);
-        } else {
-          const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(p.logits) + at);
-          x[i] = w.x; x[i + 1] = w.y; x[i + 2] = w.z; x[i + 3] = w.w;
-        }
-      }
+  // scores where they are compared: with a bias, or as sums of two
+  const bool by_score = p.bias != nullptr, by_sum = p.groups > 1 && (by_score || p.group_top == 2);
+  const bool summed = p.softmax && (by_score || by_sum || !p.renorm);      // the row's sum is needed
+  float top = -INFINITY;
+  uint32_t most = 0u;                                   // the lane's largest key
+#pragma unroll 2
+  for (int q = lane; 4 * q < E; q += 32) {
+    const float4 x = four_logits<BF16>(p, row, 4 * q);
+    top = fmaxf(fmaxf(top, fmaxf(x.x, x.y)), fmaxf(x.z, x.w));
+    if (summed) {
+      reinterpret_cast<float4*>(quad)[q] = x;
     } else {
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (e + u < E)
-          x[i + u] = BF16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p.logits)[at + u]) << 16)
-                          : static_cast<const float*>(p.logits)[at + u];
+      const float4 c = by_score ? four_sums(make_float4(sigmoid_near(x.x), sigmoid_near(x.y), sigmoid_near(x.z), sigmoid_near(x.w)),
+                                            four_biases(p, 4 * q))
+                                : x;
+      const uint4 k = four_keys(c, 4 * q, E);
+      quad[q] = k;
+      most = max(max(most, max(k.x, k.y)), max(k.z, k.w));
     }
   }
   int32_t* ids = p.ids + static_cast<long long>(t) * topk;
@@ -247,79 +355,54 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NV <= 32 ? 7 : 3) moe_route_
     }
     return;
   }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) x[i] = clean_logit(x[i]);
 
-  // scores where they are compared; `margin` bounds how far apart two of them may be and still change places
-  const bool by_score = p.bias != nullptr, by_sum = p.groups > 1 && (by_score || p.group_top == 2);
-  float top = -INFINITY, inv = 0.f, margin = 0.f;
-  if (by_score || by_sum || (p.softmax && !p.renorm)) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) top = fmaxf(top, x[i]);
-    top = warp_max(top);
-    if (p.softmax) {
-      if (top == -INFINITY) top = 0.f;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < NV; ++i) sum[i & 3] += expf(x[i] - top);
-      const float z = warp_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
-      inv = z > 0.f ? 1.f / z : 0.f;
-      margin = inv * 0x1p-18f;      // the sum's 23 roundings, and the exponentials'
-    } else {
-      margin = sigmoid(top) * (0x1p-19f + fmaxf(-top, 0.f) * 0x1p-21f);
-      if (top >= 0.f) margin *= 0.5f;
-      if (top == -INFINITY) margin = 0.f;
+  // `margin` bounds how far apart two scores may be and still change places
+  float inv = 0.f, margin = 0.f;
+  if (summed || by_score || by_sum) top = warp_max(top);
+  if (summed) {
+    if (top == -INFINITY) top = 0.f;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int q = lane; 4 * q < E; q += 32) {
+      const float4 x = reinterpret_cast<const float4*>(quad)[q];
+      sum = four_sums(sum, make_float4(expf(x.x - top), expf(x.y - top), expf(x.z - top), expf(x.w - top)));
     }
-    margin += 0x1p-120f;            // scores so small that they have lost bits
+    const float z = warp_sum((sum.x + sum.y) + (sum.z + sum.w));
+    inv = z > 0.f ? 1.f / z : 0.f;
+    margin = inv * 0x1p-18f;        // the sum's 23 roundings, and the exponentials'
+    for (int q = lane; 4 * q < E; q += 32) {
+      const float4 x = reinterpret_cast<const float4*>(quad)[q];
+      const float4 c = by_score ? four_sums(make_float4(expf(x.x - top) * inv, expf(x.y - top) * inv, expf(x.z - top) * inv,
+                                                        expf(x.w - top) * inv),
+                                            four_biases(p, 4 * q))
+                                : x;
+      const uint4 k = four_keys(c, 4 * q, E);
+      quad[q] = k;
+      most = max(max(most, max(k.x, k.y)), max(k.z, k.w));
+    }
+  } else if (by_score || by_sum) {
+    margin = sigmoid(top) * (0x1p-19f + fmaxf(-top, 0.f) * 0x1p-21f);
+    if (top >= 0.f) margin *= 0.5f;
+    if (top == -INFINITY) margin = 0.f;
   }
-  uint32_t key[NV];
-  if (by_score || by_sum) {
-    float* val = s_val + warp * p.val_stride;
-#pragma unroll
-    for (int i = 0; i < NV; i += 4) {
-      const int e = 4 * (i / 4 * 32 + lane);
-      float b[4] = {0.f, 0.f, 0.f, 0.f};
-      if (by_score) {
-        if (p.bias_vectors) {
-          if (e < E) {
-            const float4 w = *reinterpret_cast<const float4*>(p.bias + e);
-            b[0] = clean_bias(w.x); b[1] = clean_bias(w.y); b[2] = clean_bias(w.z); b[3] = clean_bias(w.w);
-          }
-        } else {
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (e + u < E) b[u] = bias_of(p, e + u);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float c = (p.softmax ? expf(x[i + u] - top) * inv : sigmoid_near(x[i + u])) + b[u];
-        key[i + u] = e + u < E ? ordered(by_score ? c : x[i + u]) : 0u;
-        if (by_sum && e + u < E) val[e + u + __umulhi(static_cast<unsigned>(e + u), p.per_recip) * p.skew] = c;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = 4 * (i / 4 * 32 + lane) + (i & 3);
-      key[i] = e < E ? ordered(x[i]) : 0u;
-      if (p.groups > 1 && e < E)
-        s_val[warp * p.val_stride + e + __umulhi(static_cast<unsigned>(e), p.per_recip) * p.skew] = x[i];
-    }
-  }
+  margin += 0x1p-120f;              // scores so small that they have lost bits
 
   bool in_64 = false;
   if (p.groups > 1) {
-    // `skew` lanes take a group; groups start that many banks apart
     __syncwarp();
-    const int L = p.skew, g = lane / L, per = E / p.groups;
+    // L lanes take a group; groups begin with different places of theirs, which lie on different banks
+    const int L = p.group_lanes, g = lane / L, per = E / p.groups, n = (per + L - 1) / L;
     float a = -INFINITY, b = -INFINITY;              // the two largest
     if (g < p.groups) {
-      const float* val = s_val + warp * p.val_stride + g * (per + L);
-      for (int j = lane & (L - 1); j < per; j += L) {
-        const float c = val[j];
-        b = fmaxf(b, fminf(a, c));
-        a = fmaxf(a, c);
+      int j = g % n;
+      for (int i = 0; i < n; ++i) {
+        const int at = j * L + (lane & (L - 1));
+        if (at < per) {
+          float c = from_ordered(keys[g * per + at]);
+          if (by_sum && !by_score) c = p.softmax ? expf(c - top) * inv : sigmoid_near(c);
+          b = fmaxf(b, fminf(a, c));
+          a = fmaxf(a, c);
+        }
+        if (++j == n) j = 0;
       }
     }
     for (int o = L >> 1; o > 0; o >>= 1) {
@@ -329,31 +412,32 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NV <= 32 ? 7 : 3) moe_route_
     }
     const float strength = __shfl_sync(kAll, strength_of(p, a, b), lane * L & 31);
     // logits are compared as they are; of a sum of two the error is twice a score's and the roundings of c and of the sum
-    float most = fmaxf(fabsf(a), p.group_top == 2 ? fabsf(b) : 0.f);
-    most = warp_max(most < INFINITY ? most : 0.f);
-    const uint32_t kept = best_groups<float>(p, strength, lane, 2.f * margin + most * 0x1p-21f, by_sum ? &in_64 : nullptr);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = 4 * (i / 4 * 32 + lane) + (i & 3);
-      const int ge = __umulhi(static_cast<unsigned>(e), p.per_recip);
-      if (e < E && (kept >> (ge & 31) & 1u) == 0u) key[i] = 0u;
+    float largest = fmaxf(fabsf(a), p.group_top == 2 ? fabsf(b) : 0.f);
+    largest = warp_max(largest < INFINITY ? largest : 0.f);
+    const uint32_t kept = best_groups<float>(p, strength, lane, 2.f * margin + largest * 0x1p-21f, by_sum ? &in_64 : nullptr);
+    most = 0u;
+    for (int q = lane; 4 * q < E; q += 32) {
+      uint4 k = quad[q];
+      const auto drop = [&](uint32_t v, int e) { return kept >> (__umulhi(static_cast<unsigned>(e), p.per_recip) & 31u) & 1u ? v : 0u; };
+      k = make_uint4(drop(k.x, 4 * q), drop(k.y, 4 * q + 1), drop(k.z, 4 * q + 2), drop(k.w, 4 * q + 3));
+      quad[q] = k;
+      most = max(max(most, max(k.x, k.y)), max(k.z, k.w));
     }
   }
 
   int id = 0;
   float xi = -INFINITY;                               // lane r < topk: the r-th expert and its logit
   if (!in_64) {
-    uint32_t most = 0u;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) most = max(most, key[i]);
     uint32_t floor_key = max(warp_kth(most, topk, s_lane[warp], lane), 1u);
     const float f = from_ordered(floor_key);
     if (by_score && fabsf(f) < INFINITY)             // (no such key: NaN)
       floor_key = max(ordered(f - (margin + fabsf(f) * 0x1p-22f)), 1u);
-    int mine = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) mine += key[i] >= floor_key;
-    int before = mine;
+    int before = 0;
+    for (int q = lane; 4 * q < E; q += 32) {
+      const uint4 k = quad[q];
+      before += (k.x >= floor_key) + (k.y >= floor_key) + (k.z >= floor_key) + (k.w >= floor_key);
+    }
+    const int mine = before;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(kAll, before, o);
@@ -365,11 +449,14 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NV <= 32 ? 7 : 3) moe_route_
     if (!in_64) {
       unsigned long long* cand = s_key[warp];
       unsigned long long* best = s_top[warp];
+      if (mine > 0) {
+        for (int q = lane; 4 * q < E; q += 32) {
+          const uint4 k = quad[q];
+          const uint32_t v[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if (key[i] >= floor_key) {
-          const unsigned e = 4 * (i / 4 * 32 + lane) + (i & 3);
-          cand[before++] = static_cast<unsigned long long>(key[i]) << 32 | (kAll - e);   // of equals the lower comes first
+          for (int u = 0; u < 4; ++u)
+            if (v[u] >= floor_key)
+              cand[before++] = static_cast<unsigned long long>(v[u]) << 32 | (kAll - (4 * q + u));   // of equals the lower first
         }
       }
       if (lane < 4) cand[n + lane] = 0ull;            // below every key: the ranks are counted four at a time
@@ -399,28 +486,46 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NV <= 32 ? 7 : 3) moe_route_
         }
       }
       if (__any_sync(kAll, near)) {
+        Pair share = {1.f, 0.f};                      // a softmax's 1 / sum
         if (p.softmax) {
-          in_64 = true;                               // the row's sum has to be known better too
-        } else {
-          for (int i = lane; i < n; i += 32) {
-            const int e = static_cast<int>(kAll - static_cast<uint32_t>(cand[i]));
-            const double v = sigmoid_64(logit<BF16>(p, t, e)) + static_cast<double>(bias_of(p, e)) + 0.0;
-            const long long b = __double_as_longlong(v);
-            s_at[warp][i] = static_cast<uint16_t>(e);
-            cand[i] = static_cast<unsigned long long>(b ^ (b >> 63 | static_cast<long long>(1ull << 63)));
+          Pair sum = {0.f, 0.f};
+          for (int q = lane; 4 * q < E; q += 32) {
+            const float4 x = four_logits<BF16>(p, row, 4 * q);
+            sum = add(sum, add(add(exp_pair(two_sum(x.x, -top)), exp_pair(two_sum(x.y, -top))),
+                               add(exp_pair(two_sum(x.z, -top)), exp_pair(two_sum(x.w, -top)))));
           }
-          __syncwarp();
-          for (int i = lane; i < n; i += 32) {
-            const unsigned long long v = cand[i];
-            const int e = s_at[warp][i];
-            int rank = 0;
-            for (int j = 0; j < n; ++j) rank += cand[j] > v || (cand[j] == v && s_at[warp][j] < e);
-            if (rank < topk) best[rank] = static_cast<unsigned>(e);
-          }
-          __syncwarp();
-          id = static_cast<int>(best[lane < topk ? lane : 0]);
-          xi = logit<BF16>(p, t, id);
+          share = reciprocal(warp_sum(sum));
         }
+        for (int i = lane; i < n; i += 32) {
+          const int e = static_cast<int>(kAll - static_cast<uint32_t>(cand[i]));
+          const float x = logit<BF16>(p, t, e);
+          const Pair score = p.softmax ? mul(exp_pair(two_sum(x, -top)), share) : sigmoid_pair(x);
+          s_at[warp][i] = static_cast<uint16_t>(e);
+          cand[i] = ordered(add(score, {bias_of(p, e), 0.f}));
+        }
+        __syncwarp();
+        for (int i = lane; i < n; i += 32) {
+          const unsigned long long v = cand[i];
+          const int e = s_at[warp][i];
+          int rank = 0;
+          for (int j = 0; j < n; ++j) rank += cand[j] > v || (cand[j] == v && s_at[warp][j] < e);
+          if (rank <= topk) best[rank] = static_cast<unsigned>(i);
+        }
+        __syncwarp();
+        const int i = static_cast<int>(best[lane < topk ? lane : 0]);
+        id = s_at[warp][i];
+        xi = logit<BF16>(p, t, id);
+        near = false;
+        if (lane < topk && lane + 1 < n) {
+          const int j = static_cast<int>(best[lane + 1]), other = s_at[warp][j];
+          const unsigned long long v = cand[i], w = cand[j];
+          const float vh = from_ordered(static_cast<uint32_t>(v >> 32)), wh = from_ordered(static_cast<uint32_t>(w >> 32));
+          const float gap = (vh - wh) + (from_ordered(static_cast<uint32_t>(v)) - from_ordered(static_cast<uint32_t>(w)));
+          const float open = (margin + fmaxf(fabsf(vh), fabsf(wh)) * 0x1p-22f) * 0x1p-20f;
+          near = !(gap > open) && (vh != wh || fabsf(vh) < INFINITY) &&
+                 (xi != logit<BF16>(p, t, other) || bias_of(p, id) != bias_of(p, other));
+        }
+        in_64 = __any_sync(kAll, near);
       }
     }
   }
@@ -456,18 +561,6 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NV <= 32 ? 7 : 3) moe_route_
   }
 }
 
-template <bool BF16>
-int launch_route_type(const RouteArgs& p, cudaStream_t st) {
-  const int grid = (p.T + kRouteWarps - 1) / kRouteWarps;
-  const size_t smem = p.groups > 1 ? sizeof(float) * kRouteWarps * p.val_stride : 0;
-  auto kern = p.E <= 128   ? moe_route_kernel<4, BF16>
-              : p.E <= 256 ? moe_route_kernel<8, BF16>
-              : p.E <= 512 ? moe_route_kernel<16, BF16>
-              : p.E <= 1024 ? moe_route_kernel<32, BF16>
-                            : moe_route_kernel<64, BF16>;
-  return launch_pdl_smem(kern, grid, 32 * kRouteWarps, smem, st, p);
-}
-
 }  // namespace
 
 int launch_moe_route(RouteArgs p, int bf16, cudaStream_t st) {
@@ -476,10 +569,11 @@ int launch_moe_route(RouteArgs p, int bf16, cudaStream_t st) {
   p.vectors = p.E % 4 == 0 && p.stride % 4 == 0 && reinterpret_cast<uintptr_t>(p.logits) % (bf16 ? 8 : 16) == 0;
   p.bias_vectors = p.E % 4 == 0 && reinterpret_cast<uintptr_t>(p.bias) % 16 == 0;
   p.per_recip = p.groups > 1 ? static_cast<unsigned>((0x100000000ull + per - 1) / per) : 0u;   // per >= 2
-  p.skew = 1;
-  while (2 * p.skew * p.groups <= 32) p.skew *= 2;
-  p.val_stride = p.E + p.groups * p.skew;
-  return bf16 ? launch_route_type<true>(p, st) : launch_route_type<false>(p, st);
+  p.group_lanes = 1;
+  while (2 * p.group_lanes * p.groups <= 32) p.group_lanes *= 2;
+  p.row_quads = (p.E + 3) / 4;
+  return launch_pdl_smem(bf16 ? moe_route_kernel<true> : moe_route_kernel<false>, (p.T + kRouteWarps - 1) / kRouteWarps,
+                         32 * kRouteWarps, sizeof(uint4) * kRouteWarps * p.row_quads, st, p);
 }
 
 }  // namespace a4w4
