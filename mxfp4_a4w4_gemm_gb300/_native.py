@@ -9,6 +9,7 @@ call raises.
 
 import ctypes
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "_lib", "liba4w4.so")
@@ -83,6 +84,13 @@ DEBUG_SIGNATURES = {
                                              _c_int, _vp, _vp, _vp, _c_size, _vp, _c_size, _vp]),
 }
 
+# calls with packed arguments (include/a4w4_binding.h): name -> the format of its words
+PACKED = {
+    "a4w4_packed_moe_route": struct.Struct("=13qd3q"),
+    "a4w4_packed_qk_norm_rope": struct.Struct("=11qd8q"),
+    "a4w4_packed_kv_append_rope": struct.Struct("=14qd9q"),
+}
+
 A4W4_GEMM_WEIGHT_PREFETCH = 1
 A4W4_F32, A4W4_BF16 = 0, 1
 A4W4_MOE_SCORE_SOFTMAX, A4W4_MOE_SCORE_SIGMOID = 0, 1
@@ -110,6 +118,10 @@ def lib():
             f = getattr(L, name)
             f.restype = res
             f.argtypes = args
+        for name in PACKED:
+            f = getattr(L, name)
+            f.restype = _c_int
+            f.argtypes = [ctypes.c_char_p]
         _lib = L
     return _lib
 
@@ -277,18 +289,38 @@ def _logits_ptr(x, stride):
     """Rows of router logits, `stride` elements apart: only the rows themselves must be contiguous."""
     if x is None or isinstance(x, int):
         return x
+    if x.stride() == (stride, 1):
+        return x.data_ptr()
     if x.dim() != 2 or (x.size(1) > 1 and x.stride(1) != 1) or (x.size(0) > 1 and x.stride(0) != stride):
         raise ValueError("logits must be a [T, E] tensor with contiguous rows and the given row stride")
     return x.data_ptr()
 
 
+def _heads_ptr(x, stride, D):
+    """_rows_ptr with a shorter way for the usual view: heads of D, rows `stride` apart."""
+    if x is None or type(x) is int:
+        return x or 0
+    try:
+        if x.stride() == (stride, D, 1):
+            return x.data_ptr()
+    except AttributeError:
+        pass
+    return _rows_ptr(x, stride) or 0
+
+
+_PACK_ROUTE = PACKED["a4w4_packed_moe_route"].pack
+_PACK_ROPE = PACKED["a4w4_packed_qk_norm_rope"].pack
+_PACK_APPEND = PACKED["a4w4_packed_kv_append_rope"].pack
+
+
 def a4w4_moe_route(logits, logits_type, stride, num_tokens, T, E, score, bias, groups, group_top, top_groups, topk,
                    renormalise, scale, topk_ids, topk_weights, stream=None):
     """logits: a [T, E] view with a row stride (in elements), float32 (A4W4_F32) or bfloat16 (A4W4_BF16)."""
-    _check("a4w4_moe_route",
-           lib().a4w4_moe_route(_logits_ptr(logits, stride), logits_type, stride, _ptr(num_tokens), T, E, score,
-                                _ptr(bias), groups, group_top, top_groups, topk, renormalise, scale, _ptr(topk_ids),
-                                _ptr(topk_weights), _stream(stream)))
+    rc = (_lib or lib()).a4w4_packed_moe_route(_PACK_ROUTE(
+        _logits_ptr(logits, stride) or 0, logits_type, stride, _ptr(num_tokens) or 0, T, E, score, _ptr(bias) or 0, groups,
+        group_top, top_groups, topk, renormalise, scale, _ptr(topk_ids) or 0, _ptr(topk_weights) or 0, _stream(stream) or 0))
+    if rc != 0:
+        raise A4W4Error("a4w4_moe_route", rc)
 
 
 def a4w4_moe_sort_aux_workspace_bytes(T, topk, E):
@@ -374,23 +406,25 @@ def a4w4_kv_append(k, k_stride, v, v_stride, slot_map, T, Hkv, D, cache, num_pag
 def a4w4_qk_norm_rope(q, q_stride, k, k_stride, positions, T, Hq, Hkv, D, q_weight, k_weight, eps, inv_freq, rot_dim,
                       interleaved, q_out, q_out_stride, k_out, k_out_stride, stream=None):
     """q, k and the results may be slices of one fused projection: [T, heads, D] views with a row stride (in elements)."""
-    _check("a4w4_qk_norm_rope",
-           lib().a4w4_qk_norm_rope(_rows_ptr(q, q_stride), q_stride, _rows_ptr(k, k_stride), k_stride, _ptr(positions),
-                                   T, Hq, Hkv, D, _ptr(q_weight), _ptr(k_weight), eps, _ptr(inv_freq), rot_dim,
-                                   interleaved, _rows_ptr(q_out, q_out_stride), q_out_stride,
-                                   _rows_ptr(k_out, k_out_stride), k_out_stride, _stream(stream)))
+    rc = (_lib or lib()).a4w4_packed_qk_norm_rope(_PACK_ROPE(
+        _heads_ptr(q, q_stride, D), q_stride, _heads_ptr(k, k_stride, D), k_stride, _ptr(positions) or 0, T, Hq, Hkv, D,
+        _ptr(q_weight) or 0, _ptr(k_weight) or 0, eps, _ptr(inv_freq) or 0, rot_dim, interleaved,
+        _heads_ptr(q_out, q_out_stride, D), q_out_stride, _heads_ptr(k_out, k_out_stride, D), k_out_stride, _stream(stream) or 0))
+    if rc != 0:
+        raise A4W4Error("a4w4_qk_norm_rope", rc)
 
 
 def a4w4_kv_append_rope(q, q_stride, k, k_stride, v, v_stride, positions, slot_map, T, Hq, Hkv, D, q_weight, k_weight,
                         eps, inv_freq, rot_dim, interleaved, q_out, q_out_stride, cache, num_pages, page_size,
                         stream=None):
     """q, k, v and q_out may be slices of one fused projection: [T, heads, D] views with a row stride (in elements)."""
-    _check("a4w4_kv_append_rope",
-           lib().a4w4_kv_append_rope(_rows_ptr(q, q_stride), q_stride, _rows_ptr(k, k_stride), k_stride,
-                                     _rows_ptr(v, v_stride), v_stride, _ptr(positions), _ptr(slot_map), T, Hq, Hkv, D,
-                                     _ptr(q_weight), _ptr(k_weight), eps, _ptr(inv_freq), rot_dim, interleaved,
-                                     _rows_ptr(q_out, q_out_stride), q_out_stride, _ptr(cache), num_pages, page_size,
-                                     _stream(stream)))
+    rc = (_lib or lib()).a4w4_packed_kv_append_rope(_PACK_APPEND(
+        _heads_ptr(q, q_stride, D), q_stride, _heads_ptr(k, k_stride, D), k_stride, _heads_ptr(v, v_stride, D), v_stride,
+        _ptr(positions) or 0, _ptr(slot_map) or 0, T, Hq, Hkv, D, _ptr(q_weight) or 0, _ptr(k_weight) or 0, eps,
+        _ptr(inv_freq) or 0, rot_dim, interleaved, _heads_ptr(q_out, q_out_stride, D), q_out_stride, _ptr(cache) or 0, num_pages,
+        page_size, _stream(stream) or 0))
+    if rc != 0:
+        raise A4W4Error("a4w4_kv_append_rope", rc)
 
 
 def a4w4_kv_read(cache, num_pages, page_size, slot_map, T, Hkv, D, k_out, v_out, stream=None):

@@ -267,9 +267,9 @@ __device__ __noinline__ int route_in_64(const RouteArgs& p, int t, int lane) {
   return id;
 }
 
-// Four logits of a row from expert e on, as they count; -infinity behind the last.
+// Four logits of a row from expert e on; -infinity behind the last.
 template <bool BF16>
-__device__ __forceinline__ float4 four_logits(const RouteArgs& p, long long row, int e) {
+__device__ __forceinline__ float4 raw_logits(const RouteArgs& p, long long row, int e) {
   float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
   const long long at = row + e;
   if (p.vectors) {                                    // E and the rows' starts are multiples of four values
@@ -290,7 +290,14 @@ __device__ __forceinline__ float4 four_logits(const RouteArgs& p, long long row,
         x[u] = BF16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p.logits)[at + u]) << 16)
                     : static_cast<const float*>(p.logits)[at + u];
   }
-  return make_float4(clean_logit(x[0]), clean_logit(x[1]), clean_logit(x[2]), clean_logit(x[3]));
+  return make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ float4 clean(float4 x) {
+  return make_float4(clean_logit(x.x), clean_logit(x.y), clean_logit(x.z), clean_logit(x.w));
+}
+template <bool BF16>
+__device__ __forceinline__ float4 four_logits(const RouteArgs& p, long long row, int e) {
+  return clean(raw_logits<BF16>(p, row, e));
 }
 __device__ __forceinline__ float4 four_biases(const RouteArgs& p, int e) {
   if (p.bias_vectors) {
@@ -331,19 +338,27 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8) moe_route_kernel(const Ro
   const bool summed = p.softmax && (by_score || by_sum || !p.renorm);      // the row's sum is needed
   float top = -INFINITY;
   uint32_t most = 0u;                                   // the lane's largest key
-#pragma unroll 2
-  for (int q = lane; 4 * q < E; q += 32) {
-    const float4 x = four_logits<BF16>(p, row, 4 * q);
-    top = fmaxf(fmaxf(top, fmaxf(x.x, x.y)), fmaxf(x.z, x.w));
-    if (summed) {
-      reinterpret_cast<float4*>(quad)[q] = x;
-    } else {
-      const float4 c = by_score ? four_sums(make_float4(sigmoid_near(x.x), sigmoid_near(x.y), sigmoid_near(x.z), sigmoid_near(x.w)),
-                                            four_biases(p, 4 * q))
-                                : x;
-      const uint4 k = four_keys(c, 4 * q, E);
-      quad[q] = k;
-      most = max(max(most, max(k.x, k.y)), max(k.z, k.w));
+  constexpr int kAhead = 4;                             // quads of a lane on their way
+  for (int q0 = lane; 4 * q0 < E; q0 += 32 * kAhead) {
+    float4 raw[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) raw[i] = raw_logits<BF16>(p, row, 4 * (q0 + 32 * i));
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int q = q0 + 32 * i;
+      if (4 * q >= E) break;
+      const float4 x = clean(raw[i]);
+      top = fmaxf(fmaxf(top, fmaxf(x.x, x.y)), fmaxf(x.z, x.w));
+      if (summed) {
+        reinterpret_cast<float4*>(quad)[q] = x;
+      } else {
+        const float4 c = by_score ? four_sums(make_float4(sigmoid_near(x.x), sigmoid_near(x.y), sigmoid_near(x.z), sigmoid_near(x.w)),
+                                              four_biases(p, 4 * q))
+                                  : x;
+        const uint4 k = four_keys(c, 4 * q, E);
+        quad[q] = k;
+        most = max(max(most, max(k.x, k.y)), max(k.z, k.w));
+      }
     }
   }
   int32_t* ids = p.ids + static_cast<long long>(t) * topk;
