@@ -502,16 +502,16 @@ struct W8S {
   static constexpr int X_STAGE = NX * 128;
   static constexpr int OFF_X = RING * kTile;
   static constexpr int OFF_SCALE = OFF_X + RING * X_STAGE;
-  static constexpr int OFF_BAR = OFF_SCALE + RING * NX * 4;
+  // up to 16 senders' shares of this block's slice of the sums ((G + S) groups of 16 bytes, G = 32 NX);
+  // this block's own sums are staged over the drained weight ring
+  static constexpr int OFF_PUSH = OFF_SCALE + RING * NX * 4;
+  static constexpr int OFF_BAR = OFF_PUSH + NX * 512 + 256;
   static constexpr int NBAR = 2 * RING + 8;            // full_w, empty_w; full_x, empty_x; acc full x 2, empty x 2; red; drain
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;
   static constexpr int ACC_COLS = NX;
   static constexpr int TMEM_COLS = 2 * NX;
-  // After the last block the rings' bytes serve the reduction: this block's partial sums,
-  // then up to 16 senders' shares of this block's slice ((G + S) groups of 16 bytes, G = 32 NX)
-  static constexpr int OFF_PUSH = NX * 512;
-  static_assert(OFF_PUSH + NX * 512 + 256 <= OFF_SCALE, "the reduction fits the rings");
+  static_assert(NX * 512 <= RING * kTile, "the sums fit the weight ring");
   static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "two thread blocks on an SM");
 };
 
@@ -519,8 +519,8 @@ struct W8S {
 //   warp 1      TMEM owner and MMA issuer (two accumulators of NX columns in turn);
 //   warps 2-5   activations: rounds of up to RING blocks of K, eight lanes per row and block;
 //   warps 6-9   a thread per weight row: scale and add each block's NX sums.
-// Then all of warps 2-9 reduce over the cluster: slice r of the 128 x NX sums belongs to
-// rank r, everyone sends its share there, the owner adds in rank order.
+// Then warps 2-9 reduce over the cluster: slice r of the 128 x NX sums belongs to rank r, everyone
+// sends its share there as soon as it has it, the owner adds in rank order.
 template <int NX>
 __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(const W8SmallArgs p) {
   using Cf = W8S<NX>;
@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
     }
   }
   // rows of tokens that do not exist: codes and scales zero, never written again
-  for (int i = threadIdx.x; i < (Cf::OFF_BAR - Cf::OFF_X) / 16; i += Cf::THREADS)
+  for (int i = threadIdx.x; i < (Cf::OFF_PUSH - Cf::OFF_X) / 16; i += Cf::THREADS)
     reinterpret_cast<uint4*>(smem + Cf::OFF_X)[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   if (warp == 1) {
@@ -576,6 +576,7 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
     tc_fence_before();
   }
   __syncthreads();
+  if (p.splits > 1) cluster_arrive_relaxed();          // this block's barriers exist; waited for before the first share is sent
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -612,9 +613,9 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
         const uint64_t ad = adesc0 + ((s * kTile) >> 4), bd = bdesc0 + ((s * Cf::X_STAGE) >> 4);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) mma_e4m3(tmem + b * Cf::ACC_COLS, ad + 2 * ks, bd + 2 * ks, idesc, ks > 0 ? 1u : 0u);
+        mma_commit(acc_full + 8u * b);
         mma_commit(empty_w + 8u * s);
         if (s == Cf::RING - 1) mma_commit(empty_x);
-        mma_commit(acc_full + 8u * b);
       }
       mma_commit(drain);
       mbar_wait(drain, 0, never, drain_ns, p.status);
@@ -732,15 +733,14 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
   }
 
   if (p.splits > 1) {
-    // every block of the cluster is through with its rings (which the shares now land in)
-    __syncthreads();
-    cluster_sync_all();
     if (warp >= 2) {
       constexpr int P = 256;
       const int et = threadIdx.x - 64;
       const int S = p.splits, G = mvalid * 32, slot = (G + S - 1) / S;
       const uint32_t rank = cluster_ctarank();
       const float4* red4 = reinterpret_cast<const float4*>(smem);
+      named_bar_sync(3, P);                            // the sums are staged
+      cluster_wait();
       // group g (four weight rows of a token) belongs to o = max{o : floor(o G / S) <= g}; sent
       // whatever happened before, so that every owner's byte count completes
       for (int g = et; g < G; g += P) {
@@ -772,6 +772,8 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
           *reinterpret_cast<uint2*>(p.C + static_cast<long long>(m0 + (g >> 5)) * p.N + w_tile * 128 + (g & 31) * 4) = o;
         }
       }
+    } else {
+      cluster_wait();
     }
   }
 
