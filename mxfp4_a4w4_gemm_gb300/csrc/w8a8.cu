@@ -504,9 +504,9 @@ struct W8S {
   static constexpr int OFF_SCALE = OFF_X + RING * X_STAGE;
   // up to 16 senders' shares of this block's slice of the sums ((G + S) groups of 16 bytes, G = 32 NX);
   // this block's own sums are staged over the drained weight ring
-  static constexpr int OFF_PUSH = OFF_SCALE + RING * NX * 4;
+  static constexpr int OFF_PUSH = OFF_SCALE + 2 * RING * NX * 4;
   static constexpr int OFF_BAR = OFF_PUSH + NX * 512 + 256;
-  static constexpr int NBAR = 2 * RING + 8;            // full_w, empty_w; full_x, empty_x; acc full x 2, empty x 2; red; drain
+  static constexpr int NBAR = 5 * RING + 6;            // full_w, empty, full_x, scales x 2; accumulators' full and empty; red; drain
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;
   static constexpr int ACC_COLS = NX;
@@ -517,7 +517,9 @@ struct W8S {
 
 //   warp 0      weight producer;
 //   warp 1      TMEM owner and MMA issuer (two accumulators of NX columns in turn);
-//   warps 2-5   activations: rounds of up to RING blocks of K, eight lanes per row and block;
+//   warps 2-5   activations: every fourth block of K each, eight lanes a row, into the ring's place
+//               for it; scales have places for two turns of the ring, since they are read after
+//               the MMAs that free the codes';
 //   warps 6-9   a thread per weight row: scale and add each block's NX sums.
 // Then warps 2-9 reduce over the cluster: slice r of the 128 x NX sums belongs to rank r, everyone
 // sends its share there as soon as it has it, the owner adds in rank order.
@@ -537,9 +539,9 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
   const int mvalid = min(NX, p.M - m0);
   const unsigned long long drain_ns = p.wait_ns > 100000000ull ? p.wait_ns : 100000000ull;
 
-  const uint32_t full_w = base + Cf::OFF_BAR, empty_w = full_w + 8u * Cf::RING;
-  const uint32_t full_x = empty_w + 8u * Cf::RING, empty_x = full_x + 8u;
-  const uint32_t acc_full = empty_x + 8u, acc_empty = acc_full + 16u;
+  const uint32_t full_w = base + Cf::OFF_BAR, empty = full_w + 8u * Cf::RING;
+  const uint32_t full_x = empty + 8u * Cf::RING, scales = full_x + 8u * Cf::RING;
+  const uint32_t acc_full = scales + 16u * Cf::RING, acc_empty = acc_full + 16u;
   const uint32_t red_bar = acc_empty + 16u, drain = red_bar + 8u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cf::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cf::OFF_MISC + 8);
@@ -547,9 +549,8 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
   volatile int* owner_ready = reinterpret_cast<volatile int*>(smem + Cf::OFF_MISC + 24);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2 * Cf::RING; ++s) mbar_init(full_w + 8u * s, 1);
-    mbar_init(full_x, 128);
-    mbar_init(empty_x, 1 + 4);                         // the MMAs' commit, and the promoters, who read the scales
+    for (int s = 0; s < 2 * Cf::RING; ++s) mbar_init(full_w + 8u * s, 1);    // full_w, empty
+    for (int s = 0; s < 3 * Cf::RING; ++s) mbar_init(full_x + 8u * s, 32);   // full_x, scales: a producer warp
     mbar_init(acc_full, 1);
     mbar_init(acc_full + 8u, 1);
     mbar_init(acc_empty, 4);
@@ -589,7 +590,7 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
       int i = 0;
       for (; i < nk; ++i) {
         const int s = i % Cf::RING;
-        if (!mbar_wait(empty_w + 8u * s, ((i / Cf::RING) & 1) ^ 1u, abort_flag, p.wait_ns, p.status)) break;
+        if (!mbar_wait(empty + 8u * s, ((i / Cf::RING) & 1) ^ 1u, abort_flag, p.wait_ns, p.status)) break;
         mbar_arrive_expect_tx(full_w + 8u * s, kTile);
         bulk_g2s(base + s * kTile, w + static_cast<long long>(i) * kTile, kTile, full_w + 8u * s, pol);
       }
@@ -605,7 +606,7 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
       bool ok = true;
       for (int i = 0; i < nk && ok; ++i) {
         const int s = i % Cf::RING, b = i & 1;
-        if (s == 0) ok = mbar_wait(full_x, static_cast<uint32_t>(i / Cf::RING) & 1u, abort_flag, p.wait_ns, p.status);
+        ok = mbar_wait(full_x + 8u * s, static_cast<uint32_t>(i / Cf::RING) & 1u, abort_flag, p.wait_ns, p.status);
         ok = ok && (i < 2 || mbar_wait(acc_empty + 8u * b, static_cast<uint32_t>((i >> 1) - 1) & 1u, abort_flag, p.wait_ns, p.status));
         ok = ok && mbar_wait(full_w + 8u * s, (i / Cf::RING) & 1u, abort_flag, p.wait_ns, p.status);
         if (!ok) break;
@@ -614,8 +615,7 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) mma_e4m3(tmem + b * Cf::ACC_COLS, ad + 2 * ks, bd + 2 * ks, idesc, ks > 0 ? 1u : 0u);
         mma_commit(acc_full + 8u * b);
-        mma_commit(empty_w + 8u * s);
-        if (s == Cf::RING - 1) mma_commit(empty_x);
+        mma_commit(empty + 8u * s);
       }
       mma_commit(drain);
       mbar_wait(drain, 0, never, drain_ns, p.status);
@@ -627,47 +627,47 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
     int ready = nk > 0;
     if (warp < 6) {
       // ---------------- activations ----------------
-      const int pt = threadIdx.x - 64, c = pt & 7;
-      constexpr int CH = 4;                            // blocks of 128 in flight per eight lanes
+      constexpr int CH = 4;                            // rows in flight per eight lanes
+      const int c = lane & 7;
       float* s_scale = reinterpret_cast<float*>(smem + Cf::OFF_SCALE);
       bool stop = false;
-      for (int r0 = 0, rnd = 0; r0 < nk && !stop; r0 += Cf::RING, ++rnd) {
-        const int total = min(nk - r0, Cf::RING) * mvalid;
-        bool waited = rnd == 0;
-        for (int t0 = pt >> 3; t0 < total + (pt >> 3) && !stop; t0 += 16 * CH) {   // (warps stay whole)
+      for (int i = warp - 2; i < nk && !stop; i += 4) {
+        const int s = i % Cf::RING, turn = i % (2 * Cf::RING);
+        bool waited = i < Cf::RING;
+        for (int r0 = 0; r0 < mvalid; r0 += 4 * CH) {
           uint4 v[CH][2];
 #pragma unroll
           for (int h = 0; h < CH; ++h) {
-            const int t = t0 + 16 * h, j = t / mvalid, r = t - j * mvalid;
+            const int r = r0 + 4 * h + (lane >> 3);
             v[h][0] = v[h][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (t < total) {
-              const uint16_t* src = p.A + static_cast<long long>(m0 + r) * p.K + (kt0 + r0 + j) * 128 + c * 16;
+            if (r < mvalid) {
+              const uint16_t* src = p.A + static_cast<long long>(m0 + r) * p.K + (kt0 + i) * 128 + c * 16;
               v[h][0] = ld_global_nc_v4(src);
               v[h][1] = ld_global_nc_v4(src + 8);
             }
           }
-          if (!waited) {                               // the round's places are free again
+          if (!waited) {                               // the MMAs of the block that had this place have run
             waited = true;
-            if (!mbar_wait(empty_x, static_cast<uint32_t>(rnd - 1) & 1u, abort_flag, p.wait_ns, p.status)) stop = true;
-          }
-          if (__any_sync(0xFFFFFFFFu, stop)) {
-            stop = true;
-            break;
+            int got = 1;
+            if (lane == 0) got = mbar_wait(empty + 8u * s, static_cast<uint32_t>(i / Cf::RING - 1) & 1u, abort_flag, p.wait_ns, p.status);
+            stop = __shfl_sync(0xFFFFFFFFu, got, 0) == 0;
+            if (stop) break;
           }
 #pragma unroll
           for (int h = 0; h < CH; ++h) {
-            const int t = t0 + 16 * h, j = t / mvalid, r = t - j * mvalid;
+            const int r = r0 + 4 * h + (lane >> 3);
             float scale;
             const uint4 code = quant128(v[h][0], v[h][1], &scale);
-            if (t < total) {
-              *reinterpret_cast<uint4*>(smem + Cf::OFF_X + j * Cf::X_STAGE + tile_piece(r, c)) = code;
-              if (c == 0) s_scale[j * NX + r] = scale;
+            if (r < mvalid) {
+              *reinterpret_cast<uint4*>(smem + Cf::OFF_X + s * Cf::X_STAGE + tile_piece(r, c)) = code;
+              if (c == 0) s_scale[turn * NX + r] = scale;
             }
           }
         }
         if (!stop) {
           fence_proxy_async_smem();
-          mbar_arrive(full_x);
+          mbar_arrive(full_x + 8u * s);
+          mbar_arrive(scales + 8u * turn);
         }
       }
       ready = ready && !stop;
@@ -680,18 +680,17 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
 #pragma unroll
       for (int i = 0; i < NX / 2; ++i) acc[i] = 0ull;
       for (int i = 0; i < nk; ++i) {
-        const int s = i % Cf::RING, b = i & 1;
+        const int turn = i % (2 * Cf::RING), b = i & 1;
         const uint32_t sw = __float_as_uint(block_scale[i]);
         const unsigned long long sw2 = pack2(sw, sw);
-        // the scales' writes are seen through the producers' own barrier
-        if ((s == 0 && !mbar_wait(full_x, static_cast<uint32_t>(i / Cf::RING) & 1u, abort_flag, p.wait_ns, p.status)) ||
+        if (!mbar_wait(scales + 8u * turn, static_cast<uint32_t>(i / (2 * Cf::RING)) & 1u, abort_flag, p.wait_ns, p.status) ||
             !mbar_wait(acc_full + 8u * b, static_cast<uint32_t>(i >> 1) & 1u, abort_flag, p.wait_ns, p.status)) {
           ready = 0;
           break;
         }
         __syncwarp();
         tc_fence_after();
-        const ulonglong2* sa = reinterpret_cast<const ulonglong2*>(smem + Cf::OFF_SCALE + s * NX * 4);
+        const ulonglong2* sa = reinterpret_cast<const ulonglong2*>(smem + Cf::OFF_SCALE + turn * NX * 4);
 #pragma unroll
         for (int c = 0; c < NX; c += 16) {
           float t[16];
@@ -707,10 +706,7 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(acc_empty + 8u * b);
-          if (s == Cf::RING - 1) mbar_arrive(empty_x);
-        }
+        if (lane == 0) mbar_arrive(acc_empty + 8u * b);
       }
       ready = __all_sync(0xFFFFFFFFu, ready);
       // weight row q * 32 + lane of every token: partial [token][weight row] over the drained ring,
