@@ -219,9 +219,9 @@ int a4w4_moe_sort(const int32_t* topk_ids, int T, int topk, int E, int block_m,
  *            weights 0 (rows of padding of a captured step; the sorts leave them out,
  *            and what a4w4_moe_gemm2 writes to those rows of Y is not defined)
  * Ties go to the lower index.  What is chosen, and the order, are those of the exact
- * c (to about 2^-50 of the largest score): fp32 first, 64 bits for the rows whose
- * order it leaves open (near ties of scores with a bias or of group strengths; some
- * 1% of rows, and a few microseconds for them).  A NaN logit counts as -infinity, a
+ * c (to about 2^-50 of the largest score): fp32 first, then sums of two floats for the
+ * candidates of a row whose order that leaves open (near ties of scores with a bias or
+ * of group strengths: some 1% of rows), then 64 bits.  A NaN logit counts as -infinity, a
  * logit of +infinity as the largest float, a NaN bias as -infinity; a row whose logits
  * are all -infinity has scores 0, and weights whose sum is 0 are 0.  The weights are
  * fp32 to about 2^-21.
@@ -436,9 +436,8 @@ int a4w4_kv_append(const void* k_bf16, long long k_stride, const void* v_bf16, l
  *   positions [T] int32; inv_freq [rot_dim / 2] float, finite, below 2^24 in
  *   magnitude.  Angles are reduced exactly (to 2^-33 turns) before they are rounded.
  * D 64 or 128, rot_dim a multiple of 16, 0 (norms only; positions and inv_freq may be
- * NULL) to D; Hq, Hkv >= 0 (0: no such heads, its pointers may be NULL), Hq + 2 Hkv <=
- * 4096; eps finite
- * and > 0 where there is a norm; T >= 0. */
+ * NULL) to D; Hq, Hkv >= 0 (0: no such heads, its pointers may be NULL),
+ * Hq + 2 Hkv <= 4096; eps finite and > 0 where there is a norm; T >= 0. */
 int a4w4_qk_norm_rope(const void* q_bf16, long long q_stride, const void* k_bf16, long long k_stride,
                       const int32_t* positions, int T, int Hq, int Hkv, int D, const float* q_weight,
                       const float* k_weight, float eps, const float* inv_freq, int rot_dim, int interleaved,

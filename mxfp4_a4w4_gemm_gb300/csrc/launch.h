@@ -185,11 +185,10 @@ int launch_kv_rope(RopeArgs p, int D, cudaStream_t st, int sms);
 // 8-bit block-scaled product (w8a8.cu).
 struct W8Plan {
   int large;          // 1: 128 x 256 tiles, activations quantised once; 0: weight rows on the matrix unit's M side
-  int nx;             // tokens per thread block (not large)
-  int x_tiles, w_tiles, splits;
+  int nx;             // not large: tokens that a thread block has room for
+  int x_tiles, w_tiles;   // of 128 tokens (large), of 128 weight rows
   int kt;             // 128-wide blocks of K
   int half_tiles;     // large: tiles of the last partial wave, run as halves
-  int cluster;        // large: thread blocks that share their weight tiles (1 or 2)
   size_t ws_bytes;
 };
 W8Plan plan_w8a8(int M, int N, int K, int sms);

@@ -535,8 +535,7 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
   const int kt0 = static_cast<int>(static_cast<long long>(split) * p.KT / p.splits);
   const int kt1 = static_cast<int>(static_cast<long long>(split + 1) * p.KT / p.splits);
   const int nk = kt1 - kt0;
-  const int m0 = blockIdx.y * NX;
-  const int mvalid = min(NX, p.M - m0);
+  const int mvalid = p.M;                              // tokens, at most NX
   const unsigned long long drain_ns = p.wait_ns > 100000000ull ? p.wait_ns : 100000000ull;
 
   const uint32_t full_w = base + Cf::OFF_BAR, empty = full_w + 8u * Cf::RING;
@@ -641,7 +640,7 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
             const int r = r0 + 4 * h + (lane >> 3);
             v[h][0] = v[h][1] = make_uint4(0u, 0u, 0u, 0u);
             if (r < mvalid) {
-              const uint16_t* src = p.A + static_cast<long long>(m0 + r) * p.K + (kt0 + i) * 128 + c * 16;
+              const uint16_t* src = p.A + static_cast<long long>(r) * p.K + (kt0 + i) * 128 + c * 16;
               v[h][0] = ld_global_nc_v4(src);
               v[h][1] = ld_global_nc_v4(src + 8);
             }
@@ -716,7 +715,7 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
 #pragma unroll
         for (int i = 0; i < NX; ++i)
           if (i < mvalid)
-            p.C[static_cast<long long>(m0 + i) * p.N + w_tile * 128 + lrow] =
+            p.C[static_cast<long long>(i) * p.N + w_tile * 128 + lrow] =
                 __bfloat16_as_ushort(__float2bfloat16_rn(i & 1 ? hi2(acc[i / 2]) : lo2(acc[i / 2])));
       } else if (ready) {
         float* red = reinterpret_cast<float*>(smem);
@@ -765,7 +764,7 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
           uint2 o;
           o.x = *reinterpret_cast<const uint32_t*>(&lo);
           o.y = *reinterpret_cast<const uint32_t*>(&hi);
-          *reinterpret_cast<uint2*>(p.C + static_cast<long long>(m0 + (g >> 5)) * p.N + w_tile * 128 + (g & 31) * 4) = o;
+          *reinterpret_cast<uint2*>(p.C + static_cast<long long>(g >> 5) * p.N + w_tile * 128 + (g & 31) * 4) = o;
         }
       }
     } else {
@@ -782,19 +781,82 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
   }
 }
 
+constexpr int kMaxW8Splits = 16;
+constexpr int kMaxDevices = 64;
+// clusters of a size that the device holds at once, filled on first use (0: not known yet)
+std::atomic<int> g_clusters[kMaxDevices][2][kMaxW8Splits + 1];
+
 template <int NX>
-int launch_small_nx(const W8SmallArgs& a, dim3 grid, cudaStream_t st) {
-  using Cf = W8S<NX>;
+int small_attrs() {
   auto kern = a4w4_w8a8_small_kernel<NX>;
   static std::atomic<unsigned long long> attr_devs{0};   // bit d: attributes set on device d
-  if (ensure_func_attrs(attr_devs, [&] {
-        // clusters of up to 16 thread blocks (more than the portable 8)
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM_BYTES) == cudaSuccess &&
-               cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
-      }) != 0)
-    return -4;
+  return ensure_func_attrs(attr_devs, [&] {
+    // clusters of up to 16 thread blocks (more than the portable 8)
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, W8S<NX>::SMEM_BYTES) == cudaSuccess &&
+           cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+  });
+}
+
+// 0: not to be had.
+template <int NX>
+int clusters_at_once(int dev, int splits) {
+  std::atomic<int>* known = dev >= 0 && dev < kMaxDevices ? &g_clusters[dev][NX == 32][splits] : nullptr;
+  int n = known != nullptr ? known->load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
+  cfg.gridDim = dim3(1, 1, static_cast<unsigned>(splits));
+  cfg.blockDim = dim3(W8S<NX>::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = W8S<NX>::SMEM_BYTES;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 1;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = static_cast<unsigned>(splits);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, a4w4_w8a8_small_kernel<NX>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  n *= 2;                                              // the count is for one block on an SM, two fit
+  if (n > 0 && known != nullptr) known->store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// Shares of K: those that take least time if a wave of clusters costs the blocks of its longest share
+// and six more, and a share an eighth of a block (2048 k's, us: 14 to 36 tiles with 2 shares 6.4, with 4
+// 4.7, with 8 3.9 to 5.1; 14 tiles with 16 4.3; 40 tiles with 8, a second wave, 8.0).
+// A cluster stays within a GPC, so that fewer fit than the SMs' number says: 32 x 4224 x 1536 with
+// 9 shares (297 thread blocks of 304, but 33 clusters are a second wave) 11.5 us, with 6 6.5.
+// Shares that do not shorten the longest one only add to the sums: 4 x 1536 x 4224 with 16 5.0, with 11 4.6.
+template <int NX>
+int small_splits(int tiles, int kt) {
+  int best = 1, dev = -1;
+  long long least = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    dev = -1;
+  }
+  for (int s = 1; s <= kt && s <= kMaxW8Splits; ++s) {
+    const int at_once = clusters_at_once<NX>(dev, s);
+    if (at_once <= 0) continue;
+    const long long cost = static_cast<long long>((tiles + at_once - 1) / at_once) * ((kt + s - 1) / s + 6) * 8 + s;
+    if (least == 0 || cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+template <int NX>
+int launch_small_nx(W8SmallArgs a, int tiles, cudaStream_t st) {
+  using Cf = W8S<NX>;
+  auto kern = a4w4_w8a8_small_kernel<NX>;
+  if (small_attrs<NX>() != 0) return -4;
+  a.splits = small_splits<NX>(tiles, a.KT);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(tiles, 1, static_cast<unsigned>(a.splits));
   cfg.blockDim = dim3(Cf::THREADS, 1, 1);
   cfg.dynamicSmemBytes = Cf::SMEM_BYTES;
   cfg.stream = st;
@@ -827,12 +889,6 @@ W8Plan plan_w8a8(int M, int N, int K, int sms) {
     return pl;
   }
   pl.nx = M <= 16 ? 16 : 32;
-  pl.x_tiles = (M + pl.nx - 1) / pl.nx;
-  const int blocks = pl.w_tiles * pl.x_tiles;
-  pl.splits = 2 * sms / (blocks > 0 ? blocks : 1);      // two thread blocks on every SM
-  if (pl.splits > 16) pl.splits = 16;
-  if (pl.splits > pl.kt) pl.splits = pl.kt;
-  if (pl.splits < 1) pl.splits = 1;
   return pl;
 }
 
@@ -844,12 +900,11 @@ int launch_w8a8(const W8Plan& pl, const void* A, int M, int K, const void* W8, c
     a.W8 = static_cast<const uint8_t*>(W8);
     a.Ws = Ws;
     a.C = static_cast<uint16_t*>(C);
-    a.M = M; a.N = N; a.K = K; a.KT = pl.kt; a.splits = pl.splits;
+    a.M = M; a.N = N; a.K = K; a.KT = pl.kt;
     a.prefetch_w = prefetch_w;
     a.wait_ns = wait_ns;
     a.status = status;
-    const dim3 grid(pl.w_tiles, pl.x_tiles, pl.splits);
-    return pl.nx == 16 ? launch_small_nx<16>(a, grid, st) : launch_small_nx<32>(a, grid, st);
+    return pl.nx == 16 ? launch_small_nx<16>(a, pl.w_tiles, st) : launch_small_nx<32>(a, pl.w_tiles, st);
   }
   const long long blocks = static_cast<long long>(pl.x_tiles) * 128 * pl.kt;
   const long long grid = (blocks * 8 + 255) / 256;
