@@ -184,12 +184,10 @@ int launch_kv_rope(RopeArgs p, int D, cudaStream_t st, int sms);
 
 // 8-bit block-scaled product (w8a8.cu).
 struct W8Plan {
-  int large;          // 1: 128 x 256 tiles, activations quantised once; 0: weight rows on the matrix unit's M side
-  int nx;             // not large: tokens that a thread block has room for
-  int x_tiles, w_tiles;   // of 128 tokens (large), of 128 weight rows
-  int kt;             // 128-wide blocks of K
-  int half_tiles;     // large: tiles of the last partial wave, run as halves
-  size_t ws_bytes;
+  int x_tiles, w_tiles;   // of 128 tokens and of 128 weight rows
+  int kt;                 // 128-wide blocks of K
+  int half_tiles;         // tiles of 128 x 256 of the last partial wave, run as halves
+  size_t ws_bytes;        // of quantised activations: more than 32 tokens
 };
 W8Plan plan_w8a8(int M, int N, int K, int sms);
 int launch_w8a8(const W8Plan& plan, const void* A, int M, int K, const void* W8, const float* Ws, int N, void* C,

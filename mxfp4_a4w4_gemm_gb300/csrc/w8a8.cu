@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
   const int kt0 = static_cast<int>(static_cast<long long>(split) * p.KT / p.splits);
   const int kt1 = static_cast<int>(static_cast<long long>(split + 1) * p.KT / p.splits);
   const int nk = kt1 - kt0;
-  const int mvalid = p.M;                              // tokens, at most NX
+  const int m0 = blockIdx.y * NX, mvalid = min(NX, p.M - m0);      // this block's tokens
   const unsigned long long drain_ns = p.wait_ns > 100000000ull ? p.wait_ns : 100000000ull;
 
   const uint32_t full_w = base + Cf::OFF_BAR, empty = full_w + 8u * Cf::RING;
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
             const int r = r0 + 4 * h + (lane >> 3);
             v[h][0] = v[h][1] = make_uint4(0u, 0u, 0u, 0u);
             if (r < mvalid) {
-              const uint16_t* src = p.A + static_cast<long long>(r) * p.K + (kt0 + i) * 128 + c * 16;
+              const uint16_t* src = p.A + static_cast<long long>(m0 + r) * p.K + (kt0 + i) * 128 + c * 16;
               v[h][0] = ld_global_nc_v4(src);
               v[h][1] = ld_global_nc_v4(src + 8);
             }
@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
 #pragma unroll
         for (int i = 0; i < NX; ++i)
           if (i < mvalid)
-            p.C[static_cast<long long>(i) * p.N + w_tile * 128 + lrow] =
+            p.C[static_cast<long long>(m0 + i) * p.N + w_tile * 128 + lrow] =
                 __bfloat16_as_ushort(__float2bfloat16_rn(i & 1 ? hi2(acc[i / 2]) : lo2(acc[i / 2])));
       } else if (ready) {
         float* red = reinterpret_cast<float*>(smem);
@@ -764,7 +764,7 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
           uint2 o;
           o.x = *reinterpret_cast<const uint32_t*>(&lo);
           o.y = *reinterpret_cast<const uint32_t*>(&hi);
-          *reinterpret_cast<uint2*>(p.C + static_cast<long long>(g >> 5) * p.N + w_tile * 128 + (g & 31) * 4) = o;
+          *reinterpret_cast<uint2*>(p.C + static_cast<long long>(m0 + (g >> 5)) * p.N + w_tile * 128 + (g & 31) * 4) = o;
         }
       }
     } else {
@@ -829,8 +829,12 @@ int clusters_at_once(int dev, int splits) {
 // A cluster stays within a GPC, so that fewer fit than the SMs' number says: 32 x 4224 x 1536 with
 // 9 shares (297 thread blocks of 304, but 33 clusters are a second wave) 11.5 us, with 6 6.5.
 // Shares that do not shorten the longest one only add to the sums: 4 x 1536 x 4224 with 16 5.0, with 11 4.6.
+struct SmallCost {
+  int splits;
+  long long cost;                                      // eighths of a block; 0: not known
+};
 template <int NX>
-int small_splits(int tiles, int kt) {
+SmallCost small_cost(long long tiles, int kt) {
   int best = 1, dev = -1;
   long long least = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -840,23 +844,21 @@ int small_splits(int tiles, int kt) {
   for (int s = 1; s <= kt && s <= kMaxW8Splits; ++s) {
     const int at_once = clusters_at_once<NX>(dev, s);
     if (at_once <= 0) continue;
-    const long long cost = static_cast<long long>((tiles + at_once - 1) / at_once) * ((kt + s - 1) / s + 6) * 8 + s;
+    const long long cost = (tiles + at_once - 1) / at_once * ((kt + s - 1) / s + 6) * 8 + s;
     if (least == 0 || cost < least) {
       least = cost;
       best = s;
     }
   }
-  return best;
+  return {best, least};
 }
 
 template <int NX>
-int launch_small_nx(W8SmallArgs a, int tiles, cudaStream_t st) {
+int launch_small(const W8SmallArgs& a, int w_tiles, cudaStream_t st) {
   using Cf = W8S<NX>;
   auto kern = a4w4_w8a8_small_kernel<NX>;
-  if (small_attrs<NX>() != 0) return -4;
-  a.splits = small_splits<NX>(tiles, a.KT);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles, 1, static_cast<unsigned>(a.splits));
+  cfg.gridDim = dim3(w_tiles, (a.M + NX - 1) / NX, static_cast<unsigned>(a.splits));
   cfg.blockDim = dim3(Cf::THREADS, 1, 1);
   cfg.dynamicSmemBytes = Cf::SMEM_BYTES;
   cfg.stream = st;
@@ -873,28 +875,40 @@ int launch_small_nx(W8SmallArgs a, int tiles, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? 0 : -4;
 }
 
+constexpr int kMaxSmallM = 1024;
+
+// What the tiles of 128 x 256 take, in blocks of K of a half of one: 0.29 us each and 12 of them
+// before the first (3.6 us).  Where the other kernel's 32 tokens x 128 weight rows, 2.5 times as much for
+// each of its blocks (small_cost), come to less, they are taken; 32 and fewer tokens always are, for the
+// sake of the workspace.  Both measured, us:   these / those
+//   64 x 1536 x 7168   19.6 /  9.5      128 x 1536 x 7168   20.2 / 13.5     128 x 1536 x 16384  40.1 / 23.2
+//   64 x 4224 x 1536    7.1 /  7.5       64 x 7168 x 4224   13.6 / 16.8      96 x  8448 x  7168  20.8 / 44.0
+//   32 x 7168 x 4224   13.2 / 10.9       32 x 7168 x  768    5.6 /  6.6      32 x 18944 x  3584  13.3 / 15.7
+long long large_cost(const W8Plan& pl, int sms) {
+  const long long full = static_cast<long long>(pl.x_tiles) * (pl.w_tiles / 2) - pl.half_tiles;
+  const long long halves = 2ll * pl.half_tiles + (pl.w_tiles % 2 ? pl.x_tiles : 0);
+  return pl.kt * (2 * ((full + sms - 1) / sms) + (halves + sms - 1) / sms) + 12;
+}
+
 }  // namespace
 
 W8Plan plan_w8a8(int M, int N, int K, int sms) {
   W8Plan pl{};
   pl.kt = K / 128;
   pl.w_tiles = N / 128;
-  pl.large = M > 32;
-  if (pl.large) {
-    pl.x_tiles = (M + 127) / 128;
+  pl.x_tiles = (M + 127) / 128;
+  if (M > 32) {
     const long long tiles = static_cast<long long>(pl.x_tiles) * (pl.w_tiles / 2), rest = tiles % sms;
     // the last, partial wave's tiles run as halves where they then still are one wave
     pl.half_tiles = 2 * rest <= sms ? static_cast<int>(rest) : 0;
     pl.ws_bytes = static_cast<size_t>(pl.x_tiles) * pl.kt * kActTile;
-    return pl;
   }
-  pl.nx = M <= 16 ? 16 : 32;
   return pl;
 }
 
 int launch_w8a8(const W8Plan& pl, const void* A, int M, int K, const void* W8, const float* Ws, int N, void* C,
                 void* ws, cudaStream_t st, unsigned long long wait_ns, unsigned int* status, int prefetch_w, int sms) {
-  if (!pl.large) {
+  if (M <= kMaxSmallM) {
     W8SmallArgs a{};
     a.A = static_cast<const uint16_t*>(A);
     a.W8 = static_cast<const uint8_t*>(W8);
@@ -904,7 +918,17 @@ int launch_w8a8(const W8Plan& pl, const void* A, int M, int K, const void* W8, c
     a.prefetch_w = prefetch_w;
     a.wait_ns = wait_ns;
     a.status = status;
-    return pl.nx == 16 ? launch_small_nx<16>(a, pl.w_tiles, st) : launch_small_nx<32>(a, pl.w_tiles, st);
+    if (M <= 16) {
+      if (small_attrs<16>() != 0) return -4;
+      a.splits = small_cost<16>(pl.w_tiles, pl.kt).splits;
+      return launch_small<16>(a, pl.w_tiles, st);
+    }
+    if (small_attrs<32>() != 0) return -4;
+    const SmallCost c = small_cost<32>(static_cast<long long>(pl.w_tiles) * ((M + 31) / 32), pl.kt);
+    if (M <= 32 || (c.cost > 0 && 5 * c.cost < 16 * large_cost(pl, sms))) {
+      a.splits = c.splits;
+      return launch_small<32>(a, pl.w_tiles, st);
+    }
   }
   const long long blocks = static_cast<long long>(pl.x_tiles) * 128 * pl.kt;
   const long long grid = (blocks * 8 + 255) / 256;
