@@ -374,6 +374,13 @@ __device__ __forceinline__ void st_async_v4(uint32_t dst, float4 v, uint32_t bar
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];"
                :: "r"(dst), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar) : "memory");
 }
+// Bulk copy from this CTA's shared memory to a peer's, counted on an mbarrier of the peer (both
+// shared::cluster addresses); 16-byte aligned, bytes a multiple of 16.  The source stays until
+// the peer has seen it complete.
+__device__ __forceinline__ void bulk_s2peer(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :: "r"(dst), "r"(src), "r"(bytes), "r"(bar) : "memory");
+}
 // Arrive (release, cluster scope) on an mbarrier in a peer CTA's shared
 // memory (`remote` from cluster_map_shared).
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t remote) {

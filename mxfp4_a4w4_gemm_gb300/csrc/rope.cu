@@ -550,8 +550,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeBlocks<CACHE>) kv_rope_k
     const bool more = t + stride < p.T;
     const int next_position = more && p.rot > 0 ? p.positions[t + stride] : 0;
     const int ahead_slot = CACHE && t + 2 * stride < p.T ? p.slot_map[t + 2 * stride] : -1;
-    const bool ok = kv_wait(bar + 8u * s, (done >> 1) & 1, abort_flag, p.wait_ns, p.status);
-    __syncwarp();
+    const bool ok = __all_sync(kAll, kv_wait(bar + 8u * s, (done >> 1) & 1, abort_flag, p.wait_ns, p.status));
     done += ok;
     const uint16_t* stage = reinterpret_cast<const uint16_t*>(smem + s * p.stage_bytes);
     const RopeCoef<D>& now = coef[s];

@@ -13,7 +13,15 @@
 //          side, K split over the thread blocks of a cluster; activations are quantised
 //          in the kernel.  Bound by the weights' bytes.
 //   large  128 tokens x 256 weight rows per tile, one persistent thread block per SM,
-//          activations quantised once beforehand into tiles in the workspace.
+//          activations quantised once beforehand into tiles in the workspace; few tiles
+//          run as halves whose K is shared by a cluster.
+//
+// Small: 1 x 7168 x 4224 7.2 us (4.2 TB/s of weights; 4.5 us would be a copy's rate; the
+// rest is the launch, the first block's latency and the exchange of sums).  Large:
+// 2048 x 8448 x 7168 115 us, 2.15 PFLOP/s: bound by the operands' way into the SM (48 KB
+// per block of K at about 64 bytes a clock) and by the loop from an accumulator read
+// to the MMAs that write it again.  A pair of SMs on one tile, more accumulators,
+// more and smaller stages, operands multicast to two blocks: none was faster.
 #include <cfloat>
 
 #include "device.cuh"
@@ -250,10 +258,15 @@ struct W8LargeArgs {
   int full_units;           // tiles 0 .. full_units - 1 (x-major) run whole
   int split_units;          // then this many halves of the other wide tiles
   int units;                // and the narrow tiles at the end of an odd N / 128
+  int shares;               // of a unit's K, each a thread block's of a cluster (1: no clusters)
   unsigned long long wait_ns;
   unsigned int* status;
 };
 
+constexpr int kMaxW8Shares = 6;
+
+// SHARED: K is shared by a cluster; halves and narrow tiles only.
+template <bool SHARED>
 struct W8L {
   static constexpr int EPI_WARPS = 8, EPI_FIRST = 4;   // the first warpgroup: producer, MMA issuer, two that only help out
   static constexpr int THREADS = 32 * (EPI_FIRST + EPI_WARPS);
@@ -262,11 +275,12 @@ struct W8L {
   static constexpr int REGS_FEW = 40, REGS_MANY = 232;
   static_assert(128 * REGS_FEW + 32 * EPI_WARPS * REGS_MANY <= THREADS * 168, "registers");
   static constexpr int STAGES = 4;
-  static constexpr int STAGE = 3 * kTile;
+  static constexpr int STAGE = (SHARED ? 2 : 3) * kTile;
   static constexpr int STG_PITCH = 80;                 // 32 BF16 columns and 16 bytes: 16-byte rows on different banks
   static constexpr int OFF_STG = STAGES * STAGE;
-  static constexpr int OFF_BAR = OFF_STG + EPI_WARPS * 32 * STG_PITCH;
-  static constexpr int NBAR = 2 * STAGES + 5;          // full, empty; accumulators' full and empty; drain
+  // SHARED: in place of the output's rows everyone's sums of this block's rows
+  static constexpr int OFF_BAR = OFF_STG + (SHARED ? (128 + kMaxW8Shares - 1) * 512 : EPI_WARPS * 32 * STG_PITCH);
+  static constexpr int NBAR = 2 * STAGES + 6;          // full, empty; accumulators' full and empty; drain; sums
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;
   static_assert(SMEM_BYTES <= 232448, "shared memory");
@@ -287,22 +301,22 @@ __device__ __forceinline__ W8Unit w8_unit(const W8LargeArgs& p, int u) {
 // One unit's blocks of K: COLS columns of this thread's row.  False: a wait gave up.
 template <int COLS>
 __device__ __forceinline__ bool w8_promote(const W8LargeArgs& p, uint32_t tmem, uint32_t acc_full, uint32_t acc_empty,
-                                           const uint8_t* row_scale, const float* block_scale, int& g,
+                                           const uint8_t* row_scale, const float* block_scale, int nk, int& g,
                                            unsigned long long* acc, volatile int* abort_flag) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < COLS / 2; ++i) acc[i] = 0ull;
   float sa = *reinterpret_cast<const float*>(row_scale), sw = block_scale[0];
-  for (int kt = 0; kt < p.KT; ++kt, ++g) {
+  for (int kt = 0; kt < nk; ++kt, ++g) {
     const uint32_t s = __float_as_uint(sa * sw);       // exact: sa is a power of two
     const unsigned long long s2 = pack2(s, s);
-    if (kt + 1 < p.KT) {
+    if (kt + 1 < nk) {
       sa = *reinterpret_cast<const float*>(row_scale + static_cast<long long>(kt + 1) * kActTile);
       sw = block_scale[kt + 1];
     }
     const int b = g & 1;
-    if (!mbar_wait(acc_full + 8u * b, static_cast<uint32_t>(g >> 1) & 1u, abort_flag, p.wait_ns, p.status)) return false;
-    __syncwarp();
+    if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_full + 8u * b, static_cast<uint32_t>(g >> 1) & 1u, abort_flag, p.wait_ns, p.status)))
+      return false;
     tc_fence_after();
     // few and large loads: the two warps of a scheduler load and add in turn
     static_assert(COLS % 64 == 0, "columns");
@@ -328,7 +342,8 @@ __device__ __forceinline__ void w8_store(const W8LargeArgs& p, const unsigned lo
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int c = 0; c < COLS; c += 32) {
-    uint4* mine = reinterpret_cast<uint4*>(stg + lane * W8L::STG_PITCH);
+    constexpr int PITCH = W8L<false>::STG_PITCH;
+    uint4* mine = reinterpret_cast<uint4*>(stg + lane * PITCH);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       mine[i] = make_uint4(bf16x2_of(acc[c / 2 + 4 * i]), bf16x2_of(acc[c / 2 + 4 * i + 1]),
@@ -337,7 +352,7 @@ __device__ __forceinline__ void w8_store(const W8LargeArgs& p, const unsigned lo
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = i * 8 + (lane >> 2), seg = lane & 3;
-      const uint4 v = *reinterpret_cast<const uint4*>(stg + r * W8L::STG_PITCH + seg * 16);
+      const uint4 v = *reinterpret_cast<const uint4*>(stg + r * PITCH + seg * 16);
       if (row0 + r < p.M)
         *reinterpret_cast<uint4*>(p.C + static_cast<long long>(row0 + r) * p.N + col0 + c + seg * 8) = v;
     }
@@ -349,36 +364,48 @@ __device__ __forceinline__ void w8_store(const W8LargeArgs& p, const unsigned lo
 //   warp 1      TMEM owner and MMA issuer: two accumulators of 256 columns in turn;
 //   warps 4-11  two per TMEM lane quadrant, a thread per token row and half of the
 //               columns: scale and add each block's sums, then BF16 rows.
-__global__ void __launch_bounds__(W8L::THREADS, 1) a4w4_w8a8_large_kernel(const W8LargeArgs p) {
-  using Cf = W8L;
+// SHARED (one unit per cluster, few of them): every rank has its share of K; of the sums rank r
+// owns rows 128 r / S .., the others send their sums there, the owner adds all in rank order.
+template <bool SHARED>
+__global__ void __launch_bounds__(W8L<SHARED>::THREADS, 1) a4w4_w8a8_large_kernel(const W8LargeArgs p) {
+  using Cf = W8L<SHARED>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = gridDim.x;
+  const int S = SHARED ? p.shares : 1, rank = SHARED ? static_cast<int>(cluster_ctarank()) : 0;
+  const int G = SHARED ? p.units : gridDim.x, u0 = SHARED ? blockIdx.x / S : blockIdx.x;      // units u0, u0 + G ..
+  const int k0 = SHARED ? rank * p.KT / S : 0, nk = (SHARED ? (rank + 1) * p.KT / S : p.KT) - k0;
+  const int own0 = rank * 128 / S, own1 = (rank + 1) * 128 / S, slot = (127 + S) / S;
   const unsigned long long drain_ns = p.wait_ns > 100000000ull ? p.wait_ns : 100000000ull;
 
   const uint32_t full = base + Cf::OFF_BAR, empty = full + 8u * Cf::STAGES;
   const uint32_t acc_full = empty + 8u * Cf::STAGES, acc_empty = acc_full + 16u, drain = acc_empty + 16u;
+  const uint32_t sums = drain + 8u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cf::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cf::OFF_MISC + 8);
   volatile int* never = reinterpret_cast<volatile int*>(smem + Cf::OFF_MISC + 16);
+  volatile int* owner_ready = reinterpret_cast<volatile int*>(smem + Cf::OFF_MISC + 24);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2 * Cf::STAGES + 2; ++s) mbar_init(full + 8u * s, 1);   // full, empty, acc_full
     mbar_init(acc_empty, Cf::EPI_WARPS);
     mbar_init(acc_empty + 8u, Cf::EPI_WARPS);
     mbar_init(drain, 1);
+    mbar_init(sums, 1);
     *abort_flag = 0;
     *never = 0;
+    *owner_ready = 0;
     fence_barrier_init();
+    if (SHARED) mbar_arrive_expect_tx(sums, static_cast<uint32_t>((S - 1) * (own1 - own0) * 512));
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tc_fence_before();
   }
   __syncthreads();
+  if (SHARED) cluster_arrive_relaxed();                 // this block's barriers exist; waited for before the first sums are sent
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_wait();                                       // the activation tiles come from the kernel before
@@ -391,11 +418,11 @@ __global__ void __launch_bounds__(W8L::THREADS, 1) a4w4_w8a8_large_kernel(const 
         const uint64_t pol = policy_evict_last();         // operands are read again by other tiles, from L2
         int g = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < p.units && ok; u += G) {
+        for (int u = u0; u < p.units && ok; u += G) {
           const W8Unit t = w8_unit(p, u);
-          const uint8_t* a = p.Aq + static_cast<long long>(t.x) * p.KT * kActTile;
-          const uint8_t* w = p.W8 + static_cast<long long>(t.w) * p.KT * kTile;
-          for (int kt = 0; kt < p.KT; ++kt, ++g) {
+          const uint8_t* a = p.Aq + (static_cast<long long>(t.x) * p.KT + k0) * kActTile;
+          const uint8_t* w = p.W8 + (static_cast<long long>(t.w) * p.KT + k0) * kTile;
+          for (int kt = 0; kt < nk; ++kt, ++g) {
             const int s = g % Cf::STAGES;
             if (!mbar_wait(empty + 8u * s, ((g / Cf::STAGES) & 1) ^ 1u, abort_flag, p.wait_ns, p.status)) {
               ok = false;
@@ -405,7 +432,7 @@ __global__ void __launch_bounds__(W8L::THREADS, 1) a4w4_w8a8_large_kernel(const 
             mbar_arrive_expect_tx(fb, (1 + t.n) * kTile);
             bulk_g2s(dst, a + static_cast<long long>(kt) * kActTile, kTile, fb, pol);
             bulk_g2s(dst + kTile, w + static_cast<long long>(kt) * kTile, kTile, fb, pol);
-            if (t.n == 2) bulk_g2s(dst + 2 * kTile, w + static_cast<long long>(p.KT + kt) * kTile, kTile, fb, pol);
+            if (!SHARED && t.n == 2) bulk_g2s(dst + 2 * kTile, w + static_cast<long long>(p.KT + kt) * kTile, kTile, fb, pol);
           }
         }
         // every copy issued lands before the shared memory is released
@@ -420,9 +447,9 @@ __global__ void __launch_bounds__(W8L::THREADS, 1) a4w4_w8a8_large_kernel(const 
         int s = 0, g = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < p.units && ok; u += G) {
+        for (int u = u0; u < p.units && ok; u += G) {
           const uint32_t idesc = idesc_e4m3(128u * w8_unit(p, u).n);
-          for (int kt = 0; kt < p.KT; ++kt, ++g) {
+          for (int kt = 0; kt < nk; ++kt, ++g) {
             const uint32_t b = g & 1, af = acc_full + 8u * b, d = tmem + b * 256, off = static_cast<uint32_t>(s * Cf::STAGE) >> 4;
             const uint64_t ad = adesc0 + off, bd = bdesc0 + off;
             if (!mbar_wait(full + 8u * s, ph, abort_flag, p.wait_ns, p.status) ||
@@ -447,6 +474,11 @@ __global__ void __launch_bounds__(W8L::THREADS, 1) a4w4_w8a8_large_kernel(const 
         mbar_wait(drain, 0, never, drain_ns, p.status);
       }
     }
+    __syncwarp();
+    if (SHARED) {
+      cluster_wait();
+      cluster_arrive_relaxed();
+    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(Cf::REGS_MANY));
     const int q = warp & 3, half = (warp - Cf::EPI_FIRST) >> 2;
@@ -454,24 +486,73 @@ __global__ void __launch_bounds__(W8L::THREADS, 1) a4w4_w8a8_large_kernel(const 
     uint8_t* stg = smem + Cf::OFF_STG + (warp - Cf::EPI_FIRST) * 32 * Cf::STG_PITCH;
     unsigned long long acc[64];
     int g = 0;
-    for (int u = blockIdx.x; u < p.units; u += G) {
+    for (int u = u0; u < p.units; u += G) {
       const W8Unit t = w8_unit(p, u);
-      const uint8_t* sa = p.Aq + static_cast<long long>(t.x) * p.KT * kActTile + kTile + 4 * (q * 32 + lane);
+      const uint8_t* sa = p.Aq + (static_cast<long long>(t.x) * p.KT + k0) * kActTile + kTile + 4 * (q * 32 + lane);
       const int row0 = t.x * 128 + q * 32;
-      if (t.n == 2) {
+      if (SHARED) {
+        const bool ok = w8_promote<64>(p, tq + half * 64, acc_full, acc_empty, sa, p.Ws + static_cast<long long>(t.w) * p.KT + k0,
+                                       nk, g, acc, abort_flag);
+        if (!ok) *abort_flag = 1;
+        // The sums by rows over the drained ring, a row's four-column pieces in an order that changes
+        // with the row, for the banks; each owner's rows leave in one bulk copy (asynchronous
+        // stores of 16 bytes, each counted on the owner's barrier: +2 us).
+        float4* mine = reinterpret_cast<float4*>(smem + (q * 32 + lane) * 512);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          mine[(half * 16 + i) ^ lane] = make_float4(lo2(acc[2 * i]), hi2(acc[2 * i]), lo2(acc[2 * i + 1]), hi2(acc[2 * i + 1]));
+        const int et = threadIdx.x - 32 * Cf::EPI_FIRST;
+        fence_proxy_async_smem();
+        named_bar_sync(3, 32 * Cf::EPI_WARPS);
+        cluster_wait();
+        // sent whatever happened before, so that every owner's count of bytes completes
+        if (warp == Cf::EPI_FIRST && lane < S && lane != rank) {
+          const int r0 = lane * 128 / S, rows = (lane + 1) * 128 / S - r0;
+          bulk_s2peer(cluster_map_shared(base + Cf::OFF_STG + rank * slot * 512, lane), base + r0 * 512, rows * 512,
+                      cluster_map_shared(sums, lane));
+        }
+        __syncwarp();
+        if (et == 0) *owner_ready = mbar_wait_cluster(sums, 0, 32ull * drain_ns, p.status) && !*abort_flag ? 1 : 0;
+        named_bar_sync(3, 32 * Cf::EPI_WARPS);
+        cluster_arrive_relaxed();                       // what came for this block is here; waited for before any leaves
+        if (*owner_ready) {
+          constexpr int ROWS = 4;                       // of a warp, in flight
+          for (int row0 = own0 + (et >> 5); row0 < own1; row0 += ROWS * Cf::EPI_WARPS) {
+            float4 sum[ROWS] = {};
+            for (int c = 0; c < S; ++c) {
+              const uint8_t* of = c == rank ? smem : smem + Cf::OFF_STG + (c * slot - own0) * 512;
+#pragma unroll
+              for (int i = 0; i < ROWS; ++i) {
+                const int row = min(row0 + i * Cf::EPI_WARPS, own1 - 1);
+                const float4 v = reinterpret_cast<const float4*>(of + row * 512)[lane ^ (row & 31)];
+                sum[i].x += v.x; sum[i].y += v.y; sum[i].z += v.z; sum[i].w += v.w;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+              const int row = row0 + i * Cf::EPI_WARPS;
+              const __nv_bfloat162 lo = __floats2bfloat162_rn(sum[i].x, sum[i].y), hi = __floats2bfloat162_rn(sum[i].z, sum[i].w);
+              const uint2 v = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+              if (row < own1 && t.x * 128 + row < p.M)
+                *reinterpret_cast<uint2*>(p.C + static_cast<long long>(t.x * 128 + row) * p.N + t.w * 128 + lane * 4) = v;
+            }
+          }
+        }
+      } else if (t.n == 2) {
         if (!w8_promote<128>(p, tq + half * 128, acc_full, acc_empty, sa,
-                             p.Ws + static_cast<long long>(t.w + half) * p.KT, g, acc, abort_flag))
+                             p.Ws + static_cast<long long>(t.w + half) * p.KT, nk, g, acc, abort_flag))
           break;
         w8_store<128>(p, acc, stg, row0, (t.w + half) * 128);
       } else {
-        if (!w8_promote<64>(p, tq + half * 64, acc_full, acc_empty, sa, p.Ws + static_cast<long long>(t.w) * p.KT, g,
-                            acc, abort_flag))
+        if (!w8_promote<64>(p, tq + half * 64, acc_full, acc_empty, sa, p.Ws + static_cast<long long>(t.w) * p.KT, nk,
+                            g, acc, abort_flag))
           break;
         w8_store<64>(p, acc, stg, row0, t.w * 128 + half * 64);
       }
     }
   }
 
+  if (SHARED) cluster_wait();                           // the peers have read this block's sums
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -682,12 +763,12 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
         const int turn = i % (2 * Cf::RING), b = i & 1;
         const uint32_t sw = __float_as_uint(block_scale[i]);
         const unsigned long long sw2 = pack2(sw, sw);
-        if (!mbar_wait(scales + 8u * turn, static_cast<uint32_t>(i / (2 * Cf::RING)) & 1u, abort_flag, p.wait_ns, p.status) ||
-            !mbar_wait(acc_full + 8u * b, static_cast<uint32_t>(i >> 1) & 1u, abort_flag, p.wait_ns, p.status)) {
+        const bool ok = mbar_wait(scales + 8u * turn, static_cast<uint32_t>(i / (2 * Cf::RING)) & 1u, abort_flag, p.wait_ns, p.status) &&
+                        mbar_wait(acc_full + 8u * b, static_cast<uint32_t>(i >> 1) & 1u, abort_flag, p.wait_ns, p.status);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
           ready = 0;
           break;
         }
-        __syncwarp();
         tc_fence_after();
         const ulonglong2* sa = reinterpret_cast<const ulonglong2*>(smem + Cf::OFF_SCALE + turn * NX * 4);
 #pragma unroll
@@ -707,7 +788,6 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty + 8u * b);
       }
-      ready = __all_sync(0xFFFFFFFFu, ready);
       // weight row q * 32 + lane of every token: partial [token][weight row] over the drained ring,
       // or, where nothing is to be reduced, BF16 (a warp writes 64 bytes of a token's row)
       const int lrow = q * 32 + lane;
@@ -783,8 +863,6 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
 
 constexpr int kMaxW8Splits = 16;
 constexpr int kMaxDevices = 64;
-// clusters of a size that the device holds at once, filled on first use (0: not known yet)
-std::atomic<int> g_clusters[kMaxDevices][2][kMaxW8Splits + 1];
 
 template <int NX>
 int small_attrs() {
@@ -796,32 +874,55 @@ int small_attrs() {
            cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
   });
 }
+template <bool SHARED>
+int large_attrs() {
+  static std::atomic<unsigned long long> attr_devs{0};   // bit d: attribute set on device d
+  return ensure_func_attrs(attr_devs, [&] {
+    return cudaFuncSetAttribute(a4w4_w8a8_large_kernel<SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                W8L<SHARED>::SMEM_BYTES) == cudaSuccess;
+  });
+}
 
-// 0: not to be had.
-template <int NX>
-int clusters_at_once(int dev, int splits) {
-  std::atomic<int>* known = dev >= 0 && dev < kMaxDevices ? &g_clusters[dev][NX == 32][splits] : nullptr;
-  int n = known != nullptr ? known->load(std::memory_order_relaxed) : 0;
-  if (n > 0) return n;
+int this_device() {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return -1;
+  }
+  return dev;
+}
+
+// Clusters of n thread blocks that the device holds at once (0: not to be had), per kernel; its
+// attributes are set.
+int clusters_at_once(int dev, int kind, const void* kern, int threads, int smem, int n) {
+  static std::atomic<int> cache[kMaxDevices][3][kMaxW8Splits + 1];     // filled on first use (0: not known yet)
+  std::atomic<int>* known = dev >= 0 && dev < kMaxDevices ? &cache[dev][kind][n] : nullptr;
+  int count = known != nullptr ? known->load(std::memory_order_relaxed) : 0;
+  if (count > 0) return count;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1, 1, static_cast<unsigned>(splits));
-  cfg.blockDim = dim3(W8S<NX>::THREADS, 1, 1);
-  cfg.dynamicSmemBytes = W8S<NX>::SMEM_BYTES;
+  cfg.gridDim = dim3(static_cast<unsigned>(n), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 1;
+  attr.val.clusterDim.x = static_cast<unsigned>(n);
   attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = static_cast<unsigned>(splits);
+  attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, a4w4_w8a8_small_kernel<NX>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&count, kern, &cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
-  n *= 2;                                              // the count is for one block on an SM, two fit
-  if (n > 0 && known != nullptr) known->store(n, std::memory_order_relaxed);
-  return n;
+  if (count > 0 && known != nullptr) known->store(count, std::memory_order_relaxed);
+  return count;
 }
+
+// What a kernel takes with K in so many shares, in eighths of a block of K (of its own; 0: not known).
+struct W8Cost {
+  int shares;
+  long long cost;
+};
 
 // Shares of K: those that take least time if a wave of clusters costs the blocks of its longest share
 // and six more, and a share an eighth of a block (2048 k's, us: 14 to 36 tiles with 2 shares 6.4, with 4
@@ -829,28 +930,19 @@ int clusters_at_once(int dev, int splits) {
 // A cluster stays within a GPC, so that fewer fit than the SMs' number says: 32 x 4224 x 1536 with
 // 9 shares (297 thread blocks of 304, but 33 clusters are a second wave) 11.5 us, with 6 6.5.
 // Shares that do not shorten the longest one only add to the sums: 4 x 1536 x 4224 with 16 5.0, with 11 4.6.
-struct SmallCost {
-  int splits;
-  long long cost;                                      // eighths of a block; 0: not known
-};
 template <int NX>
-SmallCost small_cost(long long tiles, int kt) {
-  int best = 1, dev = -1;
-  long long least = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) {
-    cudaGetLastError();
-    dev = -1;
-  }
+W8Cost small_cost(long long tiles, int kt) {
+  W8Cost best{1, 0};
+  const int dev = this_device();
   for (int s = 1; s <= kt && s <= kMaxW8Splits; ++s) {
-    const int at_once = clusters_at_once<NX>(dev, s);
+    // (the count is for one thread block on an SM, two fit)
+    const long long at_once = 2ll * clusters_at_once(dev, NX == 32, reinterpret_cast<const void*>(a4w4_w8a8_small_kernel<NX>),
+                                                     W8S<NX>::THREADS, W8S<NX>::SMEM_BYTES, s);
     if (at_once <= 0) continue;
     const long long cost = (tiles + at_once - 1) / at_once * ((kt + s - 1) / s + 6) * 8 + s;
-    if (least == 0 || cost < least) {
-      least = cost;
-      best = s;
-    }
+    if (best.cost == 0 || cost < best.cost) best = {s, cost};
   }
-  return {best, least};
+  return best;
 }
 
 template <int NX>
@@ -877,17 +969,55 @@ int launch_small(const W8SmallArgs& a, int w_tiles, cudaStream_t st) {
 
 constexpr int kMaxSmallM = 1024;
 
-// What the tiles of 128 x 256 take, in blocks of K of a half of one: 0.29 us each and 12 of them
-// before the first (3.6 us).  Where the other kernel's 32 tokens x 128 weight rows, 2.5 times as much for
-// each of its blocks (small_cost), come to less, they are taken; 32 and fewer tokens always are, for the
-// sake of the workspace.  Both measured, us:   these / those
-//   64 x 1536 x 7168   19.6 /  9.5      128 x 1536 x 7168   20.2 / 13.5     128 x 1536 x 16384  40.1 / 23.2
-//   64 x 4224 x 1536    7.1 /  7.5       64 x 7168 x 4224   13.6 / 16.8      96 x  8448 x  7168  20.8 / 44.0
-//   32 x 7168 x 4224   13.2 / 10.9       32 x 7168 x  768    5.6 /  6.6      32 x 18944 x  3584  13.3 / 15.7
-long long large_cost(const W8Plan& pl, int sms) {
-  const long long full = static_cast<long long>(pl.x_tiles) * (pl.w_tiles / 2) - pl.half_tiles;
-  const long long halves = 2ll * pl.half_tiles + (pl.w_tiles % 2 ? pl.x_tiles : 0);
-  return pl.kt * (2 * ((full + sms - 1) / sms) + (halves + sms - 1) / sms) + 12;
+// What the tiles of 128 x 256 take, in blocks of K of a half of one: 0.29 us each and 12 of them before
+// the first (3.6 us).  Few of them, one wave of halves, share K as long as a cluster for each is there at once:
+// 7 blocks' time for the exchange of sums, and one for each share (a rank takes in (S - 1) / S of 64 KB;
+// 32 KB from a peer took 1.3 us).  Us with 1, 2, 4, 6 shares (8 are never better):
+//   64 x 1536 x 7168  20.0  13.9  10.7  10.0    513 x 1536 x 4224  14.8  12.3 (60 units: no more fit)
+//   64 x  256 x 4224  13.3  10.5   8.4   8.1     64 x 4224 x 1536   7.3   7.7   8.1
+// Where 32 tokens x 128 weight rows, 2.4 times as much for each of their blocks (small_cost), come to
+// less, they are taken; 32 and fewer tokens always are, for the sake of the workspace.  These / those:
+//   64 x 1536 x 7168  10.0 /  9.6    128 x 1536 x 7168  10.0 / 13.4     64 x   256 x 4224   8.1 /  6.1
+//   64 x 7168 x 4224  11.1 / 16.8     96 x 8448 x 7168  15.4 / 44.0     32 x 18944 x 3584  13.3 / 15.7
+long long full_units(const W8Plan& pl) { return static_cast<long long>(pl.x_tiles) * (pl.w_tiles / 2) - pl.half_tiles; }
+long long half_units(const W8Plan& pl) { return 2ll * pl.half_tiles + (pl.w_tiles % 2 ? pl.x_tiles : 0); }
+
+W8Cost large_cost(const W8Plan& pl, int sms) {
+  const long long full = full_units(pl), halves = half_units(pl);
+  W8Cost best{1, 8 * (pl.kt * (2 * ((full + sms - 1) / sms) + (halves + sms - 1) / sms) + 12)};
+  if (full > 0 || 2 * halves > sms) return best;
+  const int dev = this_device();
+  for (int s = 2; s <= pl.kt && s <= kMaxW8Shares; ++s) {
+    const long long cost = 8ll * ((pl.kt + s - 1) / s + 19 + s);
+    if (cost < best.cost && halves <= clusters_at_once(dev, 2, reinterpret_cast<const void*>(a4w4_w8a8_large_kernel<true>),
+                                                       W8L<true>::THREADS, W8L<true>::SMEM_BYTES, s))
+      best = {s, cost};
+  }
+  return best;
+}
+
+int launch_large(const W8LargeArgs& a, int sms, cudaStream_t st) {
+  if (a.shares == 1) {
+    if (large_attrs<false>() != 0) return -4;
+    return launch_pdl_smem(a4w4_w8a8_large_kernel<false>, a.units < sms ? a.units : sms, W8L<false>::THREADS,
+                           W8L<false>::SMEM_BYTES, st, a);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.units * a.shares), 1, 1);
+  cfg.blockDim = dim3(W8L<true>::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = W8L<true>::SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = static_cast<unsigned>(a.shares);
+  attrs[1].val.clusterDim.y = 1;
+  attrs[1].val.clusterDim.z = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, a4w4_w8a8_large_kernel<true>, a) != cudaSuccess) return -4;
+  return cudaGetLastError() == cudaSuccess ? 0 : -4;
 }
 
 }  // namespace
@@ -908,6 +1038,11 @@ W8Plan plan_w8a8(int M, int N, int K, int sms) {
 
 int launch_w8a8(const W8Plan& pl, const void* A, int M, int K, const void* W8, const float* Ws, int N, void* C,
                 void* ws, cudaStream_t st, unsigned long long wait_ns, unsigned int* status, int prefetch_w, int sms) {
+  W8Cost large{1, 0};
+  if (M > 32) {
+    if (large_attrs<true>() != 0) return -4;
+    large = large_cost(pl, sms);
+  }
   if (M <= kMaxSmallM) {
     W8SmallArgs a{};
     a.A = static_cast<const uint16_t*>(A);
@@ -920,13 +1055,13 @@ int launch_w8a8(const W8Plan& pl, const void* A, int M, int K, const void* W8, c
     a.status = status;
     if (M <= 16) {
       if (small_attrs<16>() != 0) return -4;
-      a.splits = small_cost<16>(pl.w_tiles, pl.kt).splits;
+      a.splits = small_cost<16>(pl.w_tiles, pl.kt).shares;
       return launch_small<16>(a, pl.w_tiles, st);
     }
     if (small_attrs<32>() != 0) return -4;
-    const SmallCost c = small_cost<32>(static_cast<long long>(pl.w_tiles) * ((M + 31) / 32), pl.kt);
-    if (M <= 32 || (c.cost > 0 && 5 * c.cost < 16 * large_cost(pl, sms))) {
-      a.splits = c.splits;
+    const W8Cost small = small_cost<32>(static_cast<long long>(pl.w_tiles) * ((M + 31) / 32), pl.kt);
+    if (M <= 32 || (small.cost > 0 && 12 * small.cost < 5 * large.cost)) {
+      a.splits = small.shares;
       return launch_small<32>(a, pl.w_tiles, st);
     }
   }
@@ -936,12 +1071,6 @@ int launch_w8a8(const W8Plan& pl, const void* A, int M, int K, const void* W8, c
   int rc = launch_pdl(w8_quant_tiles_kernel, static_cast<int>(grid), 256, st, static_cast<const uint16_t*>(A), M, K,
                       pl.kt, blocks, static_cast<uint8_t*>(ws));
   if (rc != 0) return rc;
-  static std::atomic<unsigned long long> attr_devs{0};   // bit d: attribute set on device d
-  if (ensure_func_attrs(attr_devs, [&] {
-        return cudaFuncSetAttribute(a4w4_w8a8_large_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    W8L::SMEM_BYTES) == cudaSuccess;
-      }) != 0)
-    return -4;
   W8LargeArgs a{};
   a.Aq = static_cast<const uint8_t*>(ws);
   a.W8 = static_cast<const uint8_t*>(W8);
@@ -957,7 +1086,8 @@ int launch_w8a8(const W8Plan& pl, const void* A, int M, int K, const void* W8, c
   a.units = static_cast<int>(units);
   a.wait_ns = wait_ns;
   a.status = status;
-  return launch_pdl_smem(a4w4_w8a8_large_kernel, a.units < sms ? a.units : sms, W8L::THREADS, W8L::SMEM_BYTES, st, a);
+  a.shares = large.shares;
+  return launch_large(a, sms, st);
 }
 
 int launch_prepare_w8(const void* w_bf16, int N, int K, void* w8, float* ws, cudaStream_t st) {

@@ -60,7 +60,7 @@ SIZES = [(1, 128, 128), (1, 256, 2176), (3, 384, 640), (16, 128, 4224), (17, 256
          (33, 128, 128), (33, 128, 1024), (100, 384, 640), (127, 256, 128), (128, 640, 1152), (129, 1536, 256), (257, 128, 4224),
          (513, 1536, 512), (300, 8448, 384), (1100, 2304, 256),
          (33, 384, 4224), (64, 1536, 2176), (97, 256, 4224), (500, 128, 7168), (1024, 128, 9088),    # tiles of 32 tokens, ragged
-         (1100, 384, 2304), (1025, 640, 4224), (160, 19456, 1152)]                                   # tiles of 128, long sums
+         (1100, 384, 2304), (1025, 640, 4224), (650, 1536, 4224), (160, 19456, 1152)]               # tiles of 128, long sums
 
 
 @pytest.mark.parametrize("M,N,K", SIZES, ids=lambda v: str(v))
