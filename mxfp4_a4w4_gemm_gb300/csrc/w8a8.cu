@@ -1066,8 +1066,8 @@ int launch_w8a8(const W8Plan& pl, const void* A, int M, int K, const void* W8, c
     }
   }
   const long long blocks = static_cast<long long>(pl.x_tiles) * 128 * pl.kt;
-  const long long grid = (blocks * 8 + 255) / 256;
-  if (grid > INT32_MAX) return -1;
+  const long long grid = (blocks * 8 + 255) / 256, full = full_units(pl), halves = half_units(pl);
+  if (grid > INT32_MAX || full + halves > INT32_MAX) return -1;
   int rc = launch_pdl(w8_quant_tiles_kernel, static_cast<int>(grid), 256, st, static_cast<const uint16_t*>(A), M, K,
                       pl.kt, blocks, static_cast<uint8_t*>(ws));
   if (rc != 0) return rc;
@@ -1078,12 +1078,9 @@ int launch_w8a8(const W8Plan& pl, const void* A, int M, int K, const void* W8, c
   a.C = static_cast<uint16_t*>(C);
   a.M = M; a.N = N; a.KT = pl.kt;
   a.wide = pl.w_tiles / 2;
-  const long long tiles = static_cast<long long>(pl.x_tiles) * a.wide;
-  const long long units = tiles + pl.half_tiles + (pl.w_tiles % 2 ? pl.x_tiles : 0);
-  if (units > INT32_MAX) return -1;
-  a.full_units = static_cast<int>(tiles) - pl.half_tiles;
+  a.full_units = static_cast<int>(full);
   a.split_units = 2 * pl.half_tiles;
-  a.units = static_cast<int>(units);
+  a.units = static_cast<int>(full + halves);
   a.wait_ns = wait_ns;
   a.status = status;
   a.shares = large.shares;
