@@ -141,7 +141,8 @@ int a4w4_gemm_a16w4(const void* A_bf16, int M, int K, const void* Wq, const void
  *   at most 448 * 2^e; the code is x * 2^-e (exact) rounded to nearest, ties to even.  An
  *   infinity or NaN makes its block's scale, and so its row of C, NaN.
  *   C[m, n] = sum over blocks b of 2^e[m,b] * Ws[n/128, b] * (sum over b's k's of the
- *   codes' products), every sum in fp32, in a fixed order: bitwise deterministic.
+ *   codes' products), every sum and 2^e * Ws in fp32 (what lies below 2^-126 loses bits), in
+ *   an order fixed by the sizes and the device: bitwise deterministic.
  * N % 128 == 0, K % 128 == 0, M >= 1; rows >= M of C are never touched.
  *
  * Weight tiles: tile (nt, kt) = rows 128 nt .., k's 128 kt .. at byte (nt * (K/128) + kt) *

@@ -194,3 +194,29 @@ def test_expired_wait_is_reported_and_the_next_call_is_right(M, N, K):
     p.C.fill_(7.0)
     p.run()
     p.check()
+
+
+@pytest.mark.parametrize("M", [2, 40])
+def test_weights_beyond_31_bits_of_bytes(M):
+    N, K = 131072, 16512
+    free, _ = torch.cuda.mem_get_info()
+    if free < 6 * N * K:
+        pytest.skip("not enough memory")
+    g = torch.Generator(device="cuda").manual_seed(M)
+    codes = torch.randint(0, 120, (N, K), dtype=torch.uint8, device="cuda", generator=g)     # up to 240
+    codes[:, 1::2] += 128
+    a_bits, _, _ = problem(M, 128, K)
+    ws = np.exp2(np.random.default_rng(M).uniform(-12, -4, (N // 128, K // 128))).astype(np.float32)
+    W8 = torch.empty(N * K, dtype=torch.uint8, device="cuda")
+    a4w4.a4w4_shuffle_w8_weight(codes, N, K, W8)
+    Ws, A = torch.from_numpy(ws).cuda(), dev_bits(a_bits)
+    work = torch.empty(a4w4.a4w4_gemm_w8a8_workspace_bytes(M, N, K) + 16, dtype=torch.uint8, device="cuda")
+    C = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    a4w4.a4w4_gemm_w8a8(A, M, K, W8, Ws, N, C, work, work.numel())
+    assert a4w4.a4w4_get_device_status() == 0
+    a = mxfp4.bf16_bits_to_f64(a_bits)
+    for n0 in (0, 1015 * 128, 1016 * 128, N - 128):                    # byte 2^31 lies in row tile 1016 of 1024
+        rows = slice(n0, n0 + 128)
+        c, reach = w8a8.gemm(a, w8a8.decode(codes[rows].cpu().numpy()), ws[n0 // 128:n0 // 128 + 1])
+        got = mxfp4.bf16_bits_to_f64(host_bits(C[:, rows].contiguous()))
+        assert np.all(np.abs(got - c) <= w8a8.bound(c, reach, K))
