@@ -15,6 +15,8 @@
 extern "C" {
 #endif
 
+int a4w4_packed_gemm_w8a8(const void* packed);        /* 11 words */
+int a4w4_packed_kv_read(const void* packed);          /* 10 words */
 int a4w4_packed_moe_route(const void* packed);        /* 17 words */
 int a4w4_packed_qk_norm_rope(const void* packed);     /* 20 words */
 int a4w4_packed_kv_append_rope(const void* packed);   /* 24 words */

@@ -86,10 +86,18 @@ DEBUG_SIGNATURES = {
 
 # calls with packed arguments (include/a4w4_binding.h): name -> the format of its words
 PACKED = {
+    "a4w4_packed_gemm_w8a8": struct.Struct("=11q"),
+    "a4w4_packed_kv_read": struct.Struct("=10q"),
     "a4w4_packed_moe_route": struct.Struct("=13qd3q"),
     "a4w4_packed_qk_norm_rope": struct.Struct("=11qd8q"),
     "a4w4_packed_kv_append_rope": struct.Struct("=14qd9q"),
 }
+
+_PACK_GEMM_W8 = PACKED["a4w4_packed_gemm_w8a8"].pack
+_PACK_READ = PACKED["a4w4_packed_kv_read"].pack
+_PACK_ROUTE = PACKED["a4w4_packed_moe_route"].pack
+_PACK_ROPE = PACKED["a4w4_packed_qk_norm_rope"].pack
+_PACK_APPEND = PACKED["a4w4_packed_kv_append_rope"].pack
 
 A4W4_GEMM_WEIGHT_PREFETCH = 1
 A4W4_F32, A4W4_BF16 = 0, 1
@@ -250,8 +258,11 @@ def a4w4_gemm_w8a8_workspace_bytes(M, N, K):
 
 
 def a4w4_gemm_w8a8(A, M, K, W8, Ws, N, C, workspace=None, ws_bytes=0, flags=0, stream=None):
-    _check("a4w4_gemm_w8a8", lib().a4w4_gemm_w8a8(_ptr(A), M, K, _ptr(W8), _ptr(Ws), N, _ptr(C), _ptr(workspace),
-                                                   ws_bytes, flags, _stream(stream)))
+    rc = (_lib or lib()).a4w4_packed_gemm_w8a8(_PACK_GEMM_W8(
+        _ptr(A) or 0, M, K, _ptr(W8) or 0, _ptr(Ws) or 0, N, _ptr(C) or 0, _ptr(workspace) or 0, ws_bytes, flags,
+        _stream(stream) or 0))
+    if rc != 0:
+        raise A4W4Error("a4w4_gemm_w8a8", rc)
 
 
 def a4w4_mxfp4_quant(X, rows, cols, q, scales, stream=None):
@@ -306,11 +317,6 @@ def _heads_ptr(x, stride, D):
     except AttributeError:
         pass
     return _rows_ptr(x, stride) or 0
-
-
-_PACK_ROUTE = PACKED["a4w4_packed_moe_route"].pack
-_PACK_ROPE = PACKED["a4w4_packed_qk_norm_rope"].pack
-_PACK_APPEND = PACKED["a4w4_packed_kv_append_rope"].pack
 
 
 def a4w4_moe_route(logits, logits_type, stride, num_tokens, T, E, score, bias, groups, group_top, top_groups, topk,
@@ -428,8 +434,11 @@ def a4w4_kv_append_rope(q, q_stride, k, k_stride, v, v_stride, positions, slot_m
 
 
 def a4w4_kv_read(cache, num_pages, page_size, slot_map, T, Hkv, D, k_out, v_out, stream=None):
-    _check("a4w4_kv_read", lib().a4w4_kv_read(_ptr(cache), num_pages, page_size, _ptr(slot_map), T, Hkv, D,
-                                              _ptr(k_out), _ptr(v_out), _stream(stream)))
+    rc = (_lib or lib()).a4w4_packed_kv_read(_PACK_READ(
+        _ptr(cache) or 0, num_pages, page_size, _ptr(slot_map) or 0, T, Hkv, D, _ptr(k_out) or 0, _ptr(v_out) or 0,
+        _stream(stream) or 0))
+    if rc != 0:
+        raise A4W4Error("a4w4_kv_read", rc)
 
 
 def a4w4_kv_attention_workspace_bytes(B, max_q, Hq, Hkv, D):

@@ -26,6 +26,20 @@ struct Words {
 
 extern "C" {
 
+int a4w4_packed_gemm_w8a8(const void* packed) {
+  if (packed == nullptr) return A4W4_ERR_ARG;
+  const Words<11> a(packed);
+  return a4w4_gemm_w8a8(a.any(0), a.num(1), a.num(2), a.any(3), a.ptr<const float>(4), a.num(5), a.any(6), a.any(7),
+                        static_cast<size_t>(a.w[8]), static_cast<unsigned int>(a.w[9]), a.any(10));
+}
+
+int a4w4_packed_kv_read(const void* packed) {
+  if (packed == nullptr) return A4W4_ERR_ARG;
+  const Words<10> a(packed);
+  return a4w4_kv_read(a.any(0), a.num(1), a.num(2), a.ptr<const int32_t>(3), a.num(4), a.num(5), a.num(6), a.any(7),
+                      a.any(8), a.any(9));
+}
+
 int a4w4_packed_moe_route(const void* packed) {
   if (packed == nullptr) return A4W4_ERR_ARG;
   const Words<17> a(packed);

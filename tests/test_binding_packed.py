@@ -12,6 +12,8 @@ from mxfp4_a4w4_gemm_gb300 import build as build_mod
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 GOOD = {   # arguments that only the missing device refuses, in the order of include/a4w4.h
+    "a4w4_gemm_w8a8": [16, 2, 256, 16, 16, 256, 16, 0, 0, 0, 0],
+    "a4w4_kv_read": [16, 4, 16, 16, 2, 2, 128, 16, 16, 0],
     "a4w4_moe_route": [16, 0, 64, 16, 2, 64, 1, 16, 8, 2, 4, 8, 1, 2.5, 16, 16, 0],
     "a4w4_qk_norm_rope": [16, 512, 16, 256, 16, 2, 4, 2, 128, 16, 16, 1e-6, 16, 128, 0, 16, 512, 16, 256, 0],
     "a4w4_kv_append_rope": [16, 512, 16, 256, 16, 256, 16, 16, 2, 4, 2, 128, 16, 16, 1e-6, 16, 128, 0, 16, 512, 16, 4, 16, 0],
