@@ -179,7 +179,6 @@ struct RopeArgs {
   // and of keys; bytes of a part's heads
   int split, part_q, part_kv, stage_bytes;
 };
-// -1: more work than it counts.
 int launch_kv_rope(RopeArgs p, int D, cudaStream_t st, int sms);
 
 // 8-bit block-scaled product (w8a8.cu).

@@ -12,6 +12,7 @@
 // Angles: position times frequency as turns, in 64-bit integers modulo one turn
 // (F = f / 2 pi as a 64-bit binary fraction, position * F wraps): exact to 2^-33
 // turns at position 2^31, so that 32 bits are enough for what is left.
+#include <algorithm>
 #include <atomic>
 
 #include "device.cuh"
@@ -618,14 +619,13 @@ int launch_rope_d(const RopeArgs& p, cudaStream_t st, int sms) {
 int launch_kv_rope(RopeArgs p, int D, cudaStream_t st, int sms) {
   const bool cache = p.cache != nullptr;
   const int per = 256 / D, uq = (p.Hq + per - 1) / per, uk = (p.Hkv + per - 1) / per, kinds = cache ? 2 : 1;
-  // parts of a token: what a stage holds; of few tokens so many that there are four blocks on
-  // every SM, with a unit for each warp
+  // parts of a token: what a stage holds (69 at most: 4096 heads); of few tokens so many that there
+  // are four blocks on every SM, with a unit for each warp, but no more than SMs
   int split = 1;
   const auto units = [&](int n) { return (uq + n - 1) / n + kinds * ((uk + n - 1) / n); };
   while (units(split) > kRopeUnits) ++split;
-  const long long want = (4ll * sms + p.T - 1) / p.T;
+  const long long want = std::min<long long>((4ll * sms + p.T - 1) / p.T, sms);
   while (split < want && units(split) > kRopeWarps) ++split;
-  if (split > sms) return -1;
   p.split = split;
   p.part_q = (uq + split - 1) / split;
   p.part_kv = (uk + split - 1) / split;

@@ -329,3 +329,47 @@ def test_the_call_after_an_expired_wait_is_right():
     h.run(q, k)
     h.check("q", q)
     h.check("k", k)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,cached", [(2, 4094, 1, 128, False), (1, 0, 2048, 64, False), (2, 2048, 1024, 128, True), (3, 0, 2048, 64, True)])
+def test_as_many_heads_as_there_may_be(T, Hq, Hkv, D, cached):
+    h = Heads(T, Hq, Hkv, D, D, 0)
+    if cached:
+        c = Cache(h, 16, *scattered(T, 16))
+        c.run()
+        c.check()
+        return
+    q, k = h.outputs()
+    h.run(q, k)
+    for which, out in (("q", q), ("k", k)):
+        if out.numel():
+            h.check(which, out)
+
+
+def test_append_with_the_queries_in_place():
+    h = Heads(40, 6, 2, 128, 128, 0)
+    c = Cache(h, 16, *scattered(40, 16, skip=((5, -1),)))
+    before = h.x.clone()
+    c.q = h.part(h.x, "q")
+    d = h.dev
+    a4w4.a4w4_kv_append_rope(c.q, h.stride, h.part(h.x, "k"), h.stride, h.part(h.x, "v"), h.stride, d["pos"], c.map, 40, 6, 2, 128,
+                             d["wq"], d["wk"], EPS, d["freq"], 128, 0, c.q, h.stride, c.cache, c.pages, 16)
+    assert torch.equal(h.x[5], before[5]) and torch.equal(h.x[:, 6:], before[:, 6:])
+    c.q = c.q.clone()
+    c.q[5] = 7.0
+    c.check()
+
+
+def test_one_slot_given_to_two_tokens():
+    h = Heads(6, 1, 2, 64, 64, 0)
+    slots, pages = scattered(6, 16)
+    slots[4] = slots[1]
+    cells = []
+    for drop in (None, 1, 4):                                       # both; the one token alone; the other
+        s = slots.copy()
+        if drop is not None:
+            s[drop] = -1
+        c = Cache(h, 16, s, pages)
+        c.run()
+        cells.append(c.cache)
+    assert torch.all((cells[0] == cells[1]) | (cells[0] == cells[2]))
