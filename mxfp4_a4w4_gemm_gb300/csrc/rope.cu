@@ -272,7 +272,7 @@ struct RopeCells {
   // 2^-21.5 of itself, sine and cosine to 2^-21.8 of themselves, the weight's product, the two
   // products, their sum and the last product a rounding each: in all within 2^-20.2 of
   // r (|A x| + |B y|); without norm or rotation o is x.  Where that leaves a code or the scale
-  // open, 64 bits decide (some 5 codes of a million).
+  // open, 64 bits decide (some 5 codes of a million).  (A NaN has no part in the scale, as in a4w4_kv_append.)
   __device__ __forceinline__ void key_cell(const RopeCoef<D>& coef, const float* weight, const unsigned long long* turns,
                                            const uint4& v, int n, int slot, int position) const {
     using Ch = KvChunk<D>;
@@ -285,8 +285,8 @@ struct RopeCells {
     float least = 0.f, most = 0.f;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      // (tiny values lose more, zeros nothing)
-      off[u] = off[u] > 0.f ? fmaf(off[u], rel, rel > 0.f ? 0x1p-147f : 0.f) : 0.f;
+      // (tiny values lose more, zeros and what nothing is computed of nothing)
+      off[u] = off[u] > 0.f && rel > 0.f ? fmaf(off[u], rel, 0x1p-147f) : 0.f;
       least = fmaxf(least, fabsf(o[u]) - off[u]);
       most = fmaxf(most, fabsf(o[u]) + off[u]);
     }

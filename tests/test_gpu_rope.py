@@ -373,3 +373,29 @@ def test_one_slot_given_to_two_tokens():
         c.run()
         cells.append(c.cache)
     assert torch.all((cells[0] == cells[1]) | (cells[0] == cells[2]))
+
+
+def test_infinities_and_nan_in_keys_and_values():
+    # as a4w4_kv_append has them where nothing is computed on the way; with a norm and a rotation they stay in their heads
+    h = Heads(40, 2, 3, 128, 0, 0, "")
+    rng = np.random.default_rng(3)
+    for pattern in (0x7F80, 0xFF80, 0x7FC0, 0xFFC1, 0x7F7F):
+        h.bits[rng.integers(0, 40, 5), rng.integers(2, 8, 5), rng.integers(0, 128, 5)] = pattern
+    h.load()
+    c = Cache(h, 16, *scattered(40, 16))
+    c.run()
+    other = torch.full_like(c.cache, 0xA5)
+    a4w4.a4w4_kv_append(h.part(h.x, "k"), h.stride, h.part(h.x, "v"), h.stride, c.map, 40, 3, 128, other, c.pages, 16)
+    assert torch.equal(c.cache, other)
+    h = Heads(40, 2, 3, 128, 128, 0)
+    c = Cache(h, 16, *scattered(40, 16))
+    c.run()
+    clean = c.cache.clone().view(c.pages, 3, -1)
+    c.check()
+    h.bits[:, 3, 17], h.bits[::2, 3, 100] = 0x7F80, 0x7FC0          # the middle one of the heads of keys
+    h.load()
+    c.cache.fill_(0xA5)
+    c.run()
+    assert a4w4.a4w4_get_device_status() == 0
+    got = c.cache.view(c.pages, 3, -1)
+    assert torch.equal(got[:, 0], clean[:, 0]) and torch.equal(got[:, 2], clean[:, 2])
