@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2 * Cf::RING; ++s) mbar_init(full_w + 8u * s, 1);    // full_w, empty
-    for (int s = 0; s < 3 * Cf::RING; ++s) mbar_init(full_x + 8u * s, 32);   // full_x, scales: a producer warp
+    for (int s = 0; s < 3 * Cf::RING; ++s) mbar_init(full_x + 8u * s, 64);   // full_x, scales: two warps, or one twice
     mbar_init(acc_full, 1);
     mbar_init(acc_full + 8u, 1);
     mbar_init(acc_empty, 4);
@@ -705,22 +705,27 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
   } else {
     griddep_wait();                                    // A is written by the previous grid
     int ready = nk > 0;
-    if (warp < 6) {
-      // ---------------- activations ----------------
+    // ---------------- activations ----------------
+    // Warps 2-5 take every fourth block of K; the promoters, with nothing to add yet, take half of the
+    // rows of the first RING blocks.
+    {
       constexpr int CH = 4;                            // rows in flight per eight lanes
-      const int c = lane & 7;
+      const bool helper = warp >= 6;
+      const int c = lane & 7, half = (mvalid + 7) / 8 * 4;
       float* s_scale = reinterpret_cast<float*>(smem + Cf::OFF_SCALE);
       bool stop = false;
-      for (int i = warp - 2; i < nk && !stop; i += 4) {
+      for (int i = (warp - 2) & 3; i < nk && !stop; i += 4) {
         const int s = i % Cf::RING, turn = i % (2 * Cf::RING);
-        bool waited = i < Cf::RING;
-        for (int r0 = 0; r0 < mvalid; r0 += 4 * CH) {
+        const bool shared = i < Cf::RING;
+        const int end = shared && !helper ? min(half, mvalid) : mvalid;
+        bool waited = shared;
+        for (int r0 = helper ? half : 0; r0 < end; r0 += 4 * CH) {
           uint4 v[CH][2];
 #pragma unroll
           for (int h = 0; h < CH; ++h) {
             const int r = r0 + 4 * h + (lane >> 3);
             v[h][0] = v[h][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < mvalid) {
+            if (r < end) {
               const uint16_t* src = p.A + static_cast<long long>(m0 + r) * p.K + (kt0 + i) * 128 + c * 16;
               v[h][0] = ld_global_nc_v4(src);
               v[h][1] = ld_global_nc_v4(src + 8);
@@ -735,10 +740,11 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
           }
 #pragma unroll
           for (int h = 0; h < CH; ++h) {
+            if (r0 + 4 * h >= end) break;
             const int r = r0 + 4 * h + (lane >> 3);
             float scale;
             const uint4 code = quant128(v[h][0], v[h][1], &scale);
-            if (r < mvalid) {
+            if (r < end) {
               *reinterpret_cast<uint4*>(smem + Cf::OFF_X + s * Cf::X_STAGE + tile_piece(r, c)) = code;
               if (c == 0) s_scale[turn * NX + r] = scale;
             }
@@ -746,12 +752,14 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
         }
         if (!stop) {
           fence_proxy_async_smem();
-          mbar_arrive(full_x + 8u * s);
-          mbar_arrive(scales + 8u * turn);
+          mbar_arrive_n(full_x + 8u * s, shared ? 1 : 2);
+          mbar_arrive_n(scales + 8u * turn, shared ? 1 : 2);
         }
+        if (helper) break;
       }
       ready = ready && !stop;
-    } else {
+    }
+    if (warp >= 6) {
       // ---------------- promotion ----------------
       const int q = warp & 3;
       const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
