@@ -579,6 +579,7 @@ struct W8SmallArgs {
 template <int NX>
 struct W8S {
   static constexpr int RING = 4;                       // tiles in flight, of weights and of activations
+  static constexpr int ACCS = 4;                       // accumulators
   static constexpr int THREADS = 64 + 128 + 128;       // two single warps, producers, promoters
   static constexpr int X_STAGE = NX * 128;
   static constexpr int OFF_X = RING * kTile;
@@ -587,17 +588,18 @@ struct W8S {
   // this block's own sums are staged over the drained weight ring
   static constexpr int OFF_PUSH = OFF_SCALE + 2 * RING * NX * 4;
   static constexpr int OFF_BAR = OFF_PUSH + NX * 512 + 256;
-  static constexpr int NBAR = 5 * RING + 6;            // full_w, empty, full_x, scales x 2; accumulators' full and empty; red; drain
+  static constexpr int NBAR = 5 * RING + 2 * ACCS + 2; // full_w, empty, full_x, scales x 2; accumulators' full and empty; red; drain
   static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
   static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;
   static constexpr int ACC_COLS = NX;
-  static constexpr int TMEM_COLS = 2 * NX;
+  static constexpr int TMEM_COLS = ACCS * NX;
+  static_assert(ACCS <= RING, "a scale's place is written again after its block was added");
   static_assert(NX * 512 <= RING * kTile, "the sums fit the weight ring");
   static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "two thread blocks on an SM");
 };
 
 //   warp 0      weight producer;
-//   warp 1      TMEM owner and MMA issuer (two accumulators of NX columns in turn);
+//   warp 1      TMEM owner and MMA issuer (accumulators of NX columns in turn);
 //   warps 2-5   activations: every fourth block of K each, eight lanes a row, into the ring's place
 //               for it; scales have places for two turns of the ring, since they are read after
 //               the MMAs that free the codes';
@@ -621,8 +623,8 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
 
   const uint32_t full_w = base + Cf::OFF_BAR, empty = full_w + 8u * Cf::RING;
   const uint32_t full_x = empty + 8u * Cf::RING, scales = full_x + 8u * Cf::RING;
-  const uint32_t acc_full = scales + 16u * Cf::RING, acc_empty = acc_full + 16u;
-  const uint32_t red_bar = acc_empty + 16u, drain = red_bar + 8u;
+  const uint32_t acc_full = scales + 16u * Cf::RING, acc_empty = acc_full + 8u * Cf::ACCS;
+  const uint32_t red_bar = acc_empty + 8u * Cf::ACCS, drain = red_bar + 8u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cf::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cf::OFF_MISC + 8);
   volatile int* never = reinterpret_cast<volatile int*>(smem + Cf::OFF_MISC + 16);
@@ -631,10 +633,10 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2 * Cf::RING; ++s) mbar_init(full_w + 8u * s, 1);    // full_w, empty
     for (int s = 0; s < 3 * Cf::RING; ++s) mbar_init(full_x + 8u * s, 64);   // full_x, scales: two warps, or one twice
-    mbar_init(acc_full, 1);
-    mbar_init(acc_full + 8u, 1);
-    mbar_init(acc_empty, 4);
-    mbar_init(acc_empty + 8u, 4);
+    for (int s = 0; s < Cf::ACCS; ++s) {
+      mbar_init(acc_full + 8u * s, 1);
+      mbar_init(acc_empty + 8u * s, 4);
+    }
     mbar_init(red_bar, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -685,9 +687,9 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
       const uint32_t idesc = idesc_e4m3(NX);
       bool ok = true;
       for (int i = 0; i < nk && ok; ++i) {
-        const int s = i % Cf::RING, b = i & 1;
+        const int s = i % Cf::RING, b = i % Cf::ACCS;
         ok = mbar_wait(full_x + 8u * s, static_cast<uint32_t>(i / Cf::RING) & 1u, abort_flag, p.wait_ns, p.status);
-        ok = ok && (i < 2 || mbar_wait(acc_empty + 8u * b, static_cast<uint32_t>((i >> 1) - 1) & 1u, abort_flag, p.wait_ns, p.status));
+        ok = ok && (i < Cf::ACCS || mbar_wait(acc_empty + 8u * b, static_cast<uint32_t>(i / Cf::ACCS - 1) & 1u, abort_flag, p.wait_ns, p.status));
         ok = ok && mbar_wait(full_w + 8u * s, (i / Cf::RING) & 1u, abort_flag, p.wait_ns, p.status);
         if (!ok) break;
         tc_fence_after();
@@ -768,11 +770,11 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
 #pragma unroll
       for (int i = 0; i < NX / 2; ++i) acc[i] = 0ull;
       for (int i = 0; i < nk; ++i) {
-        const int turn = i % (2 * Cf::RING), b = i & 1;
+        const int turn = i % (2 * Cf::RING), b = i % Cf::ACCS;
         const uint32_t sw = __float_as_uint(block_scale[i]);
         const unsigned long long sw2 = pack2(sw, sw);
         const bool ok = mbar_wait(scales + 8u * turn, static_cast<uint32_t>(i / (2 * Cf::RING)) & 1u, abort_flag, p.wait_ns, p.status) &&
-                        mbar_wait(acc_full + 8u * b, static_cast<uint32_t>(i >> 1) & 1u, abort_flag, p.wait_ns, p.status);
+                        mbar_wait(acc_full + 8u * b, static_cast<uint32_t>(i / Cf::ACCS) & 1u, abort_flag, p.wait_ns, p.status);
         if (!__all_sync(0xFFFFFFFFu, ok)) {
           ready = 0;
           break;
