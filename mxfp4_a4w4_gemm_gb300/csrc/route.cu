@@ -10,9 +10,9 @@
 //
 // Every loop over the row is short in code: with the keys in registers, and so the
 // loops written out, a third of the time went to fetching instructions.  4096 x 896
-// experts, sigmoid with a bias, 16 of them chosen: 12.8 us (1.2 TB/s; what bounds it is
+// experts, sigmoid with a bias, 16 of them chosen: 12.2 us (1.2 TB/s; what bounds it is
 // the instructions on each logit and the chain of steps after a row's last one, not
-// memory); 1000 x 256 in 8 groups 5.6; one token of 896 3.5, most of it the latency of
+// memory); 1000 x 256 in 8 groups 4.7; one token of 896 3.2, most of it the latency of
 // a launch and of that chain.
 //
 // Choosing as exact scores would: score + bias is known to about 2^-20 of the
@@ -59,7 +59,7 @@ __device__ __forceinline__ float bias_of(const RouteArgs& p, int e) { return cle
 // To 2^-21.7 of itself (weights: chosen experts only).
 __device__ __forceinline__ float sigmoid(float x) {
   // exp of what is not positive: no overflow, and small scores keep their bits
-  const float z = expf(-fabsf(x)), r = __frcp_rn(1.f + z);
+  const float z = expf(-fabsf(x)), r = __fdividef(1.f, 1.f + z);
   return x >= 0.f ? r : z * r;
 }
 // The same in fewer instructions, to 2^-21.7 and |x| 2^-23.4 of itself where x < 0: for comparing.
@@ -71,11 +71,8 @@ __device__ __forceinline__ float sigmoid_near(float x) {
 }
 __device__ __forceinline__ double sigmoid_64(double x) { return 1.0 / (1.0 + exp(-x)); }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-  return v;
-}
+// (of no NaN)
+__device__ __forceinline__ float warp_max(float v) { return from_ordered(__reduce_max_sync(kAll, ordered(v))); }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
@@ -398,7 +395,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8) moe_route_kernel(const Ro
       most = max(max(most, max(k.x, k.y)), max(k.z, k.w));
     }
   } else if (by_score || by_sum) {
-    margin = sigmoid(top) * (0x1p-19f + fmaxf(-top, 0.f) * 0x1p-21f);
+    margin = sigmoid_near(top) * (0x1p-19f + fmaxf(-top, 0.f) * 0x1p-21f);
     if (top >= 0.f) margin *= 0.5f;
     if (top == -INFINITY) margin = 0.f;
   }
@@ -564,11 +561,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8) moe_route_kernel(const Ro
       if (p.softmax) {
         w = expf(xi - m);
       } else {
-        const float base = fminf(m, 0.f);
-        w = xi >= 0.f ? sigmoid(xi) : expf(xi - base) / (1.f + expf(xi));
+        w = m >= 0.f ? sigmoid(xi) : __fdividef(expf(xi - m), 1.f + expf(xi));
       }
       w = mine ? w : 0.f;
-      w /= warp_sum(w);
+      w = __fdividef(w, warp_sum(w));
     }
   } else {
     w = p.softmax ? expf(xi - top) * inv : sigmoid(xi);
