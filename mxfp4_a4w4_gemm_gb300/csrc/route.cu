@@ -10,9 +10,9 @@
 //
 // Every loop over the row is short in code: with the keys in registers, and so the
 // loops written out, a third of the time went to fetching instructions.  4096 x 896
-// experts, sigmoid with a bias, 16 of them chosen: 12.2 us (1.2 TB/s; what bounds it is
+// experts, sigmoid with a bias, 16 of them chosen: 12.0 us (1.2 TB/s; what bounds it is
 // the instructions on each logit and the chain of steps after a row's last one, not
-// memory); 1000 x 256 in 8 groups 4.7; one token of 896 3.2, most of it the latency of
+// memory); 1000 x 256 in 8 groups 4.6; one token of 896 3.3, most of it the latency of
 // a launch and of that chain.
 //
 // Choosing as exact scores would: score + bias is known to about 2^-20 of the
@@ -170,26 +170,15 @@ __device__ __forceinline__ Real strength_of(const RouteArgs& p, Real a, Real b) 
 }
 
 // Groups whose strength is among the p.top_groups best (ties: the lower index),
-// as a mask; lane g < groups holds group g's strength.  *near: a kept and a
-// dropped group lie within `margin` of each other.
+// as a mask; lane g < groups holds group g's strength.
 template <typename Real>
-__device__ __forceinline__ uint32_t best_groups(const RouteArgs& p, Real mine, int lane, Real margin, bool* near) {
+__device__ __forceinline__ uint32_t best_groups(const RouteArgs& p, Real mine, int lane) {
   int rank = 0;
   for (int g = 0; g < p.groups; ++g) {
     const Real other = __shfl_sync(kAll, mine, g);
     rank += other > mine || (other == mine && g < lane);
   }
-  const bool in = lane < p.groups, kept = in && rank < p.top_groups;
-  const uint32_t mask = __ballot_sync(kAll, kept);
-  if (near != nullptr) {
-    bool close = false;
-    for (int g = 0; g < p.groups; ++g) {
-      const Real other = __shfl_sync(kAll, mine, g);
-      close |= kept && (mask >> g & 1u) == 0u && !(mine - other > margin);
-    }
-    *near = __any_sync(kAll, close);
-  }
-  return mask;
+  return __ballot_sync(kAll, lane < p.groups && rank < p.top_groups);
 }
 
 // The whole choice in 64 bits.  Lane r < topk gets the r-th expert.  For what the rest leaves
@@ -235,7 +224,7 @@ __device__ __noinline__ int route_in_64(const RouteArgs& p, int t, int lane) {
       }
       if (lane == g) mine = strength_of(p, a, b);
     }
-    const uint32_t kept = best_groups<double>(p, mine, lane, 0.0, nullptr);
+    const uint32_t kept = best_groups<double>(p, mine, lane);
     for (int i = 0; i < n; ++i)
       if ((kept >> ((lane + 32 * i) / per) & 1u) == 0u) c[i] = NAN;
   }
@@ -429,7 +418,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8) moe_route_kernel(const Ro
     // logits are compared as they are; of a sum of two the error is twice a score's and the roundings of c and of the sum
     float largest = fmaxf(fabsf(a), p.group_top == 2 ? fabsf(b) : 0.f);
     largest = warp_max(largest < INFINITY ? largest : 0.f);
-    const uint32_t kept = best_groups<float>(p, strength, lane, 2.f * margin + largest * 0x1p-21f, by_sum ? &in_64 : nullptr);
+    const uint32_t kept = best_groups<float>(p, strength, lane);
+    if (by_sum && p.top_groups < p.groups) {          // do the weakest kept and the strongest dropped group lie too near?
+      const bool in = lane < p.groups, mine = kept >> lane & 1u;
+      const float least = from_ordered(__reduce_min_sync(kAll, mine ? ordered(strength + 0.f) : kAll));
+      const float next = from_ordered(__reduce_max_sync(kAll, in && !mine ? ordered(strength + 0.f) : 0u));
+      in_64 = !(least - next > 2.f * margin + largest * 0x1p-21f);
+    }
     most = 0u;
     for (int q = lane; 4 * q < E; q += 32) {
       uint4 k = quad[q];
