@@ -155,8 +155,8 @@ int a4w4_prepare_w8_weight(const void* W_bf16, int N, int K, void* W8, float* Ws
 int a4w4_shuffle_w8_weight(const void* W_e4m3, int N, int K, void* W8, void* stream);
 /* M > 32 may quantise the activations once into tiles in `workspace` (at least
  * a4w4_gemm_w8a8_workspace_bytes(M, N, K), which grows with M; 16-byte aligned,
- * overwritten before it is read); where that size is 0 it may be NULL.  flags: A4W4_GEMM_WEIGHT_PREFETCH as for
- * a4w4_gemm_ex (of W8 alone). */
+ * overwritten before it is read); where that size is 0 it may be NULL.  flags:
+ * A4W4_GEMM_WEIGHT_PREFETCH as for a4w4_gemm_ex (of W8 alone). */
 size_t a4w4_gemm_w8a8_workspace_bytes(int M, int N, int K);
 int a4w4_gemm_w8a8(const void* A_bf16, int M, int K, const void* W8, const float* Ws, int N, void* C_bf16,
                    void* workspace, size_t ws_bytes, unsigned int flags, void* stream);
