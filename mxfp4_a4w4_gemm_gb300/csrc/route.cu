@@ -305,6 +305,25 @@ __device__ __forceinline__ uint4 four_keys(float4 c, int e, int E) {
 }
 __device__ __forceinline__ float4 four_sums(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
 
+// Two candidates a >= b, by the upper words of their keys: may their exact scores lie the other way around?
+// (Infinite ones, of a bias, are equal.)
+__device__ __forceinline__ bool scores_near(unsigned long long a, unsigned long long b, float margin) {
+  const float va = from_ordered(static_cast<uint32_t>(a >> 32)), vb = from_ordered(static_cast<uint32_t>(b >> 32));
+  return !(va - vb > margin + fmaxf(fabsf(va), fabsf(vb)) * 0x1p-22f) && (va != vb || fabsf(va) < INFINITY);
+}
+// The same of sums of two floats.
+__device__ __forceinline__ bool sums_near(unsigned long long a, unsigned long long b, float margin) {
+  const float ah = from_ordered(static_cast<uint32_t>(a >> 32)), bh = from_ordered(static_cast<uint32_t>(b >> 32));
+  const float gap = (ah - bh) + (from_ordered(static_cast<uint32_t>(a)) - from_ordered(static_cast<uint32_t>(b)));
+  const float open = (margin + fmaxf(fabsf(ah), fabsf(bh)) * 0x1p-22f) * 0x1p-20f;
+  return !(gap > open) && (ah != bh || fabsf(ah) < INFINITY);
+}
+// Do experts a and b have the same score, whatever its last bits?
+template <bool BF16>
+__device__ __forceinline__ bool same_inputs(const RouteArgs& p, int t, int a, int b) {
+  return logit<BF16>(p, t, a) == logit<BF16>(p, t, b) && bias_of(p, a) == bias_of(p, b);
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(32 * kRouteWarps, 8) moe_route_kernel(const RouteArgs p) {
   __shared__ alignas(16) unsigned long long s_key[kRouteWarps][kCand + 4];
@@ -486,16 +505,26 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8) moe_route_kernel(const Ro
       const unsigned long long c = best[lane < n && lane < topk ? lane : 0];
       id = static_cast<int>(kAll - static_cast<uint32_t>(c));
       xi = by_score ? logit<BF16>(p, t, id) : from_ordered(static_cast<uint32_t>(c >> 32));
-      bool near = false;
+      bool near = false, twin = false;
       if (by_score && lane < topk && lane + 1 < n) {
         const unsigned long long d = best[lane + 1];
-        const float vc = from_ordered(static_cast<uint32_t>(c >> 32)), vd = from_ordered(static_cast<uint32_t>(d >> 32));
-        if (!(vc - vd > margin + fmaxf(fabsf(vc), fabsf(vd)) * 0x1p-22f) && (vc != vd || fabsf(vc) < INFINITY)) {
-          const int other = static_cast<int>(kAll - static_cast<uint32_t>(d));
-          near = xi != logit<BF16>(p, t, other) || bias_of(p, id) != bias_of(p, other);
+        if (scores_near(c, d, margin)) {
+          near = !same_inputs<BF16>(p, t, id, static_cast<int>(kAll - static_cast<uint32_t>(d)));
+          twin = !near && lane + 1 == topk;
         }
       }
-      if (__any_sync(kAll, near)) {
+      bool open = __any_sync(kAll, near || twin);
+      if (open && __any_sync(kAll, twin)) {
+        // The last one chosen and the first one left have the same inputs: behind them may lie others,
+        // as near, whose inputs differ.
+        const unsigned long long last = best[topk - 1];
+        const int e = static_cast<int>(kAll - static_cast<uint32_t>(last));
+        for (int i = lane; i < n; i += 32)
+          near |= cand[i] < last && scores_near(last, cand[i], margin) &&
+                  !same_inputs<BF16>(p, t, e, static_cast<int>(kAll - static_cast<uint32_t>(cand[i])));
+        open = __any_sync(kAll, near);
+      }
+      if (open) {
         Pair share = {1.f, 0.f};                      // a softmax's 1 / sum
         if (p.softmax) {
           Pair sum = {0.f, 0.f};
@@ -525,15 +554,22 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 8) moe_route_kernel(const Ro
         const int i = static_cast<int>(best[lane < topk ? lane : 0]);
         id = s_at[warp][i];
         xi = logit<BF16>(p, t, id);
-        near = false;
+        near = twin = false;
         if (lane < topk && lane + 1 < n) {
-          const int j = static_cast<int>(best[lane + 1]), other = s_at[warp][j];
-          const unsigned long long v = cand[i], w = cand[j];
-          const float vh = from_ordered(static_cast<uint32_t>(v >> 32)), wh = from_ordered(static_cast<uint32_t>(w >> 32));
-          const float gap = (vh - wh) + (from_ordered(static_cast<uint32_t>(v)) - from_ordered(static_cast<uint32_t>(w)));
-          const float open = (margin + fmaxf(fabsf(vh), fabsf(wh)) * 0x1p-22f) * 0x1p-20f;
-          near = !(gap > open) && (vh != wh || fabsf(vh) < INFINITY) &&
-                 (xi != logit<BF16>(p, t, other) || bias_of(p, id) != bias_of(p, other));
+          const int j = static_cast<int>(best[lane + 1]);
+          if (sums_near(cand[i], cand[j], margin)) {
+            near = !same_inputs<BF16>(p, t, id, s_at[warp][j]);
+            twin = !near && lane + 1 == topk;
+          }
+        }
+        if (__any_sync(kAll, twin)) {
+          const int l = static_cast<int>(best[topk - 1]), e = s_at[warp][l];
+          const unsigned long long last = cand[l];
+          for (int j = lane; j < n; j += 32) {
+            const int other = s_at[warp][j];
+            near |= (cand[j] < last || (cand[j] == last && other > e)) && sums_near(last, cand[j], margin) &&
+                    !same_inputs<BF16>(p, t, e, other);
+          }
         }
         in_64 = __any_sync(kAll, near);
       }
