@@ -225,7 +225,8 @@ int a4w4_moe_sort(const int32_t* topk_ids, int T, int topk, int E, int block_m,
  * of group strengths: some 1% of rows), then 64 bits.  A NaN logit counts as -infinity, a
  * logit of +infinity as the largest float, a NaN bias as -infinity; a row whose logits
  * are all -infinity has scores 0, and weights whose sum is 0 are 0.  The weights are
- * fp32 to about 2^-21.
+ * fp32, each within 2^-18.7 of itself (some 2^-21 in practice) however far the logits
+ * lie apart, above 2^-126.
  * 1 <= E <= 2048, groups <= 32, E % groups == 0, two experts to a group at least
  * where there are several, 1 <= topk <= 32, topk <= top_groups * E / groups, scale
  * finite, T >= 0, T * topk <= 2^30. */

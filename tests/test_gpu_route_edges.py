@@ -1,5 +1,5 @@
 """The choice of experts at its edge, where candidates with the same inputs hide others that fp32 (or sums of two floats)
-cannot tell from them: against the oracle."""
+cannot tell from them, and the weights of experts far from the largest logit: against the oracle."""
 
 import numpy as np
 import pytest
@@ -72,3 +72,27 @@ def test_equal_experts_before_one_that_sums_of_two_floats_cannot_tell():
     assert all(route.route(logits[j], False, bias, 1, 1, 1, 1, True, 1.0)[0] == [3 * j + 2] for j in range(n))
     Router(logits, False, bias, topk=1).go()
     Router(logits, False, bias, topk=2).go()
+
+
+@pytest.mark.parametrize("softmax,renorm", [(False, True), (True, True), (True, False), (False, False)])
+def test_weights_of_experts_far_below_the_largest(softmax, renorm):
+    # In 2^-24: an exponential 4 (two units in the last place) and 1 for its argument's remainder, however far the logits
+    # lie apart.  Softmax: that, the same of the chosen ones' sum and its 5 additions, the quotient 4, the scale 1: 20; not
+    # renormalised the row's 23 additions, its terms' 4 and rounded arguments (distances weighted by their exponentials: 4)
+    # instead, 1 / sum and a product: 38.  Sigmoid below 0: 5, the denominator 3, the quotient 4, in the sum again: 34.
+    rng = np.random.default_rng(7)
+    x = (rng.uniform(-45.0, 40.0, (200, 48)) - (50.0 if not softmax else 0.0)).astype(np.float32)
+    bias = np.full(48, -10.0, np.float32)
+    bias[rng.permutation(48)[:10]] = 10.0                           # the bias chooses, so that the chosen lie far apart
+    r = Router(x, softmax, bias, topk=8, renorm=renorm)
+    r.run()
+    assert a4w4.a4w4_get_device_status() == 0
+    w = r.w.cpu().numpy().astype(np.float64)
+    tol = (38 if not renorm else 20) * 2.0 ** -24 if softmax else 34 * 2.0 ** -24
+    worst = 0.0
+    for t in range(200):
+        ids, want = route.route(r.x[t], softmax, r.bias, 1, 1, 1, 8, renorm, r.scale)
+        assert r.ids[t].tolist() == ids
+        assert np.all(np.abs(w[t] - want) <= tol * want + 2.0 ** -126), (t, w[t] / want - 1.0)
+        worst = max(worst, np.max(np.where(want > 2.0 ** -100, np.abs(w[t] - want) / want, 0.0)))
+    assert worst > 0.0
