@@ -436,7 +436,8 @@ int a4w4_kv_append(const void* k_bf16, long long k_stride, const void* v_bf16, l
  * T > 1; all may be slices of one fused projection).  A result may take the place of
  * its input (the same address and stride); else they must not overlap.
  *   positions [T] int32; inv_freq [rot_dim / 2] float, finite, below 2^24 in
- *   magnitude.  Angles are reduced exactly (to 2^-33 turns) before they are rounded.
+ *   magnitude.  Angles are those of exact products to 2^-63 turns, reduced before they
+ *   are rounded, so that sines and cosines near zero keep their bits.
  * D 64 or 128, rot_dim a multiple of 16, 0 (norms only; positions and inv_freq may be
  * NULL) to D; Hq, Hkv >= 0 (0: no such heads, its pointers may be NULL),
  * Hq + 2 Hkv <= 4096; eps finite and > 0 where there is a norm; T >= 0. */

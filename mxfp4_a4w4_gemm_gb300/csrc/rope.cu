@@ -10,8 +10,9 @@
 // memory, while its heads are on their way to registers.
 //
 // Angles: position times frequency as turns, in 64-bit integers modulo one turn
-// (F = f / 2 pi as a 64-bit binary fraction, position * F wraps): exact to 2^-33
-// turns at position 2^31, so that 32 bits are enough for what is left.
+// (F = f / 2 pi as a 96-bit binary fraction, position * F wraps): within 2^-63 turns at
+// any position.  Quarter turns are taken off in integers, so that what is left keeps
+// its bits wherever a sine or cosine comes near zero.
 #include <algorithm>
 #include <atomic>
 
@@ -33,13 +34,24 @@ constexpr int kRopeBatch = 4;          // units whose norms go through one reduc
 constexpr int kRopeUnits = 32;         // of a part of a token: 16 KB a stage
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
-// f / (2 pi) modulo 1 as a 64-bit binary fraction: the 24-bit significand times
-// 128 binary places of 1 / (2 pi) (a quarter of the first 130 of 2 / pi).
-__device__ __forceinline__ unsigned long long turns_per_position(float f) {
+// A frequency in turns per position, modulo 1: hi 2^-64 + lo 2^-96.
+struct Turns {
+  unsigned long long hi;
+  uint32_t lo;
+  // position times it, in units of 2^-64 turns (cut by 1.5 of them at most)
+  __device__ __forceinline__ unsigned long long at(int position) const {
+    const long long t = position;
+    return static_cast<unsigned long long>(t) * hi + static_cast<unsigned long long>(t * static_cast<long long>(lo) >> 32);
+  }
+};
+
+// f / (2 pi) modulo 1: the 24-bit significand times 128 binary places of 1 / (2 pi) (a quarter
+// of the first 130 of 2 / pi).
+__device__ __forceinline__ Turns turns_per_position(float f) {
   constexpr unsigned long long kHi = 0x28BE60DB9391054Aull, kLo = 0x7F09D5F47D4D3770ull;
   const uint32_t b = __float_as_uint(f), ex = b >> 23 & 255u;
   const unsigned long long m = (b & 0x7FFFFFu) | (ex ? 0x800000u : 0u);
-  const int sh = static_cast<int>(ex ? ex : 1u) - 150;               // f = m 2^sh
+  const int down = max(150 - static_cast<int>(ex ? ex : 1u), 0);     // f = m 2^-down, below 2^24
   // m (kHi : kLo), 152 bits
   const unsigned long long p0 = m * kLo;
   unsigned long long p1 = m * kHi;
@@ -47,14 +59,36 @@ __device__ __forceinline__ unsigned long long turns_per_position(float f) {
   unsigned long long p2 = __umul64hi(m, kHi);
   p1 += c;
   p2 += p1 < c;
-  unsigned long long F;
-  if (sh <= -128) F = 0ull;
-  else if (sh <= -64) F = p2 >> (-sh - 64);
-  else if (sh < 0) F = p1 >> -sh | p2 << (64 + sh);
-  else if (sh == 0) F = p1;
-  else if (sh < 64) F = p1 << sh | p0 >> (64 - sh);
-  else F = sh < 128 ? p0 << (sh - 64) : 0ull;
-  return b >> 31 ? 0ull - F : F;
+  // shifted down, whole words first
+  const int words = down >> 6, bits = down & 63;
+  const unsigned long long w0 = words == 0 ? p0 : words == 1 ? p1 : words == 2 ? p2 : 0ull;
+  const unsigned long long w1 = words == 0 ? p1 : words == 1 ? p2 : 0ull, w2 = words == 0 ? p2 : 0ull;
+  unsigned long long hi = w1 >> bits | (w2 << 1) << (63 - bits);
+  uint32_t lo = static_cast<uint32_t>((w0 >> bits | (w1 << 1) << (63 - bits)) >> 32);
+  if (b >> 31) {
+    lo = 0u - lo;
+    hi = ~hi + (lo == 0u);
+  }
+  return {hi, lo};
+}
+
+// An angle less its nearest quarter turns: an eighth of a turn at most, in units of 2^-64 turns.
+__device__ __forceinline__ long long off_quarter(unsigned long long turn, uint32_t* quarters) {
+  *quarters = static_cast<uint32_t>((turn + (1ull << 61)) >> 62);
+  return static_cast<long long>(turn - (static_cast<unsigned long long>(*quarters) << 62));
+}
+// Sine and cosine of an angle so many quarter turns further.
+template <typename Real>
+__device__ __forceinline__ void turn_quarters(uint32_t quarters, Real* s, Real* c) {
+  const Real s0 = *s, c0 = *c;
+  if (quarters & 1u) {
+    *s = c0;
+    *c = -s0;
+  }
+  if (quarters & 2u) {
+    *s = -*s;
+    *c = -*c;
+  }
 }
 
 using Two = unsigned long long;         // two floats, for instructions that take pairs
@@ -123,7 +157,7 @@ __device__ __noinline__ double norm_64(uint4 x, float eps) {
 // reaches -unit in magnitude.  turns: per position, of each pair; eps 0: no norm.  One value
 // costs its warp some 3 us, for the latency of the few 64-bit units.
 template <int D>
-__device__ __noinline__ uint32_t keys_64(const float* w, const unsigned long long* turns, float eps, int rot, int pairs,
+__device__ __noinline__ uint32_t keys_64(const float* w, const Turns* turns, float eps, int rot, int pairs,
                                          int position, uint4 x, uint4 y, uint32_t open, uint32_t code, double unit) {
   constexpr int LPH = D / 8;
   const int d0 = 8 * ((threadIdx.x & 31) % LPH), half = rot / 2;
@@ -136,10 +170,10 @@ __device__ __noinline__ uint32_t keys_64(const float* w, const unsigned long lon
     double o = bf16_of(x, u) * static_cast<double>(w[d]);
     if (d0 < rot) {
       const int other = pairs ? d ^ 1 : second ? d - half : d + half;
-      const unsigned long long turn = static_cast<unsigned long long>(static_cast<long long>(position)) *
-                                      turns[pairs ? d / 2 : second ? other : d];
       double s, c;
-      sincospi(static_cast<double>(static_cast<long long>(turn)) * 0x1p-63, &s, &c);
+      uint32_t quarters;
+      sincospi(static_cast<double>(off_quarter(turns[pairs ? d / 2 : second ? other : d].at(position), &quarters)) * 0x1p-63, &s, &c);
+      turn_quarters(quarters, &s, &c);
       const double par = bf16_of(y, u) * static_cast<double>(w[other]);
       o = o * c + par * ((pairs ? (u & 1) != 0 : second) ? s : -s);
     }
@@ -162,7 +196,7 @@ template <int D, bool PAIRS>
 struct RopePair {
   bool mine, turns;
   int u, w;                                              // dimensions
-  unsigned long long per_position;
+  Turns per_position;
 
   __device__ __forceinline__ explicit RopePair(const RopeArgs& p) {
     const int i = threadIdx.x, half = p.rot / 2;
@@ -170,23 +204,17 @@ struct RopePair {
     turns = i < half;
     u = !PAIRS && turns ? i : 2 * i;
     w = !PAIRS && turns ? i + half : 2 * i + 1;
-    per_position = turns ? turns_per_position(p.inv_freq[i]) : 0ull;
+    per_position = turns ? turns_per_position(p.inv_freq[i]) : Turns{0ull, 0u};
   }
   __device__ __forceinline__ void form(int position, const float (*weight)[D], RopeCoef<D>& out) const {
     if (!mine) return;
     float c = 1.f, s = 0.f;
     if (turns) {
-      const unsigned long long turn = static_cast<unsigned long long>(static_cast<long long>(position)) * per_position;
-      // the upper half as a signed fraction of half a turn, [-1, 1): the nearest that has 24
-      // bits, and what is left to first order, so that sine and cosine are good to two of their
-      // own last bits
-      const int32_t x = static_cast<int32_t>(turn >> 32);
-      const int64_t high = (static_cast<int64_t>(x) + 128) & ~int64_t{255};
-      float c0, s0;
-      sincospif(static_cast<float>(high) * 0x1p-31f, &s0, &c0);
-      const float rest = static_cast<float>(static_cast<int32_t>(x - high)) * 0x1.921fb6p-30f;
-      c = fmaf(-rest, s0, c0);
-      s = fmaf(rest, c0, s0);
+      // at most a quarter of a half turn, rounded to 24 bits of itself: sine and cosine are within 2^-22.7
+      // of themselves (of every float there sincospif's results were within 2^-23.4)
+      uint32_t quarters;
+      sincospif(__ll2float_rn(off_quarter(per_position.at(position), &quarters)) * 0x1p-63f, &s, &c);
+      turn_quarters(quarters, &s, &c);
     }
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {
@@ -217,8 +245,8 @@ struct RopeCells {
     partner = !rotated || p.interleaved ? lane : second ? lane - half / 8 : lane + half / 8;
   }
 
-  // Reciprocal of the root mean square of a head (over the LPH threads that hold it), to 2^-21.5:
-  // eight roundings of the sum, halved, and those of the last step.
+  // Reciprocal of the root mean square of a head (over the LPH threads that hold it), to 2^-21.4:
+  // nine roundings of what is under the root, halved, and those of the last step.
   __device__ __forceinline__ float norm(const uint4& x) const {
     float ssq = squares_of(x);
 #pragma unroll
@@ -269,11 +297,11 @@ struct RopeCells {
   }
 
   // Keys to the cache, quantised from the fp32 value o = r (A x + B y).  What is known of it: r to
-  // 2^-21.5 of itself, sine and cosine to 2^-21.8 of themselves, the weight's product, the two
-  // products, their sum and the last product a rounding each: in all within 2^-20.2 of
-  // r (|A x| + |B y|); without norm or rotation o is x.  Where that leaves a code or the scale
+  // 2^-21.4 of itself, sine and cosine to 2^-22.7 of themselves, the weight's product, the two
+  // products, their sum and the last product a rounding each: in all within 2^-20.4 of
+  // r (|A x| + |B y|), and a rounding of the ends of the range that is left: `rel` is 2^-20.1; without norm or rotation o is x.  Where that leaves a code or the scale
   // open, 64 bits decide (some 5 codes of a million).  (A NaN has no part in the scale, as in a4w4_kv_append.)
-  __device__ __forceinline__ void key_cell(const RopeCoef<D>& coef, const float* weight, const unsigned long long* turns,
+  __device__ __forceinline__ void key_cell(const RopeCoef<D>& coef, const float* weight, const Turns* turns,
                                            const uint4& v, int n, int slot, int position) const {
     using Ch = KvChunk<D>;
     const bool normed = p.k_weight != nullptr;
@@ -482,7 +510,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeBlocks<CACHE>) kv_rope_k
   extern __shared__ __align__(128) uint8_t smem[];         // two stages of heads, two sets of coefficients
   __shared__ alignas(8) unsigned long long s_bar[2];
   __shared__ int s_flags[2];
-  __shared__ unsigned long long s_turns[CACHE ? D / 2 : 1];   // per position, of each pair
+  __shared__ Turns s_turns[CACHE ? D / 2 : 1];   // per position, of each pair
   __shared__ float s_weight[2][D];                       // the norms' (1 without), of queries and of keys
   using Rows = RopeRows<D, PAIRS>;
   constexpr int HPW = Rows::HPW;
@@ -603,7 +631,7 @@ int launch_rope_kind(RopeArgs p, cudaStream_t st, int sms) {
       }) != 0)
     return -4;
   // as many blocks as stay on the SMs at once
-  int fit = 233472 / (smem + 2048 + 1024);                // with what the kernel and the system hold of it
+  int fit = 233472 / (smem + 2304 + 1024);                // with what the kernel and the system hold of it
   if (fit > kRopeBlocks<CACHE>) fit = kRopeBlocks<CACHE>;
   const long long items = static_cast<long long>(p.T) * p.split, most = static_cast<long long>(fit) * sms / p.split * p.split;
   return launch_pdl_smem(kern, static_cast<int>(items < most ? items : most), 32 * kRopeWarps, smem, st, p);

@@ -1,0 +1,96 @@
+"""Norms and rotation where fp32 comes to its limits (small angles, angles near quarter turns): rows within bounds that are
+relative to each product, cells byte for byte, against the oracle."""
+
+import numpy as np
+import pytest
+
+import mxfp4_a4w4_gemm_gb300 as a4w4
+import test_gpu_rope as base
+import workloads
+from gpu_util import host_bits
+from oracle import mxfp4
+from test_gpu_rope import Cache, Heads, scattered
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from mxfp4_a4w4_gemm_gb300 import build
+    build.build()
+    a4w4.lib()
+
+
+def set_values(h, v):
+    h.bits = workloads.to_bf16_bits(v.astype(np.float32)).reshape(v.shape)
+    h.load()
+
+
+def firsts(h):
+    """The dimensions that come first in their pairs."""
+    return np.arange(0, h.rot, 2) if h.inter else np.arange(h.rot // 2)
+
+
+def cached(h, page=16, seed=0):
+    c = Cache(h, page, *scattered(h.T, page, seed))
+    c.run()
+    c.check()
+
+
+def rows_are_near(h):
+    """The result within BF16's rounding and 2^-19.5 of |y cos| + |y' sin|: the norm's reciprocal 2^-20.9 (nine roundings
+    halved, two units in the last place), sine and cosine 2^-21.7, four roundings of 2^-24."""
+    q, k = h.outputs()
+    h.run(q, k)
+    assert a4w4.a4w4_get_device_status() == 0
+    for which, out, w in (("q", q, h.wq), ("k", k, h.wk)):
+        y = mxfp4.bf16_bits_to_f64(h.part(h.bits, which))
+        if w is not None:
+            y = y / np.sqrt((y * y).mean(-1, keepdims=True) + float(np.float32(base.EPS))) * w.astype(np.float64)
+        reach = np.abs(y)
+        for i in range(h.rot // 2):
+            a, b = (2 * i, 2 * i + 1) if h.inter else (i, i + h.rot // 2)
+            wide = np.longdouble if np.abs(h.pos).max() > 1000 else np.float64        # (slow where it has 113 bits)
+            ang = np.asarray(h.pos, dtype=wide) * wide(h.freq[i])
+            c, s = (np.abs(f(ang).astype(np.float64))[:, None] for f in (np.cos, np.sin))
+            reach[..., a], reach[..., b] = (np.abs(y[..., a]) * c + np.abs(y[..., b]) * s,
+                                            np.abs(y[..., b]) * c + np.abs(y[..., a]) * s)
+        want, _ = h.want(which)
+        got = mxfp4.bf16_bits_to_f64(host_bits(out))
+        bad = ~(np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -19.5 * reach + 2.0 ** -133)
+        assert not bad.any(), (which, bad.sum(), [(tuple(i), got[tuple(i)], want[tuple(i)]) for i in np.argwhere(bad)[:5]])
+
+
+def small_angles(D, inter, norm, theta, low=0.0, T=100):
+    h = Heads(T, 2, 3, D, D, inter, norm)
+    h.freq = (theta ** (-np.arange(D // 2) / (D // 2))).astype(np.float32)
+    h.pos = np.arange(1, T + 1, dtype=np.int32)
+    v = mxfp4.bf16_bits_to_f64(h.bits)
+    v[:, :, firsts(h)] *= low                                       # first halves nearly zero, of every other head
+    v[:, 1::2] = np.where(np.isin(np.arange(D), firsts(h)), 0.0, v[:, 1::2])       # zero
+    set_values(h, v)
+    return h
+
+
+@pytest.mark.parametrize("theta", [5e5, 1e7, 1e9])
+@pytest.mark.parametrize("inter", [0, 1])
+@pytest.mark.parametrize("D", [64, 128])
+def test_small_angles(D, inter, theta):
+    for norm, low in (("", 0.0), ("qk", 2.0 ** -20)):
+        h = small_angles(D, inter, norm, theta, low)
+        rows_are_near(h)
+        cached(h)
+
+
+@pytest.mark.parametrize("inter", [0, 1])
+def test_angles_near_quarter_turns(inter):
+    # sines of 355, 710, 103993, 104348, 245850922 ... are near zero, as are cosines of halves of them
+    h = Heads(12, 2, 3, 128, 128, inter, "qk")
+    h.pos = np.array([355, 710, 1, 2, 103993, 104348, 208341, 312689, 245850922, -355, -245850922, 3], dtype=np.int32)
+    h.freq[0::4], h.freq[1::4], h.freq[2::4], h.freq[3::4] = 1.0, 0.5, np.float32(np.pi / 2), 1.5
+    v = mxfp4.bf16_bits_to_f64(h.bits)
+    for head in range(v.shape[1]):
+        v[:, head, firsts(h)[head % 2:: 2]] = 0.0
+    set_values(h, v)
+    rows_are_near(h)
+    cached(h)
