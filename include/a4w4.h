@@ -450,7 +450,8 @@ int a4w4_qk_norm_rope(const void* q_bf16, long long q_stride, const void* k_bf16
 /* The same for the queries, with the normed and rotated keys and the values
  * quantised into the cache: a4w4_qk_norm_rope and a4w4_kv_append in one pass, with one
  * rounding fewer: keys are quantised from the unrounded result (their codes and
- * scales are those of the exact value; where fp32 leaves open which, 64 bits decide),
+ * scales are those of the exact value, which is below 2^129 in magnitude unless a
+ * weight is enormous; where fp32 leaves open which, 64 bits decide),
  * values as a4w4_kv_append does.  Values are rows like the keys.  A token whose slot is
  * outside [0, num_pages * page_size) is skipped: neither its cells nor its row of
  * q_out are written.  Two tokens with one slot leave either one's bytes.  positions

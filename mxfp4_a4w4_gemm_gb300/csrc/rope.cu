@@ -5,9 +5,10 @@
 // A thread block takes one token (or, of few tokens, a part of one).  A thread holds
 // eight dimensions of a head (16 bytes), D / 8 threads a head, a warp 256 / D heads (a
 // unit) at a time.  With y = r w x (r the reciprocal of the root mean square, w
-// the norm's weight) dimension i and its partner p of a pair become r (A_i x_i + B_i x_p),
+// the norm's weight) dimension i and its partner p of a pair become A_i (r x_i) + B_i (r x_p),
 // A_i = w_i cos, B_i = +-w_p sin: the token's coefficients are formed once, in shared
-// memory, while its heads are on their way to registers.
+// memory, while its heads are on their way to registers.  r comes first, so that nothing
+// on the way passes fp32's range that the result does not.
 //
 // Angles: position times frequency as turns, in 64-bit integers modulo one turn
 // (F = f / 2 pi as a 96-bit binary fraction, position * F wraps): within 2^-63 turns at
@@ -268,9 +269,9 @@ struct RopeCells {
     return rotated ? y : make_uint4(0u, 0u, 0u, 0u);      // what stays as it is takes nothing from a neighbour
   }
 
-  // o = r (A x + B y), and what |o| may be off by: `off` r (|A x| + |B y|).
-  __device__ __forceinline__ void rotate(const RopeCoef<D>& coef, const uint4& x, const uint4& y, float r, float* o,
-                                         float* sum) const {
+  // o = A (r x) + B (r y), and rel (|A r x| + |B r y|), what it may be off by.
+  __device__ __forceinline__ void rotate(const RopeCoef<D>& coef, const uint4& x, const uint4& y, float r, float rel, float* o,
+                                         float* off) const {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
     for (int u = 0; u < 8; u += 4) {
@@ -279,10 +280,10 @@ struct RopeCells {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t wi = w[(u + i) / 2], vi = v[(u + i) / 2];
-        const float m = a[i] * __uint_as_float(i & 1 ? wi & 0xFFFF0000u : wi << 16);
-        const float n = b[i] * __uint_as_float(i & 1 ? vi & 0xFFFF0000u : vi << 16);
-        o[u + i] = r * (m + n);
-        sum[u + i] = r * (fabsf(m) + fabsf(n));
+        const float m = a[i] * (r * __uint_as_float(i & 1 ? wi & 0xFFFF0000u : wi << 16));
+        const float n = b[i] * (r * __uint_as_float(i & 1 ? vi & 0xFFFF0000u : vi << 16));
+        o[u + i] = m + n;
+        off[u + i] = fmaf(fabsf(m), rel, fabsf(n) * rel);
       }
     }
   }
@@ -296,10 +297,10 @@ struct RopeCells {
     return p.cache + kv_chunk_offset<D>(slot >> p.page_lg, h, (slot >> 4) & (chunks - 1), p.Hkv, chunks);
   }
 
-  // Keys to the cache, quantised from the fp32 value o = r (A x + B y).  What is known of it: r to
-  // 2^-21.4 of itself, sine and cosine to 2^-22.7 of themselves, the weight's product, the two
-  // products, their sum and the last product a rounding each: in all within 2^-20.4 of
-  // r (|A x| + |B y|), and a rounding of the ends of the range that is left: `rel` is 2^-20.1; without norm or rotation o is x.  Where that leaves a code or the scale
+  // Keys to the cache, quantised from the fp32 value o = A (r x) + B (r y).  What is known of it: r to
+  // 2^-21.4 of itself, sine and cosine to 2^-22.7 of themselves, the weight's product, those with r and
+  // with a coefficient and the sum a rounding each: in all within 2^-20.4 of
+  // |A r x| + |B r y|, and a rounding of the ends of the range that is left: `rel` is 2^-20.1; without norm or rotation o is x.  Where that leaves a code or the scale
   // open, 64 bits decide (some 5 codes of a million).  (A NaN has no part in the scale, as in a4w4_kv_append.)
   __device__ __forceinline__ void key_cell(const RopeCoef<D>& coef, const float* weight, const Turns* turns,
                                            const uint4& v, int n, int slot, int position) const {
@@ -308,13 +309,12 @@ struct RopeCells {
     const float r = normed ? norm(v) : 1.f;
     const uint4 y = partners(v);
     float o[8], off[8];
-    rotate(coef, v, y, r, o, off);
-    const float rel = rotated || normed ? 0x1.dp-21f : 0.f;
+    rotate(coef, v, y, r, rotated || normed ? 0x1.dp-21f : 0.f, o, off);
     float least = 0.f, most = 0.f;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       // (tiny values lose more, zeros and what nothing is computed of nothing)
-      off[u] = off[u] > 0.f && rel > 0.f ? fmaf(off[u], rel, 0x1p-147f) : 0.f;
+      off[u] = off[u] > 0.f ? off[u] + 0x1p-147f : 0.f;
       least = fmaxf(least, fabsf(o[u]) - off[u]);
       most = fmaxf(most, fabsf(o[u]) + off[u]);
     }
@@ -323,15 +323,17 @@ struct RopeCells {
     least = fmaxf(least, __shfl_xor_sync(kAll, least, 2));
     most = fmaxf(most, __shfl_xor_sync(kAll, most, 2));
     uint32_t eb = __float_as_uint(most) >> 23;
-    if (__any_sync(kAll, __float_as_uint(least) >> 23 != eb)) {
-      // does the largest magnitude reach the power of two that `most` has passed?
+    if (__any_sync(kAll, __float_as_uint(least) >> 23 != eb || eb == 255u)) {
+      // does the largest magnitude reach the power of two that `most` has passed?  (2^128: the
+      // values that fp32 has no number for tell)
+      const bool beyond = eb == 255u;
       const float power = __uint_as_float(eb << 23);
       uint32_t open = 0u;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) open |= least < power && fabsf(o[u]) + off[u] >= power ? 1u << u : 0u;
+      for (int u = 0; u < 8; ++u) open |= (least < power || beyond) && fabsf(o[u]) + off[u] >= power ? 1u << u : 0u;
       uint32_t reached = keys_64<D>(weight, turns, normed ? p.eps : 0.f, p.rot, p.interleaved, position, v, y, open, 0u,
-                                    -static_cast<double>(power));      // (the warp as a whole)
-      reached |= least >= power;
+                                    beyond ? -0x1p128 : -static_cast<double>(power));      // (the warp as a whole)
+      reached |= least >= power && !beyond;
       reached |= __shfl_xor_sync(kAll, reached, 1);
       reached |= __shfl_xor_sync(kAll, reached, 2);
       if (reached == 0u) --eb;
@@ -348,10 +350,11 @@ struct RopeCells {
     }
     uint32_t code = codes_of(lo);
     const uint32_t diff = code ^ codes_of(hi);
-    if (__any_sync(kAll, diff != 0u)) {
+    if (__any_sync(kAll, diff != 0u || eb == 255u)) {
       uint32_t open = 0u;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) open |= (diff >> (4 * u) & 15u) != 0u ? 1u << u : 0u;
+      for (int u = 0; u < 8; ++u)
+        open |= (diff >> (4 * u) & 15u) != 0u || (eb == 255u && !(fabsf(o[u]) < INFINITY)) ? 1u << u : 0u;
       code = keys_64<D>(weight, turns, normed ? p.eps : 0.f, p.rot, p.interleaved, position, v, y, open, code, inv);
     }
     const int h = n * HPW + sub;
@@ -452,15 +455,16 @@ struct RopeRows {
     }
   }
   __device__ __forceinline__ void store(const uint4& v, float r, uint16_t* x) const {
-    const Two a[2] = {two_of_bf16(v.x), two_of_bf16(v.y)}, b[2] = {two_of_bf16(v.z), two_of_bf16(v.w)};
-    const bool stays = p.rot < D && !rotated;            // what stays as it is takes nothing from a neighbour
     const Two r2 = two(r, r);
+    const Two a[2] = {mul2(r2, two_of_bf16(v.x)), mul2(r2, two_of_bf16(v.y))};
+    const Two b[2] = {mul2(r2, two_of_bf16(v.z)), mul2(r2, two_of_bf16(v.w))};
+    const bool stays = p.rot < D && !rotated;            // what stays as it is takes nothing from a neighbour
     uint32_t o[4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       Two pa = PAIRS ? swapped(a[u]) : b[u], pb = PAIRS ? swapped(b[u]) : a[u];
       if (stays) pa = pb = 0ull;
-      const Two x = mul2(r2, fma2(Aa[u], a[u], mul2(Ba[u], pa))), y = mul2(r2, fma2(Ab[u], b[u], mul2(Bb[u], pb)));
+      const Two x = fma2(Aa[u], a[u], mul2(Ba[u], pa)), y = fma2(Ab[u], b[u], mul2(Bb[u], pb));
       o[u] = pack_bf16(lo_of(x), hi_of(x));
       o[2 + u] = pack_bf16(lo_of(y), hi_of(y));
     }

@@ -1,5 +1,5 @@
-"""Norms and rotation where fp32 comes to its limits (small angles, angles near quarter turns): rows within bounds that are
-relative to each product, cells byte for byte, against the oracle."""
+"""Norms and rotation where fp32 comes to its limits (small angles, angles near quarter turns, the largest heads): rows within bounds
+that are relative to each product, cells byte for byte, against the oracle."""
 
 import numpy as np
 import pytest
@@ -94,3 +94,19 @@ def test_angles_near_quarter_turns(inter):
     set_values(h, v)
     rows_are_near(h)
     cached(h)
+
+
+def test_the_largest_heads():
+    # A x passes fp32's range where r A x does not
+    rng = np.random.default_rng(2)
+    for D, inter in ((128, 0), (64, 1)):
+        h = Heads(24, 3, 4, D, D, inter, "qk")
+        v = np.sign(rng.standard_normal(h.bits.shape)) * rng.uniform(0.5, 0.99, h.bits.shape) * 2.0 ** 128
+        v[::3] *= rng.choice([1.0, 2.0 ** -3, 2.0 ** -40], v[::3].shape)
+        h.wq, h.wk = (3.0 * h.wq).astype(np.float32), (np.float32(2.0 ** 20) * h.wk).astype(np.float32)
+        set_values(h, v)
+        rows_are_near(h)
+        cached(h)
+        h = Heads(24, 0, 4, D, D, inter, "")                        # rotated keys up to sqrt(2) 2^128
+        set_values(h, v[:, :9])
+        cached(h)
