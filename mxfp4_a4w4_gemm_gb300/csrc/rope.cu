@@ -221,9 +221,10 @@ struct RopePair {
     for (int kind = 0; kind < 2; ++kind) {
       const float wu = weight[kind][u], ww = weight[kind][w];
       out.a[kind][u] = wu * c;
-      out.b[kind][u] = -ww * s;
       out.a[kind][w] = ww * c;
-      out.b[kind][w] = wu * s;
+      // (-0: what does not turn adds -0, which leaves a zero its sign)
+      out.b[kind][u] = turns ? -ww * s : -0.f;
+      out.b[kind][w] = turns ? wu * s : -0.f;
     }
   }
 };

@@ -1,8 +1,9 @@
-"""Norms and rotation where fp32 comes to its limits (small angles, angles near quarter turns, the largest heads): rows within bounds
-that are relative to each product, cells byte for byte, against the oracle."""
+"""Norms and rotation where fp32 comes to its limits (small angles, angles near quarter turns, the largest heads, signs of
+zeros): rows within bounds that are relative to each product, cells byte for byte, against the oracle."""
 
 import numpy as np
 import pytest
+import torch
 
 import mxfp4_a4w4_gemm_gb300 as a4w4
 import test_gpu_rope as base
@@ -110,3 +111,21 @@ def test_the_largest_heads():
         h = Heads(24, 0, 4, D, D, inter, "")                        # rotated keys up to sqrt(2) 2^128
         set_values(h, v[:, :9])
         cached(h)
+
+
+@pytest.mark.parametrize("D,rot,inter,norm", [(128, 0, 0, ""), (64, 0, 1, "k"), (128, 64, 0, ""), (64, 32, 1, "qk"), (128, 128, 0, ""),
+                                              (64, 64, 1, "qk")])
+def test_zeros_keep_their_sign(D, rot, inter, norm):
+    h = Heads(30, 2, 3, D, rot, inter, norm)
+    rng = np.random.default_rng(3)
+    h.bits[rng.random(h.bits.shape) < 0.3] = 0x8000
+    h.bits[rng.random(h.bits.shape) < 0.2] = 0x0000
+    h.bits[5], h.bits[6] = 0x8000, 0x0000
+    h.load()
+    cached(h)
+    if rot == 0 and not norm:
+        c = Cache(h, 16, *scattered(30, 16))
+        c.run()
+        other = torch.full_like(c.cache, 0xA5)
+        a4w4.a4w4_kv_append(h.part(h.x, "k"), h.stride, h.part(h.x, "v"), h.stride, c.map, 30, 3, D, other, c.pages, 16)
+        assert torch.equal(c.cache, other)
