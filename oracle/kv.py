@@ -5,6 +5,8 @@ text: requests one after another for the plan, the byte formulas for the cache,
 float64 for the attention.
 """
 
+import functools
+
 import numpy as np
 
 from . import mxfp4
@@ -75,6 +77,7 @@ def chunk_bytes(codes_k, scales_k, codes_v, scales_v):
     return out
 
 
+@functools.lru_cache(maxsize=None)
 def byte_places(D):
     """Offsets in a chunk of (key codes [16, D/2], key scales [16, D/32], value codes, value scales), found
     from chunk_bytes one byte at a time."""
@@ -92,21 +95,17 @@ def byte_places(D):
                 assert hit.size == 1
                 place[r, c] = hit[0]
         places.append(place)
-    return places
-
-
-_places = {}
+    return tuple(places)
 
 
 def cache_from_rows(k_codes, k_scales, v_codes, v_scales, page_size):
     """Rows in slot order (codes [slots, H, D], scales [slots, H, D/32]) -> cache bytes, flat."""
     S, H, D = k_codes.shape
-    if D not in _places:
-        _places[D] = byte_places(D)
+    places = byte_places(D)
     out = np.zeros((S // page_size, H, page_size // 16, 17 * D), dtype=np.uint8)
     for part, x in enumerate((mxfp4.pack_codes(k_codes), k_scales, mxfp4.pack_codes(v_codes), v_scales)):
         x = x.reshape(S // page_size, page_size // 16, 16, H, -1).transpose(0, 3, 1, 2, 4)
-        out[..., _places[D][part]] = x
+        out[..., places[part]] = x
     return out.reshape(-1)
 
 
