@@ -41,8 +41,8 @@ struct Turns {
   uint32_t lo;
   // position times it, in units of 2^-64 turns (cut by 1.5 of them at most)
   __device__ __forceinline__ unsigned long long at(int position) const {
-    const long long t = position;
-    return static_cast<unsigned long long>(t) * hi + static_cast<unsigned long long>(t * static_cast<long long>(lo) >> 32);
+    const int32_t low = static_cast<int32_t>(__umulhi(static_cast<uint32_t>(position), lo) - (position < 0 ? lo : 0u));
+    return static_cast<unsigned long long>(static_cast<long long>(position)) * hi + static_cast<unsigned long long>(static_cast<long long>(low));
   }
 };
 
@@ -75,8 +75,9 @@ __device__ __forceinline__ Turns turns_per_position(float f) {
 
 // An angle less its nearest quarter turns: an eighth of a turn at most, in units of 2^-64 turns.
 __device__ __forceinline__ long long off_quarter(unsigned long long turn, uint32_t* quarters) {
-  *quarters = static_cast<uint32_t>((turn + (1ull << 61)) >> 62);
-  return static_cast<long long>(turn - (static_cast<unsigned long long>(*quarters) << 62));
+  const uint32_t up = static_cast<uint32_t>(turn >> 32);
+  *quarters = (up + (1u << 29)) >> 30;
+  return static_cast<long long>(static_cast<unsigned long long>(up - (*quarters << 30)) << 32 | (turn & 0xFFFFFFFFull));
 }
 // Sine and cosine of an angle so many quarter turns further.
 template <typename Real>
@@ -134,6 +135,10 @@ __device__ __forceinline__ float squares_of(const uint4& v) {
   const Two s = fma2(a, a, fma2(b, b, fma2(c, c, mul2(d, d))));
   return lo_of(s) + hi_of(s);
 }
+
+// Is a mean square (with eps) one that fp32 sums are good for?  Above, squares may have passed its range;
+// below, lost bits.
+__device__ __forceinline__ bool in_range(float v) { return v > 0x1p-100f && v < 0x1p119f; }
 
 // What follows runs seldom.  It stands apart and takes values: a member function that is called
 // would keep its object in memory, which the loops would then read again and again.
@@ -238,9 +243,16 @@ struct RopeCells {
   const int lane, d0, sub;                               // first dimension of this thread, head of the HPW
   int partner;                                           // thread with the pairs' other halves (half split)
   bool rotated, second;                                  // whether d0 .. d0 + 7 turn; are second halves of their pairs
+  float lost;                                            // what a key may be off by besides `rel`, for subnormal numbers on the way
 
-  __device__ __forceinline__ explicit RopeCells(const RopeArgs& args)
+  // weight: of keys.  In 2^-150: r x is off by 1 if it is subnormal, A times that, a subnormal A by 1, r |x| <= sqrt(D) times
+  // that, each of two terms; their products by 1 each, `off`'s own terms too: 2 max |w| + 2 sqrt(D) + 6.
+  __device__ __forceinline__ RopeCells(const RopeArgs& args, const float* weight)
       : p(args), lane(threadIdx.x & 31), d0(8 * (lane % LPH)), sub(lane / LPH) {
+    uint32_t most = 0u;
+#pragma unroll
+    for (int i = 0; i < D; i += 32) most = max(most, __float_as_uint(fabsf(weight[i + lane])));
+    lost = fmaf(__uint_as_float(__reduce_max_sync(kAll, most)), 0x1p-149f, 0x1p-145f);
     const int half = p.rot / 2;
     rotated = d0 < p.rot;
     second = !p.interleaved && d0 >= half;
@@ -253,8 +265,8 @@ struct RopeCells {
     float ssq = squares_of(x);
 #pragma unroll
     for (int o = LPH / 2; o > 0; o >>= 1) ssq += __shfl_xor_sync(kAll, ssq, o);
-    if (__any_sync(kAll, !(ssq < 1e38f))) return static_cast<float>(norm_64<LPH>(x, p.eps));   // the squares may have passed fp32's range
     const float v = fmaf(ssq, 1.f / D, p.eps), r = rsqrtf(v);
+    if (__any_sync(kAll, !in_range(v))) return static_cast<float>(norm_64<LPH>(x, p.eps));
     return fmaf(0.5f * r, fmaf(-v * r, r, 1.f), r);
   }
 
@@ -270,9 +282,11 @@ struct RopeCells {
     return rotated ? y : make_uint4(0u, 0u, 0u, 0u);      // what stays as it is takes nothing from a neighbour
   }
 
-  // o = A (r x) + B (r y), and rel (|A r x| + |B r y|), what it may be off by.
-  __device__ __forceinline__ void rotate(const RopeCoef<D>& coef, const uint4& x, const uint4& y, float r, float rel, float* o,
+  // o = A (r x) + B (r y), and what it may be off by (nothing where it is x).
+  __device__ __forceinline__ void rotate(const RopeCoef<D>& coef, const uint4& x, const uint4& y, float r, float* o,
                                          float* off) const {
+    constexpr float rel = 0x1.dp-21f;
+    const bool exact = !rotated && p.k_weight == nullptr;
     const uint32_t w[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
     for (int u = 0; u < 8; u += 4) {
@@ -284,7 +298,7 @@ struct RopeCells {
         const float m = a[i] * (r * __uint_as_float(i & 1 ? wi & 0xFFFF0000u : wi << 16));
         const float n = b[i] * (r * __uint_as_float(i & 1 ? vi & 0xFFFF0000u : vi << 16));
         o[u + i] = m + n;
-        off[u + i] = fmaf(fabsf(m), rel, fabsf(n) * rel);
+        off[u + i] = exact ? 0.f : fmaf(fabsf(m), rel, fmaf(fabsf(n), rel, lost));
       }
     }
   }
@@ -300,9 +314,10 @@ struct RopeCells {
 
   // Keys to the cache, quantised from the fp32 value o = A (r x) + B (r y).  What is known of it: r to
   // 2^-21.4 of itself, sine and cosine to 2^-22.7 of themselves, the weight's product, those with r and
-  // with a coefficient and the sum a rounding each: in all within 2^-20.4 of
-  // |A r x| + |B r y|, and a rounding of the ends of the range that is left: `rel` is 2^-20.1; without norm or rotation o is x.  Where that leaves a code or the scale
-  // open, 64 bits decide (some 5 codes of a million).  (A NaN has no part in the scale, as in a4w4_kv_append.)
+  // with a coefficient and the sum a rounding each: in all within 2^-20.4 of |A r x| + |B r y| and, with
+  // a rounding of the ends of the range that this leaves, 2^-20.1 (and `lost`); without norm or
+  // rotation o is x.  Where that leaves a code or the scale open, 64 bits decide (some 5 codes of a
+  // million).  (A NaN has no part in the scale, as in a4w4_kv_append.)
   __device__ __forceinline__ void key_cell(const RopeCoef<D>& coef, const float* weight, const Turns* turns,
                                            const uint4& v, int n, int slot, int position) const {
     using Ch = KvChunk<D>;
@@ -310,12 +325,10 @@ struct RopeCells {
     const float r = normed ? norm(v) : 1.f;
     const uint4 y = partners(v);
     float o[8], off[8];
-    rotate(coef, v, y, r, rotated || normed ? 0x1.dp-21f : 0.f, o, off);
+    rotate(coef, v, y, r, o, off);
     float least = 0.f, most = 0.f;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      // (tiny values lose more, zeros and what nothing is computed of nothing)
-      off[u] = off[u] > 0.f ? off[u] + 0x1p-147f : 0.f;
       least = fmaxf(least, fabsf(o[u]) - off[u]);
       most = fmaxf(most, fabsf(o[u]) + off[u]);
     }
@@ -352,11 +365,18 @@ struct RopeCells {
     uint32_t code = codes_of(lo);
     const uint32_t diff = code ^ codes_of(hi);
     if (__any_sync(kAll, diff != 0u || eb == 255u)) {
-      uint32_t open = 0u;
+      // (of zeros nothing is lost: they have the code of o)
+      const uint32_t in[4] = {v.x | y.x, v.y | y.y, v.z | y.z, v.w | y.w};
+      uint32_t open = 0u, zeros = 0u;
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        open |= (diff >> (4 * u) & 15u) != 0u || (eb == 255u && !(fabsf(o[u]) < INFINITY)) ? 1u << u : 0u;
-      code = keys_64<D>(weight, turns, normed ? p.eps : 0.f, p.rot, p.interleaved, position, v, y, open, code, inv);
+      for (int u = 0; u < 8; ++u) {
+        const bool zero = (in[u / 2] & (u & 1 ? 0x7FFF0000u : 0x7FFFu)) == 0u;
+        zeros |= zero ? 15u << (4 * u) : 0u;
+        open |= !zero && ((diff >> (4 * u) & 15u) != 0u || (eb == 255u && !(fabsf(o[u]) < INFINITY))) ? 1u << u : 0u;
+      }
+      const Two mid[4] = {mul2(two(o[0], o[1]), i2), mul2(two(o[2], o[3]), i2), mul2(two(o[4], o[5]), i2), mul2(two(o[6], o[7]), i2)};
+      code = (code & ~zeros) | (codes_of(mid) & zeros);
+      if (__any_sync(kAll, open != 0u)) code = keys_64<D>(weight, turns, normed ? p.eps : 0.f, p.rot, p.interleaved, position, v, y, open, code, inv);
     }
     const int h = n * HPW + sub;
     if (h < p.Hkv) {
@@ -435,7 +455,8 @@ struct RopeRows {
     float s = squares_of(v);
 #pragma unroll
     for (int o = 1; o < LPH; o <<= 1) s += __shfl_xor_sync(kAll, s, o);
-    return __any_sync(kAll, !(s < 1e38f)) ? static_cast<float>(norm_64<LPH>(v, p.eps)) : rsqrtf(s * (1.f / D) + p.eps);
+    const float mean = s * (1.f / D) + p.eps;
+    return __any_sync(kAll, !in_range(mean)) ? static_cast<float>(norm_64<LPH>(v, p.eps)) : rsqrtf(mean);
   }
   // The same for four units.
   __device__ __forceinline__ void norms(const uint4* v, float* r) const {
@@ -447,10 +468,10 @@ struct RopeRows {
     float s = (upper ? b : a) + __shfl_xor_sync(kAll, upper ? a : b, 2);
 #pragma unroll
     for (int o = 4; o < LPH; o <<= 1) s += __shfl_xor_sync(kAll, s, o);
-    const float q = rsqrtf(s * (1.f / D) + p.eps);
+    const float mean = s * (1.f / D) + p.eps, q = rsqrtf(mean);
 #pragma unroll
     for (int i = 0; i < 4; ++i) r[i] = __shfl_sync(kAll, q, (lane & ~3) | i);
-    if (__any_sync(kAll, !(s < 1e38f))) {                // the squares may have passed fp32's range
+    if (__any_sync(kAll, !in_range(mean))) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) r[i] = static_cast<float>(norm_64<LPH>(v[i], p.eps));
     }
@@ -568,7 +589,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeBlocks<CACHE>) kv_rope_k
   }
   __syncthreads();
   Rows rows(p);
-  const RopeCells<D> cells(p);
+  const RopeCells<D> cells(p, s_weight[1]);
   const RopePair<D, PAIRS> pair(p);
   if (CACHE && pair.turns) s_turns[threadIdx.x] = pair.per_position;
   // queries, keys and values begin with the warp after the last one of those before

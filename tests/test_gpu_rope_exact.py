@@ -1,5 +1,6 @@
-"""Norms and rotation where fp32 comes to its limits (small angles, angles near quarter turns, the largest heads, signs of
-zeros): rows within bounds that are relative to each product, cells byte for byte, against the oracle."""
+"""Norms and rotation where fp32 comes to its limits (small angles, angles near quarter turns, the smallest and the largest
+heads, any eps, signs of zeros): rows within bounds that are relative to each product, cells byte for byte, against the
+oracle."""
 
 import numpy as np
 import pytest
@@ -129,3 +130,40 @@ def test_zeros_keep_their_sign(D, rot, inter, norm):
         other = torch.full_like(c.cache, 0xA5)
         a4w4.a4w4_kv_append(h.part(h.x, "k"), h.stride, h.part(h.x, "v"), h.stride, c.map, 30, 3, D, other, c.pages, 16)
         assert torch.equal(c.cache, other)
+
+
+@pytest.mark.parametrize("scale", [-100, -120, -126, -130])
+def test_the_smallest_keys(scale):
+    for D, inter, rot, norm in ((128, 0, 128, ""), (64, 1, 32, ""), (128, 0, 64, "qk"), (64, 1, 64, "k")):
+        h = Heads(40, 1, 4, D, rot, inter, norm)
+        v = mxfp4.bf16_bits_to_f64(h.bits)
+        v[::2, 1:3] = 0.0                                           # heads of zeros and of zeros but for a few dimensions
+        v[::4, 1, 3], v[::4, 1, D // 2 + 3], v[::4, 2, 5] = 1.0, -1.0, -1.0
+        set_values(h, np.ldexp(v, scale))
+        cached(h)
+        rows_are_near(h)
+
+
+def test_the_smallest_weights_and_heads_of_few_large_values():
+    h = Heads(40, 1, 4, 128, 128, 0, "qk")
+    h.wk = np.ldexp(h.wk, np.random.default_rng(1).choice([-140, -120, -60, 0], 128)).astype(np.float32)
+    h.load()
+    cached(h)
+    h = Heads(40, 1, 4, 128, 128, 0, "qk")
+    v = mxfp4.bf16_bits_to_f64(h.bits)
+    v[:, :, 32:64] *= 2.0 ** -120                                   # next to others of the head their squares are nothing
+    v[:, :, 96:] *= 2.0 ** -125
+    v[::2] *= 2.0 ** 90
+    set_values(h, v)
+    cached(h)
+    rows_are_near(h)
+
+
+@pytest.mark.parametrize("eps", [1e-45, 1e-42, 1e-38, 1e-30, 1e-12, 1.0])
+def test_any_eps(eps, monkeypatch):
+    monkeypatch.setattr(base, "EPS", eps)
+    for scale in (-64, -67, -70, -75, -110, 0):
+        h = Heads(24, 3, 3, 128, 128, 0, "qk")
+        set_values(h, np.ldexp(mxfp4.bf16_bits_to_f64(h.bits), scale))
+        rows_are_near(h)
+        cached(h)
