@@ -1038,7 +1038,7 @@ W8Plan plan_w8a8(int M, int N, int K, int sms) {
   W8Plan pl{};
   pl.kt = K / 128;
   pl.w_tiles = N / 128;
-  pl.x_tiles = (M + 127) / 128;
+  pl.x_tiles = M / 128 + (M % 128 != 0);
   if (M > 32) {
     const long long tiles = static_cast<long long>(pl.x_tiles) * (pl.w_tiles / 2), rest = tiles % sms;
     // the last, partial wave's tiles run as halves where they then still are one wave
