@@ -139,11 +139,13 @@ int a4w4_gemm_a16w4(const void* A_bf16, int M, int K, const void* Wq, const void
  *   Activations: BF16, quantised here to E4M3 with a power-of-two scale for each row and
  *   128 k's: 2^e with the smallest e >= -126 such that the block's largest magnitude is
  *   at most 448 * 2^e; the code is x * 2^-e (exact) rounded to nearest, ties to even.  An
- *   infinity or NaN makes its block's scale, and so its row of C, NaN.
+ *   infinity or NaN makes its row of C NaN (an infinity by its block's scale, a NaN by its code).
  *   C[m, n] = sum over blocks b of 2^e[m,b] * Ws[n/128, b] * (sum over b's k's of the
  *   codes' products), every sum and 2^e * Ws in fp32 (what lies below 2^-126 loses bits), in
  *   an order fixed by the sizes and the device: bitwise deterministic.
- * N % 128 == 0, K % 128 == 0, M >= 1; rows >= M of C are never touched.
+ * N % 128 == 0, K % 128 == 0, M >= 1; rows >= M of C are never touched.  A checkpoint's
+ * other N: pad its codes with rows of zeros to a multiple of 128 (its last blocks' scales
+ * stay); C then has that many columns, the padding's zero.  Other K: columns of zeros, of A too.
  *
  * Weight tiles: tile (nt, kt) = rows 128 nt .., k's 128 kt .. at byte (nt * (K/128) + kt) *
  * 16384; byte b of row r at (r/8)*1024 + (r%8)*128 + ((b/16) ^ (r%8))*16 + b%16.
