@@ -129,20 +129,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-// Two fp32 operations at a time.
-__device__ __forceinline__ uint64_t pair_f32(uint32_t lo, uint32_t hi) {
-  return static_cast<uint64_t>(hi) << 32 | lo;
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
+// pack2 by a shift: with a move the loops that use it spill more, with a shift the 8-bit product is slower (126 for 118 us).
+__device__ __forceinline__ Two pair_f32(uint32_t lo, uint32_t hi) { return static_cast<Two>(hi) << 32 | lo; }
 template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
@@ -188,11 +176,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, ui
       "mov.b64 b, {%2, %3};\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}"
       :: "r"(d), "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate) : "memory");
-}
-__device__ __forceinline__ bool elect_one() {
-  uint32_t e;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
-  return e != 0;
 }
 // Shared-memory descriptor of a B operand stored K x N with N contiguous
 // (MN-major, 128-byte swizzle): blocks of 64 N elements `lead` bytes apart,
@@ -531,11 +514,11 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
               uint32_t y[8], rest[8];
 #pragma unroll
               for (int u = 0; u < 8; ++u) {
-                const uint64_t z = fma_f32x2(pair_f32(x[16 * c + 2 * u], x[16 * c + 2 * u + 1]), f2, off2);
+                const uint64_t z = fma2(pair_f32(x[16 * c + 2 * u], x[16 * c + 2 * u + 1]), f2, off2);
                 const float e0 = ex2(__uint_as_float(static_cast<uint32_t>(z)));
                 const float e1 = ex2(__uint_as_float(static_cast<uint32_t>(z >> 32)));
                 const uint64_t e = pair_f32(__float_as_uint(e0), __float_as_uint(e1));
-                if (u & 1) sum1 = add_f32x2(sum1, e); else sum0 = add_f32x2(sum0, e);
+                if (u & 1) sum1 = add2(sum1, e); else sum0 = add2(sum0, e);
                 y[u] = pack_bf16(e0, e1);
                 if constexpr (REST) rest[u] = pack_bf16(e0 - __uint_as_float(y[u] << 16), e1 - __uint_as_float(y[u] & 0xFFFF0000u));
               }
@@ -548,7 +531,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1) a4w4_kv_prefill_kernel(
                 if (lane == 0) mbar_arrive(p_half(tile));
               }
             }
-            sum0 = add_f32x2(sum0, sum1);
+            sum0 = add2(sum0, sum1);
             l += __uint_as_float(static_cast<uint32_t>(sum0)) + __uint_as_float(static_cast<uint32_t>(sum0 >> 32));
             tmem_wait_st();
             tc_fence_before();

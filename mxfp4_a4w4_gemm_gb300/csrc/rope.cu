@@ -93,28 +93,10 @@ __device__ __forceinline__ void turn_quarters(uint32_t quarters, Real* s, Real* 
   }
 }
 
-using Two = unsigned long long;         // two floats, for instructions that take pairs
-__device__ __forceinline__ Two two(float lo, float hi) {
-  Two d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
 __device__ __forceinline__ Two two_of_bf16(uint32_t w) {
-  return two(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-  Two d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ Two mul2(Two a, Two b) {
-  Two d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ float lo_of(Two v) { return __uint_as_float(static_cast<uint32_t>(v)); }
-__device__ __forceinline__ float hi_of(Two v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
-__device__ __forceinline__ Two swapped(Two v) { return two(hi_of(v), lo_of(v)); }
+__device__ __forceinline__ Two swapped(Two v) { return pack2(hi_of(v), lo_of(v)); }
 
 // E2M1 code (with its sign) of a 64-bit value: rounded towards zero to fp32, with the last bit set
 // where something was lost, which no border of E2M1 has.
@@ -354,11 +336,11 @@ struct RopeCells {
     }
     const uint32_t e = eb > 2u ? eb - 2u : 0u;
     const float inv = __uint_as_float((254u - e) << 23);
-    const Two i2 = two(inv, inv), j2 = two(-inv, -inv);
+    const Two i2 = pack2(inv, inv), j2 = pack2(-inv, -inv);
     Two lo[4], hi[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const Two m = mul2(two(o[2 * u], o[2 * u + 1]), i2), d = two(off[2 * u], off[2 * u + 1]);
+      const Two m = mul2(pack2(o[2 * u], o[2 * u + 1]), i2), d = pack2(off[2 * u], off[2 * u + 1]);
       lo[u] = fma2(d, j2, m);
       hi[u] = fma2(d, i2, m);
     }
@@ -374,7 +356,7 @@ struct RopeCells {
         zeros |= zero ? 15u << (4 * u) : 0u;
         open |= !zero && ((diff >> (4 * u) & 15u) != 0u || (eb == 255u && !(fabsf(o[u]) < INFINITY))) ? 1u << u : 0u;
       }
-      const Two mid[4] = {mul2(two(o[0], o[1]), i2), mul2(two(o[2], o[3]), i2), mul2(two(o[4], o[5]), i2), mul2(two(o[6], o[7]), i2)};
+      const Two mid[4] = {mul2(pack2(o[0], o[1]), i2), mul2(pack2(o[2], o[3]), i2), mul2(pack2(o[4], o[5]), i2), mul2(pack2(o[6], o[7]), i2)};
       code = (code & ~zeros) | (codes_of(mid) & zeros);
       if (__any_sync(kAll, open != 0u)) code = keys_64<D>(weight, turns, normed ? p.eps : 0.f, p.rot, p.interleaved, position, v, y, open, code, inv);
     }
@@ -477,7 +459,7 @@ struct RopeRows {
     }
   }
   __device__ __forceinline__ void store(const uint4& v, float r, uint16_t* x) const {
-    const Two r2 = two(r, r);
+    const Two r2 = pack2(r, r);
     const Two a[2] = {mul2(r2, two_of_bf16(v.x)), mul2(r2, two_of_bf16(v.y))};
     const Two b[2] = {mul2(r2, two_of_bf16(v.z)), mul2(r2, two_of_bf16(v.w))};
     const bool stays = p.rot < D && !rotated;            // what stays as it is takes nothing from a neighbour

@@ -174,17 +174,6 @@ __global__ void __launch_bounds__(256) w8_quant_tiles_kernel(const uint16_t* __r
 // E4M3 x E4M3, both K-major, fp32 D, M = 128, K = 32: formats 0 at bits 7 and 10.
 __device__ __forceinline__ uint32_t idesc_e4m3(uint32_t n) { return (1u << 4) | ((n >> 3) << 17) | ((128u >> 4) << 24); }
 
-// One thread of a whole warp, in a form that the compiler knows to be one.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t e;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xFFFFFFFF;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(e));
-  return e != 0;
-}
-
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                          uint32_t accumulate) {
   asm volatile(
@@ -224,26 +213,9 @@ __device__ __forceinline__ void tmem_ld64_now(uint32_t taddr, uint32_t* r) {
                  "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63])
                :: "memory");
 }
-__device__ __forceinline__ unsigned long long pack2(uint32_t lo, uint32_t hi) {
-  unsigned long long d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
-  return d;
-}
-__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
-  unsigned long long d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
-  unsigned long long d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ float lo2(unsigned long long v) { return __uint_as_float(static_cast<uint32_t>(v)); }
-__device__ __forceinline__ float hi2(unsigned long long v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
 
-__device__ __forceinline__ uint32_t bf16x2_of(unsigned long long v) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo2(v), hi2(v));
+__device__ __forceinline__ uint32_t bf16x2_of(Two v) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo_of(v), hi_of(v));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
@@ -304,14 +276,14 @@ __device__ __forceinline__ W8Unit w8_unit(const W8LargeArgs& p, int u) {
 template <int COLS>
 __device__ __forceinline__ bool w8_promote(const W8LargeArgs& p, uint32_t tmem, uint32_t acc_full, uint32_t acc_empty,
                                            const uint8_t* row_scale, const float* block_scale, int nk, int& g,
-                                           unsigned long long* acc, volatile int* abort_flag) {
+                                           Two* acc, volatile int* abort_flag) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < COLS / 2; ++i) acc[i] = 0ull;
   float sa = *reinterpret_cast<const float*>(row_scale), sw = block_scale[0];
   for (int kt = 0; kt < nk; ++kt, ++g) {
     const uint32_t s = __float_as_uint(sa * sw);       // exact: sa is a power of two
-    const unsigned long long s2 = pack2(s, s);
+    const Two s2 = pack2(s, s);
     if (kt + 1 < nk) {
       sa = *reinterpret_cast<const float*>(row_scale + static_cast<long long>(kt + 1) * kActTile);
       sw = block_scale[kt + 1];
@@ -340,7 +312,7 @@ __device__ __forceinline__ bool w8_promote(const W8LargeArgs& p, uint32_t tmem, 
 }
 
 template <int COLS>
-__device__ __forceinline__ void w8_store(const W8LargeArgs& p, const unsigned long long* acc, uint8_t* stg, int row0, int col0) {
+__device__ __forceinline__ void w8_store(const W8LargeArgs& p, const Two* acc, uint8_t* stg, int row0, int col0) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int c = 0; c < COLS; c += 32) {
@@ -486,7 +458,7 @@ __global__ void __launch_bounds__(W8L<SHARED>::THREADS, 1) a4w4_w8a8_large_kerne
     const int q = warp & 3, half = (warp - Cf::EPI_FIRST) >> 2;
     const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
     uint8_t* stg = smem + Cf::OFF_STG + (warp - Cf::EPI_FIRST) * 32 * Cf::STG_PITCH;
-    unsigned long long acc[64];
+    Two acc[64];
     int g = 0;
     for (int u = u0; u < p.units; u += G) {
       const W8Unit t = w8_unit(p, u);
@@ -502,7 +474,7 @@ __global__ void __launch_bounds__(W8L<SHARED>::THREADS, 1) a4w4_w8a8_large_kerne
         float4* mine = reinterpret_cast<float4*>(smem + (q * 32 + lane) * 512);
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          mine[(half * 16 + i) ^ lane] = make_float4(lo2(acc[2 * i]), hi2(acc[2 * i]), lo2(acc[2 * i + 1]), hi2(acc[2 * i + 1]));
+          mine[(half * 16 + i) ^ lane] = make_float4(lo_of(acc[2 * i]), hi_of(acc[2 * i]), lo_of(acc[2 * i + 1]), hi_of(acc[2 * i + 1]));
         const int et = threadIdx.x - 32 * Cf::EPI_FIRST;
         fence_proxy_async_smem();
         named_bar_sync(3, 32 * Cf::EPI_WARPS);
@@ -768,13 +740,13 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
       const int q = warp & 3;
       const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
       const float* block_scale = p.Ws + static_cast<long long>(w_tile) * p.KT + kt0;
-      unsigned long long acc[NX / 2];
+      Two acc[NX / 2];
 #pragma unroll
       for (int i = 0; i < NX / 2; ++i) acc[i] = 0ull;
       for (int i = 0; i < nk; ++i) {
         const int turn = i % (2 * Cf::RING), b = i % Cf::ACCS;
         const uint32_t sw = __float_as_uint(block_scale[i]);
-        const unsigned long long sw2 = pack2(sw, sw);
+        const Two sw2 = pack2(sw, sw);
         const bool ok = mbar_wait(scales + 8u * turn, static_cast<uint32_t>(i / (2 * Cf::RING)) & 1u, abort_flag, p.wait_ns, p.status) &&
                         mbar_wait(acc_full + 8u * b, static_cast<uint32_t>(i / Cf::ACCS) & 1u, abort_flag, p.wait_ns, p.status);
         if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -808,12 +780,12 @@ __global__ void __launch_bounds__(W8S<NX>::THREADS, 2) a4w4_w8a8_small_kernel(co
         for (int i = 0; i < NX; ++i)
           if (i < mvalid)
             p.C[static_cast<long long>(m0 + i) * p.N + w_tile * 128 + lrow] =
-                __bfloat16_as_ushort(__float2bfloat16_rn(i & 1 ? hi2(acc[i / 2]) : lo2(acc[i / 2])));
+                __bfloat16_as_ushort(__float2bfloat16_rn(i & 1 ? hi_of(acc[i / 2]) : lo_of(acc[i / 2])));
       } else if (ready) {
         float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
         for (int i = 0; i < NX; ++i)
-          if (i < mvalid) red[i * 128 + lrow] = i & 1 ? hi2(acc[i / 2]) : lo2(acc[i / 2]);
+          if (i < mvalid) red[i * 128 + lrow] = i & 1 ? hi_of(acc[i / 2]) : lo_of(acc[i / 2]);
       }
     }
     if (p.splits > 1 && !ready) *abort_flag = 1;       // this block's sums are not whole
