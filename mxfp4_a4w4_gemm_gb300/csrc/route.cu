@@ -19,8 +19,10 @@
 // largest score.  Where two neighbours of the chosen order (or a kept and a
 // dropped group) are nearer than that and do not come from the same inputs, the
 // candidates are compared again as sums of two floats (2^-44), and what then still is
-// open, or groups, the row over in 64 bits, of which an SM has few units (some 90 us
-// for 896 experts: of the rows met in practice none).
+// open, or groups, the row over in 64 bits, of which an SM has few units (some 65 us
+// for 896 experts).  Rows with more than 256 candidates go that way too, whatever they are
+// compared by: such as tie widely, of ordinary ones none.  4096 rows of equal logits take
+// 350 us for 896 experts, 130 for 257, 65 for 256; 256 in 8 groups of equal strength 180.
 #include <cfloat>
 
 #include "device.cuh"

@@ -11,15 +11,17 @@
 //
 //   small  few tokens: 128 weight rows are the MMA's M side, 16 or 32 tokens its N
 //          side, K split over the thread blocks of a cluster; activations are quantised
-//          in the kernel.  Bound by the weights' bytes.
+//          in the kernel.  Bound by latencies one after another (below).
 //   large  128 tokens x 256 weight rows per tile, one persistent thread block per SM,
 //          activations quantised once beforehand into tiles in the workspace; few tiles
 //          run as halves whose K is shared by a cluster.
 //
-// Small: 1 x 7168 x 4224 7.3 us (4.2 TB/s of weights; 4.5 us would be a copy's rate; the
-// rest is the launch, the first block's latency and the exchange of sums); 32 x 1536 x 7168
-// 7.6 us: set-up 0.8, first quantisation 1.4, products and sums of a share's four blocks 1.9,
-// exchange 1.0, output 0.4.  Large:
+// Small, call after call with the weights in L2 / over a ring of weights larger than L2, so
+// that they come from memory: 1 x 7168 x 4224 7.2 / 9.0 us (30 MB at a copy's rate: 4.5; the
+// rest is the launch, the first block's latency and the exchange of sums, which memory's
+// latency lengthens), 1 x 8448 x 7168 10.0 / 12.9, 32 x 1536 x 7168 7.5 / 7.9: set-up 0.8,
+// first quantisation 1.4, products and sums of a share's four blocks 1.9, exchange 1.0,
+// output 0.4.  Large:
 // 2048 x 8448 x 7168 115 us, 2.15 PFLOP/s: bound by the operands' way into the SM (48 KB
 // per block of K at about 64 bytes a clock) and by the loop from an accumulator read
 // to the MMAs that write it again.  A pair of SMs on one tile, more accumulators,
@@ -71,7 +73,8 @@ __device__ __forceinline__ void unpack16(const uint4& a, const uint4& b, float f
 // One row's block of 128 over eight neighbouring lanes (16 BF16 each, a and b):
 // amax 2^-e <= 448 with the smallest such e >= -126; codes of x 2^-e and the scale 2^e.
 // E4M3 is a floating type, so a power of two costs no precision against amax / 448, and
-// the scaling is exact.  An infinity or NaN in the block makes the scale NaN.
+// the scaling is exact.  An infinity in the block, or nothing but NaN, makes the scale NaN; a
+// NaN beside numbers has no part in it and goes on as a code.
 __device__ __forceinline__ uint4 quant128(const uint4& a, const uint4& b, float* scale) {
   uint32_t m = max_abs_of(a, b);
   uint32_t amax = max(m & 0xFFFFu, m >> 16);
@@ -282,7 +285,7 @@ __device__ __forceinline__ bool w8_promote(const W8LargeArgs& p, uint32_t tmem, 
   for (int i = 0; i < COLS / 2; ++i) acc[i] = 0ull;
   float sa = *reinterpret_cast<const float*>(row_scale), sw = block_scale[0];
   for (int kt = 0; kt < nk; ++kt, ++g) {
-    const uint32_t s = __float_as_uint(sa * sw);       // exact: sa is a power of two
+    const uint32_t s = __float_as_uint(sa * sw);       // exact above 2^-126: sa is a power of two
     const Two s2 = pack2(s, s);
     if (kt + 1 < nk) {
       sa = *reinterpret_cast<const float*>(row_scale + static_cast<long long>(kt + 1) * kActTile);
@@ -914,6 +917,7 @@ struct W8Cost {
 // A cluster stays within a GPC, so that fewer fit than the SMs' number says: 32 x 4224 x 1536 with
 // 9 shares (297 thread blocks of 304, but 33 clusters are a second wave) 11.5 us, with 6 6.5.
 // Shares that do not shorten the longest one only add to the sums: 4 x 1536 x 4224 with 16 5.0, with 11 4.6.
+// (All with the weights in L2; not fitted with weights that come from memory.)
 template <int NX>
 W8Cost small_cost(long long tiles, int kt) {
   W8Cost best{1, 0};

@@ -26,5 +26,5 @@ def heads(x, weight, eps, positions, inv_freq, rot, interleaved):
 
 
 def bound(want, reach):
-    """fp32 within 2^-20.2 of reach (the norm's reciprocal 2^-21.5, sine and cosine 2^-21.8, four roundings), then BF16."""
+    """fp32 within 2^-20.1 of reach (the norm's reciprocal 2^-20.9, sine and cosine 2^-22.7, four roundings), then BF16."""
     return 2.0 ** -8 * np.abs(want) + 2.0 ** -20 * reach + 2.0 ** -133
